@@ -1,0 +1,100 @@
+// Device helpers of the full-attention kernels: rotation angles, head rows of
+// eight channels a lane, e8m0 scales, page lookups.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gdn {
+namespace attn {
+
+// cos and sin of position * frequency.  freq is in turns per position as a
+// 64-bit binary fraction, so the product mod 2^64 is the angle's exact
+// fraction of a turn (the integer multiply drops whole turns); its upper 32
+// bits, signed, are within [-1/2, 1/2) turns and enter sincospi as f32 (2^-25
+// of a turn's half: below the f32 rounding of cos and sin themselves).
+__device__ __forceinline__ void rope_angle(long long pos, uint64_t freq, float &c, float &s) {
+    const uint64_t turns = (uint64_t)pos * freq;
+    const float x = (float)(int32_t)(turns >> 32) * (1.0f / 2147483648.0f);   // half turns, [-1, 1)
+    sincospif(x, &s, &c);
+}
+
+// Eight bf16 (16 bytes) to f32 and back.
+__device__ __forceinline__ void unpack8(const uint4 &r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+// The value of an e8m0 byte, 2^(byte - 127); 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
+}
+
+// The e8m0 byte of the smallest power of two s >= 2^-127 with amax <= 448 s,
+// from amax's bits (448 = 1.75 * 2^8); 255 for an infinity or NaN.
+__device__ __forceinline__ uint32_t e8m0_for(uint32_t amax_bits) {
+    const int e = (int)(amax_bits >> 23);
+    if (e == 255) return 255u;
+    const int byte = e - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return (uint32_t)(byte < 0 ? 0 : byte);
+}
+
+// 1 / e8m0_value(byte), exact (byte <= 247 for a finite row); NaN for 255.
+__device__ __forceinline__ float e8m0_inverse(uint32_t byte) {
+    return __uint_as_float(byte == 255 ? 0x7fffffffu : (254u - byte) << 23);
+}
+
+// Eight f32 to e4m3 codes, round to nearest even.
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i], x[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2], x[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void unpack8_e4m3(const uint2 &r, float (&x)[8]) {
+    const uint32_t w[2] = {r.x, r.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+// The cache row (in units of D channels) of head h at position p of a row
+// whose page-table line is `line`, or -1 without a valid page.
+__device__ __forceinline__ long long cache_row(const PagedCache &c, int Hkv, const int32_t *line, long long p, int h) {
+    if (p < 0 || (p >> c.shift) >= c.width) return -1;
+    const int32_t page = line[p >> c.shift];
+    if (page < 0 || page >= c.n_pages) return -1;
+    return (((long long)page * Hkv + h) << c.shift) + (p & (c.page - 1));
+}
+
+__device__ __forceinline__ int clamp_new(const int32_t *n_new, int b, int T) {
+    return n_new == nullptr ? T : min(max(n_new[b], 0), T);
+}
+
+}  // namespace attn
+}  // namespace gdn

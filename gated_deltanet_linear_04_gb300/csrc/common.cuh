@@ -8,10 +8,12 @@
 
 namespace gdn {
 
-// Error word bits set by kernels whose bounded waits give up.
+// Error word bits: kernels whose bounded waits give up, and cache positions
+// without a valid page.
 enum : unsigned {
     kErrMbarTimeout = 1u,
     kErrMmaTimeout = 2u,
+    kErrBadPage = 4u,
 };
 
 // Spin limit of every bounded wait: try_wait suspends for a hardware-chosen

@@ -18,6 +18,7 @@ struct Sizes {
 };
 
 int num_sms();  // SMs of the current device (cached per device)
+unsigned *device_error_word();  // the current device's error word (nullptr if it cannot be had)
 
 // Kernel attributes (dynamic shared memory, cluster size) belong to the
 // device context that was current when they were set, so a launcher applies
@@ -134,5 +135,54 @@ cudaError_t launch_backward_chunked(const Sizes &s, const uint16_t *q, const uin
                                     const uint16_t *dy, const float *dstate_out, float *dq, float *dk, float *dv,
                                     float *dg, float *dbeta, float *dstate_in, void *ws, unsigned *err,
                                     cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// Full-attention layers (attn_api.cu validates)
+// ---------------------------------------------------------------------------
+struct AttnSizes {
+    int B, T, Hq, Hkv, D, Drot;
+    bool inter;
+    float eps;
+};
+
+// A [B, T, heads, D] input: element (bt, h, d) at p[bt * ts + h * hs + d].
+struct HeadsIn {
+    const uint16_t *p;
+    long long ts, hs;
+};
+
+// A paged cache with the rows' page table (layouts in gdn.h).
+struct PagedCache {
+    void *k, *v;
+    uint8_t *ks, *vs;
+    const int32_t *table;
+    long long n_pages;
+    int width, page, shift;   // table columns; tokens per page = 1 << shift
+    bool fp8;
+};
+
+cudaError_t launch_qk_norm_rope(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
+                                const float *wk, const uint64_t *freqs, const int32_t *pos, const uint8_t *mask,
+                                uint16_t *q_out, uint16_t *k_out, cudaStream_t st);
+
+size_t qk_norm_rope_backward_workspace(const AttnSizes &s);
+cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
+                                         const float *wk, const uint64_t *freqs, const int32_t *pos,
+                                         const uint8_t *mask, const uint16_t *dq_out, const uint16_t *dk_out,
+                                         uint16_t *dq, uint16_t *dk, float *dwq, float *dwk, void *ws,
+                                         cudaStream_t st);
+
+cudaError_t launch_kv_append(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                             const float *wq, const float *wk, const uint64_t *freqs, const PagedCache &c,
+                             const int32_t *pos, const int32_t *n_new, uint16_t *q_out, unsigned *err,
+                             cudaStream_t st);
+
+cudaError_t launch_kv_read(const AttnSizes &s, const PagedCache &c, const int32_t *start, const int32_t *n,
+                           uint16_t *k_out, uint16_t *v_out, unsigned *err, cudaStream_t st);
+
+size_t attn_decode_workspace(const AttnSizes &s);
+cudaError_t launch_attn_decode(const AttnSizes &s, const uint16_t *q, const PagedCache &c, const int32_t *pos,
+                               const int32_t *n_new, const HeadsIn &gate, float scale, uint16_t *out, float *lse,
+                               void *ws, unsigned *err, cudaStream_t st);
 
 }  // namespace gdn

@@ -21,7 +21,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libgdn.so")
 
-GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT = range(5)
+GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, GDN_ERR_BAD_PAGE = range(6)
 
 # batch rows gdn_prefill_noalloc accepts (GDN_NOALLOC_MAX_ROWS in gdn.h)
 GDN_NOALLOC_MAX_ROWS = 4096
@@ -38,9 +38,24 @@ class GdnDims(ctypes.Structure):
                 ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("K", ctypes.c_int32), ("eps_qk", ctypes.c_float)]
 
 
+class GdnAttnDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("Drot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
+_HEADS = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64]      # pointer, token stride, head stride
+_ATTN = [ctypes.POINTER(GdnAttnDims)]
+_CACHE = [ctypes.POINTER(GdnKvCache), _P, ctypes.c_int32]       # cache, page table, its width
 _SIGS = {
     "gdn_conv_update": (ctypes.c_int, [ctypes.POINTER(GdnDims), _P, _P, _P, _P, _P, _P, _P, _P]),
     "gdn_gating": (ctypes.c_int, [ctypes.POINTER(GdnDims), _P, _P, _P, _P, _P, _P, _P]),
@@ -64,6 +79,14 @@ _SIGS = {
                                         [ctypes.c_size_t, _P]),
     "gdn_decode_host_staging_size": (ctypes.c_size_t, [ctypes.POINTER(GdnDims)]),
     "gdn_rmsnorm_gated": (ctypes.c_int, [ctypes.POINTER(GdnDims), _P, _P, _P, ctypes.c_float, _P, _P]),
+    "gdn_qk_norm_rope": (ctypes.c_int, _ATTN + _HEADS * 2 + [_P] * 8),
+    "gdn_qk_norm_rope_backward_workspace_size": (ctypes.c_size_t, _ATTN),
+    "gdn_qk_norm_rope_backward": (ctypes.c_int, _ATTN + _HEADS * 2 + [_P] * 12 + [ctypes.c_size_t, _P]),
+    "gdn_kv_append": (ctypes.c_int, _ATTN + _HEADS * 3 + [_P] * 3 + _CACHE + [_P] * 4),
+    "gdn_kv_read": (ctypes.c_int, _ATTN + _CACHE + [_P] * 5),
+    "gdn_attn_decode_workspace_size": (ctypes.c_size_t, _ATTN),
+    "gdn_attn_decode": (ctypes.c_int, _ATTN + [_P] + _CACHE + [_P] * 2 + _HEADS + [ctypes.c_float] + [_P] * 3 +
+                        [ctypes.c_size_t, _P]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_device_status": (ctypes.c_int, [_P]),
     "gdn_selftest_timeout": (ctypes.c_int, [_P]),

@@ -61,6 +61,25 @@ class Dims:
 
 
 @dataclasses.dataclass(frozen=True)
+class AttnDims:
+    """Sizes of one full-attention layer's core (``gdn_attn_dims``): B rows of
+    T tokens, Hq query and Hkv key/value heads of D channels, of which the
+    first Drot are rotated (in halves, or in adjacent pairs if interleaved)."""
+
+    B: int
+    T: int
+    Hq: int
+    Hkv: int
+    D: int
+    Drot: int = 0
+    interleaved: bool = False
+    eps: float = 1e-6
+
+    def with_(self, **kw) -> "AttnDims":
+        return dataclasses.replace(self, **kw)
+
+
+@dataclasses.dataclass(frozen=True)
 class Workload:
     name: str
     index: int

@@ -33,6 +33,12 @@
  *   - Channel order of qkv / conv_state / conv_w: C = 2*Hk*Dk + Hv*Dv channels,
  *     q heads [0, Hk*Dk), k heads [Hk*Dk, 2*Hk*Dk), v heads [2*Hk*Dk, C), each
  *     head's channels contiguous.
+ *
+ * The second half of this header (gdn_attn_dims on) holds the core of the
+ * full-attention layers that stand between the Gated DeltaNet layers of those
+ * models: per-head q/k norm with the rotary embedding, a paged key-value
+ * cache and the attention of new tokens over it.  Its conventions are the ones
+ * above except where it says otherwise.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -60,7 +66,8 @@ typedef enum gdn_status {
     GDN_ERR_INVALID_ARG = 1,   /* null / misaligned pointer, negative size, Hv % Hk != 0 */
     GDN_ERR_UNSUPPORTED = 2,   /* a size outside the supported set above */
     GDN_ERR_CUDA = 3,          /* a CUDA launch or attribute call failed */
-    GDN_ERR_TIMEOUT = 4        /* a bounded on-device wait gave up (see gdn_device_status) */
+    GDN_ERR_TIMEOUT = 4,       /* a bounded on-device wait gave up (see gdn_device_status) */
+    GDN_ERR_BAD_PAGE = 5       /* a cache position had no valid page (see gdn_device_status) */
 } gdn_status;
 
 /* Problem sizes: the fields of GatedDeltaConfig (mlex gated_delta.rs) plus the
@@ -384,8 +391,11 @@ GDN_API const char *gdn_status_string(gdn_status status);
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word, which a kernel sets when one of its bounded waits (on an mbarrier or
- * a tensor-core commit) gives up.  Returns GDN_OK, GDN_ERR_TIMEOUT, or
- * GDN_ERR_CUDA if the synchronisation itself failed. */
+ * a tensor-core commit) gives up, or when a position of a paged cache has no
+ * page (a page-table entry outside [0, n_pages), a negative position, or one
+ * past the table).  Returns GDN_OK, GDN_ERR_TIMEOUT (also when both kinds
+ * were recorded), GDN_ERR_BAD_PAGE, or GDN_ERR_CUDA if the synchronisation
+ * itself failed. */
 GDN_API gdn_status gdn_device_status(gdn_stream stream);
 
 /* Self-test of the failure path: launches a kernel whose bounded wait (on an
@@ -395,6 +405,145 @@ GDN_API gdn_status gdn_device_status(gdn_stream stream);
  * was not (or the device failed).  No fault or unbounded wait is involved;
  * the context stays usable. */
 GDN_API gdn_status gdn_selftest_timeout(gdn_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Full-attention layers
+ * ------------------------------------------------------------------------
+ * Sizes of one attention layer's core: B rows of T tokens, Hq query heads,
+ * Hkv key/value heads (Hq % Hkv == 0, query head h reads key head
+ * h / (Hq/Hkv)), D channels per head, of which the first Drot are rotated.
+ * Supported: D in {64, 128, 256}; Drot a multiple of 16 in [0, D];
+ * Hq/Hkv <= 16; Hq, Hkv <= 1024; B <= 65535; B, T >= 0 (a zero size is a
+ * no-op).  Others give GDN_ERR_UNSUPPORTED.
+ *   interleaved  0: channel i < Drot/2 turns with channel i + Drot/2;
+ *                1: channel 2i turns with channel 2i + 1
+ *   eps          epsilon of the per-head RMS norm, >= 0
+ *
+ * Inputs marked "heads" may be views of a packed projection: element
+ * (b, t, h, d) lies at ptr[(b*T + t)*token_stride + h*head_stride + d], both
+ * strides in elements, non-negative and multiples of 8 (so that every head
+ * starts on a 16-byte boundary).  Outputs are dense.  Index arrays (pos,
+ * n_new, page_table) need only 4-byte, masks no alignment.
+ *
+ * Rotation: `freqs` u64 [Drot/2] holds each pair's frequency in turns per
+ * position as a 64-bit binary fraction, round(f / (2 pi) * 2^64) mod 2^64 for
+ * f in radians.  The angle of position p is p * freqs[i] mod 2^64, exact to
+ * p * 2^-65 turns at any position.  NULL is allowed when Drot = 0. */
+typedef struct gdn_attn_dims {
+    int32_t B, T, Hq, Hkv, D, Drot, interleaved;
+    float eps;
+} gdn_attn_dims;
+
+/* A paged cache of keys and values: pages of page_size tokens, each page
+ * [Hkv, page_size, D], so that one head's tokens of a page are contiguous.
+ *   format     0: bf16.  1: e4m3 with one e8m0 scale byte per token and head,
+ *              [n_pages, Hkv, page_size]: the value is code * 2^(byte - 127),
+ *              byte 255 is NaN.  A row x of D values is written with the
+ *              smallest power of two s >= 2^-127 such that max|x| <= 448 s, as
+ *              codes rne(x / s); a row holding an infinity or NaN reads back
+ *              as NaN.  (A power of two costs an e4m3 code no precision but at
+ *              its subnormal end, and makes x / s and code * s exact.)
+ *   page_size  16, 32, 64, 128 or 256; n_pages * Hkv * page_size < 2^31
+ *   k_scale, v_scale are NULL for format 0.
+ * A page table i32 [B, table_width] names each row's pages in order: position
+ * p of row b lies in page page_table[b][p / page_size].  Rows may share pages.
+ * Entries that no accessed position needs are not looked at.  A position
+ * without a valid page is not written, reads as zeros and is not attended to;
+ * the device error word records it (GDN_ERR_BAD_PAGE). */
+typedef struct gdn_kv_cache {
+    void *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int64_t n_pages;
+    int32_t page_size, format;
+} gdn_kv_cache;
+
+/* Per-head RMS norm and rotary embedding of q and k in one pass.  Per head
+ * row x:  z = w x / sqrt(mean(x^2) + eps);  pair (a, b) of z at angle th:
+ * y_a = z_a cos th - z_b sin th, y_b = z_b cos th + z_a sin th; the channels
+ * from Drot on are z.  f32 arithmetic, one rounding to bf16.
+ *   q      bf16 heads [B, T, Hq, D] (in);  k bf16 heads [B, T, Hkv, D] (in)
+ *   wq, wk f32 [D] (in), or both NULL: no norm, z = x.  (A model that stores
+ *          its weights around zero passes 1 + w.)
+ *   pos    i32 [B, T] (in): the position of every token (may be negative)
+ *   mask   u8 [B, T] or NULL: a step with mask 0 writes zeros
+ *   q_out  bf16 [B, T, Hq, D] (out);  k_out bf16 [B, T, Hkv, D] (out); may be
+ *          q and k themselves if those are dense */
+GDN_API gdn_status gdn_qk_norm_rope(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                    int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                    int64_t k_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
+                                    const int32_t *pos, const uint8_t *mask, uint16_t *q_out, uint16_t *k_out,
+                                    gdn_stream stream);
+
+/* Its gradients.  dz = the inverse rotation of dy, xhat = x rstd:
+ *   dw = sum over tokens and heads of dz xhat
+ *   dx = rstd (w dz - xhat mean(w dz xhat))          (no norm: dx = dz)
+ * A masked step has zero gradients and does not enter dw.
+ *   q, k, wq, wk, freqs, pos, mask as above (the forward inputs)
+ *   dq_out bf16 [B, T, Hq, D], dk_out bf16 [B, T, Hkv, D] (in)
+ *   dq, dk bf16, dense, shaped alike (out): they feed the projections'
+ *          bf16 products, so they are rounded once here
+ *   dwq, dwk f32 [D] (out); NULL when wq, wk are
+ *   workspace  device scratch of gdn_qk_norm_rope_backward_workspace_size()
+ *          bytes on the device that runs the call (required with weights)
+ * The sums over tokens run in a fixed order: equal calls give equal bits. */
+GDN_API size_t gdn_qk_norm_rope_backward_workspace_size(const gdn_attn_dims *dims);
+GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                             int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                             int64_t k_head_stride, const float *wq, const float *wk,
+                                             const uint64_t *freqs, const int32_t *pos, const uint8_t *mask,
+                                             const uint16_t *dq_out, const uint16_t *dk_out, uint16_t *dq,
+                                             uint16_t *dk, float *dwq, float *dwk, void *workspace, size_t ws_bytes,
+                                             gdn_stream stream);
+
+/* New tokens of every row: norm and rotation of q and k as gdn_qk_norm_rope,
+ * keys and values quantised and written into the cache in the same pass.
+ *   q, k   as above; v bf16 heads [B, T, Hkv, D] (in)
+ *   pos    i32 [B] (in): tokens already in row b's cache; token t has
+ *          position pos[b] + t
+ *   n_new  i32 [B] or NULL (= T): row b's valid new tokens, clamped to [0, T];
+ *          the others are not written and give zero q
+ *   q_out  bf16 [B, T, Hq, D] (out)
+ * Keys and values are rounded to the cache's type once, from f32. */
+GDN_API gdn_status gdn_kv_append(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                 int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                 int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
+                                 int64_t v_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
+                                 const gdn_kv_cache *cache, const int32_t *page_table, int32_t table_width,
+                                 const int32_t *pos, const int32_t *n_new, uint16_t *q_out, gdn_stream stream);
+
+/* Positions start[b] .. start[b] + T - 1 of every row read back as bf16 (of an
+ * e4m3 cache exactly: code * 2^e is a bf16 value, but where it underflows).
+ *   start  i32 [B] (in);  n i32 [B] or NULL (= T): steps from n[b] on are zeros
+ *   k_out, v_out bf16 [B, T, Hkv, D] (out)
+ * dims->Hq, Drot are not used (but must be valid). */
+GDN_API gdn_status gdn_kv_read(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const int32_t *page_table,
+                               int32_t table_width, const int32_t *start, const int32_t *n, uint16_t *k_out,
+                               uint16_t *v_out, gdn_stream stream);
+
+/* Attention of dims->T (1..8) new tokens per row over the paged cache, which
+ * already holds them (gdn_kv_append): token t of row b sees the positions
+ * 0 .. pos[b] + t.  Per query row: s_j = scale q.k_j, out = softmax(s) V,
+ * lse = log sum_j exp(s_j).
+ *   q      bf16 [B, T, Hq, D] (in), dense: gdn_kv_append's q_out
+ *   pos, n_new as gdn_kv_append; a token past n_new[b], or one that sees no
+ *          key, gives zeros and lse = -inf
+ *   gate   bf16 heads [B, T, Hq, D] or NULL: out is multiplied by
+ *          sigmoid(gate), in f32 before its one rounding to bf16
+ *   scale  of the scores (usually 1/sqrt(D)); finite
+ *   out    bf16 [B, T, Hq, D] (out);  lse f32 [B, T, Hq] (out) or NULL
+ *   workspace  device scratch of gdn_attn_decode_workspace_size() bytes on the
+ *          device that runs the call: the partial results of rows whose
+ *          length is split over several CTAs.  They are joined in a fixed
+ *          order: equal calls give equal bits.
+ * Scores and sums are f32.  Softmax weights are rounded to 16 bits for the
+ * product with V.  Values and keys at positions that a token does not see do
+ * not enter its results, whatever they hold. */
+GDN_API size_t gdn_attn_decode_workspace_size(const gdn_attn_dims *dims);
+GDN_API gdn_status gdn_attn_decode(const gdn_attn_dims *dims, const uint16_t *q, const gdn_kv_cache *cache,
+                                   const int32_t *page_table, int32_t table_width, const int32_t *pos,
+                                   const int32_t *n_new, const uint16_t *gate, int64_t gate_token_stride,
+                                   int64_t gate_head_stride, float scale, uint16_t *out, float *lse, void *workspace,
+                                   size_t ws_bytes, gdn_stream stream);
 
 /* ABI version of this header (incremented on any signature change). */
 GDN_API int gdn_abi_version(void);
