@@ -130,6 +130,24 @@ bool encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_strided(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank,
+                         const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                         CUtensorMapSwizzle swizzle) {
+    const auto fn = tmap_encoder();
+    if (fn == nullptr || rank < 1 || rank > 5) return false;
+    cuuint64_t gdims[5], gstrides[4];
+    cuuint32_t gbox[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        gdims[i] = dims[i];
+        gbox[i] = box[i];
+        estr[i] = 1;
+        if (i > 0) gstrides[i - 1] = strides[i - 1];
+    }
+    return fn(map, dtype, (cuuint32_t)rank, const_cast<void *>(base), gdims, gstrides, gbox, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int elem_bytes, uint64_t rows,
                     uint64_t cols, uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
     const auto fn = tmap_encoder();

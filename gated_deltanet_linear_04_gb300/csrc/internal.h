@@ -72,6 +72,12 @@ bool encode_tmap_3d(CUtensorMap *map, const void *base, CUtensorMapDataType dtyp
 bool encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int elem_bytes, int rank,
                  const uint64_t *dims, const uint32_t *box, CUtensorMapSwizzle swizzle);
 
+// Encodes a tensor map of `rank` dimensions with the byte strides of all but
+// the innermost (dims and box innermost first).
+bool encode_tmap_strided(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank,
+                         const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                         CUtensorMapSwizzle swizzle);
+
 // Encodes a 2-D row-major tensor map (rows x cols, box rows x box_cols).
 bool encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int elem_bytes,
                     uint64_t rows, uint64_t cols, uint32_t box_rows, uint32_t box_cols,
