@@ -37,7 +37,7 @@ using namespace attn;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxRows = 64;      // query rows of a unit
 constexpr int kMinTiles = 4;      // least tiles of a share
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 24;
 constexpr int kSmemLimit = 227 * 1024;
 
 template <int D_, bool FP8_>
@@ -51,7 +51,7 @@ struct Geo {
     static constexpr int MT = KT / 16;
     static constexpr int KV = KT * ROWB;                       // bytes of a tile's keys
     static constexpr int STAGE = 2 * KV;
-    static constexpr int OSTR = D + 4;                         // row stride of the join buffer (floats)
+    static constexpr int OSTR = D + 4;                         // row stride of a join buffer (floats)
 };
 
 struct Params {
@@ -67,7 +67,7 @@ struct Params {
     unsigned *err;
     int B, T, Hq, Hkv, G, R;
     int RB, rows;       // row blocks of a (b, h), query rows of one
-    int RG, KL, stages, box_log2;
+    int RG, KL, stages, box_log2, copies;
     float scale2;       // scale * log2(e)
 };
 
@@ -77,12 +77,12 @@ struct Layout {
 };
 
 template <class G>
-__host__ __device__ Layout layout(int RG, int NT, int KL, int stages) {
+__host__ __device__ Layout layout(int RG, int NT, int KL, int copies, int stages) {
     const int rows = RG * NT * 8;
     Layout l;
     l.qf = stages * G::STAGE;
     l.obuf = l.qf + rows * G::D * 2;
-    l.ml = l.obuf + rows * G::OSTR * 4;
+    l.ml = l.obuf + copies * rows * G::OSTR * 4;
     l.qscale = l.ml + KL * rows * 8;
     l.scales = l.qscale + rows * 4;
     l.total = l.scales + (G::FP8 ? stages * 2 * G::KT : 0);
@@ -132,10 +132,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (low 16 bits) as an f16 pair, exactly.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes as two f16 pairs, exactly.
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 template <bool F16>
@@ -176,14 +178,33 @@ __device__ __forceinline__ RowLen row_len(const Params &p, int b) {
     return r;
 }
 
-// A share: tiles [start, end) of the list.  CTA c of `act` active ones has
-// start = floor(c * total / act).
-__device__ __forceinline__ long long share_start(long long c, long long total, long long act) {
-    return c * total / act;
+// The list of all units' tiles in `act` shares that differ by at most one
+// tile, the longer ones first.
+struct Shares {
+    unsigned act, base, extra;   // base or base + 1 tiles; `extra` shares have one more
+
+    __device__ Shares(unsigned total, unsigned ctas) {
+        act = min(ctas, max(total / kMinTiles, 1u));
+        base = total / act;
+        extra = total - base * act;
+    }
+    __device__ unsigned start(unsigned c) const { return c * base + min(c, extra); }
+    // the share that holds a tile
+    __device__ unsigned of(unsigned tile) const {
+        const unsigned cut = extra * (base + 1);
+        return tile < cut ? tile / (base + 1) : extra + (tile - cut) / base;
+    }
+};
+
+// Consumer warps at most: 11 and the producer leave 168 registers a thread,
+// 7 leave 255, which the widest accumulators (16 rows of 256 channels) need.
+template <class G, int NT>
+constexpr int max_consumers() {
+    return G::D * NT >= 512 ? 7 : 11;
 }
 
 template <class G, int NT>
-__global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v,
                                                              const Params p) {
     constexpr int D = G::D, KT = G::KT, MT = G::MT;
@@ -191,12 +212,12 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ uint32_t bad_boxes[kMaxStages];
-    __shared__ long long warp_sum_sh[8], found_off;
+    __shared__ unsigned warp_sum_sh[12], found_off;
     __shared__ int found_b;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int RG = p.RG, KL = p.KL, W = RG * KL, NST = p.stages;
-    const Layout lay = layout<G>(RG, NT, KL, NST);
+    const Layout lay = layout<G>(RG, NT, KL, p.copies, NST);
     grid_dep_launch();
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -210,57 +231,55 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
     }
     grid_dep_wait();
 
-    // the share: prefix sums of the rows' tiles, blockDim rows at a time
+    // the share: prefix sums of the rows' tiles, blockDim rows at a time (twice, if that is not all of them)
     const int heads = p.Hkv * p.RB, nthr = blockDim.x, nwarp = nthr / 32;
-    long long total = 0, start = 0, end = 0;
-    int act = 0;
+    const bool once = p.B <= nthr;
+    Shares sh(1, 1);
+    unsigned start = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        long long run = 0;
+        unsigned run = 0;
         for (int base = 0; base < p.B; base += nthr) {
             const int b = base + tid;
-            const long long v = b < p.B ? (long long)row_len<G>(p, b).tiles * heads : 0;
-            long long x = v;
+            const unsigned v = b < p.B ? (unsigned)(row_len<G>(p, b).tiles * heads) : 0;
+            unsigned x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
             __syncthreads();   // (also: barrier initialisation, the previous chunk's readers)
             if (lane == 31) warp_sum_sh[warp] = x;
             __syncthreads();
-            long long before = run, all = 0;
+            unsigned before = run, all = 0;
             for (int w = 0; w < nwarp; ++w) {
                 if (w < warp) before += warp_sum_sh[w];
                 all += warp_sum_sh[w];
             }
-            if (p.B <= nthr) {   // one chunk: its sum is the total
-                total = all;
-                act = (int)min((long long)gridDim.x, max(total / kMinTiles, 1LL));
-                start = share_start(blockIdx.x, total, act);
+            if (once) {
+                sh = Shares(all, gridDim.x);
+                start = sh.start(blockIdx.x);
             }
-            if ((pass == 1 || p.B <= nthr) && b < p.B && before + x - v <= start && start < before + x) {
+            if ((pass == 1 || once) && b < p.B && before + x - v <= start && start < before + x) {
                 found_b = b;
                 found_off = start - (before + x - v);
             }
             run += all;
         }
-        if (p.B <= nthr) break;
+        if (once) break;
         if (pass == 0) {
-            total = run;
-            act = (int)min((long long)gridDim.x, max(total / kMinTiles, 1LL));
-            start = share_start(blockIdx.x, total, act);
+            sh = Shares(run, gridDim.x);
+            start = sh.start(blockIdx.x);
         }
     }
     __syncthreads();
-    if ((int)blockIdx.x >= act) {
+    if (blockIdx.x >= sh.act) {
         if (tid == 0) p.meta[3 * blockIdx.x] = -1;
         return;
     }
-    end = share_start(blockIdx.x + 1, total, act);
     int b = found_b;
     RowLen len = row_len<G>(p, b);
-    int ui = (int)(found_off / len.tiles), ta = (int)(found_off % len.tiles);
-    long long left = end - start;
+    int ui = (int)(found_off / (unsigned)len.tiles), ta = (int)(found_off % (unsigned)len.tiles);
+    int left = (int)(sh.start(blockIdx.x + 1) - start);
     const int boxrows = 1 << p.box_log2;
     bool dead = false;
 
@@ -273,7 +292,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
         uint32_t ph = 1;
         uint32_t used = 0;
         while (left > 0) {
-            const int n = (int)min((long long)(len.tiles - ta), left);
+            const int n = min(len.tiles - ta, left);
             const int h = ui / p.RB;
             const int32_t *line = p.c.table + (long long)b * p.c.width;
             const int nbox = (int)((len.keys + boxrows - 1) >> p.box_log2);
@@ -365,13 +384,13 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
     constexpr uint32_t XMASK = G::SUBB - 16;
 
     int it = 0;                       // tiles of this CTA before the unit
-    int st = kl % NST;                // this lane's next tile: its stage and parity
+    int st = kl;                      // this lane's next tile: its stage and parity
     uint32_t ph = 0;
     int next = kl;                    // ... its number in the CTA
     bool first = true;
     if (tid == 0) p.meta[3 * blockIdx.x] = -1;
     while (left > 0) {
-        const int n = (int)min((long long)(len.tiles - ta), left);
+        const int n = min(len.tiles - ta, left);
         const int h = ui / p.RB, r0 = (ui % p.RB) * p.rows;
         const int nrows = min(p.rows, p.R - r0);
         const int n_new = len.n;
@@ -459,7 +478,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                 }
                 // S^T = K Q^T
                 if constexpr (!FP8) {
-#pragma unroll
+#pragma unroll 4
                     for (int ks = 0; ks < D / 16; ++ks) {
                         uint2 q[NT];
 #pragma unroll
@@ -474,7 +493,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                         }
                     }
                 } else {
-#pragma unroll
+#pragma unroll 2
                     for (int ks = 0; ks < D / 16; ks += 2) {
                         uint2 q[2][NT];
 #pragma unroll
@@ -488,8 +507,9 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                             ldsm4(kbase + mrow[a] + off, k);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const uint32_t a0 = codes_f16(k[2 * e]), a1 = codes_f16(k[2 * e + 1]);
-                                const uint32_t a2 = codes_f16(k[2 * e] >> 16), a3 = codes_f16(k[2 * e + 1] >> 16);
+                                uint32_t a0, a1, a2, a3;
+                                codes_f16(k[2 * e], a0, a2);
+                                codes_f16(k[2 * e + 1], a1, a3);
 #pragma unroll
                                 for (int c = 0; c < NT; ++c) mma<true>(s[a][c], a0, a1, a2, a3, q[e][c].x, q[e][c].y);
                             }
@@ -664,8 +684,9 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                                     }
                                     lo = __byte_perm(lo, 0, 0x3120);   // (key, key + 1) of channel 2g, then of 2g + 1
                                     hi = __byte_perm(hi, 0, 0x3120);
-                                    const uint32_t a0 = codes_f16(lo), a1 = codes_f16(lo >> 16);
-                                    const uint32_t a2 = codes_f16(hi), a3 = codes_f16(hi >> 16);
+                                    uint32_t a0, a1, a2, a3;
+                                    codes_f16(lo, a0, a1);
+                                    codes_f16(hi, a2, a3);
 #pragma unroll
                                     for (int c = 0; c < NT; ++c)
                                         mma<true>(acc[i + e][c], a0, a1, a2, a3, pf[a][c][0], pf[a][c][1]);
@@ -697,10 +718,8 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                                     if (FP8) {
                                         const uint32_t lo = __byte_perm(v[2 * e] & cut[0], 0, 0x3120);
                                         const uint32_t hi = __byte_perm(v[2 * e + 1] & cut[1], 0, 0x3120);
-                                        a0 = codes_f16(lo);
-                                        a1 = codes_f16(lo >> 16);
-                                        a2 = codes_f16(hi);
-                                        a3 = codes_f16(hi >> 16);
+                                        codes_f16(lo, a0, a1);
+                                        codes_f16(hi, a2, a3);
                                     } else {
                                         a0 = v[0] & cut[0];
                                         a1 = v[1] & cut[0];
@@ -725,9 +744,8 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
-            st += KL;
-            while (st >= NST) {
-                st -= NST;
+            if ((st += KL) >= NST) {
+                st = kl;
                 ph ^= 1;
             }
         }
@@ -762,8 +780,10 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                     acc[i][c][2 + x] *= f;
                 }
             }
-        for (int k = 0; k < KL; ++k) {
-            if (kl == k) {
+        // each round, one lane writes or adds to each copy of the join buffer
+        float *mine = obuf + (size_t)(kl % p.copies) * rows_pad * G::OSTR;
+        for (int round = 0; round * p.copies < KL; ++round) {
+            if (kl / p.copies == round) {
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -772,8 +792,8 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
                         for (int e = 0; e < 4; ++e) {
                             const int r = rg * NT * 8 + c * 8 + 2 * j + (e & 1);
                             const int d = i * 16 + (FP8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
-                            float *o = obuf + r * G::OSTR + d;
-                            *o = k == 0 ? acc[i][c][e] : *o + acc[i][c][e];
+                            float *o = mine + r * G::OSTR + d;
+                            *o = round == 0 ? acc[i][c][e] : *o + acc[i][c][e];
                         }
             }
             consumer_sync(threads);
@@ -791,6 +811,9 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = obuf[r * G::OSTR + d0 + e];
+            for (int k = 1; k < p.copies; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += obuf[(k * rows_pad + r) * G::OSTR + d0 + e];
             if (whole) {
                 const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
                 const long long bt = (long long)b * p.T + t;
@@ -814,9 +837,9 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
         }
         if (ta == 0 && !whole && tid == 0) {
             // the unit goes on: its last tile lies in the last share that starts at or before it
-            const long long last = start + (it - n) + len.tiles - 1;
+            const unsigned last = start + (it - n) + len.tiles - 1;
             p.meta[3 * blockIdx.x] = b * heads + ui;
-            p.meta[3 * blockIdx.x + 1] = (int)(((last + 1) * act + total - 1) / total - 1);
+            p.meta[3 * blockIdx.x + 1] = (int)sh.of(last);
             p.meta[3 * blockIdx.x + 2] = slot;
         }
         first = false;
@@ -830,12 +853,14 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(const __grid_consta
 }
 
 // Joins the partial results of the unit that starts in share blockIdx.x and
-// goes on, if there is one: rows blockIdx.y, + gridDim.y ...
+// goes on, if there is one: rows blockIdx.y, + gridDim.y ...  D/4 threads take
+// four channels each of a group of parts; a chain of few loads: what the
+// parts hold is asked for before their weights are known.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const Params p, int max_parts) {
-    constexpr int COLS = D / 4, GROUPS = 256 / COLS;
-    extern __shared__ float weight[];             // [max_parts], then [GROUPS][D]
-    __shared__ float red[8];
+__global__ void __launch_bounds__(512) attn_join_kernel(const Params p) {
+    constexpr int COLS = D / 4, GROUPS = 512 / COLS, UNROLL = 4;
+    __shared__ float4 sums[GROUPS][COLS];
+    __shared__ float red_m[GROUPS], red_l[GROUPS];
     grid_dep_launch();
     grid_dep_wait();
     const int c0 = blockIdx.x, unit = p.meta[3 * c0];
@@ -844,50 +869,60 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const Params p, int max_
     const int n = p.meta[3 * c0 + 1] - c0 + 1, first_slot = p.meta[3 * c0 + 2];
     const int heads = p.Hkv * p.RB, b = unit / heads, h = unit % heads / p.RB, r0 = (unit % heads % p.RB) * p.rows;
     const int nrows = min(p.rows, p.R - r0);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float *sums = weight + max_parts;
+    const int tid = threadIdx.x, col = tid % COLS, grp = tid / COLS;
     for (int r = blockIdx.y; r < nrows; r += gridDim.y) {
-        __syncthreads();
-        float top = -INFINITY;
-        for (int i = tid; i < n; i += 256) {
-            const int slot = i == 0 ? first_slot : 2 * (c0 + i);
-            top = fmaxf(top, p.part_ml[(size_t)slot * p.rows + r].x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) red[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
-        for (int i = tid; i < n; i += 256) {
-            const int slot = i == 0 ? first_slot : 2 * (c0 + i);
-            const float2 v = p.part_ml[(size_t)slot * p.rows + r];
-            weight[i] = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
-        }
-        __syncthreads();
-        const int col = tid % COLS, grp = tid / COLS;
+        // this group's parts, with a running maximum
+        float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-#pragma unroll 4
-        for (int i = grp; i < n; i += GROUPS) {
-            const int slot = i == 0 ? first_slot : 2 * (c0 + i);
-            const float w = weight[i];
-            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + ((size_t)slot * p.rows + r) * D + col * 4);
-            o.x = fmaf(w, x.x, o.x);
-            o.y = fmaf(w, x.y, o.y);
-            o.z = fmaf(w, x.z, o.z);
-            o.w = fmaf(w, x.w, o.w);
-            sum = fmaf(w, p.part_ml[(size_t)slot * p.rows + r].y, sum);
+        for (int i0 = grp; i0 < n; i0 += GROUPS * UNROLL) {
+            float2 v[UNROLL];
+            float4 x[UNROLL];
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k) {
+                const int i = i0 + k * GROUPS;
+                const size_t slot = i == 0 ? first_slot : 2 * (c0 + i);
+                v[k] = make_float2(-INFINITY, 0.0f);
+                x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < n) {
+                    v[k] = p.part_ml[slot * p.rows + r];
+                    x[k] = *reinterpret_cast<const float4 *>(p.part_o + (slot * p.rows + r) * D + col * 4);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k) top = fmaxf(top, v[k].x);
+            const float f = m == -INFINITY ? 0.0f : ex2(m - top);
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k) {
+                if (v[k].x == -INFINITY) continue;   // (a part in which the row saw nothing)
+                const float w = ex2(v[k].x - top);
+                l = fmaf(w, v[k].y, l);
+                o.x = fmaf(w, x[k].x, o.x);
+                o.y = fmaf(w, x[k].y, o.y);
+                o.z = fmaf(w, x[k].z, o.z);
+                o.w = fmaf(w, x[k].w, o.w);
+            }
+            m = top;
         }
-        reinterpret_cast<float4 *>(sums)[grp * COLS + col] = o;
-        __shared__ float gsum[32];
-        if (col == 0) gsum[grp] = sum;
+        __syncthreads();   // (the previous row's readers)
+        sums[grp][col] = o;
+        if (col == 0) {
+            red_m[grp] = m;
+            red_l[grp] = l;
+        }
         __syncthreads();
         if (tid < D) {
-            float acc = 0.0f, total = 0.0f;
+            float top = -INFINITY, acc = 0.0f, total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, red_m[i]);
+#pragma unroll
             for (int i = 0; i < GROUPS; ++i) {
-                acc += sums[i * D + tid];
-                total += gsum[i];
+                if (red_m[i] == -INFINITY) continue;
+                const float w = ex2(red_m[i] - top);
+                acc = fmaf(w, reinterpret_cast<const float *>(sums[i])[tid], acc);
+                total = fmaf(w, red_l[i], total);
             }
             const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
             const long long bt = (long long)b * p.T + t;
@@ -927,13 +962,22 @@ Workspace workspace(const AttnSizes &s) {
 template <class G, int NT>
 cudaError_t launch_t(Params &p, cudaStream_t st) {
     p.RG = (p.rows + NT * 8 - 1) / (NT * 8);
-    p.KL = p.RG == 1 ? 4 : p.RG == 2 ? 3 : p.RG == 3 ? 2 : 1;   // at most 8 warps with the producer: 255 registers
+    p.KL = max_consumers<G, NT>() / p.RG;
+    p.copies = 64 * 1024 / (p.RG * NT * 8 * G::OSTR * 4);
+    p.copies = p.copies < 1 ? 1 : p.copies > 4 ? 4 : p.copies;
+    if (p.copies > p.KL) p.copies = p.KL;
     int lg = 0;
     while ((1 << lg) < G::KT) ++lg;
     p.box_log2 = p.c.shift < lg ? p.c.shift : lg;
-    p.stages = 1;
-    while (p.stages < kMaxStages && layout<G>(p.RG, NT, p.KL, p.stages + 1).total <= kSmemLimit - 1024) ++p.stages;
-    const int smem = layout<G>(p.RG, NT, p.KL, p.stages).total;
+    // A stage always belongs to the same lane (stages a multiple of KL): fills may land out of order, and a lane
+    // that waits for a stage's fill k by its parity must have seen fill k - 1 land itself, or the parity of a fill
+    // k - 1 still on its way would read as fill k.
+    p.stages = p.KL;
+    while (p.stages + p.KL <= kMaxStages &&
+           layout<G>(p.RG, NT, p.KL, p.copies, p.stages + p.KL).total <= kSmemLimit - 1024)
+        p.stages += p.KL;
+    if (layout<G>(p.RG, NT, p.KL, p.copies, p.stages).total > kSmemLimit - 1024) return cudaErrorInvalidConfiguration;
+    const int smem = layout<G>(p.RG, NT, p.KL, p.copies, p.stages).total;
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, attn_decode_kernel<G, NT>, kSmemLimit - 1024);
     if (e != cudaSuccess) return e;
@@ -951,6 +995,9 @@ cudaError_t launch_t(Params &p, cudaStream_t st) {
                                  G::SUBB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
     }
+    // the tiles of a call are counted in 32 bits
+    if ((unsigned long long)p.B * p.Hkv * p.RB * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1) > 0x7fffffffULL)
+        return cudaErrorNotSupported;
     const int ctas = num_sms();
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -965,9 +1012,9 @@ cudaError_t launch_t(Params &p, cudaStream_t st) {
     e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<G, NT>, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ctas, p.rows < 8 ? p.rows : 8);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = (ctas + 3) / 4 * 16 + 256 / (G::D / 4) * G::D * sizeof(float);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D>, p, (ctas + 3) / 4 * 4);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D>, p);
 }
 
 template <int D>

@@ -427,6 +427,29 @@ def test_decode(attn, case, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(16, 2, 256, 1), (32, 8, 128, 4), (16, 2, 64, 3)])
+def test_decode_repeats_bit_for_bit(attn, Hq, Hkv, D, T, fp8):
+    """Many tiles per CTA, many calls back to back: the ring's fills land in
+    any order, the results are the same."""
+    d = wl.AttnDims(3, T, Hq, Hkv, D)
+    P, pos = 16, [60000, 45001, 70]
+    width = -(-(max(pos) + T) // P)
+    cache = make_cache(attn, d.with_(B=1), width, P, fp8)
+    (cache.k.view(torch.uint8) if fp8 else cache.k).random_(0, 120)
+    (cache.v.view(torch.uint8) if fp8 else cache.v).random_(0, 120)
+    if fp8:
+        cache.k_scale.view(torch.uint8).fill_(118)
+        cache.v_scale.view(torch.uint8).random_(115, 121)
+    table = torch.stack([torch.randperm(width, generator=gen(i)) for i in range(3)]).to(I32).to(DEV)
+    q = normal(gen(5), 3, T, Hq, D).to(DEV)
+    pg = torch.tensor(pos, dtype=I32, device=DEV)
+    want = attn.attn_decode(d, q, cache, table, pg)
+    got = [attn.attn_decode(d, q, cache, table, pg) for _ in range(100)]
+    same = [torch.equal(g, want) for g in got]
+    assert all(same) and status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_decode_ignores_unseen_slots(attn, fp8):
     """NaN and infinities in every slot past the rows' keys, and in a draft
     token's own key and value for the tokens before it."""
