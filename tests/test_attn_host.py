@@ -171,25 +171,24 @@ def test_binding_refuses_bad_heads(attn, kw, error, text):
 
 
 def test_head_views(attn):
-    """Strides of packed views, checked as far as the device check allows."""
-    class Fake(torch.Tensor):
-        is_cuda = property(lambda self: True)
-
-    def strides(t, shape):
-        return attn._heads(t.as_subclass(Fake), torch.Size(shape), "x")[1:]
+    """Views of a packed projection get as far as the device check; views
+    without one token stride, dense channels or 16-byte heads are refused."""
+    def call(t):
+        d = dims(B=t.shape[0], T=t.shape[1], Hq=t.shape[2], Hkv=1)
+        bt = (d.B, d.T)
+        attn.gdn_qk_norm_rope(d, t, meta(*bt, 1, 64), None, None, None, meta(*bt, dtype=torch.int32), None,
+                              meta(*bt, d.Hq, 64), meta(*bt, 1, 64))
 
     x = meta(2, 3, 12 * 64)
-    assert strides(x[..., 64:5 * 64].view(2, 3, 4, 64), (2, 3, 4, 64)) == (768, 64)
-    # every other half of heads twice as wide
-    assert strides(x[..., :512].view(2, 3, 4, 128)[..., 64:], (2, 3, 4, 64)) == (768, 128)
-    # one token per row: the rows' stride is the tokens'
-    assert strides(meta(5, 7, 4, 64)[:, 2:3], (5, 1, 4, 64)) == (7 * 256, 64)
-    assert strides(meta(1, 1, 1, 64), (1, 1, 1, 64)) == (0, 0)
-    assert strides(meta(2, 3, 4, 64).expand(2, 3, 4, 64), (2, 3, 4, 64)) == (256, 64)
+    for good in (x[..., 64:5 * 64].view(2, 3, 4, 64), x[..., :512].view(2, 3, 4, 128)[..., 64:],
+                 meta(5, 7, 4, 64)[:, 2:3], meta(1, 1, 1, 64), meta(1, 3, 4, 64).expand(1, 3, 4, 64),
+                 meta(2, 3, 1, 68)[..., :64].contiguous(), meta(1, 1, 1, 68)[..., :64]):
+        with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+            call(good)
     for bad in (meta(2, 4, 4, 64)[:, :3], meta(2, 3, 64, 4).transpose(2, 3), meta(2, 3, 4, 66)[..., :64],
                 meta(2, 3, 4, 128)[..., ::2], meta(3, 2, 4, 64).transpose(0, 1)):
-        with pytest.raises(ValueError):
-            strides(bad, (2, 3, 4, 64))
+        with pytest.raises(ValueError, match="stride"):
+            call(bad)
 
 
 def test_cache_handle_refusals(attn):
