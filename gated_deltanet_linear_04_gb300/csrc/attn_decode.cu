@@ -6,27 +6,32 @@
 // byte for 8 query heads per key head, bf16).
 //
 // Work.  A unit is one (row b, key head h, block of at most 64 of its T * Hq/Hkv
-// query rows); its keys come in tiles of KT.  The tiles of all units form one
-// list, cut into equal shares for one CTA per SM, so ragged batches and a
-// single long row both fill the GPU; each CTA finds its share from pos / n_new
-// itself.  A unit that crosses shares leaves partial results (m, sum, weighted
-// sum) in the workspace, and a second kernel joins them in share order.
+// query rows); its keys come in tiles of KT (32 KB of keys, 32 KB of values).
+// The tiles of all units form one list, cut into equal shares for one CTA per
+// SM, so ragged batches and a single long row both fill the GPU; each CTA
+// finds its share from pos / n_new itself.  A unit that crosses shares leaves
+// partial results (m, sum, weighted sum) in the workspace, and a second kernel
+// joins them in share order.
 //
-// CTA.  One warp keeps a ring of tiles filled with TMA box loads (a box: the
-// tokens of one page, or KT of them, 128-byte swizzled; a page that does not
-// exist is skipped and marked).  Consumer warps are RG groups of 8*NT query
-// rows times KL lanes: a tile goes to the RG warps of one lane, which keep
-// their own running maximum, sum and weighted sum, so nothing but the ring's
-// barriers is waited for inside a unit.  At its end the lanes are joined in
-// order through shared memory.
+// CTA.  Producer warps keep two rings (keys, values) filled with TMA box loads
+// (a box: the tokens of one page, or KT of them, 128-byte swizzled; a page
+// that does not exist is skipped and marked).  Eight consumer warps go through
+// a tile together: each takes 16 or 32 keys for S^T = K Q^T; each then takes
+// every eighth query row for the softmax; each then takes 1/8 of the channels
+// for O^T += V^T P^T.  S and P pass through shared memory, two barriers a tile.
+// So a warp's accumulators are small (16 to 32 channels of all rows), nothing
+// has to be joined at the end of a unit, and a tile is held only for the
+// microsecond that it takes all warps together, while the next two are on
+// their way.  (Warps that take whole tiles on their own, with all channels and
+// a join at the end of each unit, held each tile three times as long and lost
+// 5 us at each unit's end: 69 against 61 us for B = 128, e4m3, 2048 keys.)
 //
 // Products.  mma.sync m16n8k16 with keys (then channels) as the 16 and query
-// rows as the 8: S^T = K Q^T, O^T = V^T P^T.  Eight heads per key head fill
-// n = 8 exactly, where a 128-row tcgen05 tile would hold 8 rows of use, and
-// the tensor work is far from the bound.  S^T becomes P^T's operand by one
-// movmatrix per 8x8 block.  e4m3 codes are turned into f16 pairs on the way
-// from shared memory to the operand (exactly); their scales go to the scores
-// (keys) and into the exponent of the weights (values).
+// rows as the 8: eight heads per key head fill n = 8 exactly, where a 128-row
+// tcgen05 tile would hold 8 rows of use, and the tensor work is far from the
+// bound.  e4m3 codes are turned into f16 pairs on the way from shared memory to
+// the operand (exactly); their scales go to the scores (keys) and into the
+// exponent of the weights (values).
 #include "attn.cuh"
 
 namespace gdn {
@@ -35,10 +40,10 @@ namespace {
 using namespace attn;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kMaxRows = 64;      // query rows of a unit
-constexpr int kMinTiles = 4;      // least tiles of a share
-constexpr int kMaxStages = 24;
-constexpr int kSmemLimit = 227 * 1024;
+constexpr int kWarps = 8;         // consumer warps
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxStages = 4;
+constexpr int kSmemLimit = 226 * 1024;
 
 template <int D_, bool FP8_>
 struct Geo {
@@ -47,11 +52,15 @@ struct Geo {
     static constexpr int ROWB = FP8 ? D : 2 * D;               // bytes of a key
     static constexpr int SUBB = ROWB < 128 ? ROWB : 128;       // ... in sub-tiles of one swizzle span
     static constexpr int NSUB = ROWB / SUBB;
-    static constexpr int KT = FP8 ? (D == 256 ? 32 : 64) : 4096 / D;   // keys of a tile
-    static constexpr int MT = KT / 16;
-    static constexpr int KV = KT * ROWB;                       // bytes of a tile's keys
-    static constexpr int STAGE = 2 * KV;
-    static constexpr int OSTR = D + 4;                         // row stride of a join buffer (floats)
+    static constexpr int KT = 32768 / ROWB > 256 ? 256 : 32768 / ROWB;   // keys of a tile: 64, 128 or 256
+    static constexpr int TILE = KT * ROWB;                     // bytes of a tile's keys, or values
+    static constexpr int SPLIT = KT == 64 ? 2 : 1;             // 64 keys: two warps share 16 keys, half the channels each
+    static constexpr int MPW = KT == 256 ? 2 : 1;              // blocks of 16 keys of a warp
+    static constexpr int DPW = D == 256 ? 2 : 1;               // blocks of 16 channels of a warp (D = 64: of four warps)
+    static constexpr int SSTR = KT + 4;                        // row stride of S (floats): banks 8 apart for rows 2 apart
+    static constexpr int PSTR = KT + 8;                        // row stride of P (16-bit): banks 4 apart
+    static constexpr int PRODUCERS = FP8 ? 4 : 2;              // warps: keys, values, key scales, value scales
+    static constexpr int MAXROWS = KT == 256 ? 32 : 64;        // query rows of a unit (shared memory)
 };
 
 struct Params {
@@ -67,27 +76,27 @@ struct Params {
     unsigned *err;
     int B, T, Hq, Hkv, G, R;
     int RB, rows;       // row blocks of a (b, h), query rows of one
-    int RG, KL, stages, box_log2, copies;
+    int box_log2;
     float scale2;       // scale * log2(e)
 };
 
-// Offsets into dynamic shared memory (after the ring).
-struct Layout {
-    int qf, obuf, ml, qscale, scales, total;
+// Dynamic shared memory: the rings, then
+template <class G, int NT>
+struct Smem {
+    static constexpr int rows = NT * 8;
+    static constexpr int q_bytes = rows * G::D * 2;
+    static constexpr int s_bytes = G::SPLIT * rows * G::SSTR * 4;
+    static constexpr int p_bytes = rows * G::PSTR * 2;
+    static constexpr int row_bytes = rows * 20;                // corr, qscale, (m, l), fin
+    static constexpr int sc_bytes = G::FP8 ? 2 * G::KT : 0;    // a stage's scales
+    static constexpr int fixed = q_bytes + s_bytes + p_bytes + row_bytes;
+    static constexpr int pair = 2 * G::TILE + sc_bytes;        // a stage of both rings
+    static constexpr int fit = (kSmemLimit - 1024 - fixed) / pair;
+    static constexpr int stages = fit > kMaxStages ? kMaxStages : fit;
+    static constexpr int q = stages * 2 * G::TILE, s = q + q_bytes, p = s + s_bytes, row = p + p_bytes,
+                         sc = row + row_bytes, total = sc + stages * sc_bytes;
+    static_assert(stages >= 2, "");
 };
-
-template <class G>
-__host__ __device__ Layout layout(int RG, int NT, int KL, int copies, int stages) {
-    const int rows = RG * NT * 8;
-    Layout l;
-    l.qf = stages * G::STAGE;
-    l.obuf = l.qf + rows * G::D * 2;
-    l.ml = l.obuf + copies * rows * G::OSTR * 4;
-    l.qscale = l.ml + KL * rows * 8;
-    l.scales = l.qscale + rows * 4;
-    l.total = l.scales + (G::FP8 ? stages * 2 * G::KT : 0);
-    return l;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -107,13 +116,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
-}
-
-// The 8x8 matrix of 16-bit values held by the warp, transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
 }
 
 // d += a (16x16) b (16x8); f16 operands for an e4m3 cache, else bf16.
@@ -149,15 +151,6 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return pack2(a, b);
 }
 
-template <class G>
-__device__ __forceinline__ uint32_t sub_offset(int chunk, int substride) {
-    return (uint32_t)(chunk / (G::SUBB / 16)) * substride;
-}
-
-__device__ __forceinline__ void consumer_sync(int threads) {
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-}
-
 // The keys of row b (the new tokens' own included) and its tiles; a row
 // without keys still has one, empty, tile, so that its outputs get written.
 struct RowLen {
@@ -183,8 +176,8 @@ __device__ __forceinline__ RowLen row_len(const Params &p, int b) {
 struct Shares {
     unsigned act, base, extra;   // base or base + 1 tiles; `extra` shares have one more
 
-    __device__ Shares(unsigned total, unsigned ctas) {
-        act = min(ctas, max(total / kMinTiles, 1u));
+    __device__ void set(unsigned total, unsigned ctas) {
+        act = min(ctas, total);
         base = total / act;
         extra = total - base * act;
     }
@@ -196,45 +189,43 @@ struct Shares {
     }
 };
 
-// Consumer warps at most: 11 and the producer leave 168 registers a thread,
-// 7 leave 255, which the widest accumulators (16 rows of 256 channels) need.
-template <class G, int NT>
-constexpr int max_consumers() {
-    return G::D * NT >= 512 ? 7 : 11;
-}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 template <class G, int NT>
-__global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
-                                                             const __grid_constant__ CUtensorMap tm_v,
-                                                             const Params p) {
-    constexpr int D = G::D, KT = G::KT, MT = G::MT;
+__global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const Params p) {
+    using L = Smem<G, NT>;
+    constexpr int D = G::D, KT = G::KT, NST = L::stages;
     constexpr bool FP8 = G::FP8;
+    constexpr bool QREG = NT <= 2;           // query operands in registers; else read from shared memory each time
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
-    __shared__ uint32_t bad_boxes[kMaxStages];
-    __shared__ unsigned warp_sum_sh[12], found_off;
-    __shared__ int found_b;
+    __shared__ __align__(8) uint64_t full_k[NST], full_v[NST], empty_k[NST], empty_v[NST];
+    __shared__ uint32_t bad_boxes[NST];
+    __shared__ unsigned warp_sum_sh[kWarps + 4], found_off;
+    __shared__ int found_b, any_corr;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int RG = p.RG, KL = p.KL, W = RG * KL, NST = p.stages;
-    const Layout lay = layout<G>(RG, NT, KL, p.copies, NST);
     grid_dep_launch();
     if (tid == 0) {
+#pragma unroll
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], RG);
+            mbar_init(&full_k[i], FP8 ? 3 : 1);
+            mbar_init(&full_v[i], 1);
+            mbar_init(&empty_k[i], kWarps);
+            mbar_init(&empty_v[i], kWarps);
         }
         fence_mbar_init();
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
-        found_b = -1;
     }
     grid_dep_wait();
 
     // the share: prefix sums of the rows' tiles, blockDim rows at a time (twice, if that is not all of them)
-    const int heads = p.Hkv * p.RB, nthr = blockDim.x, nwarp = nthr / 32;
+    const int heads = p.Hkv * p.RB;
+    constexpr int nthr = (kWarps + G::PRODUCERS) * 32, nwarp = nthr / 32;
     const bool once = p.B <= nthr;
-    Shares sh(1, 1);
+    Shares sh;
     unsigned start = 0;
     for (int pass = 0; pass < 2; ++pass) {
         unsigned run = 0;
@@ -251,99 +242,90 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
             if (lane == 31) warp_sum_sh[warp] = x;
             __syncthreads();
             unsigned before = run, all = 0;
+#pragma unroll
             for (int w = 0; w < nwarp; ++w) {
                 if (w < warp) before += warp_sum_sh[w];
                 all += warp_sum_sh[w];
             }
+            run += all;
             if (once) {
-                sh = Shares(all, gridDim.x);
+                sh.set(all, gridDim.x);
                 start = sh.start(blockIdx.x);
             }
             if ((pass == 1 || once) && b < p.B && before + x - v <= start && start < before + x) {
                 found_b = b;
                 found_off = start - (before + x - v);
             }
-            run += all;
         }
         if (once) break;
         if (pass == 0) {
-            sh = Shares(run, gridDim.x);
+            sh.set(run, gridDim.x);
             start = sh.start(blockIdx.x);
         }
     }
     __syncthreads();
-    if (blockIdx.x >= sh.act) {
-        if (tid == 0) p.meta[3 * blockIdx.x] = -1;
-        return;
-    }
+    if (tid == 0) p.meta[3 * blockIdx.x] = -1;
+    if (blockIdx.x >= sh.act) return;
     int b = found_b;
     RowLen len = row_len<G>(p, b);
     int ui = (int)(found_off / (unsigned)len.tiles), ta = (int)(found_off % (unsigned)len.tiles);
     int left = (int)(sh.start(blockIdx.x + 1) - start);
     const int boxrows = 1 << p.box_log2;
     bool dead = false;
+    int st = 0;           // the tile's stage, and the parity of its fill
+    uint32_t ph = 0;
 
-    if (warp == W) {
-        // ---- producer -----------------------------------------------------
+    if (warp >= kWarps) {
+        // ---- producers: lane i < bpt fills box i of every tile -------------------------------------------
+        const int role = warp - kWarps;                  // keys, values, key scales, value scales
         const int bpt = KT >> p.box_log2, page_sh = p.c.shift - p.box_log2;   // boxes per tile; pages = boxes >> page_sh
-        const uint32_t box_bytes = (uint32_t)boxrows * G::ROWB;
-        const uint32_t tx = 2 * box_bytes + (FP8 ? 2 * boxrows : 0);
-        int st = 0;
-        uint32_t ph = 1;
+        const uint32_t bytes = role < 2 ? (uint32_t)boxrows * G::ROWB : (uint32_t)boxrows;
+        uint64_t *full = role == 1 ? full_v : full_k, *empty = role == 1 ? empty_v : empty_k;
+        unsigned char *ring = role < 2 ? smem + (role == 0 ? 0 : G::TILE) : smem + L::sc + (role - 2) * KT;
+        const int pitch = role < 2 ? 2 * G::TILE : 2 * KT;
+        const uint8_t *scales = role == 2 ? p.c.ks : p.c.vs;
         uint32_t used = 0;
         while (left > 0) {
-            const int n = min(len.tiles - ta, left);
-            const int h = ui / p.RB;
+            const int n = min(len.tiles - ta, left), h = ui / p.RB;
             const int32_t *line = p.c.table + (long long)b * p.c.width;
             const int nbox = (int)((len.keys + boxrows - 1) >> p.box_log2);
-            const int npage = (int)((len.keys + p.c.page - 1) >> p.c.shift);
-            if (len.short_table && lane == 0) atomicOr(p.err, kErrBadPage);
-            // page numbers, 32 at a time, the next 32 on their way
-            int w0 = ((ta * bpt) >> page_sh) & ~31;
-            int cur = w0 + lane < npage ? line[w0 + lane] : -1;
-            int nxt = w0 + 32 + lane < npage ? line[w0 + 32 + lane] : -1;
+            if (len.short_table && role == 0 && lane == 0) atomicOr(p.err, kErrBadPage);
+            int box = ta * bpt + lane;
+            auto ask = [&](int i, int bx) { return lane < bpt && i < n && bx < nbox ? line[bx >> page_sh] : -1; };
+            int id = ask(0, box), id1 = ask(1, box + bpt);   // page numbers, asked for two tiles ahead
             for (int i = 0; i < n; ++i) {
-                const int box0 = (ta + i) * bpt;
-                if ((box0 >> page_sh) >= w0 + 32) {
-                    w0 += 32;
-                    cur = nxt;
-                    nxt = w0 + 32 + lane < npage ? line[w0 + 32 + lane] : -1;
-                }
-                const int box = box0 + lane;
-                const int page = __shfl_sync(0xffffffffu, cur, ((lane < bpt ? box : box0) >> page_sh) - w0);
-                const bool want = lane < bpt && box < nbox;
-                const bool ok = want && page >= 0 && page < p.c.n_pages;
-                if (want && !ok) atomicOr(p.err, kErrBadPage);
+                const int id2 = ask(i + 2, box + 2 * bpt);
+                const bool want = lane < bpt && box < nbox, ok = want && id >= 0 && id < p.c.n_pages;
+                if (want && !ok && role == 0) atomicOr(p.err, kErrBadPage);
                 const uint32_t good = __ballot_sync(0xffffffffu, ok);
-                if (!dead && !mbar_wait(&empty[st], ph, p.err)) dead = true;
+                if (!dead && !mbar_wait(&empty[st], ph ^ 1, p.err)) dead = true;
                 dead = __any_sync(0xffffffffu, dead);
                 if (!dead) {
                     if (lane == 0) {
-                        bad_boxes[st] = ~good & ((1u << bpt) - 1);
+                        if (role == 0) bad_boxes[st] = ~good & (bpt == 32 ? 0xffffffffu : (1u << bpt) - 1);
                         if (good != 0)
-                            mbar_expect_tx(&full[st], __popc(good) * tx);
+                            mbar_expect_tx(&full[st], __popc(good) * bytes);
                         else
                             mbar_arrive(&full[st]);
-                        used |= 1u << st;
                     }
                     __syncwarp();
                     if (ok) {
-                        const int row =
-                            (int)((((long long)page * p.Hkv + h) << p.c.shift) + (((long long)box << p.box_log2) & (p.c.page - 1)));
-                        unsigned char *dst = smem + st * G::STAGE + lane * box_bytes;
-                        tma_load_3d(dst, &tm_k, 0, row, 0, &full[st]);
-                        tma_load_3d(dst + G::KV, &tm_v, 0, row, 0, &full[st]);
-                        if (FP8) {
-                            unsigned char *sc = smem + lay.scales + st * 2 * KT + lane * boxrows;
-                            bulk_load(sc, p.c.ks + row, boxrows, &full[st]);
-                            bulk_load(sc + KT, p.c.vs + row, boxrows, &full[st]);
-                        }
+                        const int row = ((id * p.Hkv + h) << p.c.shift) + ((box << p.box_log2) & (p.c.page - 1));
+                        unsigned char *dst = ring + st * pitch + lane * bytes;
+                        if (role < 2)
+                            tma_load_3d(dst, role == 0 ? &tm_k : &tm_v, 0, row, 0, &full[st]);
+                        else
+                            bulk_load(dst, scales + row, bytes, &full[st]);
                     }
+                    used |= 1u << st;
                     if (++st == NST) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
+                box += bpt;
+                id = id1;
+                id1 = id2;
             }
             left -= n;
             ta = 0;
@@ -353,10 +335,10 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
             }
         }
         // after a wait that gave up: let the copies in flight land before the CTA ends
-        if (dead && lane == 0) {
+        if (dead) {
             for (int i = 0; i < NST; ++i) {
                 if ((used >> i & 1) == 0) continue;
-                const uint32_t phase = i < st ? ph ^ 1 : ph;   // the parity of stage i's last fill
+                const uint32_t phase = i < st ? ph : ph ^ 1;   // the parity of stage i's last fill
                 for (uint32_t k = 0; k < kSpinLimit && !mbar_try_wait(&full[i], phase); ++k) {
                 }
             }
@@ -365,13 +347,13 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
     }
 
     // ---- consumers -----------------------------------------------------------
-    const int rg = warp % RG, kl = warp / RG, threads = W * 32;
     const int g = lane >> 2, j = lane & 3;
-    const int rows_pad = RG * NT * 8;
-    uint2 *qf = reinterpret_cast<uint2 *>(smem + lay.qf);
-    float *obuf = reinterpret_cast<float *>(smem + lay.obuf);
-    float2 *ml = reinterpret_cast<float2 *>(smem + lay.ml);        // [KL][rows_pad]
-    float *qscale = reinterpret_cast<float *>(smem + lay.qscale);
+    uint2 *qf = reinterpret_cast<uint2 *>(smem + L::q);            // [D/16][NT][32]
+    float *sS = reinterpret_cast<float *>(smem + L::s);            // [SPLIT][rows][SSTR]
+    uint16_t *sP = reinterpret_cast<uint16_t *>(smem + L::p);      // [rows][PSTR]
+    float *corr = reinterpret_cast<float *>(smem + L::row), *qscale = corr + L::rows;
+    float2 *ml = reinterpret_cast<float2 *>(qscale + L::rows);
+    float *fin = reinterpret_cast<float *>(ml + L::rows);
     const uint32_t ring = smem_u32(smem);
     // ldmatrix rows and 16-byte chunks of this lane: matrix mi holds rows (mi & 1) * 8 .. and chunk + (mi >> 1)
     // (keys; e4m3 values), or rows (mi >> 1) * 8 .. and chunk + (mi & 1) (bf16 values)
@@ -380,25 +362,33 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
     const uint32_t k_row = ((mi & 1) * 8 + mr) * G::SUBB, k_x = ((mi >> 1) ^ swz) << 4;
     const uint32_t v_row = FP8 ? k_row : (uint32_t)((mi >> 1) * 8 + mr) * G::SUBB;
     const uint32_t v_x = FP8 ? k_x : (uint32_t)((mi & 1) ^ swz) << 4;
-    const int substride = boxrows * G::SUBB;
-    constexpr uint32_t XMASK = G::SUBB - 16;
+    const uint32_t substride = boxrows * G::SUBB;
+    // the byte offset of 16-byte chunk `c` (even: a pair of chunks) of the rows at `row`, of this lane
+    auto at = [&](uint32_t row, uint32_t x, int c) {
+        return (uint32_t)(c / (G::SUBB / 16)) * substride + row + (x ^ ((c * 16) & (G::SUBB - 16)));
+    };
+    // ... and of key k0 (a multiple of 16) of a tile
+    auto key_base = [&](int k0) {
+        return (uint32_t)(k0 >> p.box_log2) * (boxrows * G::ROWB) + (k0 & (boxrows - 1)) * G::SUBB;
+    };
+    // this warp's part of S: keys and channels
+    const int s_key = G::SPLIT == 2 ? (warp & 3) * 16 : warp * 16 * G::MPW;
+    const int s_half = G::SPLIT == 2 ? warp >> 2 : 0;
+    constexpr int KS = D / 16 / G::SPLIT;                          // steps of 16 channels
+    // ... and of O: blocks of 16 channels (D = 64: the first four warps)
+    const bool has_o = warp * G::DPW * 16 < D;
+    // ... and of the softmax: rows warp, warp + 8, ...; keys 2 lane, 2 lane + 1 of every 64
 
-    int it = 0;                       // tiles of this CTA before the unit
-    int st = kl;                      // this lane's next tile: its stage and parity
-    uint32_t ph = 0;
-    int next = kl;                    // ... its number in the CTA
+    int done = 0;                     // tiles of this CTA before the unit
     bool first = true;
-    if (tid == 0) p.meta[3 * blockIdx.x] = -1;
     while (left > 0) {
         const int n = min(len.tiles - ta, left);
         const int h = ui / p.RB, r0 = (ui % p.RB) * p.rows;
         const int nrows = min(p.rows, p.R - r0);
-        const int n_new = len.n;
 
         // queries to operand order: 8 channels of a row per thread
-        for (int i = tid; i < rows_pad * (D / 8); i += threads) {
+        for (int i = tid; i < L::rows * (D / 8); i += kThreads) {
             const int r = i / (D / 8), d0 = (i % (D / 8)) * 8;
-            float x[8];
             uint4 raw = make_uint4(0, 0, 0, 0);
             if (r < nrows) {
                 const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
@@ -408,6 +398,7 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
             if (FP8) {
                 // a power of two per row brings the largest query to [1, 4): f16 then holds every bit but those
                 // below 2^-24 of it
+                float x[8];
                 unpack8(raw, x);
                 uint32_t top = 0;
 #pragma unroll
@@ -421,427 +412,374 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
                 for (int e = 0; e < 4; ++e) w[e] = pack16<true>(x[2 * e] * inv, x[2 * e + 1] * inv);
                 if (d0 == 0) qscale[r] = __uint_as_float((uint32_t)e2 << 23);
             }
-            const int rt = r >> 3, rr = r & 7, ks = d0 >> 4, hi = (d0 >> 3) & 1;
-            uint32_t *base = reinterpret_cast<uint32_t *>(qf) + ((((rt / NT) * (D / 16) + ks) * 32) * NT + rt % NT) * 2;
+            const int ks = d0 >> 4, hi = (d0 >> 3) & 1;
+            uint32_t *base = reinterpret_cast<uint32_t *>(qf + (ks * NT + (r >> 3)) * 32 + (r & 7) * 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 // bf16: k = 2e (+8 hi) of the 16; e4m3: channels 4j .. 4j+3 are k = 2j, 2j+1, 2j+8, 2j+9
-                const int ln = rr * 4 + (FP8 ? hi * 2 + (e >> 1) : e), reg = FP8 ? e & 1 : hi;
-                base[ln * NT * 2 + reg] = w[e];
+                const int ln = FP8 ? hi * 2 + (e >> 1) : e, reg = FP8 ? e & 1 : hi;
+                base[ln * 2 + reg] = w[e];
             }
         }
-        consumer_sync(threads);
-
-        float acc[D / 16][NT][4];
-        float m[NT][2], l[NT][2], mv[NT][2], rs[NT][2];
-        int lim[NT][2];               // visible keys of the lane's query rows (relative to 0), 0 for none
+        consumer_sync();
+        uint2 qr[QREG ? KS : 1][QREG ? NT : 1];
+        if (QREG) {
 #pragma unroll
-        for (int a = 0; a < NT; ++a) {
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m[a][c] = mv[a][c] = -INFINITY;
-                l[a][c] = 0.0f;
-                const int r = rg * NT * 8 + a * 8 + 2 * j + c;
-                const int t = (r0 + r) / p.G;
-                lim[a][c] = r < nrows && t < n_new ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : 0;
-                rs[a][c] = p.scale2 * (FP8 ? qscale[r] : 1.0f);
-            }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[i][a][c] = 0.0f;
+                for (int c = 0; c < NT; ++c) qr[ks][c] = qf[((s_half * KS + ks) * NT + c) * 32 + lane];
         }
+        // softmax state of this warp's rows
+        float m[NT], l[NT], mv[NT], rs[NT];
+        int lim[NT];                  // visible keys, 0 for a row that is not there
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            m[c] = mv[c] = -INFINITY;
+            l[c] = 0.0f;
+            const int r = c * 8 + warp, t = (r0 + r) / p.G;
+            lim[c] = r < nrows && t < len.n ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : 0;
+            rs[c] = p.scale2 * (FP8 ? qscale[r] : 1.0f);
+        }
+        float acc[G::DPW][NT][4];
+#pragma unroll
+        for (int i = 0; i < G::DPW; ++i)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.0f;
         const int all_see = (int)min(max(len.pos + 1, 0LL), len.keys);   // keys that every live row sees
-        const uint2 *myq = qf + (size_t)rg * (D / 16) * 32 * NT;
 
-        for (; next < it + n; next += KL) {
-            const int tile = ta + next - it;
-            if (!dead && !mbar_wait(&full[st], ph, p.err)) dead = true;
+        for (int i = 0; i < n; ++i) {
+            const int key0 = (ta + i) * KT;
+            const uint32_t kbase = ring + st * 2 * G::TILE, vbase = kbase + G::TILE;
+            // S^T = K Q^T
+            if (!dead && !mbar_wait(&full_k[st], ph, p.err)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
+            const uint32_t bad = *static_cast<volatile uint32_t *>(&bad_boxes[st]);
+            const bool tail = bad != 0 || key0 + KT > all_see;
             if (!dead) {
-                const uint32_t kbase = ring + st * G::STAGE, vbase = kbase + G::KV;
-                const uint32_t bad = bad_boxes[st];
-                const int key0 = tile * KT;
-                const bool tail = bad != 0 || key0 + KT > all_see;
-                float s[MT][NT][4];
 #pragma unroll
-                for (int a = 0; a < MT; ++a)
+                for (int a = 0; a < G::MPW; ++a) {
+                    const uint32_t base = kbase + key_base(s_key + a * 16);
+                    float s[NT][4];
 #pragma unroll
                     for (int c = 0; c < NT; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[a][c][e] = 0.0f;
-                uint32_t mrow[MT];
+                        for (int e = 0; e < 4; ++e) s[c][e] = 0.0f;
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                    const int k0 = a * 16;
-                    mrow[a] = (uint32_t)(k0 >> p.box_log2) * (boxrows * G::ROWB) + (k0 & (boxrows - 1)) * G::SUBB;
-                }
-                // S^T = K Q^T
-                if constexpr (!FP8) {
-#pragma unroll 4
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        uint2 q[NT];
+                    for (int ks = 0; ks < KS; ks += FP8 ? 2 : 1) {
+                        uint32_t k[4];
+                        ldsm4(base + at(k_row, k_x, FP8 ? ks : 2 * (s_half * KS + ks)), k);
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) q[c] = myq[(ks * 32 + lane) * NT + c];
-                        const uint32_t off = sub_offset<G>(2 * ks, substride) + k_row + (k_x ^ ((ks * 32) & XMASK));
-#pragma unroll
-                        for (int a = 0; a < MT; ++a) {
-                            uint32_t k[4];
-                            ldsm4(kbase + mrow[a] + off, k);
-#pragma unroll
-                            for (int c = 0; c < NT; ++c) mma<false>(s[a][c], k[0], k[1], k[2], k[3], q[c].x, q[c].y);
-                        }
-                    }
-                } else {
-#pragma unroll 2
-                    for (int ks = 0; ks < D / 16; ks += 2) {
-                        uint2 q[2][NT];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int c = 0; c < NT; ++c) q[e][c] = myq[((ks + e) * 32 + lane) * NT + c];
-                        const uint32_t off = sub_offset<G>(ks, substride) + k_row + (k_x ^ ((ks * 16) & XMASK));
-#pragma unroll
-                        for (int a = 0; a < MT; ++a) {
-                            uint32_t k[4];
-                            ldsm4(kbase + mrow[a] + off, k);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                uint32_t a0, a1, a2, a3;
+                        for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
+                            uint32_t a0 = k[0], a1 = k[1], a2 = k[2], a3 = k[3];
+                            if (FP8) {
                                 codes_f16(k[2 * e], a0, a2);
                                 codes_f16(k[2 * e + 1], a1, a3);
+                            }
 #pragma unroll
-                                for (int c = 0; c < NT; ++c) mma<true>(s[a][c], a0, a1, a2, a3, q[e][c].x, q[e][c].y);
+                            for (int c = 0; c < NT; ++c) {
+                                const uint2 q = QREG ? qr[QREG ? ks + e : 0][QREG ? c : 0]
+                                                     : qf[((s_half * KS + ks + e) * NT + c) * 32 + lane];
+                                mma<FP8>(s[c], a0, a1, a2, a3, q.x, q.y);
                             }
                         }
                     }
-                }
-                // scores in units of log2, the unseen ones -inf
-                float ve[MT][2];
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                    float ksc[2] = {1.0f, 1.0f};
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sS[(s_half * L::rows + c * 8 + 2 * j + (e & 1)) * G::SSTR + s_key + a * 16 + g + 8 * (e >> 1)] =
+                                s[c][e];
+                }
+                if (!FP8) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty_k[st]);
+                }
+            }
+            consumer_sync();
+
+            // softmax: weights of this warp's rows
+            bool moved = false;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int r = c * 8 + warp;
+                if (NT > 1 && r >= nrows) continue;
+                float s[KT / 64][2], ve[KT / 64][2];
+                float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < KT / 64; ++x) {
+                    const int key = x * 64 + 2 * lane;
+                    float2 v = *reinterpret_cast<const float2 *>(sS + r * G::SSTR + key);
+                    if (G::SPLIT == 2) {
+                        const float2 u = *reinterpret_cast<const float2 *>(sS + (L::rows + r) * G::SSTR + key);
+                        v.x += u.x;
+                        v.y += u.y;
+                    }
+                    s[x][0] = v.x * rs[c];
+                    s[x][1] = v.y * rs[c];
                     if (FP8) {
-                        const unsigned char *sc = smem + lay.scales + st * 2 * KT + a * 16 + g;
+                        const unsigned char *sc = smem + L::sc + st * 2 * KT + key;
+                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc);
+                        const uint32_t vb = *reinterpret_cast<const uint16_t *>(sc + KT);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            ksc[e] = e8m0_value(sc[e * 8]);
-                            const int vb = sc[KT + e * 8];
-                            ve[a][e] = vb == 255 ? __uint_as_float(0x7fffffffu) : (float)(vb - 127);
+                            s[x][e] *= e8m0_value(kb >> (8 * e) & 255u);
+                            const int y = vb >> (8 * e) & 255;
+                            ve[x][e] = y == 255 ? __uint_as_float(0x7fffffffu) : (float)(y - 127);
                         }
                     }
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[a][c][e] *= rs[c][e & 1] * ksc[e >> 1];
                     if (tail) {
+                        const bool there = (bad >> (key >> p.box_log2) & 1) == 0;   // (a box holds both keys)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = a * 16 + e * 8 + g;
-                            const bool there = (bad >> (key >> p.box_log2) & 1) == 0;
-                            if (FP8 && (!there || key0 + key >= len.keys)) ve[a][e] = 0.0f;
+                        for (int e = 0; e < 2; ++e)
+                            if (!there || key0 + key + e >= lim[c]) {
+                                s[x][e] = -INFINITY;
+                                ve[x][e] = 0.0f;
+                            }
+                    }
 #pragma unroll
-                            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    if (!there || key0 + key >= lim[c][x]) s[a][c][2 * e + x] = -INFINITY;
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        top = fmaxf(top, s[x][e]);
+                        if (FP8) topv = fmaxf(topv, s[x][e] + ve[x][e]);
                     }
                 }
-                // running maxima
-                bool moved = false;
-                float mnew[NT][2], mvnew[NT][2];
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
+                for (int o = 16; o > 0; o >>= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (FP8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+                }
+                const float mn = fmaxf(m[c], top), mvn = FP8 ? fmaxf(mv[c], topv) : mn;
+                // (an infinite maximum only where nothing, or an infinity, was seen)
+                const float base = mn == -INFINITY ? 0.0f : mn, basev = mvn == -INFINITY ? 0.0f : mvn;
+                l[c] *= ex2(m[c] - base);
+                float f = FP8 ? ex2(mv[c] - basev) : ex2(m[c] - base);
+                if (m[c] == -INFINITY && (!FP8 || mv[c] == -INFINITY)) f = 1.0f;   // (nothing to scale yet)
+                moved |= f != 1.0f;
+                if (lane == 0) corr[r] = f;
+                m[c] = mn;
+                mv[c] = mvn;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float t = s[0][c][x], tv = -INFINITY;
+                for (int x = 0; x < KT / 64; ++x) {
+                    float w[2];
 #pragma unroll
-                        for (int a = 0; a < MT; ++a) t = fmaxf(t, fmaxf(s[a][c][x], s[a][c][2 + x]));
-                        if (FP8) {
-#pragma unroll
-                            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    tv = fmaxf(tv, tail && s[a][c][2 * e + x] == -INFINITY ? -INFINITY
-                                                                                       : s[a][c][2 * e + x] + ve[a][e]);
-                        }
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                            if (FP8) tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
-                        }
-                        mnew[c][x] = fmaxf(m[c][x], t);
-                        mvnew[c][x] = FP8 ? fmaxf(mv[c][x], tv) : mnew[c][x];
-                        moved |= mnew[c][x] > m[c][x] || (FP8 && mvnew[c][x] > mv[c][x]);
+                    for (int e = 0; e < 2; ++e) {
+                        w[e] = ex2(s[x][e] - base);
+                        l[c] += w[e];
+                        if (FP8) w[e] = ex2(s[x][e] + ve[x][e] - basev);
                     }
-                if (__any_sync(0xffffffffu, moved)) {
+                    *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
+                }
+            }
+            if (moved && lane == 0) any_corr = done + i + 1;      // (the tile's number: no reset needed)
+            if (FP8 && !dead) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty_k[st]);          // (the scales lie in the key ring)
+            }
+            consumer_sync();
+
+            // O^T += V^T P^T
+            if (!dead && !mbar_wait(&full_v[st], ph, p.err)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            if (!dead) {
+                if (has_o) {
+                    if (*static_cast<volatile int *>(&any_corr) == done + i + 1) {
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
+                        for (int c = 0; c < NT; ++c) {
+                            const float2 f = *reinterpret_cast<const float2 *>(corr + c * 8 + 2 * j);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float f = mnew[c][x] == -INFINITY ? 1.0f : ex2(m[c][x] - mnew[c][x]);
-                            const float fv = !FP8 ? f : mvnew[c][x] == -INFINITY ? 1.0f : ex2(mv[c][x] - mvnew[c][x]);
-                            l[c][x] *= f;
-                            m[c][x] = mnew[c][x];
-                            mv[c][x] = mvnew[c][x];
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                acc[i][c][x] *= fv;
-                                acc[i][c][2 + x] *= fv;
+                            for (int d = 0; d < G::DPW; ++d) {
+                                acc[d][c][0] *= f.x;
+                                acc[d][c][1] *= f.y;
+                                acc[d][c][2] *= f.x;
+                                acc[d][c][3] *= f.y;
                             }
                         }
-                }
-                // weights, and P^T in operand order
-                uint32_t pf[MT][NT][2];
-#pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    float base[2], basev[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        base[x] = m[c][x] == -INFINITY ? 0.0f : m[c][x];
-                        basev[x] = mv[c][x] == -INFINITY ? 0.0f : mv[c][x];
                     }
-#pragma unroll
-                    for (int a = 0; a < MT; ++a)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float w[2];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float v = s[a][c][2 * e + x], wl = ex2(v - base[x]);
-                                l[c][x] += wl;
-                                w[x] = !FP8 ? wl : tail && v == -INFINITY ? 0.0f : ex2(v + ve[a][e] - basev[x]);
-                            }
-                            pf[a][c][e] = transpose8x8(pack16<FP8>(w[0], w[1]));
-                        }
-                }
-                // O^T += V^T P^T; values of slots that hold no key are zeroed (0 times NaN is NaN)
-                uint32_t keep[MT][2];
-                bool window = false;          // a NaN or infinity among the values that only later tokens see
-                if (tail) {
-#pragma unroll
-                    for (int a = 0; a < MT; ++a)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = a * 16 + e * 8 + 2 * j;
-                            const bool there = (bad >> (key >> p.box_log2) & 1) == 0;
-                            keep[a][e] = there ? (key0 + key < len.keys ? 0xffffu : 0u) |
-                                                     (key0 + key + 1 < len.keys ? 0xffff0000u : 0u)
-                                               : 0u;
-                        }
-                    if (p.T > 1) {
+                    // a NaN or infinity among the values that only later tokens see: 0 times it is not 0
+                    bool window = false;
+                    if (tail && p.T > 1) {
                         for (int key = max(all_see - key0, 0); key < KT && key0 + key < len.keys; ++key) {
                             if (bad >> (key >> p.box_log2) & 1) continue;
-                            const unsigned char *row = smem + st * G::STAGE + G::KV +
+                            const unsigned char *row = smem + st * 2 * G::TILE + G::TILE +
                                                        (key >> p.box_log2) * (boxrows * G::ROWB) +
                                                        (key & (boxrows - 1)) * G::SUBB;
-                            for (int i = lane; i < G::ROWB / 4; i += 32) {
-                                const uint32_t x = *reinterpret_cast<const uint32_t *>(
-                                    row + (i / (G::SUBB / 4)) * substride + (i % (G::SUBB / 4)) * 4);
+                            for (int x = lane; x < G::ROWB / 4; x += 32) {
+                                const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                                    row + (x / (G::SUBB / 4)) * substride + (x % (G::SUBB / 4)) * 4);
                                 if (FP8) {
-                                    const uint32_t y = x & 0x7f7f7f7fu;
+                                    const uint32_t y = v & 0x7f7f7f7fu;
                                     window |= (y & 0xff) == 0x7f || (y & 0xff00) == 0x7f00 ||
                                               (y & 0xff0000) == 0x7f0000 || (y >> 24) == 0x7f;
                                 } else {
-                                    window |= (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+                                    window |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
                                 }
                             }
                         }
                         window = __any_sync(0xffffffffu, window);
                     }
-                }
-                if (!window) {
+                    // the usual pass, or one pass per token over the values it sees, the other rows' sums dropped
+                    const int passes = window ? len.n : 1;
+                    for (int t = 0; t < passes; ++t) {
+                        const int see = window ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : (int)len.keys;
+                        auto step = [&](int kk, bool masked, float (&sum)[G::DPW][NT][4]) {
+                            uint32_t pf[NT][2], vraw[4];
 #pragma unroll
-                    for (int a = 0; a < MT; ++a) {
-                        if constexpr (!FP8) {
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                uint32_t v[4];
-                                ldsm4t(vbase + mrow[a] + sub_offset<G>(2 * i, substride) + v_row + (v_x ^ ((i * 32) & XMASK)),
-                                       v);
-                                if (tail) {
-                                    v[0] &= keep[a][0];
-                                    v[1] &= keep[a][0];
-                                    v[2] &= keep[a][1];
-                                    v[3] &= keep[a][1];
-                                }
-#pragma unroll
-                                for (int c = 0; c < NT; ++c)
-                                    mma<false>(acc[i][c], v[0], v[1], v[2], v[3], pf[a][c][0], pf[a][c][1]);
+                            for (int c = 0; c < NT; ++c) {
+                                const uint16_t *row = sP + (c * 8 + g) * G::PSTR + kk * 16 + 2 * j;
+                                pf[c][0] = *reinterpret_cast<const uint32_t *>(row);
+                                pf[c][1] = *reinterpret_cast<const uint32_t *>(row + 8);
                             }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < D / 16; i += 2) {
-                                uint32_t v[4];
-                                ldsm4t(vbase + mrow[a] + sub_offset<G>(i, substride) + v_row + (v_x ^ ((i * 16) & XMASK)), v);
+                            // values of slots that hold no key are zeroed
+                            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                            if (masked) {
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    uint32_t lo = v[2 * e], hi = v[2 * e + 1];
-                                    if (tail) {
-                                        lo &= keep[a][0];
-                                        hi &= keep[a][1];
+                                    const int key = kk * 16 + e * 8 + 2 * j;
+                                    const bool there = (bad >> (key >> p.box_log2) & 1) == 0;
+                                    keep[e] = there ? (key0 + key < see ? 0xffffu : 0u) |
+                                                          (key0 + key + 1 < see ? 0xffff0000u : 0u)
+                                                    : 0u;
+                                }
+                            }
+                            const uint32_t base = vbase + key_base(kk * 16);
+#pragma unroll
+                            for (int d = 0; d < G::DPW; ++d) {
+                                const int dt = warp * G::DPW + d;      // block of 16 channels
+                                uint32_t v[4];
+                                if (!FP8) {
+                                    ldsm4t(base + at(v_row, v_x, 2 * dt), v);
+                                    if (masked) {
+                                        v[0] &= keep[0];
+                                        v[1] &= keep[0];
+                                        v[2] &= keep[1];
+                                        v[3] &= keep[1];
+                                    }
+                                } else {
+                                    // (two warps of D <= 128 read the same pair of blocks and use one each)
+                                    if (G::DPW == 1 || d == 0) ldsm4t(base + at(v_row, v_x, dt & ~1), vraw);
+                                    const int e = G::DPW == 1 ? dt & 1 : d;
+                                    uint32_t lo = e ? vraw[2] : vraw[0], hi = e ? vraw[3] : vraw[1];
+                                    if (masked) {
+                                        lo &= keep[0];
+                                        hi &= keep[1];
                                     }
                                     lo = __byte_perm(lo, 0, 0x3120);   // (key, key + 1) of channel 2g, then of 2g + 1
                                     hi = __byte_perm(hi, 0, 0x3120);
-                                    uint32_t a0, a1, a2, a3;
-                                    codes_f16(lo, a0, a1);
-                                    codes_f16(hi, a2, a3);
-#pragma unroll
-                                    for (int c = 0; c < NT; ++c)
-                                        mma<true>(acc[i + e][c], a0, a1, a2, a3, pf[a][c][0], pf[a][c][1]);
+                                    codes_f16(lo, v[0], v[1]);
+                                    codes_f16(hi, v[2], v[3]);
                                 }
+#pragma unroll
+                                for (int c = 0; c < NT; ++c)
+                                    mma<FP8>(sum[d][c], v[0], v[1], v[2], v[3], pf[c][0], pf[c][1]);
                             }
-                        }
-                    }
-                } else {
-                    // one token at a time: its rows' products over the values it sees, the others' dropped
-                    for (int t = 0; t < n_new; ++t) {
-                        const int see = (int)min(max(len.pos + t + 1, 0LL), len.keys) - key0;
+                        };
+                        if (!tail) {
+#pragma unroll 4
+                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, false, acc);
+                        } else if (!window) {
+#pragma unroll 1
+                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, true, acc);
+                        } else {
+                            float one[G::DPW][NT][4] = {};
+#pragma unroll 1
+                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, true, one);
 #pragma unroll
-                        for (int a = 0; a < MT; ++a) {
-                            uint32_t cut[2];
+                            for (int c = 0; c < NT; ++c)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = a * 16 + e * 8 + 2 * j;
-                                cut[e] = keep[a][e] & ((key < see ? 0xffffu : 0u) | (key + 1 < see ? 0xffff0000u : 0u));
-                            }
+                                for (int e = 0; e < 4; ++e)
+                                    if ((r0 + c * 8 + 2 * j + (e & 1)) / p.G == t) {
 #pragma unroll
-                            for (int i = 0; i < D / 16; i += FP8 ? 2 : 1) {
-                                uint32_t v[4];
-                                ldsm4t(vbase + mrow[a] + sub_offset<G>(FP8 ? i : 2 * i, substride) + v_row +
-                                           (v_x ^ ((FP8 ? i * 16 : i * 32) & XMASK)),
-                                       v);
-#pragma unroll
-                                for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
-                                    uint32_t a0, a1, a2, a3;
-                                    if (FP8) {
-                                        const uint32_t lo = __byte_perm(v[2 * e] & cut[0], 0, 0x3120);
-                                        const uint32_t hi = __byte_perm(v[2 * e + 1] & cut[1], 0, 0x3120);
-                                        codes_f16(lo, a0, a1);
-                                        codes_f16(hi, a2, a3);
-                                    } else {
-                                        a0 = v[0] & cut[0];
-                                        a1 = v[1] & cut[0];
-                                        a2 = v[2] & cut[1];
-                                        a3 = v[3] & cut[1];
+                                        for (int d = 0; d < G::DPW; ++d) acc[d][c][e] += one[d][c][e];
                                     }
-#pragma unroll
-                                    for (int c = 0; c < NT; ++c) {
-                                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                        mma<FP8>(d, a0, a1, a2, a3, pf[a][c][0], pf[a][c][1]);
-#pragma unroll
-                                        for (int x = 0; x < 4; ++x) {
-                                            const int r = r0 + rg * NT * 8 + c * 8 + 2 * j + (x & 1);
-                                            if (r / p.G == t) acc[i + e][c][x] += d[x];
-                                        }
-                                    }
-                                }
-                            }
                         }
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
+                if (lane == 0) mbar_arrive(&empty_v[st]);
             }
-            if ((st += KL) >= NST) {
-                st = kl;
+            if (++st == NST) {
+                st = 0;
                 ph ^= 1;
             }
         }
-        it += n;
 
-        // join the lanes, in their order
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[c][x] += __shfl_xor_sync(0xffffffffu, l[c][x], o);
-                if (lim[c][x] == 0) {   // (a token that is not there saw what the first one sees)
-                    m[c][x] = -INFINITY;
-                    l[c][x] = 0.0f;
-                }
-                if (g == 0) ml[kl * rows_pad + rg * NT * 8 + c * 8 + 2 * j + x] = make_float2(m[c][x], l[c][x]);
-            }
-        consumer_sync(threads);
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = rg * NT * 8 + c * 8 + 2 * j + x;
-                float top = -INFINITY;
-                for (int k = 0; k < KL; ++k) top = fmaxf(top, ml[k * rows_pad + r].x);
-                // this lane's sums in units of 2^top
-                const float f = m[c][x] == -INFINITY ? 0.0f : ex2(m[c][x] - top) * (FP8 ? ex2(mv[c][x] - m[c][x]) : 1.0f);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    acc[i][c][x] *= f;
-                    acc[i][c][2 + x] *= f;
-                }
-            }
-        // each round, one lane writes or adds to each copy of the join buffer
-        float *mine = obuf + (size_t)(kl % p.copies) * rows_pad * G::OSTR;
-        for (int round = 0; round * p.copies < KL; ++round) {
-            if (kl / p.copies == round) {
-#pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = rg * NT * 8 + c * 8 + 2 * j + (e & 1);
-                            const int d = i * 16 + (FP8 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
-                            float *o = mine + r * G::OSTR + d;
-                            *o = round == 0 ? acc[i][c][e] : *o + acc[i][c][e];
-                        }
-            }
-            consumer_sync(threads);
-        }
         // the unit's output, or this share's part of it
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            float sum = l[c];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) {
+                // (a token that is not there has no visible key; mv - m: the weighted sum in units of 2^m)
+                const bool none = lim[c] == 0 || m[c] == -INFINITY;
+                ml[c * 8 + warp] = make_float2(none ? -INFINITY : m[c], none ? 0.0f : sum);
+                fin[c * 8 + warp] = none ? 0.0f : FP8 ? ex2(mv[c] - m[c]) : 1.0f;
+            }
+        }
+        consumer_sync();
         const bool whole = ta == 0 && n == len.tiles;
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
-        for (int i = tid; i < nrows * (D / 8); i += threads) {
-            const int r = i / (D / 8), d0 = (i % (D / 8)) * 8;
-            float top = -INFINITY, sum = 0.0f, o[8];
-            for (int k = 0; k < KL; ++k) top = fmaxf(top, ml[k * rows_pad + r].x);
-            for (int k = 0; k < KL; ++k) {
-                const float2 v = ml[k * rows_pad + r];
-                sum += v.x == -INFINITY ? 0.0f : v.y * ex2(v.x - top);
-            }
+        if (has_o) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = obuf[r * G::OSTR + d0 + e];
-            for (int k = 1; k < p.copies; ++k)
+            for (int c = 0; c < NT; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] += obuf[(k * rows_pad + r) * G::OSTR + d0 + e];
-            if (whole) {
-                const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
-                const long long bt = (long long)b * p.T + t;
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                for (int x = 0; x < 2; ++x) {
+                    const int r = c * 8 + 2 * j + x;
+                    if (r >= nrows) continue;
+                    const float2 v = ml[r];
+                    const float f = fin[r];
+                    const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
+                    const long long bt = (long long)b * p.T + t;
+                    const float inv = v.y == 0.0f ? 0.0f : 1.0f / v.y;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = sum == 0.0f ? 0.0f : o[e] * inv;
-                if (p.gate.p != nullptr) {
-                    float z[8];
-                    unpack8(*reinterpret_cast<const uint4 *>(p.gate.p + bt * p.gate.ts + hq * p.gate.hs + d0), z);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] *= sigmoid(z[e]);
+                    for (int d = 0; d < G::DPW; ++d) {
+                        // channels d0, d1 of this thread's two values
+                        const int dt = (warp * G::DPW + d) * 16, d0 = FP8 ? dt + 2 * g : dt + g, d1 = FP8 ? d0 + 1 : d0 + 8;
+                        float o0 = acc[d][c][x], o1 = acc[d][c][2 + x];
+                        if (v.y == 0.0f) o0 = o1 = 0.0f;           // (also of a token that is not there)
+                        o0 *= f;
+                        o1 *= f;
+                        if (!whole) {
+                            float *dst = p.part_o + ((size_t)slot * p.rows + r) * D;
+                            dst[d0] = o0;
+                            dst[d1] = o1;
+                            continue;
+                        }
+                        o0 *= inv;
+                        o1 *= inv;
+                        if (p.gate.p != nullptr) {
+                            const uint16_t *z = p.gate.p + bt * p.gate.ts + hq * p.gate.hs;
+                            o0 *= sigmoid(bf16_to_f32(z[d0]));
+                            o1 *= sigmoid(bf16_to_f32(z[d1]));
+                        }
+                        uint16_t *dst = p.out + (bt * p.Hq + hq) * D;
+                        if (FP8) {
+                            *reinterpret_cast<uint32_t *>(dst + d0) = pack2(o0, o1);
+                        } else {
+                            dst[d0] = f32_to_bf16(o0);
+                            dst[d1] = f32_to_bf16(o1);
+                        }
+                    }
                 }
-                *reinterpret_cast<uint4 *>(p.out + (bt * p.Hq + hq) * D + d0) = pack8(o);
-                if (d0 == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(sum)) * kLn2;
-            } else {
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((size_t)slot * p.rows + r) * D + d0);
-                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-                if (d0 == 0) p.part_ml[(size_t)slot * p.rows + r] = make_float2(top, sum);
+        }
+        if (tid < nrows) {
+            const float2 v = ml[tid];
+            if (!whole) {
+                p.part_ml[(size_t)slot * p.rows + tid] = v;
+            } else if (p.lse != nullptr) {
+                const int rr = r0 + tid, t = rr / p.G, hq = h * p.G + rr % p.G;
+                p.lse[((long long)b * p.T + t) * p.Hq + hq] = (v.x + log2f(v.y)) * kLn2;
             }
         }
         if (ta == 0 && !whole && tid == 0) {
             // the unit goes on: its last tile lies in the last share that starts at or before it
-            const unsigned last = start + (it - n) + len.tiles - 1;
+            const unsigned last = start + done + len.tiles - 1;
             p.meta[3 * blockIdx.x] = b * heads + ui;
             p.meta[3 * blockIdx.x + 1] = (int)sh.of(last);
             p.meta[3 * blockIdx.x + 2] = slot;
         }
+        done += n;
         first = false;
         left -= n;
         ta = 0;
@@ -856,9 +794,9 @@ __global__ void __launch_bounds__((max_consumers<G, NT>() + 1) * 32, 1) attn_dec
 // goes on, if there is one: rows blockIdx.y, + gridDim.y ...  D/4 threads take
 // four channels each of a group of parts; a chain of few loads: what the
 // parts hold is asked for before their weights are known.
-template <int D>
-__global__ void __launch_bounds__(512) attn_join_kernel(const Params p) {
-    constexpr int COLS = D / 4, GROUPS = 512 / COLS, UNROLL = 4;
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
+    constexpr int COLS = D / 4, GROUPS = THREADS / COLS, UNROLL = 4;
     __shared__ float4 sums[GROUPS][COLS];
     __shared__ float red_m[GROUPS], red_l[GROUPS];
     grid_dep_launch();
@@ -913,7 +851,7 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const Params p) {
             red_l[grp] = l;
         }
         __syncthreads();
-        if (tid < D) {
+        for (int d = tid; d < D; d += THREADS) {
             float top = -INFINITY, acc = 0.0f, total = 0.0f;
 #pragma unroll
             for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, red_m[i]);
@@ -921,23 +859,23 @@ __global__ void __launch_bounds__(512) attn_join_kernel(const Params p) {
             for (int i = 0; i < GROUPS; ++i) {
                 if (red_m[i] == -INFINITY) continue;
                 const float w = ex2(red_m[i] - top);
-                acc = fmaf(w, reinterpret_cast<const float *>(sums[i])[tid], acc);
+                acc = fmaf(w, reinterpret_cast<const float *>(sums[i])[d], acc);
                 total = fmaf(w, red_l[i], total);
             }
             const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
             const long long bt = (long long)b * p.T + t;
             float y = total == 0.0f ? 0.0f : acc / total;
-            if (p.gate.p != nullptr) y *= sigmoid(bf16_to_f32(p.gate.p[bt * p.gate.ts + hq * p.gate.hs + tid]));
-            p.out[(bt * p.Hq + hq) * D + tid] = f32_to_bf16(y);
-            if (tid == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;
+            if (p.gate.p != nullptr) y *= sigmoid(bf16_to_f32(p.gate.p[bt * p.gate.ts + hq * p.gate.hs + d]));
+            p.out[(bt * p.Hq + hq) * D + d] = f32_to_bf16(y);
+            if (d == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;
         }
     }
 }
 
 // Row blocks of a (b, h) and the query rows of one.
-void row_blocks(const AttnSizes &s, int *blocks, int *rows) {
+void row_blocks(const AttnSizes &s, int most, int *blocks, int *rows) {
     const int R = s.T * (s.Hq / s.Hkv);
-    *blocks = (R + kMaxRows - 1) / kMaxRows;
+    *blocks = (R + most - 1) / most;
     *rows = (R + *blocks - 1) / *blocks;
 }
 
@@ -948,38 +886,26 @@ struct Workspace {
 };
 
 Workspace workspace(const AttnSizes &s) {
-    int blocks, rows;
-    row_blocks(s, &blocks, &rows);
-    const size_t slots = 2 * (size_t)num_sms();
+    int blocks, rows;   // (the most rows of a unit with either cache format)
+    row_blocks(s, 64, &blocks, &rows);
+    const size_t ctas = (size_t)num_sms(), slots = 2 * ctas;
     Workspace w;
     w.o = 0;
     w.ml = up256(slots * rows * s.D * sizeof(float));
     w.meta = w.ml + up256(slots * rows * sizeof(float2));
-    w.total = w.meta + up256((size_t)num_sms() * 3 * sizeof(int));
+    w.total = w.meta + up256(ctas * 3 * sizeof(int));
     return w;
 }
 
 template <class G, int NT>
-cudaError_t launch_t(Params &p, cudaStream_t st) {
-    p.RG = (p.rows + NT * 8 - 1) / (NT * 8);
-    p.KL = max_consumers<G, NT>() / p.RG;
-    p.copies = 64 * 1024 / (p.RG * NT * 8 * G::OSTR * 4);
-    p.copies = p.copies < 1 ? 1 : p.copies > 4 ? 4 : p.copies;
-    if (p.copies > p.KL) p.copies = p.KL;
+cudaError_t launch_t(const Params &p0, cudaStream_t st) {
+    Params p = p0;
     int lg = 0;
     while ((1 << lg) < G::KT) ++lg;
     p.box_log2 = p.c.shift < lg ? p.c.shift : lg;
-    // A stage always belongs to the same lane (stages a multiple of KL): fills may land out of order, and a lane
-    // that waits for a stage's fill k by its parity must have seen fill k - 1 land itself, or the parity of a fill
-    // k - 1 still on its way would read as fill k.
-    p.stages = p.KL;
-    while (p.stages + p.KL <= kMaxStages &&
-           layout<G>(p.RG, NT, p.KL, p.copies, p.stages + p.KL).total <= kSmemLimit - 1024)
-        p.stages += p.KL;
-    if (layout<G>(p.RG, NT, p.KL, p.copies, p.stages).total > kSmemLimit - 1024) return cudaErrorInvalidConfiguration;
-    const int smem = layout<G>(p.RG, NT, p.KL, p.copies, p.stages).total;
+    constexpr int smem = Smem<G, NT>::total;
     static unsigned long long done = 0;
-    cudaError_t e = set_max_smem(done, attn_decode_kernel<G, NT>, kSmemLimit - 1024);
+    cudaError_t e = set_max_smem(done, attn_decode_kernel<G, NT>, smem);
     if (e != cudaSuccess) return e;
 
     CUtensorMap maps[2];
@@ -996,15 +922,15 @@ cudaError_t launch_t(Params &p, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     // the tiles of a call are counted in 32 bits
-    if ((unsigned long long)p.B * p.Hkv * p.RB * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1) > 0x7fffffffULL)
-        return cudaErrorNotSupported;
+    const unsigned long long units = (unsigned long long)p.B * p.Hkv * p.RB;
+    if (units * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1) > 0x7fffffffULL) return cudaErrorNotSupported;
     const int ctas = num_sms();
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3((p.RG * p.KL + 1) * 32);
+    cfg.blockDim = dim3((kWarps + G::PRODUCERS) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -1012,16 +938,29 @@ cudaError_t launch_t(Params &p, cudaStream_t st) {
     e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<G, NT>, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ctas, p.rows < 8 ? p.rows : 8);
-    cfg.blockDim = dim3(512);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D>, p);
+    // few units: many parts each, many threads to read them; many units: mostly two parts, small CTAs
+    if (units * 8 < (unsigned)ctas) {
+        cfg.blockDim = dim3(512);
+        return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 512>, p);
+    }
+    cfg.blockDim = dim3(128);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 128>, p);
+}
+
+template <class G>
+cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
+    row_blocks(s, G::MAXROWS, &p.RB, &p.rows);
+    if (p.rows <= 8) return launch_t<G, 1>(p, st);
+    if (p.rows <= 16) return launch_t<G, 2>(p, st);
+    if (p.rows <= 32) return launch_t<G, 4>(p, st);
+    if constexpr (G::MAXROWS > 32) return launch_t<G, 8>(p, st);
+    return cudaErrorInvalidValue;
 }
 
 template <int D>
-cudaError_t launch_d(Params &p, cudaStream_t st) {
-    const bool one = p.rows <= 8;
-    if (p.c.fp8) return one ? launch_t<Geo<D, true>, 1>(p, st) : launch_t<Geo<D, true>, 2>(p, st);
-    return one ? launch_t<Geo<D, false>, 1>(p, st) : launch_t<Geo<D, false>, 2>(p, st);
+cudaError_t launch_d(Params &p, const AttnSizes &s, cudaStream_t st) {
+    return p.c.fp8 ? launch_g<Geo<D, true>>(p, s, st) : launch_g<Geo<D, false>>(p, s, st);
 }
 
 }  // namespace
@@ -1046,16 +985,15 @@ cudaError_t launch_attn_decode(const AttnSizes &s, const uint16_t *q, const Page
     p.Hkv = s.Hkv;
     p.G = s.Hq / s.Hkv;
     p.R = s.T * p.G;
-    row_blocks(s, &p.RB, &p.rows);
     p.scale2 = scale * kLog2e;
     const Workspace w = workspace(s);
     char *base = static_cast<char *>(ws);
     p.part_o = reinterpret_cast<float *>(base + w.o);
     p.part_ml = reinterpret_cast<float2 *>(base + w.ml);
     p.meta = reinterpret_cast<int *>(base + w.meta);
-    if (s.D == 64) return launch_d<64>(p, st);
-    if (s.D == 128) return launch_d<128>(p, st);
-    return launch_d<256>(p, st);
+    if (s.D == 64) return launch_d<64>(p, s, st);
+    if (s.D == 128) return launch_d<128>(p, s, st);
+    return launch_d<256>(p, s, st);
 }
 
 }  // namespace gdn
