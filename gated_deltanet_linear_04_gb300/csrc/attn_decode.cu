@@ -40,27 +40,32 @@ namespace {
 using namespace attn;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 8;         // consumer warps
-constexpr int kThreads = kWarps * 32;
 constexpr int kMaxStages = 4;
 constexpr int kSmemLimit = 226 * 1024;
 
-template <int D_, bool FP8_>
+// The geometry of a tile for W consumer warps.
+template <int D_, bool FP8_, int W_>
 struct Geo {
-    static constexpr int D = D_;
+    static constexpr int D = D_, W = W_, THREADS = W * 32;
     static constexpr bool FP8 = FP8_;
     static constexpr int ROWB = FP8 ? D : 2 * D;               // bytes of a key
     static constexpr int SUBB = ROWB < 128 ? ROWB : 128;       // ... in sub-tiles of one swizzle span
     static constexpr int NSUB = ROWB / SUBB;
     static constexpr int KT = 32768 / ROWB > 256 ? 256 : 32768 / ROWB;   // keys of a tile: 64, 128 or 256
     static constexpr int TILE = KT * ROWB;                     // bytes of a tile's keys, or values
-    static constexpr int SPLIT = KT == 64 ? 2 : 1;             // 64 keys: two warps share 16 keys, half the channels each
-    static constexpr int MPW = KT == 256 ? 2 : 1;              // blocks of 16 keys of a warp
-    static constexpr int DPW = D == 256 ? 2 : 1;               // blocks of 16 channels of a warp (D = 64: of four warps)
+    static constexpr int KB = KT / 16, DB = D / 16;            // blocks of 16 keys, of 16 channels
+    static constexpr int SPLIT = W > KB ? W / KB : 1;          // S: warps that share 16 keys, part of the channels each
+    static constexpr int MPW = KB > W ? KB / W : 1;            // ... or blocks of 16 keys of a warp
+    static constexpr int KS = DB / SPLIT;                      // ... channel blocks of a warp
+    // O: channel blocks of a warp (e4m3: pairs, which is what one ldmatrix brings), and warps that share them, part of
+    // the keys each
+    static constexpr int DPW = DB > W ? DB / W : FP8 ? 2 : 1;
+    static constexpr int KSPL = W * DPW / DB;
+    static constexpr int KK = KB / KSPL;                       // ... key blocks of a warp
     static constexpr int SSTR = KT + 4;                        // row stride of S (floats): banks 8 apart for rows 2 apart
     static constexpr int PSTR = KT + 8;                        // row stride of P (16-bit): banks 4 apart
     static constexpr int PRODUCERS = FP8 ? 4 : 2;              // warps: keys, values, key scales, value scales
-    static constexpr int MAXROWS = KT == 256 ? 32 : 64;        // query rows of a unit (shared memory)
+    static_assert(KS >= (FP8 ? 2 : 1) && KK >= 2 && KK % 2 == 0, "");
 };
 
 struct Params {
@@ -85,7 +90,9 @@ template <class G, int NT>
 struct Smem {
     static constexpr int rows = NT * 8;
     static constexpr int q_bytes = rows * G::D * 2;
-    static constexpr int s_bytes = G::SPLIT * rows * G::SSTR * 4;
+    // S, and in its place at a unit's end the parts of O that went over other keys
+    static constexpr int s_only = G::SPLIT * rows * G::SSTR * 4, o_parts = (G::KSPL - 1) * rows * G::D * 4;
+    static constexpr int s_bytes = s_only > o_parts ? s_only : o_parts;
     static constexpr int p_bytes = rows * G::PSTR * 2;
     static constexpr int row_bytes = rows * 20;                // corr, qscale, (m, l), fin
     static constexpr int sc_bytes = G::FP8 ? 2 * G::KT : 0;    // a stage's scales
@@ -132,6 +139,20 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The warp's largest value; a NaN is passed over.
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The values of two e8m0 bytes.
+__device__ __forceinline__ float2 e8m0_pair(uint32_t bytes) {
+    uint32_t b;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"((uint16_t)bytes));
+    return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
 }
 
 // Four e4m3 codes as two f16 pairs, exactly.
@@ -189,21 +210,24 @@ struct Shares {
     }
 };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 template <class G, int NT>
-__global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
+__global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const Params p) {
     using L = Smem<G, NT>;
-    constexpr int D = G::D, KT = G::KT, NST = L::stages;
+    constexpr int D = G::D, KT = G::KT, W = G::W, NST = L::stages;
     constexpr bool FP8 = G::FP8;
     constexpr bool QREG = NT <= 2;           // query operands in registers; else read from shared memory each time
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) uint64_t full_k[NST], full_v[NST], empty_k[NST], empty_v[NST];
     __shared__ uint32_t bad_boxes[NST];
-    __shared__ unsigned warp_sum_sh[kWarps + 4], found_off;
-    __shared__ int found_b, any_corr;
+    __shared__ unsigned warp_sum_sh[G::W + 4], found_off;
+    __shared__ int found_b;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_launch();
@@ -212,8 +236,8 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full_k[i], FP8 ? 3 : 1);
             mbar_init(&full_v[i], 1);
-            mbar_init(&empty_k[i], kWarps);
-            mbar_init(&empty_v[i], kWarps);
+            mbar_init(&empty_k[i], W);
+            mbar_init(&empty_v[i], W);
         }
         fence_mbar_init();
         prefetch_tmap(&tm_k);
@@ -223,7 +247,7 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
 
     // the share: prefix sums of the rows' tiles, blockDim rows at a time (twice, if that is not all of them)
     const int heads = p.Hkv * p.RB;
-    constexpr int nthr = (kWarps + G::PRODUCERS) * 32, nwarp = nthr / 32;
+    constexpr int nthr = (W + G::PRODUCERS) * 32, nwarp = nthr / 32;
     const bool once = p.B <= nthr;
     Shares sh;
     unsigned start = 0;
@@ -275,9 +299,9 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
     int st = 0;           // the tile's stage, and the parity of its fill
     uint32_t ph = 0;
 
-    if (warp >= kWarps) {
+    if (warp >= W) {
         // ---- producers: lane i < bpt fills box i of every tile -------------------------------------------
-        const int role = warp - kWarps;                  // keys, values, key scales, value scales
+        const int role = warp - W;                  // keys, values, key scales, value scales
         const int bpt = KT >> p.box_log2, page_sh = p.c.shift - p.box_log2;   // boxes per tile; pages = boxes >> page_sh
         const uint32_t bytes = role < 2 ? (uint32_t)boxrows * G::ROWB : (uint32_t)boxrows;
         uint64_t *full = role == 1 ? full_v : full_k, *empty = role == 1 ? empty_v : empty_k;
@@ -367,18 +391,31 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
     auto at = [&](uint32_t row, uint32_t x, int c) {
         return (uint32_t)(c / (G::SUBB / 16)) * substride + row + (x ^ ((c * 16) & (G::SUBB - 16)));
     };
-    // ... and of key k0 (a multiple of 16) of a tile
+    // ... and of key k0 (a multiple of 16) of a tile: a box's sub-tiles follow each other
+    const uint32_t box_gap = (uint32_t)boxrows * (G::ROWB - G::SUBB);
     auto key_base = [&](int k0) {
-        return (uint32_t)(k0 >> p.box_log2) * (boxrows * G::ROWB) + (k0 & (boxrows - 1)) * G::SUBB;
+        return (uint32_t)k0 * G::SUBB + (G::NSUB > 1 ? (uint32_t)(k0 >> p.box_log2) * box_gap : 0u);
     };
     // this warp's part of S: keys and channels
-    const int s_key = G::SPLIT == 2 ? (warp & 3) * 16 : warp * 16 * G::MPW;
-    const int s_half = G::SPLIT == 2 ? warp >> 2 : 0;
-    constexpr int KS = D / 16 / G::SPLIT;                          // steps of 16 channels
-    // ... and of O: blocks of 16 channels (D = 64: the first four warps)
-    const bool has_o = warp * G::DPW * 16 < D;
-    // ... and of the softmax: rows warp, warp + 8, ...; keys 2 lane, 2 lane + 1 of every 64
+    const int s_key = G::SPLIT > 1 ? warp / G::SPLIT * 16 : warp * 16 * G::MPW;
+    const int s_part = G::SPLIT > 1 ? warp % G::SPLIT : 0;
+    // ... of O: its channel block and key blocks
+    constexpr int OW = G::DB / G::DPW;
+    const int o_blk = warp % OW * G::DPW, o_part = warp / OW;
+    // ldmatrix offsets: of the key operands, one per load; of the value operands
+    constexpr int KL = G::KS / (FP8 ? 2 : 1), VL = G::DPW / (FP8 ? 2 : 1);
+    uint32_t koff[KL], voff[VL], kkey[G::MPW];
+#pragma unroll
+    for (int i = 0; i < KL; ++i) koff[i] = at(k_row, k_x, 2 * (s_part * KL + i));
+#pragma unroll
+    for (int i = 0; i < VL; ++i) voff[i] = at(v_row, v_x, 2 * (o_blk / (FP8 ? 2 : 1) + i));
+#pragma unroll
+    for (int i = 0; i < G::MPW; ++i) kkey[i] = key_base(s_key + i * 16);
+    // ... and of the softmax: rows warp, warp + W, ...; keys 2 lane, 2 lane + 1 of every 64
+    constexpr int RPW = (L::rows + W - 1) / W;
 
+    int stv = 0;                      // the stage of the tile's values (st: of the next tile's keys), and their parity
+    uint32_t phv = 0;
     int done = 0;                     // tiles of this CTA before the unit
     bool first = true;
     while (left > 0) {
@@ -387,7 +424,7 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
         const int nrows = min(p.rows, p.R - r0);
 
         // queries to operand order: 8 channels of a row per thread
-        for (int i = tid; i < L::rows * (D / 8); i += kThreads) {
+        for (int i = tid; i < L::rows * (D / 8); i += G::THREADS) {
             const int r = i / (D / 8), d0 = (i % (D / 8)) * 8;
             uint4 raw = make_uint4(0, 0, 0, 0);
             if (r < nrows) {
@@ -421,24 +458,24 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
                 base[ln * 2 + reg] = w[e];
             }
         }
-        consumer_sync();
-        uint2 qr[QREG ? KS : 1][QREG ? NT : 1];
+        consumer_sync<G::THREADS>();
+        uint2 qr[QREG ? G::KS : 1][QREG ? NT : 1];
         if (QREG) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int ks = 0; ks < G::KS; ++ks)
 #pragma unroll
-                for (int c = 0; c < NT; ++c) qr[ks][c] = qf[((s_half * KS + ks) * NT + c) * 32 + lane];
+                for (int c = 0; c < NT; ++c) qr[ks][c] = qf[((s_part * G::KS + ks) * NT + c) * 32 + lane];
         }
         // softmax state of this warp's rows
-        float m[NT], l[NT], mv[NT], rs[NT];
-        int lim[NT];                  // visible keys, 0 for a row that is not there
+        float m[RPW], l[RPW], mv[RPW], rs[RPW];
+        int lim[RPW];                 // visible keys, 0 for a row that is not there
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
+        for (int c = 0; c < RPW; ++c) {
             m[c] = mv[c] = -INFINITY;
             l[c] = 0.0f;
-            const int r = c * 8 + warp, t = (r0 + r) / p.G;
+            const int r = c * W + warp, t = (r0 + r) / p.G;
             lim[c] = r < nrows && t < len.n ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : 0;
-            rs[c] = p.scale2 * (FP8 ? qscale[r] : 1.0f);
+            rs[c] = p.scale2 * (FP8 && r < nrows ? qscale[r] : 1.0f);
         }
         float acc[G::DPW][NT][4];
 #pragma unroll
@@ -449,84 +486,99 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
                 for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.0f;
         const int all_see = (int)min(max(len.pos + 1, 0LL), len.keys);   // keys that every live row sees
 
-        for (int i = 0; i < n; ++i) {
-            const int key0 = (ta + i) * KT;
-            const uint32_t kbase = ring + st * 2 * G::TILE, vbase = kbase + G::TILE;
-            // S^T = K Q^T
+        // S^T = K Q^T of the tile in stage st, into registers ...
+        float s[G::MPW][NT][4];
+        uint32_t bad_next = 0;
+        auto scores = [&] {
             if (!dead && !mbar_wait(&full_k[st], ph, p.err)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
-            const uint32_t bad = *static_cast<volatile uint32_t *>(&bad_boxes[st]);
-            const bool tail = bad != 0 || key0 + KT > all_see;
-            if (!dead) {
+            bad_next = *static_cast<volatile uint32_t *>(&bad_boxes[st]);
+            if (dead) return;
+            const uint32_t kbase = ring + st * 2 * G::TILE;
 #pragma unroll
-                for (int a = 0; a < G::MPW; ++a) {
-                    const uint32_t base = kbase + key_base(s_key + a * 16);
-                    float s[NT][4];
+            for (int a = 0; a < G::MPW; ++a) {
+                const uint32_t base = kbase + kkey[a];
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
+                for (int c = 0; c < NT; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[c][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) s[a][c][e] = 0.0f;
 #pragma unroll
-                    for (int ks = 0; ks < KS; ks += FP8 ? 2 : 1) {
-                        uint32_t k[4];
-                        ldsm4(base + at(k_row, k_x, FP8 ? ks : 2 * (s_half * KS + ks)), k);
+                for (int ks = 0; ks < G::KS; ks += FP8 ? 2 : 1) {
+                    uint32_t k[4];
+                    ldsm4(base + koff[ks / (FP8 ? 2 : 1)], k);
 #pragma unroll
-                        for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
-                            uint32_t a0 = k[0], a1 = k[1], a2 = k[2], a3 = k[3];
-                            if (FP8) {
-                                codes_f16(k[2 * e], a0, a2);
-                                codes_f16(k[2 * e + 1], a1, a3);
-                            }
+                    for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
+                        uint32_t a0 = k[0], a1 = k[1], a2 = k[2], a3 = k[3];
+                        if (FP8) {
+                            codes_f16(k[2 * e], a0, a2);
+                            codes_f16(k[2 * e + 1], a1, a3);
+                        }
 #pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                const uint2 q = QREG ? qr[QREG ? ks + e : 0][QREG ? c : 0]
-                                                     : qf[((s_half * KS + ks + e) * NT + c) * 32 + lane];
-                                mma<FP8>(s[c], a0, a1, a2, a3, q.x, q.y);
-                            }
+                        for (int c = 0; c < NT; ++c) {
+                            const uint2 q = QREG ? qr[QREG ? ks + e : 0][QREG ? c : 0]
+                                                 : qf[((s_part * G::KS + ks + e) * NT + c) * 32 + lane];
+                            mma<FP8>(s[a][c], a0, a1, a2, a3, q.x, q.y);
                         }
                     }
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sS[(s_half * L::rows + c * 8 + 2 * j + (e & 1)) * G::SSTR + s_key + a * 16 + g + 8 * (e >> 1)] =
-                                s[c][e];
-                }
-                if (!FP8) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty_k[st]);
                 }
             }
-            consumer_sync();
+        };
+        // ... and from there to shared memory, the keys' stage given back (with e4m3, after the softmax: its scales)
+        auto put_scores = [&] {
+            if (dead) return;
+#pragma unroll
+            for (int a = 0; a < G::MPW; ++a)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sS[(s_part * L::rows + c * 8 + 2 * j + (e & 1)) * G::SSTR + s_key + a * 16 + g + 8 * (e >> 1)] =
+                            s[a][c][e];
+            if (!FP8) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty_k[st]);
+            }
+        };
+        scores();
+        put_scores();
+
+        for (int i = 0; i < n; ++i) {
+            const int key0 = (ta + i) * KT;
+            const uint32_t bad = bad_next;
+            const bool tail = bad != 0 || key0 + KT > all_see;
+            consumer_sync<G::THREADS>();
 
             // softmax: weights of this warp's rows
-            bool moved = false;
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const int r = c * 8 + warp;
-                if (NT > 1 && r >= nrows) continue;
-                float s[KT / 64][2], ve[KT / 64][2];
+            for (int c = 0; c < RPW; ++c) {
+                const int r = c * W + warp;
+                if (r >= nrows) continue;
+                float z[KT / 64][2], ve[KT / 64][2];
                 float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < KT / 64; ++x) {
                     const int key = x * 64 + 2 * lane;
                     float2 v = *reinterpret_cast<const float2 *>(sS + r * G::SSTR + key);
-                    if (G::SPLIT == 2) {
-                        const float2 u = *reinterpret_cast<const float2 *>(sS + (L::rows + r) * G::SSTR + key);
+#pragma unroll
+                    for (int y = 1; y < G::SPLIT; ++y) {
+                        const float2 u = *reinterpret_cast<const float2 *>(sS + (y * L::rows + r) * G::SSTR + key);
                         v.x += u.x;
                         v.y += u.y;
                     }
-                    s[x][0] = v.x * rs[c];
-                    s[x][1] = v.y * rs[c];
+                    z[x][0] = v.x * rs[c];
+                    z[x][1] = v.y * rs[c];
                     if (FP8) {
                         const unsigned char *sc = smem + L::sc + st * 2 * KT + key;
-                        const uint32_t kb = *reinterpret_cast<const uint16_t *>(sc);
+                        const float2 ks = e8m0_pair(*reinterpret_cast<const uint16_t *>(sc));
                         const uint32_t vb = *reinterpret_cast<const uint16_t *>(sc + KT);
+                        z[x][0] *= ks.x;
+                        z[x][1] *= ks.y;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            s[x][e] *= e8m0_value(kb >> (8 * e) & 255u);
-                            const int y = vb >> (8 * e) & 255;
-                            ve[x][e] = y == 255 ? __uint_as_float(0x7fffffffu) : (float)(y - 127);
+                            // the exponent as a float, by way of 2^23 + byte; byte 255 is NaN
+                            const uint32_t y = vb >> (8 * e) & 255u;
+                            ve[x][e] = y == 255u ? __uint_as_float(0x7fffffffu)
+                                                 : __uint_as_float(0x4b000000u | y) - 8388735.0f;
                         }
                     }
                     if (tail) {
@@ -534,28 +586,24 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             if (!there || key0 + key + e >= lim[c]) {
-                                s[x][e] = -INFINITY;
+                                z[x][e] = -INFINITY;
                                 ve[x][e] = 0.0f;
                             }
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        top = fmaxf(top, s[x][e]);
-                        if (FP8) topv = fmaxf(topv, s[x][e] + ve[x][e]);
+                        top = fmaxf(top, z[x][e]);
+                        if (FP8) topv = fmaxf(topv, z[x][e] + ve[x][e]);
                     }
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    if (FP8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
-                }
+                top = warp_max(top);
+                if (FP8) topv = warp_max(topv);
                 const float mn = fmaxf(m[c], top), mvn = FP8 ? fmaxf(mv[c], topv) : mn;
                 // (an infinite maximum only where nothing, or an infinity, was seen)
                 const float base = mn == -INFINITY ? 0.0f : mn, basev = mvn == -INFINITY ? 0.0f : mvn;
                 l[c] *= ex2(m[c] - base);
                 float f = FP8 ? ex2(mv[c] - basev) : ex2(m[c] - base);
                 if (m[c] == -INFINITY && (!FP8 || mv[c] == -INFINITY)) f = 1.0f;   // (nothing to scale yet)
-                moved |= f != 1.0f;
                 if (lane == 0) corr[r] = f;
                 m[c] = mn;
                 mv[c] = mvn;
@@ -564,44 +612,103 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
                     float w[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        w[e] = ex2(s[x][e] - base);
+                        w[e] = ex2(z[x][e] - base);
                         l[c] += w[e];
-                        if (FP8) w[e] = ex2(s[x][e] + ve[x][e] - basev);
+                        if (FP8) w[e] = ex2(z[x][e] + ve[x][e] - basev);
                     }
                     *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
                 }
             }
-            if (moved && lane == 0) any_corr = done + i + 1;      // (the tile's number: no reset needed)
             if (FP8 && !dead) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty_k[st]);          // (the scales lie in the key ring)
+                if (lane == 0) mbar_arrive(&empty_k[st]);
             }
-            consumer_sync();
+            if (++st == NST) {
+                st = 0;
+                ph ^= 1;
+            }
+            consumer_sync<G::THREADS>();
 
-            // O^T += V^T P^T
-            if (!dead && !mbar_wait(&full_v[st], ph, p.err)) dead = true;
+            // the next tile's scores and this one's O^T += V^T P^T, which do not wait for each other
+            if (i + 1 < n) scores();
+            if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (!dead) {
-                if (has_o) {
-                    if (*static_cast<volatile int *>(&any_corr) == done + i + 1) {
+                const uint32_t vbase = ring + stv * 2 * G::TILE + G::TILE;
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) {
-                            const float2 f = *reinterpret_cast<const float2 *>(corr + c * 8 + 2 * j);
+                for (int c = 0; c < NT; ++c) {
+                    const float2 f = *reinterpret_cast<const float2 *>(corr + c * 8 + 2 * j);
 #pragma unroll
-                            for (int d = 0; d < G::DPW; ++d) {
-                                acc[d][c][0] *= f.x;
-                                acc[d][c][1] *= f.y;
-                                acc[d][c][2] *= f.x;
-                                acc[d][c][3] *= f.y;
+                    for (int d = 0; d < G::DPW; ++d) {
+                        acc[d][c][0] *= f.x;
+                        acc[d][c][1] *= f.y;
+                        acc[d][c][2] *= f.x;
+                        acc[d][c][3] *= f.y;
+                    }
+                }
+                // two key blocks (32 keys)
+                auto step = [&](int kk, bool masked, int see, float (&sum)[G::DPW][NT][4]) {
+                    uint32_t pf[NT][4];
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        ldsm4(smem_u32(sP) + ((c * 8 + mr) * G::PSTR + kk * 16 + mi * 8) * 2, pf[c]);
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        const int kb = kk + k2;
+                        // values of slots that hold no key are zeroed
+                        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = kb * 16 + e * 8 + 2 * j;
+                                const bool there = (bad >> (key >> p.box_log2) & 1) == 0;
+                                keep[e] = there ? (key0 + key < see ? 0xffffu : 0u) |
+                                                      (key0 + key + 1 < see ? 0xffff0000u : 0u)
+                                                : 0u;
                             }
                         }
+                        const uint32_t base = vbase + key_base(kb * 16);
+                        uint32_t vraw[4];
+#pragma unroll
+                        for (int d = 0; d < G::DPW; ++d) {
+                            uint32_t v[4];
+                            if (!FP8) {
+                                ldsm4t(base + voff[FP8 ? 0 : d], v);
+                                if (masked) {
+                                    v[0] &= keep[0];
+                                    v[1] &= keep[0];
+                                    v[2] &= keep[1];
+                                    v[3] &= keep[1];
+                                }
+                            } else {
+                                if (d % 2 == 0) ldsm4t(base + voff[d / 2], vraw);
+                                uint32_t lo = vraw[2 * (d % 2)], hi = vraw[2 * (d % 2) + 1];
+                                if (masked) {
+                                    lo &= keep[0];
+                                    hi &= keep[1];
+                                }
+                                lo = __byte_perm(lo, 0, 0x3120);   // (key, key + 1) of channel 2g, then of 2g + 1
+                                hi = __byte_perm(hi, 0, 0x3120);
+                                codes_f16(lo, v[0], v[1]);
+                                codes_f16(hi, v[2], v[3]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < NT; ++c)
+                                mma<FP8>(sum[d][c], v[0], v[1], v[2], v[3], pf[c][2 * k2], pf[c][2 * k2 + 1]);
+                        }
                     }
+                };
+                const int kk0 = o_part * G::KK;
+                if (!tail) {
+#pragma unroll
+                    for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, false, 0, acc);
+                } else {
                     // a NaN or infinity among the values that only later tokens see: 0 times it is not 0
                     bool window = false;
-                    if (tail && p.T > 1) {
+                    if (p.T > 1) {
                         for (int key = max(all_see - key0, 0); key < KT && key0 + key < len.keys; ++key) {
                             if (bad >> (key >> p.box_log2) & 1) continue;
-                            const unsigned char *row = smem + st * 2 * G::TILE + G::TILE +
+                            const unsigned char *row = smem + stv * 2 * G::TILE + G::TILE +
                                                        (key >> p.box_log2) * (boxrows * G::ROWB) +
                                                        (key & (boxrows - 1)) * G::SUBB;
                             for (int x = lane; x < G::ROWB / 4; x += 32) {
@@ -618,72 +725,16 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
                         }
                         window = __any_sync(0xffffffffu, window);
                     }
-                    // the usual pass, or one pass per token over the values it sees, the other rows' sums dropped
-                    const int passes = window ? len.n : 1;
-                    for (int t = 0; t < passes; ++t) {
-                        const int see = window ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : (int)len.keys;
-                        auto step = [&](int kk, bool masked, float (&sum)[G::DPW][NT][4]) {
-                            uint32_t pf[NT][2], vraw[4];
-#pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                const uint16_t *row = sP + (c * 8 + g) * G::PSTR + kk * 16 + 2 * j;
-                                pf[c][0] = *reinterpret_cast<const uint32_t *>(row);
-                                pf[c][1] = *reinterpret_cast<const uint32_t *>(row + 8);
-                            }
-                            // values of slots that hold no key are zeroed
-                            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                            if (masked) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int key = kk * 16 + e * 8 + 2 * j;
-                                    const bool there = (bad >> (key >> p.box_log2) & 1) == 0;
-                                    keep[e] = there ? (key0 + key < see ? 0xffffu : 0u) |
-                                                          (key0 + key + 1 < see ? 0xffff0000u : 0u)
-                                                    : 0u;
-                                }
-                            }
-                            const uint32_t base = vbase + key_base(kk * 16);
-#pragma unroll
-                            for (int d = 0; d < G::DPW; ++d) {
-                                const int dt = warp * G::DPW + d;      // block of 16 channels
-                                uint32_t v[4];
-                                if (!FP8) {
-                                    ldsm4t(base + at(v_row, v_x, 2 * dt), v);
-                                    if (masked) {
-                                        v[0] &= keep[0];
-                                        v[1] &= keep[0];
-                                        v[2] &= keep[1];
-                                        v[3] &= keep[1];
-                                    }
-                                } else {
-                                    // (two warps of D <= 128 read the same pair of blocks and use one each)
-                                    if (G::DPW == 1 || d == 0) ldsm4t(base + at(v_row, v_x, dt & ~1), vraw);
-                                    const int e = G::DPW == 1 ? dt & 1 : d;
-                                    uint32_t lo = e ? vraw[2] : vraw[0], hi = e ? vraw[3] : vraw[1];
-                                    if (masked) {
-                                        lo &= keep[0];
-                                        hi &= keep[1];
-                                    }
-                                    lo = __byte_perm(lo, 0, 0x3120);   // (key, key + 1) of channel 2g, then of 2g + 1
-                                    hi = __byte_perm(hi, 0, 0x3120);
-                                    codes_f16(lo, v[0], v[1]);
-                                    codes_f16(hi, v[2], v[3]);
-                                }
-#pragma unroll
-                                for (int c = 0; c < NT; ++c)
-                                    mma<FP8>(sum[d][c], v[0], v[1], v[2], v[3], pf[c][0], pf[c][1]);
-                            }
-                        };
-                        if (!tail) {
-#pragma unroll 4
-                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, false, acc);
-                        } else if (!window) {
+                    if (!window) {
 #pragma unroll 1
-                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, true, acc);
-                        } else {
+                        for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, true, (int)len.keys, acc);
+                    } else {
+                        // one pass per token over the values it sees, the other rows' sums dropped
+                        for (int t = 0; t < len.n; ++t) {
                             float one[G::DPW][NT][4] = {};
+                            const int see = (int)min(max(len.pos + t + 1, 0LL), len.keys);
 #pragma unroll 1
-                            for (int kk = 0; kk < KT / 16; ++kk) step(kk, true, one);
+                            for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, true, see, one);
 #pragma unroll
                             for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -696,31 +747,54 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty_v[st]);
+                if (lane == 0) mbar_arrive(&empty_v[stv]);
             }
-            if (++st == NST) {
-                st = 0;
-                ph ^= 1;
+            if (++stv == NST) {
+                stv = 0;
+                phv ^= 1;
             }
+            if (i + 1 < n) put_scores();
         }
 
         // the unit's output, or this share's part of it
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
+        for (int c = 0; c < RPW; ++c) {
             float sum = l[c];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) {
+            if (lane == 0 && c * W + warp < L::rows) {
                 // (a token that is not there has no visible key; mv - m: the weighted sum in units of 2^m)
                 const bool none = lim[c] == 0 || m[c] == -INFINITY;
-                ml[c * 8 + warp] = make_float2(none ? -INFINITY : m[c], none ? 0.0f : sum);
-                fin[c * 8 + warp] = none ? 0.0f : FP8 ? ex2(mv[c] - m[c]) : 1.0f;
+                ml[c * W + warp] = make_float2(none ? -INFINITY : m[c], none ? 0.0f : sum);
+                fin[c * W + warp] = none ? 0.0f : FP8 ? ex2(mv[c] - m[c]) : 1.0f;
             }
         }
-        consumer_sync();
+        // the parts of O that went over other keys, joined in their order in S's place
+        auto part = [&](int y, int d, int c, int e) -> float & {
+            return sS[(((y * NT + c) * G::DB + o_blk + d) * 4 + e) * 32 + lane];
+        };
+        if (G::KSPL > 1 && o_part > 0) {
+#pragma unroll
+            for (int d = 0; d < G::DPW; ++d)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part(o_part - 1, d, c, e) = acc[d][c][e];
+        }
+        consumer_sync<G::THREADS>();
+        if (G::KSPL > 1 && o_part == 0) {
+#pragma unroll 1
+            for (int y = 0; y < G::KSPL - 1; ++y)
+#pragma unroll
+                for (int d = 0; d < G::DPW; ++d)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[d][c][e] += part(y, d, c, e);
+        }
         const bool whole = ta == 0 && n == len.tiles;
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
-        if (has_o) {
+        if (o_part == 0) {
 #pragma unroll
             for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -735,7 +809,7 @@ __global__ void __launch_bounds__((kWarps + G::PRODUCERS) * 32, 1)
 #pragma unroll
                     for (int d = 0; d < G::DPW; ++d) {
                         // channels d0, d1 of this thread's two values
-                        const int dt = (warp * G::DPW + d) * 16, d0 = FP8 ? dt + 2 * g : dt + g, d1 = FP8 ? d0 + 1 : d0 + 8;
+                        const int dt = (o_blk + d) * 16, d0 = FP8 ? dt + 2 * g : dt + g, d1 = FP8 ? d0 + 1 : d0 + 8;
                         float o0 = acc[d][c][x], o1 = acc[d][c][2 + x];
                         if (v.y == 0.0f) o0 = o1 = 0.0f;           // (also of a token that is not there)
                         o0 *= f;
@@ -930,7 +1004,7 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3((kWarps + G::PRODUCERS) * 32);
+    cfg.blockDim = dim3((G::W + G::PRODUCERS) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -948,19 +1022,22 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 128>, p);
 }
 
-template <class G>
+// Sixteen consumer warps up to 32 query rows; more rows take more registers and
+// more shared memory for S and P: eight warps, which halves S's parts.
+template <int D, bool FP8>
 cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
-    row_blocks(s, G::MAXROWS, &p.RB, &p.rows);
-    if (p.rows <= 8) return launch_t<G, 1>(p, st);
-    if (p.rows <= 16) return launch_t<G, 2>(p, st);
-    if (p.rows <= 32) return launch_t<G, 4>(p, st);
-    if constexpr (G::MAXROWS > 32) return launch_t<G, 8>(p, st);
+    constexpr int most = Geo<D, FP8, 8>::KT == 256 ? 32 : 64;
+    row_blocks(s, most, &p.RB, &p.rows);
+    if (p.rows <= 8) return launch_t<Geo<D, FP8, 16>, 1>(p, st);
+    if (p.rows <= 16) return launch_t<Geo<D, FP8, 16>, 2>(p, st);
+    if (p.rows <= 32) return launch_t<Geo<D, FP8, 16>, 4>(p, st);
+    if constexpr (most > 32) return launch_t<Geo<D, FP8, 8>, 8>(p, st);
     return cudaErrorInvalidValue;
 }
 
 template <int D>
 cudaError_t launch_d(Params &p, const AttnSizes &s, cudaStream_t st) {
-    return p.c.fp8 ? launch_g<Geo<D, true>>(p, s, st) : launch_g<Geo<D, false>>(p, s, st);
+    return p.c.fp8 ? launch_g<D, true>(p, s, st) : launch_g<D, false>(p, s, st);
 }
 
 }  // namespace
