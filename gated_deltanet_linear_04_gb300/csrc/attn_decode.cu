@@ -1028,8 +1028,8 @@ template <int D, bool FP8>
 cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
     constexpr int most = Geo<D, FP8, 8>::KT == 256 ? 32 : 64;
     row_blocks(s, most, &p.RB, &p.rows);
-    if (p.rows <= 8) return launch_t<Geo<D, FP8, 16>, 1>(p, st);
-    if (p.rows <= 16) return launch_t<Geo<D, FP8, 16>, 2>(p, st);
+    if (p.rows <= 8) return launch_t<Geo<D, FP8, 8>, 1>(p, st);
+    if (p.rows <= 16) return launch_t<Geo<D, FP8, 8>, 2>(p, st);
     if (p.rows <= 32) return launch_t<Geo<D, FP8, 16>, 4>(p, st);
     if constexpr (most > 32) return launch_t<Geo<D, FP8, 8>, 8>(p, st);
     return cudaErrorInvalidValue;
