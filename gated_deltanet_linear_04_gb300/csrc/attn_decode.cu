@@ -489,19 +489,24 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         // S^T = K Q^T of the tile in stage st, into registers ...
         float s[G::MPW][NT][4];
         uint32_t bad_next = 0;
-        auto scores = [&] {
+        auto wait_keys = [&] {
             if (!dead && !mbar_wait(&full_k[st], ph, p.err)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
             bad_next = *static_cast<volatile uint32_t *>(&bad_boxes[st]);
-            if (dead) return;
+        };
+        auto scores = [&] {
+            constexpr int CH = NT <= 2 && KL > 1 ? 2 : 1;   // chains of products that do not wait for each other
             const uint32_t kbase = ring + st * 2 * G::TILE;
 #pragma unroll
             for (int a = 0; a < G::MPW; ++a) {
                 const uint32_t base = kbase + kkey[a];
+                float t[CH][NT][4];
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
+                for (int x = 0; x < CH; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[a][c][e] = 0.0f;
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) t[x][c][e] = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < G::KS; ks += FP8 ? 2 : 1) {
                     uint32_t k[4];
@@ -517,10 +522,14 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                         for (int c = 0; c < NT; ++c) {
                             const uint2 q = QREG ? qr[QREG ? ks + e : 0][QREG ? c : 0]
                                                  : qf[((s_part * G::KS + ks + e) * NT + c) * 32 + lane];
-                            mma<FP8>(s[a][c], a0, a1, a2, a3, q.x, q.y);
+                            mma<FP8>(t[(ks + e) % CH][c], a0, a1, a2, a3, q.x, q.y);
                         }
                     }
                 }
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[a][c][e] = CH == 2 ? t[0][c][e] + t[CH - 1][c][e] : t[0][c][e];
             }
         };
         // ... and from there to shared memory, the keys' stage given back (with e4m3, after the softmax: its scales)
@@ -539,7 +548,8 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                 if (lane == 0) mbar_arrive(&empty_k[st]);
             }
         };
-        scores();
+        wait_keys();
+        if (!dead) scores();
         put_scores();
 
         for (int i = 0; i < n; ++i) {
@@ -630,8 +640,9 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
             consumer_sync<G::THREADS>();
 
             // the next tile's scores and this one's O^T += V^T P^T, which do not wait for each other
-            if (i + 1 < n) scores();
+            const bool more = i + 1 < n;
             if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
+            if (more) wait_keys();
             dead = __any_sync(0xffffffffu, dead);
             if (!dead) {
                 const uint32_t vbase = ring + stv * 2 * G::TILE + G::TILE;
@@ -699,10 +710,15 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                     }
                 };
                 const int kk0 = o_part * G::KK;
-                if (!tail) {
+                if (!tail && more) {
+                    scores();
 #pragma unroll
                     for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, false, 0, acc);
+                } else if (!tail) {
+#pragma unroll 2
+                    for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, false, 0, acc);
                 } else {
+                    if (more) scores();
                     // a NaN or infinity among the values that only later tokens see: 0 times it is not 0
                     bool window = false;
                     if (p.T > 1) {
@@ -753,7 +769,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                 stv = 0;
                 phv ^= 1;
             }
-            if (i + 1 < n) put_scores();
+            if (more) put_scores();
         }
 
         // the unit's output, or this share's part of it
@@ -1022,16 +1038,17 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 128>, p);
 }
 
-// Sixteen consumer warps up to 32 query rows; more rows take more registers and
-// more shared memory for S and P: eight warps, which halves S's parts.
+// Eight consumer warps (B = 128, 8 query heads per key head, 2048 keys of 256
+// channels in e4m3: 53.5 us; four 56.9, sixteen 58.6).
 template <int D, bool FP8>
 cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
-    constexpr int most = Geo<D, FP8, 8>::KT == 256 ? 32 : 64;
+    using G = Geo<D, FP8, 8>;
+    constexpr int most = G::KT == 256 ? 32 : 64;   // query rows of a unit: S and P of a tile have to fit
     row_blocks(s, most, &p.RB, &p.rows);
-    if (p.rows <= 8) return launch_t<Geo<D, FP8, 8>, 1>(p, st);
-    if (p.rows <= 16) return launch_t<Geo<D, FP8, 8>, 2>(p, st);
-    if (p.rows <= 32) return launch_t<Geo<D, FP8, 16>, 4>(p, st);
-    if constexpr (most > 32) return launch_t<Geo<D, FP8, 8>, 8>(p, st);
+    if (p.rows <= 8) return launch_t<G, 1>(p, st);
+    if (p.rows <= 16) return launch_t<G, 2>(p, st);
+    if (p.rows <= 32) return launch_t<G, 4>(p, st);
+    if constexpr (most > 32) return launch_t<G, 8>(p, st);
     return cudaErrorInvalidValue;
 }
 
