@@ -7,9 +7,10 @@
 //
 // Work.  A unit is one (row b, key head h, block of at most 64 of its T * Hq/Hkv
 // query rows); its keys come in tiles of KT (32 KB of keys, 32 KB of values).
-// The tiles of all units form one list, cut into equal shares for one CTA per
-// SM, so ragged batches and a single long row both fill the GPU; each CTA
-// finds its share from pos / n_new itself.  A unit that crosses shares leaves
+// The tiles of all units form one list (with a blank slot before each unit's
+// first tile, for what its start and end cost), cut into equal shares for one
+// CTA per SM, so ragged batches and a single long row both fill the GPU; each
+// CTA finds its share from pos / n_new itself.  A unit that crosses shares leaves
 // partial results (m, sum, weighted sum) in the workspace, and a second kernel
 // joins them in share order.
 //
@@ -41,6 +42,7 @@ using namespace attn;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
+constexpr int kBlank = 1;         // blank slots of a unit in the list of tiles
 constexpr int kSmemLimit = 226 * 1024;
 
 // The geometry of a tile for W consumer warps.
@@ -81,6 +83,7 @@ struct Params {
     unsigned *err;
     int B, T, Hq, Hkv, G, R;
     int RB, rows;       // row blocks of a (b, h), query rows of one
+    int g_mul;          // r / G = r * g_mul >> 16 for the r < 128 there are
     int box_log2;
     float scale2;       // scale * log2(e)
 };
@@ -192,10 +195,10 @@ __device__ __forceinline__ RowLen row_len(const Params &p, int b) {
     return r;
 }
 
-// The list of all units' tiles in `act` shares that differ by at most one
-// tile, the longer ones first.
+// The list of all units' slots in `act` shares that differ by at most one slot,
+// the longer ones first.
 struct Shares {
-    unsigned act, base, extra;   // base or base + 1 tiles; `extra` shares have one more
+    unsigned act, base, extra;   // base or base + 1 slots; `extra` shares have one more
 
     __device__ void set(unsigned total, unsigned ctas) {
         act = min(ctas, total);
@@ -203,10 +206,48 @@ struct Shares {
         extra = total - base * act;
     }
     __device__ unsigned start(unsigned c) const { return c * base + min(c, extra); }
-    // the share that holds a tile
-    __device__ unsigned of(unsigned tile) const {
+    // the share that holds a slot
+    __device__ unsigned of(unsigned slot) const {
         const unsigned cut = extra * (base + 1);
-        return tile < cut ? tile / (base + 1) : extra + (tile - cut) / base;
+        return slot < cut ? slot / (base + 1) : extra + (slot - cut) / base;
+    }
+};
+
+// A stretch of one unit's tiles in a share.
+struct Seg {
+    int b, h, r0, ta, n;      // row, key head, first query row; tiles [ta, ta + n)
+    RowLen len;
+    unsigned first_slot;      // of the unit's first tile, in the list
+    __device__ bool whole() const { return ta == 0 && n == len.tiles; }
+};
+
+// Goes through a share's stretches.
+template <class G>
+struct Walk {
+    int b, ui, so, left;      // row; unit of it; slot of the unit; slots left of the share
+    unsigned slot;
+    RowLen len;
+
+    __device__ bool next(const Params &p, Seg &s) {
+        while (left > 0) {
+            const int all = len.tiles + kBlank, take = min(all - so, left);
+            s.b = b;
+            s.h = p.RB == 1 ? ui : ui / p.RB;
+            s.r0 = p.RB == 1 ? 0 : (ui - s.h * p.RB) * p.rows;
+            s.ta = max(so - kBlank, 0);
+            s.n = so + take - kBlank - s.ta;
+            s.len = len;
+            s.first_slot = slot - so + kBlank;
+            left -= take;
+            slot += take;
+            so = 0;
+            if (left > 0 && ++ui == p.Hkv * p.RB) {
+                ui = 0;
+                len = row_len<G>(p, ++b);
+            }
+            if (s.n > 0) return true;
+        }
+        return false;
     }
 };
 
@@ -255,7 +296,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         unsigned run = 0;
         for (int base = 0; base < p.B; base += nthr) {
             const int b = base + tid;
-            const unsigned v = b < p.B ? (unsigned)(row_len<G>(p, b).tiles * heads) : 0;
+            const unsigned v = b < p.B ? (unsigned)((row_len<G>(p, b).tiles + kBlank) * heads) : 0;
             unsigned x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -290,10 +331,17 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
     __syncthreads();
     if (tid == 0) p.meta[3 * blockIdx.x] = -1;
     if (blockIdx.x >= sh.act) return;
-    int b = found_b;
-    RowLen len = row_len<G>(p, b);
-    int ui = (int)(found_off / (unsigned)len.tiles), ta = (int)(found_off % (unsigned)len.tiles);
-    int left = (int)(sh.start(blockIdx.x + 1) - start);
+    Walk<G> walk;
+    walk.b = found_b;
+    walk.len = row_len<G>(p, walk.b);
+    walk.slot = start;
+    walk.left = (int)(sh.start(blockIdx.x + 1) - start);
+    {
+        const unsigned all = walk.len.tiles + kBlank;
+        walk.ui = (int)(found_off / all);
+        walk.so = (int)(found_off - walk.ui * all);
+    }
+    Seg seg;
     const int boxrows = 1 << p.box_log2;
     bool dead = false;
     int st = 0;           // the tile's stage, and the parity of its fill
@@ -309,12 +357,13 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         const int pitch = role < 2 ? 2 * G::TILE : 2 * KT;
         const uint8_t *scales = role == 2 ? p.c.ks : p.c.vs;
         uint32_t used = 0;
-        while (left > 0) {
-            const int n = min(len.tiles - ta, left), h = ui / p.RB;
-            const int32_t *line = p.c.table + (long long)b * p.c.width;
+        while (walk.next(p, seg)) {
+            const int n = seg.n, h = seg.h;
+            const RowLen &len = seg.len;
+            const int32_t *line = p.c.table + (long long)seg.b * p.c.width;
             const int nbox = (int)((len.keys + boxrows - 1) >> p.box_log2);
             if (len.short_table && role == 0 && lane == 0) atomicOr(p.err, kErrBadPage);
-            int box = ta * bpt + lane;
+            int box = seg.ta * bpt + lane;
             auto ask = [&](int i, int bx) { return lane < bpt && i < n && bx < nbox ? line[bx >> page_sh] : -1; };
             int id = ask(0, box), id1 = ask(1, box + bpt);   // page numbers, asked for two tiles ahead
             for (int i = 0; i < n; ++i) {
@@ -350,12 +399,6 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                 box += bpt;
                 id = id1;
                 id1 = id2;
-            }
-            left -= n;
-            ta = 0;
-            if (left > 0 && ++ui == heads) {
-                ui = 0;
-                len = row_len<G>(p, ++b);
             }
         }
         // after a wait that gave up: let the copies in flight land before the CTA ends
@@ -416,21 +459,39 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
 
     int stv = 0;                      // the stage of the tile's values (st: of the next tile's keys), and their parity
     uint32_t phv = 0;
-    int done = 0;                     // tiles of this CTA before the unit
     bool first = true;
-    while (left > 0) {
-        const int n = min(len.tiles - ta, left);
-        const int h = ui / p.RB, r0 = (ui % p.RB) * p.rows;
+    // 8 channels of a query row per thread, asked for a unit ahead (where the registers allow it)
+    constexpr bool EARLY = NT <= 2;
+    constexpr int QV = (L::rows * (D / 8) + G::THREADS - 1) / G::THREADS;
+    uint4 qraw[QV];
+    auto ask_queries = [&](const Seg &u) {
+        const int nrows = min(p.rows, p.R - u.r0);
+#pragma unroll
+        for (int x = 0; x < QV; ++x) {
+            const int i = x * G::THREADS + tid, r = i / (D / 8), d0 = (i % (D / 8)) * 8;
+            qraw[x] = make_uint4(0, 0, 0, 0);
+            if (r < nrows) {
+                const int rr = u.r0 + r, t = rr * p.g_mul >> 16, hq = u.h * p.G + rr - t * p.G;
+                qraw[x] = *reinterpret_cast<const uint4 *>(p.q + (((long long)u.b * p.T + t) * p.Hq + hq) * D + d0);
+            }
+        }
+    };
+    Seg ahead;
+    bool have = walk.next(p, ahead);
+    if (EARLY && have) ask_queries(ahead);
+    while (have) {
+        seg = ahead;
+        if (!EARLY) ask_queries(seg);
+        const int b = seg.b, h = seg.h, r0 = seg.r0, ta = seg.ta, n = seg.n;
+        const RowLen &len = seg.len;
         const int nrows = min(p.rows, p.R - r0);
 
-        // queries to operand order: 8 channels of a row per thread
-        for (int i = tid; i < L::rows * (D / 8); i += G::THREADS) {
-            const int r = i / (D / 8), d0 = (i % (D / 8)) * 8;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (r < nrows) {
-                const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
-                raw = *reinterpret_cast<const uint4 *>(p.q + (((long long)b * p.T + t) * p.Hq + hq) * D + d0);
-            }
+        // queries to operand order
+#pragma unroll
+        for (int x8 = 0; x8 < QV; ++x8) {
+            const int i = x8 * G::THREADS + tid, r = i / (D / 8), d0 = (i % (D / 8)) * 8;
+            if (QV * G::THREADS != L::rows * (D / 8) && r >= L::rows) continue;
+            const uint4 raw = qraw[x8];
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             if (FP8) {
                 // a power of two per row brings the largest query to [1, 4): f16 then holds every bit but those
@@ -458,6 +519,8 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                 base[ln * 2 + reg] = w[e];
             }
         }
+        have = walk.next(p, ahead);
+        if (EARLY && have) ask_queries(ahead);
         consumer_sync<G::THREADS>();
         uint2 qr[QREG ? G::KS : 1][QREG ? NT : 1];
         if (QREG) {
@@ -473,7 +536,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         for (int c = 0; c < RPW; ++c) {
             m[c] = mv[c] = -INFINITY;
             l[c] = 0.0f;
-            const int r = c * W + warp, t = (r0 + r) / p.G;
+            const int r = c * W + warp, t = (r0 + r) * p.g_mul >> 16;
             lim[c] = r < nrows && t < len.n ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : 0;
             rs[c] = p.scale2 * (FP8 && r < nrows ? qscale[r] : 1.0f);
         }
@@ -755,7 +818,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                             for (int c = 0; c < NT; ++c)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    if ((r0 + c * 8 + 2 * j + (e & 1)) / p.G == t) {
+                                    if (((r0 + c * 8 + 2 * j + (e & 1)) * p.g_mul >> 16) == t) {
 #pragma unroll
                                         for (int d = 0; d < G::DPW; ++d) acc[d][c][e] += one[d][c][e];
                                     }
@@ -808,7 +871,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[d][c][e] += part(y, d, c, e);
         }
-        const bool whole = ta == 0 && n == len.tiles;
+        const bool whole = seg.whole();
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
         if (o_part == 0) {
 #pragma unroll
@@ -819,7 +882,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                     if (r >= nrows) continue;
                     const float2 v = ml[r];
                     const float f = fin[r];
-                    const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
+                    const int rr = r0 + r, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
                     const long long bt = (long long)b * p.T + t;
                     const float inv = v.y == 0.0f ? 0.0f : 1.0f / v.y;
 #pragma unroll
@@ -858,25 +921,17 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
             if (!whole) {
                 p.part_ml[(size_t)slot * p.rows + tid] = v;
             } else if (p.lse != nullptr) {
-                const int rr = r0 + tid, t = rr / p.G, hq = h * p.G + rr % p.G;
+                const int rr = r0 + tid, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
                 p.lse[((long long)b * p.T + t) * p.Hq + hq] = (v.x + log2f(v.y)) * kLn2;
             }
         }
         if (ta == 0 && !whole && tid == 0) {
-            // the unit goes on: its last tile lies in the last share that starts at or before it
-            const unsigned last = start + done + len.tiles - 1;
-            p.meta[3 * blockIdx.x] = b * heads + ui;
-            p.meta[3 * blockIdx.x + 1] = (int)sh.of(last);
+            // the unit goes on: its last tile lies in the share that holds that tile's slot
+            p.meta[3 * blockIdx.x] = (b * p.Hkv + h) * p.RB + (p.RB == 1 ? 0 : r0 / p.rows);
+            p.meta[3 * blockIdx.x + 1] = (int)sh.of(seg.first_slot + len.tiles - 1);
             p.meta[3 * blockIdx.x + 2] = slot;
         }
-        done += n;
         first = false;
-        left -= n;
-        ta = 0;
-        if (left > 0 && ++ui == heads) {
-            ui = 0;
-            len = row_len<G>(p, ++b);
-        }
     }
 }
 
@@ -1013,7 +1068,7 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     }
     // the tiles of a call are counted in 32 bits
     const unsigned long long units = (unsigned long long)p.B * p.Hkv * p.RB;
-    if (units * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1) > 0x7fffffffULL) return cudaErrorNotSupported;
+    if (units * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1 + kBlank) > 0x7fffffffULL) return cudaErrorNotSupported;
     const int ctas = num_sms();
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1078,6 +1133,7 @@ cudaError_t launch_attn_decode(const AttnSizes &s, const uint16_t *q, const Page
     p.Hq = s.Hq;
     p.Hkv = s.Hkv;
     p.G = s.Hq / s.Hkv;
+    p.g_mul = 65536 / p.G + 1;
     p.R = s.T * p.G;
     p.scale2 = scale * kLog2e;
     const Workspace w = workspace(s);
