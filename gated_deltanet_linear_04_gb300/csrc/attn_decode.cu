@@ -42,7 +42,8 @@ using namespace attn;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
-constexpr int kBlank = 1;         // blank slots of a unit in the list of tiles
+constexpr int kRowCache = 64;      // rows whose lengths a CTA keeps
+constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles
 constexpr int kSmemLimit = 226 * 1024;
 
 // The geometry of a tile for W consumer warps.
@@ -184,15 +185,20 @@ struct RowLen {
 };
 
 template <class G>
-__device__ __forceinline__ RowLen row_len(const Params &p, int b) {
+__device__ __forceinline__ RowLen row_len(const Params &p, int pos, int n) {
     RowLen r;
-    r.n = clamp_new(p.n_new, b, p.T);
-    r.pos = p.pos[b];
+    r.n = n;
+    r.pos = pos;
     const long long want = r.n == 0 ? 0 : max(r.pos + r.n, 0LL);
     r.keys = min(min(want, (long long)p.c.width << p.c.shift), 0x7fffff00LL);   // (key indexes are 32 bits)
     r.short_table = r.n > 0 && (r.keys < want || r.pos < 0);
     r.tiles = (int)max((r.keys + G::KT - 1) / G::KT, 1LL);
     return r;
+}
+
+template <class G>
+__device__ __forceinline__ RowLen row_len(const Params &p, int b) {
+    return row_len<G>(p, p.pos[b], clamp_new(p.n_new, b, p.T));
 }
 
 // The list of all units' slots in `act` shares that differ by at most one slot,
@@ -227,6 +233,9 @@ struct Walk {
     int b, ui, so, left;      // row; unit of it; slot of the unit; slots left of the share
     unsigned slot;
     RowLen len;
+    // (pos, n) of the rows from `row0` on: with the memory's queues full a load takes microseconds
+    const int2 *rows;
+    int row0;
 
     __device__ bool next(const Params &p, Seg &s) {
         while (left > 0) {
@@ -243,7 +252,8 @@ struct Walk {
             so = 0;
             if (left > 0 && ++ui == p.Hkv * p.RB) {
                 ui = 0;
-                len = row_len<G>(p, ++b);
+                const int i = ++b - row0;
+                len = i < kRowCache ? row_len<G>(p, rows[i].x, rows[i].y) : row_len<G>(p, b);
             }
             if (s.n > 0) return true;
         }
@@ -269,6 +279,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
     __shared__ uint32_t bad_boxes[NST];
     __shared__ unsigned warp_sum_sh[G::W + 4], found_off;
     __shared__ int found_b;
+    __shared__ int2 row_cache[kRowCache];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_launch();
@@ -333,6 +344,11 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
     if (blockIdx.x >= sh.act) return;
     Walk<G> walk;
     walk.b = found_b;
+    walk.rows = row_cache;
+    walk.row0 = found_b;
+    if (tid < kRowCache && found_b + tid < p.B)
+        row_cache[tid] = make_int2(p.pos[found_b + tid], clamp_new(p.n_new, found_b + tid, p.T));
+    __syncthreads();
     walk.len = row_len<G>(p, walk.b);
     walk.slot = start;
     walk.left = (int)(sh.start(blockIdx.x + 1) - start);
@@ -357,17 +373,27 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         const int pitch = role < 2 ? 2 * G::TILE : 2 * KT;
         const uint8_t *scales = role == 2 ? p.c.ks : p.c.vs;
         uint32_t used = 0;
-        while (walk.next(p, seg)) {
-            const int n = seg.n, h = seg.h;
-            const RowLen &len = seg.len;
-            const int32_t *line = p.c.table + (long long)seg.b * p.c.width;
-            const int nbox = (int)((len.keys + boxrows - 1) >> p.box_log2);
-            if (len.short_table && role == 0 && lane == 0) atomicOr(p.err, kErrBadPage);
-            int box = seg.ta * bpt + lane;
-            auto ask = [&](int i, int bx) { return lane < bpt && i < n && bx < nbox ? line[bx >> page_sh] : -1; };
-            int id = ask(0, box), id1 = ask(1, box + bpt);   // page numbers, asked for two tiles ahead
+        // page numbers, asked for two tiles ahead, those of a unit's first two during the unit before
+        auto boxes = [&](const Seg &u) { return (int)((u.len.keys + boxrows - 1) >> p.box_log2); };
+        auto ask = [&](const Seg &u, int i) {
+            const int box = (u.ta + i) * bpt + lane;
+            return lane < bpt && i < u.n && box < boxes(u) ? p.c.table[(long long)u.b * p.c.width + (box >> page_sh)] : -1;
+        };
+        Seg ahead;
+        bool have = walk.next(p, ahead);
+        int next0 = have ? ask(ahead, 0) : -1, next1 = have ? ask(ahead, 1) : -1;
+        while (have) {
+            seg = ahead;
+            const int n = seg.n, h = seg.h, nbox = boxes(seg);
+            if (seg.len.short_table && role == 0 && lane == 0) atomicOr(p.err, kErrBadPage);
+            int box = seg.ta * bpt + lane, id = next0, id1 = next1;
+            have = walk.next(p, ahead);
+            if (have) {
+                next0 = ask(ahead, 0);
+                next1 = ask(ahead, 1);
+            }
             for (int i = 0; i < n; ++i) {
-                const int id2 = ask(i + 2, box + 2 * bpt);
+                const int id2 = ask(seg, i + 2);
                 const bool want = lane < bpt && box < nbox, ok = want && id >= 0 && id < p.c.n_pages;
                 if (want && !ok && role == 0) atomicOr(p.err, kErrBadPage);
                 const uint32_t good = __ballot_sync(0xffffffffu, ok);
@@ -547,6 +573,27 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
             for (int c = 0; c < NT; ++c)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.0f;
+        // the gates of this thread's outputs, asked for before they are needed
+        const bool gated = p.gate.p != nullptr && seg.whole() && o_part == 0;
+        uint32_t gates[EARLY ? G::DPW : 1][EARLY ? NT : 1][2];
+        auto gate_pair = [&](int r, int d) {
+            // channels as the outputs below; two bf16 in one word
+            const int rr = r0 + r, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G, dt = (o_blk + d) * 16;
+            const uint16_t *z = p.gate.p + ((long long)b * p.T + t) * p.gate.ts + hq * p.gate.hs + dt;
+            if (FP8) return *reinterpret_cast<const uint32_t *>(z + 2 * g);
+            return (uint32_t)z[g] | (uint32_t)z[g + 8] << 16;
+        };
+        if (EARLY && gated) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int d = 0; d < G::DPW; ++d) {
+                        const int r = c * 8 + 2 * j + x;
+                        gates[EARLY ? d : 0][EARLY ? c : 0][x] = r < nrows ? gate_pair(r, d) : 0u;
+                    }
+        }
         const int all_see = (int)min(max(len.pos + 1, 0LL), len.keys);   // keys that every live row sees
 
         // S^T = K Q^T of the tile in stage st, into registers ...
@@ -555,6 +602,8 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         auto wait_keys = [&] {
             if (!dead && !mbar_wait(&full_k[st], ph, p.err)) dead = true;
             dead = __any_sync(0xffffffffu, dead);
+        };
+        auto see_keys = [&] {
             bad_next = *static_cast<volatile uint32_t *>(&bad_boxes[st]);
         };
         auto scores = [&] {
@@ -612,6 +661,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
             }
         };
         wait_keys();
+        see_keys();
         if (!dead) scores();
         put_scores();
 
@@ -700,13 +750,18 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                 st = 0;
                 ph ^= 1;
             }
+            // usually both are there already: one look on the way to the barrier instead of two waits after it
+            const bool more = i + 1 < n;
+            const bool there = mbar_test(&full_v[stv], phv) && (!more || mbar_test(&full_k[st], ph));
             consumer_sync<G::THREADS>();
 
             // the next tile's scores and this one's O^T += V^T P^T, which do not wait for each other
-            const bool more = i + 1 < n;
-            if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
-            if (more) wait_keys();
-            dead = __any_sync(0xffffffffu, dead);
+            if (!__all_sync(0xffffffffu, there)) {
+                if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
+                dead = __any_sync(0xffffffffu, dead);
+                if (more) wait_keys();
+            }
+            if (more) see_keys();
             if (!dead) {
                 const uint32_t vbase = ring + stv * 2 * G::TILE + G::TILE;
 #pragma unroll
@@ -901,10 +956,10 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                         }
                         o0 *= inv;
                         o1 *= inv;
-                        if (p.gate.p != nullptr) {
-                            const uint16_t *z = p.gate.p + bt * p.gate.ts + hq * p.gate.hs;
-                            o0 *= sigmoid(bf16_to_f32(z[d0]));
-                            o1 *= sigmoid(bf16_to_f32(z[d1]));
+                        if (gated) {
+                            const uint32_t z = EARLY ? gates[EARLY ? d : 0][EARLY ? c : 0][x] : gate_pair(r, d);
+                            o0 *= sigmoid(__uint_as_float(z << 16));
+                            o1 *= sigmoid(__uint_as_float(z & 0xffff0000u));
                         }
                         uint16_t *dst = p.out + (bt * p.Hq + hq) * D;
                         if (FP8) {
