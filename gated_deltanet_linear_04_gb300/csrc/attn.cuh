@@ -12,13 +12,21 @@ namespace attn {
 
 // cos and sin of position * frequency.  freq is in turns per position as a
 // 64-bit binary fraction, so the product mod 2^64 is the angle's exact
-// fraction of a turn (the integer multiply drops whole turns); its upper 32
-// bits, signed, are within [-1/2, 1/2) turns and enter sincospi as f32 (2^-25
-// of a turn's half: below the f32 rounding of cos and sin themselves).
+// fraction of a turn (the integer multiply drops whole turns).  Its upper 32
+// bits, plus an eighth of a turn, give the quadrant (two bits) and the angle
+// from the quadrant's middle, t within +-pi/4, rounded to f32; there the Taylor
+// series to t^9 and t^8 are off by less than 2^-25 (t^11/11!, t^10/10!).
 __device__ __forceinline__ void rope_angle(long long pos, uint64_t freq, float &c, float &s) {
-    const uint64_t turns = (uint64_t)pos * freq;
-    const float x = (float)(int32_t)(turns >> 32) * (1.0f / 2147483648.0f);   // half turns, [-1, 1)
-    sincospif(x, &s, &c);
+    const uint32_t turns = (uint32_t)(((uint64_t)pos * freq) >> 32) + 0x20000000u;
+    const float t = (float)((int32_t)(turns & 0x3fffffffu) - 0x20000000) * 1.4629180792671596e-9f;   // pi 2^-31
+    const float t2 = t * t;
+    const float sn = t * fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), 1.0f);
+    const float cs = fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+    const bool odd = turns & 0x40000000u, neg = turns & 0x80000000u;
+    // quadrants 0..3: (cos, sin), (-sin, cos), (-cos, -sin), (sin, -cos)
+    const float x = odd ? -sn : cs, y = odd ? cs : sn;
+    c = neg ? -x : x;
+    s = neg ? -y : y;
 }
 
 // Eight bf16 (16 bytes) to f32 and back.

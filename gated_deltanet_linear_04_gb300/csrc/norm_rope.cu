@@ -8,13 +8,24 @@
 // turns dy by the opposite angle (dz), and with xhat = x rstd
 //   dw = sum dz xhat,   dx = rstd (w dz - xhat mean(w dz xhat)).
 //
-// Every element is read and written once: HBM-bound.  D/8 lanes hold one head
-// row, eight channels (16 bytes) a lane, so a warp holds RPW = 32 / (D/8) rows
-// at once; the partner of a channel in the half-split form sits R/16 lanes
-// away.  A warp takes one token and up to ROWS * RPW heads of one kind: all
-// their loads go out first, then the token's angles are computed once (one or
-// more per lane, shared through shared memory), then the rows.
-// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): XXF us.
+// Every element is read and written once: HBM-bound, if a row of 256 channels
+// takes a warp fewer than about 90 instructions (a load and a store of 512
+// bytes take an SM 46 clocks).  So:
+//   - D/8 lanes hold one head row, RPW = 32 / (D/8) rows a warp; a lane holds
+//     two pieces of four channels (8 bytes each) that turn with each other: in
+//     the half-split form i .. i+3 and R/2 + i .. R/2 + i+3, so no lane needs
+//     another's channels.  The pieces of neighbouring lanes are adjacent.
+//   - a warp takes one token and up to eight (backward: four) times RPW heads of
+//     one kind: all their rows are asked for at once, into its shared memory
+//     (cp.async), while it computes the token's angles (one or more per lane,
+//     shared through shared memory) and multiplies them with the weights; then
+//     each head row is y = rstd (x A + x' B), x' the partners.
+//   - four rows' sums go over the lanes together; arithmetic goes two channels
+//     at a time (f32x2 instructions).
+// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): 27.5 us forward (a plain
+// copy of as much takes 23.5), 50.5 backward (227 MB).  Steps on the way: a warp per
+// head row 89 us; four rows a warp, into registers, partners by shuffle, sincospi
+// 31.4 (164 instructions a row, most of them a token's angles and addresses).
 #include "attn.cuh"
 
 namespace gdn {
@@ -37,15 +48,28 @@ struct RowParams {
     PagedCache c;
     unsigned *err;
     int B, T, Hq, Hkv, R;
-    int cq, ck;                // chunks of heads of a token: of q, of k (and of v)
+    int cq, ck;                // parts of a token's heads: of q, of k (and of v)
+    int aq, ak;                // backward: CTAs of a part of q, of k
     float eps;
 };
 
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x) {
+// Four sums over the LPR lanes of a head row at once: the first two exchanges
+// halve the values as well as the lanes, so that 6 exchanges do what 20 would;
+// f is applied to each sum by the lanes that end up with it.
+template <int LPR, typename F>
+__device__ __forceinline__ void row_sums4(float (&v)[4], F &&f) {
+    const int lane = threadIdx.x & 31;
+    constexpr int O1 = LPR / 2, O2 = LPR / 4;
+    const bool b1 = lane & O1, b2 = lane & O2;
+    const float s0 = (b1 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b1 ? v[0] : v[2], O1);
+    const float s1 = (b1 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b1 ? v[1] : v[3], O1);
+    float t = (b2 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, b2 ? s0 : s1, O2);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    for (int o = LPR / 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    t = f(t);
+    const int base = lane & ~(LPR - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, t, base + (i & 2 ? O1 : 0) + (i & 1 ? O2 : 0));
 }
 
 template <int LPR>
@@ -55,233 +79,438 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
     return x;
 }
 
-// The warp's table of a position's angles, then cos and sin of the lane's eight
-// channels (interleaved: of its four pairs); channels past R do not turn.
+// Two f32 in one register pair.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 swap2(F2 a) {
+    const float2 x = parts(a);
+    return f2(x.y, x.x);
+}
+
+// The eight channels of a lane: piece 0 is x[0], x[1], piece 1 is x[2], x[3].
+struct Row {
+    F2 x[4];
+};
+struct RawRow {
+    uint2 p[2];
+};
+
+__device__ __forceinline__ Row unpack_row(const RawRow &r) {
+    Row o;
+    const uint32_t w[4] = {r.p[0].x, r.p[0].y, r.p[1].x, r.p[1].y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return o;
+}
+
+__device__ __forceinline__ RawRow pack_row(const Row &x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = parts(x.x[i]);
+        w[i] = pack2(v.x, v.y);
+    }
+    return {{make_uint2(w[0], w[1]), make_uint2(w[2], w[3])}};
+}
+
+// Where a lane's pieces are: channels c[0] .. + 3 and c[1] .. + 3 of its row.
+struct Pieces {
+    int c[2];
+    bool turns;
+    template <int LPR, bool INTER>
+    static __device__ __forceinline__ Pieces of(int R) {
+        constexpr int D = LPR * 8;
+        const int l = (threadIdx.x & 31) % LPR, r = R / 8;   // the first R/8 lanes turn
+        Pieces p;
+        p.turns = l < r;
+        const int first = p.turns ? 0 : R, n = p.turns ? R : D - R, m = p.turns ? l : l - r;
+        p.c[0] = first + 4 * m;
+        p.c[1] = first + n / 2 + 4 * m;
+        return p;
+    }
+};
+
+// A turned channel is own * a + partner * b.  The partners of a lane's pair k:
+// the other piece's (half-split), or its own two swapped (interleaved).
 template <bool INTER>
-__device__ __forceinline__ void lane_angles(const RowParams &p, float2 *table, int d0, long long pos, float (&c)[8],
-                                            float (&s)[8]) {
+__device__ __forceinline__ F2 partners(const Row &x, int k) {
+    return INTER ? swap2(x.x[k]) : x.x[k ^ 2];
+}
+
+// a = cos and b = the sine with the sign of the channel's place in its pair
+// (`back`: of the opposite turn) of the lane's channels at a position; 1 and 0
+// for channels that do not turn.  The warp computes the angles together, into
+// its table; four entries behind them hold (1, 0).
+template <bool INTER>
+__device__ __forceinline__ void lane_angles(const RowParams &p, float2 *table, const Pieces &pc, long long pos,
+                                            bool back, Row &a, Row &b) {
     const int lane = threadIdx.x & 31, half = p.R / 2;
     __syncwarp();   // (the previous token's readers)
-    for (int i = lane; i < half; i += 32) {
-        float2 a;
-        rope_angle(pos, p.freqs[i], a.x, a.y);
-        table[i] = a;
-    }
+    for (int i = lane; i < half; i += 32) rope_angle(pos, p.freqs[i], table[i].x, table[i].y);
+    if (lane < 4) table[half + lane] = make_float2(1.0f, 0.0f);
     __syncwarp();
-    const int first = INTER ? d0 / 2 : d0 < half ? d0 : d0 - half;
+    const float sg = back ? -1.0f : 1.0f;
+    const float4 *t4 = reinterpret_cast<const float4 *>(table);
+    if (INTER) {
+        // a piece is two pairs: two entries, in order
 #pragma unroll
-    for (int i = 0; i < (INTER ? 4 : 8); ++i) {
-        const float2 a = d0 < p.R ? table[first + i] : make_float2(1.0f, 0.0f);
-        c[i] = a.x;
-        s[i] = a.y;
+        for (int i = 0; i < 2; ++i) {
+            const float4 t = t4[(pc.turns ? pc.c[i] / 2 : half) / 2];
+            a.x[2 * i] = f2(t.x, t.x);
+            a.x[2 * i + 1] = f2(t.z, t.z);
+            b.x[2 * i] = f2(-sg * t.y, sg * t.y);
+            b.x[2 * i + 1] = f2(-sg * t.w, sg * t.w);
+        }
+    } else {
+        // the two pieces are four pairs: four entries
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 t = t4[(pc.turns ? pc.c[0] : half) / 2 + i];
+            a.x[i] = a.x[2 + i] = f2(t.x, t.z);
+            b.x[i] = f2(-sg * t.y, -sg * t.w);
+            b.x[2 + i] = f2(sg * t.y, sg * t.w);
+        }
     }
 }
 
-// Turns the lane's channels by the angles (sign = -1: back).
+// y += partners * b in the lanes whose channels turn; in the others nothing is
+// added (an infinity times a sine of 0 is not 0).
 template <bool INTER>
-__device__ __forceinline__ void rotate(float (&z)[8], const float (&c)[8], const float (&s)[8], int d0, int R,
-                                       float sign) {
-    if (INTER) {
+__device__ __forceinline__ void add_turned(Row &y, const Row &x, const Row &b, bool turns) {
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %12, 0;\n\t"
+        "@p fma.rn.f32x2 %0, %4, %8, %0;\n\t@p fma.rn.f32x2 %1, %5, %9, %1;\n\t"
+        "@p fma.rn.f32x2 %2, %6, %10, %2;\n\t@p fma.rn.f32x2 %3, %7, %11, %3;\n\t}"
+        : "+l"(y.x[0].v), "+l"(y.x[1].v), "+l"(y.x[2].v), "+l"(y.x[3].v)
+        : "l"(partners<INTER>(x, 0).v), "l"(partners<INTER>(x, 1).v), "l"(partners<INTER>(x, 2).v),
+          "l"(partners<INTER>(x, 3).v), "l"(b.x[0].v), "l"(b.x[1].v), "l"(b.x[2].v), "l"(b.x[3].v),
+          "r"((uint32_t)turns));
+}
+
+__device__ __forceinline__ Row load_weights(const float *w, const Pieces &pc) {
+    Row r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = z[2 * i], b = z[2 * i + 1], sn = sign * s[i];
-            z[2 * i] = a * c[i] - b * sn;
-            z[2 * i + 1] = b * c[i] + a * sn;
-        }
-        return;
+    for (int i = 0; i < 2; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(w + pc.c[i]);
+        r.x[2 * i] = f2(v.x, v.y);
+        r.x[2 * i + 1] = f2(v.z, v.w);
     }
-    if (R == 0) return;
-    const int lane = threadIdx.x & 31;
-    const bool low = d0 < R / 2;
-    const int partner = d0 >= R ? lane : low ? lane + R / 16 : lane - R / 16;
-    const float sg = low ? -sign : sign;
+    return r;
+}
+
+// The sum of the products of two rows' channels, over the lanes of a head row.
+__device__ __forceinline__ float dot_lane(const Row &a, const Row &b) {
+    F2 s = mul2(a.x[0], b.x[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xffffffffu, z[i], partner);
-        z[i] = z[i] * c[i] + sg * s[i] * o;
-    }
+    for (int k = 1; k < 4; ++k) s = fma2(a.x[k], b.x[k], s);
+    const float2 v = parts(s);
+    return v.x + v.y;
 }
 
 enum { kDense = 0, kAppend = 1, kAppendE4M3 = 2 };
 
-template <int D, bool INTER, int MODE, int ROWS>
-__global__ void __launch_bounds__(kThreads) row_forward_kernel(const RowParams p, unsigned items) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
-    __shared__ float2 tables[kWarps][D / 2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned chunks = p.cq + p.ck * (MODE == kDense ? 1 : 2);
-    const unsigned item = blockIdx.x * kWarps + warp;
-    if (item >= items) return;
-    const unsigned bt = item / chunks, chunk = item - bt * chunks;
-    const int b = (int)(bt / (unsigned)p.T), t = (int)(bt - (unsigned)b * p.T);
-    const bool isq = chunk < (unsigned)p.cq, isv = MODE != kDense && chunk >= (unsigned)(p.cq + p.ck);
-    const int h0 = (int)(isq ? chunk : isv ? chunk - p.cq - p.ck : chunk - p.cq) * ROWS * RPW + lane / LPR;
-    const int H = isq ? p.Hq : p.Hkv, d0 = (lane % LPR) * 8;
-    const HeadsIn &in = isq ? p.q : isv ? p.v : p.k;
-    const bool on = MODE == kDense ? p.mask == nullptr || p.mask[bt] != 0 : t < clamp_new(p.n_new, b, p.T);
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
-    uint4 raw[ROWS];
-    const uint16_t *src = in.p + (long long)bt * in.ts + d0;
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (on && h0 + u * RPW < H) raw[u] = *reinterpret_cast<const uint4 *>(src + (h0 + u * RPW) * in.hs);
+template <int D, bool INTER, int MODE, int ROWS>
+__global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParams p) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, GROUP = ROWS < 4 ? ROWS : 4;
+    extern __shared__ __align__(16) uint16_t stages[];
+    __shared__ __align__(16) float2 tables[kWarps][D / 2 + 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+    const unsigned bt = blockIdx.x * kWarps + warp, part = blockIdx.y;
+    if (bt >= (unsigned)(p.B * p.T)) return;
+    const bool isq = part < (unsigned)p.cq, isv = MODE != kDense && part >= (unsigned)(p.cq + p.ck);
+    const int h0 = (int)(isq ? part : isv ? part - p.cq - p.ck : part - p.cq) * ROWS * RPW + sub;
+    const int H = isq ? p.Hq : p.Hkv, rows = H - h0;   // (of this lane's, RPW apart)
+    int b = 0, t = 0;
+    bool on;
+    if (MODE == kDense) {
+        on = p.mask == nullptr || p.mask[bt] != 0;
+    } else {
+        b = (int)(bt / (unsigned)p.T);
+        t = (int)(bt - (unsigned)b * p.T);
+        on = t < clamp_new(p.n_new, b, p.T);
     }
+    uint16_t *ring = stages + warp * (ROWS * RPW * D);
+    if (on) {
+        const HeadsIn &in = isq ? p.q : isv ? p.v : p.k;
+        const uint16_t *src = in.p + (long long)bt * in.ts + (long long)h0 * in.hs + (lane % LPR) * 8;
+        const long long hop = RPW * in.hs;
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+            cp_async16(ring + u * RPW * D + lane * 8, src, u * RPW < rows);
+            if (u * RPW + RPW < rows) src += hop;
+            if ((u + 1) % GROUP == 0) cp_async_commit();
+        }
+    }
+    const Pieces pc = Pieces::of<LPR, INTER>(p.R);
     uint16_t *out = nullptr;
     if (isq || MODE == kDense) {
-        out = (isq ? p.q_out + (long long)bt * p.Hq * D : p.k_out + (long long)bt * p.Hkv * D) + d0;
+        out = (isq ? p.q_out + (long long)bt * p.Hq * D : p.k_out + (long long)bt * p.Hkv * D) + h0 * D;
         if (!on) {
 #pragma unroll
             for (int u = 0; u < ROWS; ++u)
-                if (h0 + u * RPW < H) *reinterpret_cast<uint4 *>(out + (h0 + u * RPW) * D) = make_uint4(0, 0, 0, 0);
+                if (u * RPW < rows)
+                    *reinterpret_cast<uint4 *>(out + u * RPW * D + (lane % LPR) * 8) = make_uint4(0, 0, 0, 0);
             return;
         }
     } else if (!on) {
         return;
     }
     const long long pos = MODE == kDense ? p.pos[bt] : (long long)p.pos[b] + t;
-    long long page_row = -1;   // of head 0
+    long long at = -1;   // the cache row of head h0
     if (MODE != kDense && !isq) {
-        page_row = cache_row(p.c, p.Hkv, p.c.table + (long long)b * p.c.width, pos, 0);
-        if (page_row < 0) {
+        at = cache_row(p.c, p.Hkv, p.c.table + (long long)b * p.c.width, pos, 0);
+        if (at < 0) {
             if (lane == 0) atomicOr(p.err, kErrBadPage);
+            cp_async_wait<0>();
             return;
         }
+        at += (long long)h0 << p.c.shift;
     }
-    float w[8], c[8], s[8];
+    // y = rstd (x A + x' B), x' the partners' x: A = w cos, B = +- w' sin
+    Row A, B;
     const float *wp = isq ? p.wq : p.wk;
     const bool norm = !isv && wp != nullptr;
+    if (!isv) lane_angles<INTER>(p, tables[warp], pc, pos, false, A, B);
     if (norm) {
-        const float4 w0 = *reinterpret_cast<const float4 *>(wp + d0), w1 = *reinterpret_cast<const float4 *>(wp + d0 + 4);
-        w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+        const Row w = load_weights(wp, pc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            A.x[k] = mul2(A.x[k], w.x[k]);
+            B.x[k] = mul2(B.x[k], partners<INTER>(w, k));
+        }
     }
-    if (!isv) lane_angles<INTER>(p, tables[warp], d0, pos, c, s);
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        const int h = h0 + u * RPW;
-        if (u > 0 && h0 - lane / LPR + u * RPW >= H) break;   // (no row of the warp)
-        float x[8];
-        unpack8(raw[u], x);
-        if (norm) {
-            float ss = 0.0f;
+    for (int u0 = 0; u0 < ROWS; u0 += GROUP) {
+        if (u0 + GROUP < ROWS)
+            cp_async_wait<1>();
+        else
+            cp_async_wait<0>();
+        __syncwarp();
+        const int n = (rows + sub - u0 * RPW + RPW - 1) / RPW;   // rows of the group that hold a head
+        if (n <= 0) break;
+        Row xs[GROUP];
+        float rstd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
+        for (int u = 0; u < GROUP; ++u) {
+            if (u >= n) break;
+            const uint16_t *src = ring + ((u0 + u) * RPW + sub) * D;
+            RawRow raw;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= rstd * w[i];
+            for (int i = 0; i < 2; ++i) raw.p[i] = *reinterpret_cast<const uint2 *>(src + pc.c[i]);
+            xs[u] = unpack_row(raw);
+            if (norm) rstd[u] = dot_lane(xs[u], xs[u]);
         }
-        if (!isv) rotate<INTER>(x, c, s, d0, p.R, 1.0f);
-        if (isq || MODE == kDense) {
-            if (h < H) *reinterpret_cast<uint4 *>(out + h * D) = pack8(x);
-            continue;
-        }
-        const long long at = page_row + ((long long)h << p.c.shift);
-        if (MODE == kAppend) {
-            if (h < H) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(isv ? p.c.v : p.c.k) + at * D + d0) = pack8(x);
-            continue;
-        }
-        uint32_t amax = 0;
+        if (norm) row_sums4<LPR>(rstd, [&](float ss) { return rsqrtf(ss * (1.0f / D) + p.eps); });
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-        amax = row_max<LPR>(amax);
-        const uint32_t byte = e8m0_for(amax);
-        const float inv = e8m0_inverse(byte);
+        for (int u = 0; u < GROUP; ++u) {
+            if (u >= n) break;
+            const bool there = (u0 + u) * RPW < rows;
+            Row &x = xs[u];
+            if (!isv) {
+                Row y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= inv;
-        if (h < H) {
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(isv ? p.c.v : p.c.k) + at * D + d0) = pack8_e4m3(x);
-            if (d0 == 0) (isv ? p.c.vs : p.c.ks)[at] = (uint8_t)byte;
+                for (int k = 0; k < 4; ++k) y.x[k] = mul2(x.x[k], A.x[k]);
+                add_turned<INTER>(y, x, B, pc.turns);
+                x = y;
+                if (norm) {
+                    const F2 r2 = f2(rstd[u], rstd[u]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x.x[k] = mul2(y.x[k], r2);
+                }
+            }
+            const long long row = at + ((long long)((u0 + u) * RPW) << p.c.shift);
+            if (isq || MODE != kAppendE4M3) {
+                const RawRow o = pack_row(x);
+                uint16_t *dst = isq || MODE == kDense ? out + (u0 + u) * RPW * D
+                                                      : static_cast<uint16_t *>(isv ? p.c.v : p.c.k) + row * D;
+                if (there) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint2 *>(dst + pc.c[i]) = o.p[i];
+                }
+                continue;
+            }
+            float2 v[4];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = parts(x.x[k]);
+                amax = max(amax, max(__float_as_uint(v[k].x) & 0x7fffffffu, __float_as_uint(v[k].y) & 0x7fffffffu));
+            }
+            amax = row_max<LPR>(amax);
+            const uint32_t byte = e8m0_for(amax);
+            const float inv = e8m0_inverse(byte);
+            const float y[8] = {v[0].x * inv, v[0].y * inv, v[1].x * inv, v[1].y * inv,
+                                v[2].x * inv, v[2].y * inv, v[3].x * inv, v[3].y * inv};
+            const uint2 codes = pack8_e4m3(y);
+            if (there) {
+                uint8_t *dst = static_cast<uint8_t *>(isv ? p.c.v : p.c.k) + row * D;
+                *reinterpret_cast<uint32_t *>(dst + pc.c[0]) = codes.x;
+                *reinterpret_cast<uint32_t *>(dst + pc.c[1]) = codes.y;
+                if (lane % LPR == 0) (isv ? p.c.vs : p.c.ks)[row] = (uint8_t)byte;
+            }
         }
     }
 }
 
-// Backward: CTAs below nq take head rows of q, the others of k (in proportion),
-// each warp one token and ROWS * RPW heads at a time; a CTA sums its share of
-// dw and leaves it in `partial`.
+constexpr int kCtasPerSm = 2;
+constexpr int kStages = 2;   // backward: tokens of a warp in shared memory, one in work, one on its way
+constexpr int kBwdRows = 4;
+
+// Backward: a CTA belongs to one part of the heads (p.aq CTAs to each of q's, the
+// first; p.ak to each of k's), its warps go from token to token; it sums its share
+// of dw and leaves it in `partial`.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) row_backward_kernel(const RowParams p, int nq) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = 4;
-    __shared__ float2 tables[kWarps][D / 2];
-    __shared__ float sum[kWarps * RPW][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int d0 = (lane % LPR) * 8;
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(const RowParams p) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kBwdRows, HALF = ROWS * RPW * D, STAGE = 2 * HALF;
+    extern __shared__ __align__(16) uint16_t stages[];
+    __shared__ __align__(16) float2 tables[kWarps][D / 2 + 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+    uint16_t *ring = stages + warp * kStages * STAGE;
+    const int nq = p.cq * p.aq;
     const bool isq = (int)blockIdx.x < nq;
     const HeadsIn &in = isq ? p.q : p.k;
-    const int H = isq ? p.Hq : p.Hkv;
-    const uint16_t *dy_p = (isq ? p.dq_out : p.dk_out) + d0;
-    uint16_t *dx_p = (isq ? p.q_out : p.k_out) + d0;
+    const int H = isq ? p.Hq : p.Hkv, cta = isq ? blockIdx.x : blockIdx.x - nq, parts_n = isq ? p.cq : p.ck;
+    const int h0 = cta % parts_n * ROWS * RPW + sub, rows = H - h0;
     const float *wp = isq ? p.wq : p.wk;
     const bool norm = wp != nullptr;
-    float w[8], acc[8];
+    const Pieces pc = Pieces::of<LPR, INTER>(p.R);
+    Row w, acc;
+    if (norm) w = load_weights(wp, pc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w[i] = norm ? wp[d0 + i] : 1.0f;
-        acc[i] = 0.0f;
-    }
-    const unsigned chunks = isq ? p.cq : p.ck, items = (unsigned)p.B * p.T * chunks;
-    const unsigned cta = isq ? blockIdx.x : blockIdx.x - nq, ctas = isq ? nq : gridDim.x - nq;
-    for (unsigned item = cta * kWarps + warp; item < items; item += ctas * kWarps) {
-        const unsigned bt = item / chunks, chunk = item - bt * chunks;
-        const int h0 = (int)chunk * ROWS * RPW + lane / LPR;
-        const long long row0 = (long long)bt * H;
+    for (int k = 0; k < 4; ++k) acc.x[k] = f2(0.0f, 0.0f);
+    const unsigned tokens = (unsigned)(p.B * p.T), step = (isq ? p.aq : p.ak) * kWarps;
+    const uint16_t *x_p = in.p + (long long)h0 * in.hs + (lane % LPR) * 8;
+    const uint16_t *dy_p = (isq ? p.dq_out : p.dk_out) + (long long)h0 * D + (lane % LPR) * 8;
+    uint16_t *dx_p = (isq ? p.q_out : p.k_out) + (long long)h0 * D;
+
+    auto ask = [&](unsigned bt, int stage) {
+        if (p.mask != nullptr && p.mask[bt] == 0) return;
+        const uint16_t *src = x_p + (long long)bt * in.ts, *dy = dy_p + (long long)bt * H * D;
+        uint16_t *dst = ring + stage * STAGE + lane * 8;
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+            const bool there = u * RPW < rows;
+            cp_async16(dst + u * RPW * D, there ? src + u * RPW * in.hs : in.p, there && norm);
+            cp_async16(dst + HALF + u * RPW * D, there ? dy + u * RPW * D : dy_p, there);
+        }
+    };
+    unsigned bt = cta / parts_n * kWarps + warp;
+    if (bt < tokens) ask(bt, 0);
+    cp_async_commit();
+    for (int stage = 0; bt < tokens; bt += step, stage ^= 1) {
+        if (bt + step < tokens) ask(bt + step, stage ^ 1);
+        cp_async_commit();
+        uint16_t *out = dx_p + (long long)bt * H * D;
         if (p.mask != nullptr && p.mask[bt] == 0) {
 #pragma unroll
             for (int u = 0; u < ROWS; ++u)
-                if (h0 + u * RPW < H)
-                    *reinterpret_cast<uint4 *>(dx_p + (row0 + h0 + u * RPW) * D) = make_uint4(0, 0, 0, 0);
+                if (u * RPW < rows)
+                    *reinterpret_cast<uint4 *>(out + u * RPW * D + (lane % LPR) * 8) = make_uint4(0, 0, 0, 0);
             continue;
         }
-        uint4 rx[ROWS], rdy[ROWS];
-        const uint16_t *src = in.p + (long long)bt * in.ts + d0;
+        Row a, b;
+        lane_angles<INTER>(p, tables[warp], pc, p.pos[bt], true, a, b);
+        cp_async_wait<1>();
+        __syncwarp();
+        const uint16_t *src = ring + stage * STAGE + sub * D;
 #pragma unroll
-        for (int u = 0; u < ROWS; ++u) {
-            const int h = h0 + u * RPW;
-            rx[u] = rdy[u] = make_uint4(0, 0, 0, 0);
-            if (h < H) {
-                if (norm) rx[u] = *reinterpret_cast<const uint4 *>(src + h * in.hs);
-                rdy[u] = *reinterpret_cast<const uint4 *>(dy_p + (row0 + h) * D);
+        for (int u0 = 0; u0 < ROWS; u0 += 2) {
+            if (u0 > 0 && u0 * RPW - sub >= rows) break;   // (no row of the warp)
+            Row x[2], dz[2];
+            float sums[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                RawRow rx, rdy;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    rx.p[i] = *reinterpret_cast<const uint2 *>(src + (u0 + u) * RPW * D + pc.c[i]);
+                    rdy.p[i] = *reinterpret_cast<const uint2 *>(src + HALF + (u0 + u) * RPW * D + pc.c[i]);
+                }
+                const Row dy = unpack_row(rdy);
+                x[u] = unpack_row(rx);
+                // (channels that do not turn: a = 1)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dz[u].x[k] = mul2(dy.x[k], a.x[k]);
+                add_turned<INTER>(dz[u], dy, b, pc.turns);
+                if (!norm) continue;
+                Row g;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g.x[k] = mul2(w.x[k], dz[u].x[k]);
+                // x.x, and (w dz).x, which times rstd is (w dz).xhat
+                sums[2 * u] = dot_lane(x[u], x[u]);
+                sums[2 * u + 1] = dot_lane(g, x[u]);
+            }
+            if (norm) row_sums4<LPR>(sums, [](float t) { return t; });
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool there = (u0 + u) * RPW < rows;
+                if (norm) {
+                    float rstd = rsqrtf(sums[2 * u] * (1.0f / D) + p.eps);
+                    if (!there) rstd = 0.0f;   // (a row that is not there; eps = 0 would make it an infinity)
+                    const float m = -sums[2 * u + 1] * rstd * (1.0f / D);
+                    const F2 r2 = f2(rstd, rstd), m2 = f2(m, m);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const F2 xhat = mul2(x[u].x[k], r2);
+                        acc.x[k] = fma2(dz[u].x[k], xhat, acc.x[k]);
+                        dz[u].x[k] = mul2(fma2(xhat, m2, mul2(w.x[k], dz[u].x[k])), r2);
+                    }
+                }
+                const RawRow o = pack_row(dz[u]);
+                if (there) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint2 *>(out + (u0 + u) * RPW * D + pc.c[i]) = o.p[i];
+                }
             }
         }
-        float c[8], s[8];
-        lane_angles<INTER>(p, tables[warp], d0, p.pos[bt], c, s);
-#pragma unroll
-        for (int u = 0; u < ROWS; ++u) {
-            const int h = h0 + u * RPW;
-            if (u > 0 && h0 - lane / LPR + u * RPW >= H) break;   // (no row of the warp)
-            float x[8], dz[8];
-            unpack8(rx[u], x);
-            unpack8(rdy[u], dz);
-            rotate<INTER>(dz, c, s, d0, p.R, -1.0f);
-            if (norm) {
-                // two sums at once: x.x, and (w dz).x, which times rstd is (w dz).xhat
-                float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    dot = fmaf(w[i] * dz[i], x[i], dot);
-                }
-                ss = row_sum<LPR>(ss);
-                dot = row_sum<LPR>(dot);
-                float rstd = rsqrtf(ss * (1.0f / D) + p.eps);
-                if (h >= H) rstd = 0.0f;   // (a row that is not there; eps = 0 would make it an infinity)
-                const float k = dot * rstd * rstd * (1.0f / D);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i] = fmaf(dz[i], x[i] * rstd, acc[i]);
-                    dz[i] = rstd * fmaf(-k, x[i], w[i] * dz[i]);
-                }
-            }
-            if (h < H) *reinterpret_cast<uint4 *>(dx_p + (row0 + h) * D) = pack8(dz);
-        }
+        __syncwarp();   // (the stage is free for the next rows)
     }
+    cp_async_wait<0>();
     grid_dep_launch();
     if (!norm) return;
+    __syncthreads();
+    float *sum = reinterpret_cast<float *>(stages);   // [kWarps * RPW][D]: no more than the stages
+    static_assert(kWarps * RPW * D * 4 <= kWarps * kStages * STAGE * 2, "");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[warp * RPW + lane / LPR][d0 + i] = acc[i];
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = parts(acc.x[k]);
+        *reinterpret_cast<float2 *>(sum + (warp * RPW + sub) * D + pc.c[k >> 1] + 2 * (k & 1)) = v;
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kThreads) {
         float t = 0.0f;
-        for (int i = 0; i < kWarps * RPW; ++i) t += sum[i][d];
+        for (int i = 0; i < kWarps * RPW; ++i) t += sum[i * D + d];
         p.partial[(size_t)blockIdx.x * D + d] = t;
     }
 }
@@ -307,30 +536,45 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *partial, 
 
 int chunks_of(int heads, int rows) { return (heads + rows - 1) / rows; }
 
-template <int D, int MODE, int ROWS>
-cudaError_t launch_forward_rows(RowParams p, bool inter, cudaStream_t st) {
+template <int D, bool INTER, int MODE, int ROWS>
+cudaError_t launch_forward_rows(RowParams p, cudaStream_t st) {
     constexpr int RPW = 32 / (D / 8);
+    constexpr size_t smem = (size_t)kWarps * ROWS * RPW * D * 2;
     p.cq = chunks_of(p.Hq, ROWS * RPW);
     p.ck = chunks_of(p.Hkv, ROWS * RPW);
-    const unsigned long long items = (unsigned long long)p.B * p.T * (p.cq + p.ck * (MODE == kDense ? 1 : 2));
-    if (items > 0xffffff00ull) return cudaErrorNotSupported;
-    const unsigned grid = (unsigned)((items + kWarps - 1) / kWarps);
-    if (inter)
-        row_forward_kernel<D, true, MODE, ROWS><<<grid, kThreads, 0, st>>>(p, (unsigned)items);
-    else
-        row_forward_kernel<D, false, MODE, ROWS><<<grid, kThreads, 0, st>>>(p, (unsigned)items);
+    const long long tokens = (long long)p.B * p.T, ctas = (tokens + kWarps - 1) / kWarps;
+    if (tokens > 0x7fffffffLL - kWarps) return cudaErrorNotSupported;
+    static unsigned long long done = 0;
+    cudaError_t e = set_max_smem(done, row_forward_kernel<D, INTER, MODE, ROWS>, smem);
+    if (e != cudaSuccess) return e;
+    row_forward_kernel<D, INTER, MODE, ROWS>
+        <<<dim3((unsigned)ctas, p.cq + p.ck * (MODE == kDense ? 1 : 2)), kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-// Four rows a warp hide each other's latency when there are warps enough to
-// fill the GPU; with few tokens (B = 128, T = 1: XXA against XXB us) one row a
-// warp spreads wider.
+// Eight rows a warp, or one where there are too few tokens to fill the GPU.
 template <int D, int MODE>
 cudaError_t launch_forward(const RowParams &p, bool inter, cudaStream_t st) {
     constexpr int RPW = 32 / (D / 8);
-    const long long warps = (long long)p.B * p.T * (p.Hq + 2 * p.Hkv) / RPW;
-    return warps >= 64LL * num_sms() ? launch_forward_rows<D, MODE, 4>(p, inter, st)
-                                     : launch_forward_rows<D, MODE, 1>(p, inter, st);
+    const long long rows = (long long)p.B * p.T * (p.Hq + p.Hkv) / RPW;
+    if (rows < 64LL * num_sms())
+        return inter ? launch_forward_rows<D, true, MODE, 1>(p, st) : launch_forward_rows<D, false, MODE, 1>(p, st);
+    return inter ? launch_forward_rows<D, true, MODE, 8>(p, st) : launch_forward_rows<D, false, MODE, 8>(p, st);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_backward_i(const RowParams &p, cudaStream_t st) {
+    constexpr size_t smem = (size_t)kWarps * kStages * 2 * kBwdRows * 512;   // (a warp's rows: 512 bytes)
+    static unsigned long long done = 0;
+    cudaError_t e = set_max_smem(done, row_backward_kernel<D, INTER>, smem);
+    if (e != cudaSuccess) return e;
+    row_backward_kernel<D, INTER><<<p.cq * p.aq + p.ck * p.ak, kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_backward_rows(const RowParams &p, bool inter, cudaStream_t st) {
+    return inter ? launch_backward_i<D, true>(p, st) : launch_backward_i<D, false>(p, st);
 }
 
 template <int MODE>
@@ -361,20 +605,23 @@ RowParams row_params(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, con
     return p;
 }
 
-// CTAs of the backward pass for q and for k: in proportion to their rows, and
-// no more than there is work for.
-void backward_grid(const AttnSizes &s, int *nq, int *nk) {
-    const int rows = 4 * (32 / (s.D / 8));
-    const long long tokens = (long long)s.B * s.T;
-    const long long wq = (tokens * chunks_of(s.Hq, rows) + kWarps - 1) / kWarps;
-    const long long wk = (tokens * chunks_of(s.Hkv, rows) + kWarps - 1) / kWarps;
-    const int total = 2 * num_sms();
-    const int k = (int)((long long)total * s.Hkv / (s.Hq + s.Hkv));
-    *nk = k < 1 ? 1 : k;
-    *nq = total - *nk;
-    if (*nk > wk) *nk = wk < 1 ? 1 : (int)wk;
-    if (*nq > wq) *nq = wq < 1 ? 1 : (int)wq;
-}
+// The backward pass's parts of the heads and the CTAs of each: in proportion to
+// its rows, kCtasPerSm per SM in all, no more than there are tokens for.
+struct BackwardGrid {
+    int cq, ck, aq, ak;
+    explicit BackwardGrid(const AttnSizes &s) {
+        const int rows = kBwdRows * (32 / (s.D / 8));
+        cq = chunks_of(s.Hq, rows);
+        ck = chunks_of(s.Hkv, rows);
+        const long long total = (long long)kCtasPerSm * num_sms(), heads = s.Hq + s.Hkv;
+        const long long most = ((long long)s.B * s.T + kWarps - 1) / kWarps;
+        long long k = total * s.Hkv / heads / ck, q = (total - (k < 1 ? 1 : k) * ck) / cq;
+        if (k > most) k = most;
+        if (q > most) q = most;
+        aq = q < 1 ? 1 : (int)q;
+        ak = k < 1 ? 1 : (int)k;
+    }
+};
 
 }  // namespace
 
@@ -402,9 +649,8 @@ cudaError_t launch_kv_append(const AttnSizes &s, const HeadsIn &q, const HeadsIn
 }
 
 size_t qk_norm_rope_backward_workspace(const AttnSizes &s) {
-    int nq, nk;
-    backward_grid(s, &nq, &nk);
-    return (size_t)(nq + nk) * s.D * sizeof(float);
+    const BackwardGrid g(s);
+    return (size_t)(g.cq * g.aq + g.ck * g.ak) * s.D * sizeof(float);
 }
 
 cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
@@ -419,17 +665,16 @@ cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, c
     p.q_out = dq;
     p.k_out = dk;
     p.partial = static_cast<float *>(ws);
-    const int rows = 4 * (32 / (s.D / 8));
-    p.cq = chunks_of(s.Hq, rows);
-    p.ck = chunks_of(s.Hkv, rows);
-    if ((unsigned long long)s.B * s.T * p.cq > 0x7fffffffull) return cudaErrorNotSupported;
-    int nq, nk;
-    backward_grid(s, &nq, &nk);
-    auto run = [&](auto kernel) { kernel<<<nq + nk, kThreads, 0, st>>>(p, nq); };
-    if (s.D == 64) s.inter ? run(row_backward_kernel<64, true>) : run(row_backward_kernel<64, false>);
-    else if (s.D == 128) s.inter ? run(row_backward_kernel<128, true>) : run(row_backward_kernel<128, false>);
-    else s.inter ? run(row_backward_kernel<256, true>) : run(row_backward_kernel<256, false>);
-    cudaError_t e = cudaGetLastError();
+    const BackwardGrid g(s);
+    p.cq = g.cq;
+    p.ck = g.ck;
+    p.aq = g.aq;
+    p.ak = g.ak;
+    const int nq = g.cq * g.aq, nk = g.ck * g.ak;
+    if ((long long)s.B * s.T > 0x7fffffffLL - (long long)(g.aq + g.ak) * kWarps) return cudaErrorNotSupported;
+    cudaError_t e = s.D == 64    ? launch_backward_rows<64>(p, s.inter, st)
+                    : s.D == 128 ? launch_backward_rows<128>(p, s.inter, st)
+                                 : launch_backward_rows<256>(p, s.inter, st);
     if (e != cudaSuccess || wq == nullptr) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
