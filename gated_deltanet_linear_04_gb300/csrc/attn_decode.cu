@@ -44,17 +44,19 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
 constexpr int kRowCache = 64;      // rows whose lengths a CTA keeps
 constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles
-constexpr int kSmemLimit = 226 * 1024;
+constexpr int kSmemSM = 228 * 1024;   // shared memory of an SM
+constexpr int kMaxCtas = 2;       // CTAs on an SM
 
-// The geometry of a tile for W consumer warps.
-template <int D_, bool FP8_, int W_>
+// The geometry of a tile: eight consumer warps and 32 KB of keys, or (SMALL) two CTAs on an SM with half of both.
+template <int D_, bool FP8_, bool SMALL_>
 struct Geo {
-    static constexpr int D = D_, W = W_, THREADS = W * 32;
+    static constexpr int D = D_, W = SMALL_ ? 4 : 8, THREADS = W * 32, CTAS = SMALL_ ? 2 : 1;
+    static constexpr int SMEM = kSmemSM / CTAS - 2048;         // (1 KB of a CTA is the system's; static shared memory)
     static constexpr bool FP8 = FP8_;
     static constexpr int ROWB = FP8 ? D : 2 * D;               // bytes of a key
     static constexpr int SUBB = ROWB < 128 ? ROWB : 128;       // ... in sub-tiles of one swizzle span
     static constexpr int NSUB = ROWB / SUBB;
-    static constexpr int KT = 32768 / ROWB > 256 ? 256 : 32768 / ROWB;   // keys of a tile: 64, 128 or 256
+    static constexpr int KT = 32768 / CTAS / ROWB > 256 ? 256 : 32768 / CTAS / ROWB;   // keys of a tile: 64, 128 or 256
     static constexpr int TILE = KT * ROWB;                     // bytes of a tile's keys, or values
     static constexpr int KB = KT / 16, DB = D / 16;            // blocks of 16 keys, of 16 channels
     static constexpr int SPLIT = W > KB ? W / KB : 1;          // S: warps that share 16 keys, part of the channels each
@@ -67,7 +69,7 @@ struct Geo {
     static constexpr int KK = KB / KSPL;                       // ... key blocks of a warp
     static constexpr int SSTR = KT + 4;                        // row stride of S (floats): banks 8 apart for rows 2 apart
     static constexpr int PSTR = KT + 8;                        // row stride of P (16-bit): banks 4 apart
-    static constexpr int PRODUCERS = FP8 ? 4 : 2;              // warps: keys, values, key scales, value scales
+    static constexpr int PRODUCERS = FP8 && !SMALL_ ? 4 : 2;   // warps: keys, values, key scales, value scales (or the first: all scales)
     static_assert(KS >= (FP8 ? 2 : 1) && KK >= 2 && KK % 2 == 0, "");
 };
 
@@ -102,7 +104,7 @@ struct Smem {
     static constexpr int sc_bytes = G::FP8 ? 2 * G::KT : 0;    // a stage's scales
     static constexpr int fixed = q_bytes + s_bytes + p_bytes + row_bytes;
     static constexpr int pair = 2 * G::TILE + sc_bytes;        // a stage of both rings
-    static constexpr int fit = (kSmemLimit - 1024 - fixed) / pair;
+    static constexpr int fit = (G::SMEM - 1024 - fixed) / pair;
     static constexpr int stages = fit > kMaxStages ? kMaxStages : fit;
     static constexpr int q = stages * 2 * G::TILE, s = q + q_bytes, p = s + s_bytes, row = p + p_bytes,
                          sc = row + row_bytes, total = sc + stages * sc_bytes;
@@ -267,7 +269,7 @@ __device__ __forceinline__ void consumer_sync() {
 }
 
 template <class G, int NT>
-__global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
+__global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const Params p) {
     using L = Smem<G, NT>;
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
     if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full_k[i], FP8 ? 3 : 1);
+            mbar_init(&full_k[i], G::PRODUCERS == 4 ? 3 : 1);
             mbar_init(&full_v[i], 1);
             mbar_init(&empty_k[i], W);
             mbar_init(&empty_v[i], W);
@@ -367,7 +369,9 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
         // ---- producers: lane i < bpt fills box i of every tile -------------------------------------------
         const int role = warp - W;                  // keys, values, key scales, value scales
         const int bpt = KT >> p.box_log2, page_sh = p.c.shift - p.box_log2;   // boxes per tile; pages = boxes >> page_sh
+        constexpr bool all_scales = FP8 && G::PRODUCERS == 2;
         const uint32_t bytes = role < 2 ? (uint32_t)boxrows * G::ROWB : (uint32_t)boxrows;
+        const uint32_t box_bytes = bytes + (all_scales && role == 0 ? 2 * boxrows : 0);
         uint64_t *full = role == 1 ? full_v : full_k, *empty = role == 1 ? empty_v : empty_k;
         unsigned char *ring = role < 2 ? smem + (role == 0 ? 0 : G::TILE) : smem + L::sc + (role - 2) * KT;
         const int pitch = role < 2 ? 2 * G::TILE : 2 * KT;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                     if (lane == 0) {
                         if (role == 0) bad_boxes[st] = ~good & (bpt == 32 ? 0xffffffffu : (1u << bpt) - 1);
                         if (good != 0)
-                            mbar_expect_tx(&full[st], __popc(good) * bytes);
+                            mbar_expect_tx(&full[st], __popc(good) * box_bytes);
                         else
                             mbar_arrive(&full[st]);
                     }
@@ -415,6 +419,11 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, 1)
                             tma_load_3d(dst, role == 0 ? &tm_k : &tm_v, 0, row, 0, &full[st]);
                         else
                             bulk_load(dst, scales + row, bytes, &full[st]);
+                        if (all_scales && role == 0) {
+                            unsigned char *sc = smem + L::sc + st * 2 * KT + lane * boxrows;
+                            bulk_load(sc, p.c.ks + row, boxrows, &full[st]);
+                            bulk_load(sc + KT, p.c.vs + row, boxrows, &full[st]);
+                        }
                     }
                     used |= 1u << st;
                     if (++st == NST) {
@@ -1088,7 +1097,7 @@ struct Workspace {
 Workspace workspace(const AttnSizes &s) {
     int blocks, rows;   // (the most rows of a unit with either cache format)
     row_blocks(s, 64, &blocks, &rows);
-    const size_t ctas = (size_t)num_sms(), slots = 2 * ctas;
+    const size_t ctas = (size_t)num_sms() * kMaxCtas, slots = 2 * ctas;
     Workspace w;
     w.o = 0;
     w.ml = up256(slots * rows * s.D * sizeof(float));
@@ -1124,7 +1133,7 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     // the tiles of a call are counted in 32 bits
     const unsigned long long units = (unsigned long long)p.B * p.Hkv * p.RB;
     if (units * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1 + kBlank) > 0x7fffffffULL) return cudaErrorNotSupported;
-    const int ctas = num_sms();
+    const int ctas = num_sms() * G::CTAS;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1137,6 +1146,8 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<G, NT>, maps[0], maps[1], p);
     if (e != cudaSuccess) return e;
+    // (a table with no room for a second tile: no unit has parts; 1 key: 4.7 us, with a join that finds none 7.3)
+    if (((long long)p.c.width << p.c.shift) <= G::KT) return cudaSuccess;
     cfg.gridDim = dim3(ctas, p.rows < 8 ? p.rows : 8);
     cfg.dynamicSmemBytes = 0;
     // few units: many parts each, many threads to read them; many units: mostly two parts, small CTAs
@@ -1152,9 +1163,18 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
 // channels in e4m3: 53.5 us; four 56.9, sixteen 58.6).
 template <int D, bool FP8>
 cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
-    using G = Geo<D, FP8, 8>;
+    using G = Geo<D, FP8, false>;
     constexpr int most = G::KT == 256 ? 32 : 64;   // query rows of a unit: S and P of a tile have to fit
     row_blocks(s, most, &p.RB, &p.rows);
+    if constexpr (FP8 || D < 256) {
+        // Short tables: a unit's start and end cost more than its keys, and two CTAs go through them side by side (B =
+        // 128, 32 and 8 heads of 128 channels, e4m3: one tile of up to 128 keys 15.7 us, with 32 KB tiles 26.4; 300
+        // keys 27.1 against 38.3).  With few units and more keys the larger tile is ahead (B = 1, 2 heads, 600 keys:
+        // 9.0 against 10.2 us), and so it is with more than 8 query rows (16, 100 keys: 8.6 against 9.2 us).
+        using GS = Geo<D, FP8, true>;
+        const long long cap = (long long)p.c.width << p.c.shift, units = (long long)p.B * p.Hkv;
+        if (p.rows <= 8 && cap <= (units >= 4 * num_sms() ? 4 : 1) * GS::KT) return launch_t<GS, 1>(p, st);
+    }
     if (p.rows <= 8) return launch_t<G, 1>(p, st);
     if (p.rows <= 16) return launch_t<G, 2>(p, st);
     if (p.rows <= 32) return launch_t<G, 4>(p, st);

@@ -422,8 +422,29 @@ def test_decode(attn, case, fp8):
     assert torch.equal(out, again)                                       # fixed order of the joins
     # a table wider than needed, its further entries never looked at
     wide = torch.cat((table, torch.full((B, 3), 1 << 30, dtype=I32)), 1).to(DEV)
-    more = attn.attn_decode(d, args[1], cache, wide, *args[4:])
-    assert torch.equal(out, more)
+    more, lse = attn.attn_decode(d, args[1], cache, wide, *args[4:], return_lse=True)
+    check_decode(more, lse, q, cache, table, pos, nn, D ** -0.5, gate)   # (what a table could hold chooses the tiles)
+
+
+@pytest.mark.parametrize("spare", [0, 64])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 64), (24, 8, 128), (32, 8, 256)])
+def test_decode_short_rows(attn, Hq, Hkv, D, fp8, spare):
+    """Many rows of few keys: lengths around every tile's end, in tables with
+    and without room for more (`spare` further pages per row)."""
+    B, P = 80, 16
+    d = wl.AttnDims(B, 1, Hq, Hkv, D)
+    g = gen(B + D + spare)
+    ends = (1, 16, 63, 64, 65, 127, 128, 129, 192, 193, 255, 256, 257)
+    pos = [ends[i % len(ends)] - 1 for i in range(B)]
+    width = -(-max(ends) // P)
+    cache = make_cache(attn, d, B * width + 1, P, fp8, g)
+    table = tables(g, B, width, B * width + 1)
+    q, gate = normal(g, B, 1, Hq, D, std=1.5), normal(g, B, 1, Hq, D)
+    wide = torch.cat((table, torch.full((B, spare), -1, dtype=I32)), 1)
+    out, lse = attn.attn_decode(d, q.to(DEV), cache, wide.to(DEV), torch.tensor(pos, dtype=I32).to(DEV),
+                                gate=gate.to(DEV), return_lse=True)
+    check_decode(out, lse, q, cache, table, pos, None, D ** -0.5, gate)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
