@@ -26,6 +26,11 @@
 // their way.  (Warps that take whole tiles on their own, with all channels and
 // a join at the end of each unit, held each tile three times as long and lost
 // 5 us at each unit's end: 69 against 61 us for B = 128, e4m3, 2048 keys.)
+// What it came to (16 query and 2 key heads of 256 channels): one row of 262144
+// keys in bf16 85.7 us, 6.3 TB/s of keys and values; B = 128, up to 4096 keys in
+// e4m3 53.6 us, 5.1 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
+// channels, bf16 58.5 us, 5.2 TB/s.  A tile takes the consumers about 3000
+// clocks with e4m3 (its conversions alone take 770 of them), the memory 2700.
 //
 // Products.  mma.sync m16n8k16 with keys (then channels) as the 16 and query
 // rows as the 8: eight heads per key head fill n = 8 exactly, where a 128-row
@@ -43,7 +48,8 @@ using namespace attn;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
 constexpr int kRowCache = 64;      // rows whose lengths a CTA keeps
-constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles
+constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles (B = 128, ragged, e4m3: 1, 2, 3 of
+                                  // them 56.2, 53.6, 53.7 us)
 constexpr int kSmemSM = 228 * 1024;   // shared memory of an SM
 constexpr int kMaxCtas = 2;       // CTAs on an SM
 
@@ -1150,10 +1156,12 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     if (((long long)p.c.width << p.c.shift) <= G::KT) return cudaSuccess;
     cfg.gridDim = dim3(ctas, p.rows < 8 ? p.rows : 8);
     cfg.dynamicSmemBytes = 0;
-    // few units: many parts each, many threads to read them; many units: mostly two parts, small CTAs
+    // few units: many parts each, more threads to read them; many units: mostly two parts, small CTAs (2 key heads of
+    // 256 channels, 8000 keys, one row: 11.6 us for the whole call with 256 threads, 17.0 with 128; 4000 keys, 64
+    // rows: 87.0 and 86.0; 512 threads gain 0.5 us on the first and lose 0.8 at 1000 keys)
     if (units * 8 < (unsigned)ctas) {
-        cfg.blockDim = dim3(512);
-        return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 512>, p);
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 256>, p);
     }
     cfg.blockDim = dim3(128);
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 128>, p);
