@@ -10,6 +10,15 @@
 namespace gdn {
 namespace attn {
 
+// Waits for the previous grid on the stream, then lets the next one be
+// scheduled: not before, as a kernel that reads constants ahead of its own wait
+// (the delta-rule decode its convolution taps) would read them before a copy
+// still running two launches back.
+__device__ __forceinline__ void grid_dep_enter() {
+    grid_dep_wait();
+    grid_dep_launch();
+}
+
 // cos and sin of position * frequency.  freq is in turns per position as a
 // 64-bit binary fraction, so the product mod 2^64 is the angle's exact
 // fraction of a turn (the integer multiply drops whole turns).  Its upper 32

@@ -290,7 +290,6 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     __shared__ int2 row_cache[kRowCache];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dep_launch();
     if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    grid_dep_wait();
+    grid_dep_enter();
 
     // the share: prefix sums of the rows' tiles, blockDim rows at a time (twice, if that is not all of them)
     const int heads = p.Hkv * p.RB;
@@ -1014,8 +1013,7 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
     constexpr int COLS = D / 4, GROUPS = THREADS / COLS, UNROLL = 4;
     __shared__ float4 sums[GROUPS][COLS];
     __shared__ float red_m[GROUPS], red_l[GROUPS];
-    grid_dep_launch();
-    grid_dep_wait();
+    grid_dep_enter();
     const int c0 = blockIdx.x, unit = p.meta[3 * c0];
     if (unit < 0) return;
     // its first part lies in that share's slot, the others in the first slots of the shares that follow
@@ -1140,31 +1138,17 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
     const unsigned long long units = (unsigned long long)p.B * p.Hkv * p.RB;
     if (units * (((unsigned long long)p.c.width << p.c.shift) / G::KT + 1 + kBlank) > 0x7fffffffULL) return cudaErrorNotSupported;
     const int ctas = num_sms() * G::CTAS;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3((G::W + G::PRODUCERS) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<G, NT>, maps[0], maps[1], p);
+    e = DependentLaunch(dim3(ctas), dim3((G::W + G::PRODUCERS) * 32), smem, st)(attn_decode_kernel<G, NT>, maps[0],
+                                                                               maps[1], p);
     if (e != cudaSuccess) return e;
     // (a table with no room for a second tile: no unit has parts; 1 key: 4.7 us, with a join that finds none 7.3)
     if (((long long)p.c.width << p.c.shift) <= G::KT) return cudaSuccess;
-    cfg.gridDim = dim3(ctas, p.rows < 8 ? p.rows : 8);
-    cfg.dynamicSmemBytes = 0;
+    const dim3 grid(ctas, p.rows < 8 ? p.rows : 8);
     // few units: many parts each, more threads to read them; many units: mostly two parts, small CTAs (2 key heads of
     // 256 channels, 8000 keys, one row: 11.6 us for the whole call with 256 threads, 17.0 with 128; 4000 keys, 64
     // rows: 87.0 and 86.0; 512 threads gain 0.5 us on the first and lose 0.8 at 1000 keys)
-    if (units * 8 < (unsigned)ctas) {
-        cfg.blockDim = dim3(256);
-        return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 256>, p);
-    }
-    cfg.blockDim = dim3(128);
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<G::D, 128>, p);
+    if (units * 8 < (unsigned)ctas) return DependentLaunch(grid, dim3(256), 0, st)(attn_join_kernel<G::D, 256>, p);
+    return DependentLaunch(grid, dim3(128), 0, st)(attn_join_kernel<G::D, 128>, p);
 }
 
 // Eight consumer warps (B = 128, 8 query heads per key head, 2048 keys of 256

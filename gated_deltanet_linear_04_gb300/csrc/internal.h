@@ -45,6 +45,30 @@ cudaError_t set_max_smem(unsigned long long &done, K kernel, size_t bytes) {
     });
 }
 
+// A launch whose grid may be scheduled while the one before it on the stream
+// still runs; the kernel waits for that one (grid_dep_wait) before it touches
+// memory.
+struct DependentLaunch {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+
+    DependentLaunch(dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    DependentLaunch(const DependentLaunch &) = delete;
+    template <typename... K, typename... A>
+    cudaError_t operator()(void (*kernel)(K...), A &&...args) const {
+        return cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
+    }
+};
+
 cudaError_t launch_conv_update(const Sizes &s, const uint16_t *qkv, const uint16_t *conv_w, uint16_t *conv_state,
                                const uint8_t *mask, uint16_t *q, uint16_t *k, uint16_t *v, unsigned *err,
                                cudaStream_t st);

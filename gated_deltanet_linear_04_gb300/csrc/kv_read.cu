@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p, unsign
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31;
     const unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5);
+    grid_dep_enter();
     if (item >= items) return;
     const unsigned bt = item / chunks, chunk = item - bt * chunks;
     const int b = (int)(bt / (unsigned)p.T), t = (int)(bt - (unsigned)b * p.T);
@@ -81,8 +82,8 @@ cudaError_t launch_read(const ReadParams &p, cudaStream_t st) {
     const unsigned chunks = (p.Hkv + ROWS * RPW - 1) / (ROWS * RPW);
     const unsigned long long items = (unsigned long long)p.B * p.T * chunks;
     if (items > 0xffffff00ull) return cudaErrorNotSupported;
-    kv_read_kernel<D, FP8, ROWS><<<(unsigned)((items + 7) / 8), 256, 0, st>>>(p, (unsigned)items, chunks);
-    return cudaGetLastError();
+    return DependentLaunch(dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st)(kv_read_kernel<D, FP8, ROWS>, p,
+                                                                                (unsigned)items, chunks);
 }
 
 template <int D>

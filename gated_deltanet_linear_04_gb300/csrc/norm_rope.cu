@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
     __shared__ __align__(16) float2 tables[kWarps][D / 2 + 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
     const unsigned bt = blockIdx.x * kWarps + warp, part = blockIdx.y;
+    grid_dep_enter();
     if (bt >= (unsigned)(p.B * p.T)) return;
     const bool isq = part < (unsigned)p.cq, isv = MODE != kDense && part >= (unsigned)(p.cq + p.ck);
     const int h0 = (int)(isq ? part : isv ? part - p.cq - p.ck : part - p.cq) * ROWS * RPW + sub;
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
     const float *wp = isq ? p.wq : p.wk;
     const bool norm = wp != nullptr;
     const Pieces pc = Pieces::of<LPR, INTER>(p.R);
+    grid_dep_enter();
     Row w, acc;
     if (norm) w = load_weights(wp, pc);
 #pragma unroll
@@ -497,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
         __syncwarp();   // (the stage is free for the next rows)
     }
     cp_async_wait<0>();
-    grid_dep_launch();
     if (!norm) return;
     __syncthreads();
     float *sum = reinterpret_cast<float *>(stages);   // [kWarps * RPW][D]: no more than the stages
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
 __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *partial, int nq, int n, int D, float *dwq,
                                                           float *dwk) {
     __shared__ float sum[32][33];
-    grid_dep_wait();
+    grid_dep_enter();
     const bool isq = blockIdx.x == 0;
     const int d = blockIdx.y * 32 + threadIdx.x, part = threadIdx.y;
     float t = 0.0f;
@@ -547,9 +548,8 @@ cudaError_t launch_forward_rows(RowParams p, cudaStream_t st) {
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, row_forward_kernel<D, INTER, MODE, ROWS>, smem);
     if (e != cudaSuccess) return e;
-    row_forward_kernel<D, INTER, MODE, ROWS>
-        <<<dim3((unsigned)ctas, p.cq + p.ck * (MODE == kDense ? 1 : 2)), kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return DependentLaunch(dim3((unsigned)ctas, p.cq + p.ck * (MODE == kDense ? 1 : 2)), dim3(kThreads), smem,
+                           st)(row_forward_kernel<D, INTER, MODE, ROWS>, p);
 }
 
 // Eight rows a warp, or one where there are too few tokens to fill the GPU (16 +
@@ -570,8 +570,8 @@ cudaError_t launch_backward_i(const RowParams &p, cudaStream_t st) {
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, row_backward_kernel<D, INTER>, smem);
     if (e != cudaSuccess) return e;
-    row_backward_kernel<D, INTER><<<p.cq * p.aq + p.ck * p.ak, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return DependentLaunch(dim3(p.cq * p.aq + p.ck * p.ak), dim3(kThreads), smem,
+                           st)(row_backward_kernel<D, INTER>, p);
 }
 
 template <int D>
@@ -678,16 +678,8 @@ cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, c
                     : s.D == 128 ? launch_backward_rows<128>(p, s.inter, st)
                                  : launch_backward_rows<256>(p, s.inter, st);
     if (e != cudaSuccess || wq == nullptr) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, s.D / 32);
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weight_sum_kernel, (const float *)p.partial, nq, nq + nk, (int)s.D, dwq, dwk);
+    return DependentLaunch(dim3(2, s.D / 32), dim3(32, 32), 0, st)(weight_sum_kernel, (const float *)p.partial, nq,
+                                                                   nq + nk, (int)s.D, dwq, dwk);
 }
 
 }  // namespace gdn
