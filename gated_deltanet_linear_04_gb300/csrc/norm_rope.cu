@@ -22,8 +22,8 @@
 //     each head row is y = rstd (x A + x' B), x' the partners.
 //   - four rows' sums go over the lanes together; arithmetic goes two channels
 //     at a time (f32x2 instructions).
-// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): 27.5 us forward (a plain
-// copy of as much takes 23.5), 50.5 backward (227 MB).  Steps on the way: a warp per
+// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): 27.4 us forward (a plain
+// copy of as much takes 23.5), 42.9 backward (227 MB).  Steps on the way: a warp per
 // head row 89 us; four rows a warp, into registers, partners by shuffle, sincospi
 // 31.4 (164 instructions a row, most of them a token's angles and addresses).
 #include "attn.cuh"
@@ -608,16 +608,20 @@ RowParams row_params(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, con
 }
 
 // The backward pass's parts of the heads and the CTAs of each: in proportion to
-// its rows, kCtasPerSm per SM in all, no more than there are tokens for.
+// their work (a token's angles and addresses cost a warp as much as three rows),
+// kCtasPerSm per SM in all, no more than there are tokens for.
 struct BackwardGrid {
     int cq, ck, aq, ak;
     explicit BackwardGrid(const AttnSizes &s) {
         const int rows = kBwdRows * (32 / (s.D / 8));
         cq = chunks_of(s.Hq, rows);
         ck = chunks_of(s.Hkv, rows);
-        const long long total = (long long)kCtasPerSm * num_sms(), heads = s.Hq + s.Hkv;
+        const int rpw = 32 / (s.D / 8);
+        const long long total = (long long)kCtasPerSm * num_sms();
+        const long long work_q = 3 * cq + chunks_of(s.Hq, rpw), work_k = 3 * ck + chunks_of(s.Hkv, rpw);
         const long long most = ((long long)s.B * s.T + kWarps - 1) / kWarps;
-        long long k = total * s.Hkv / heads / ck, q = (total - (k < 1 ? 1 : k) * ck) / cq;
+        long long k = (2 * total * work_k / (work_q + work_k) + ck) / (2 * ck);   // (rounded)
+        long long q = (total - (k < 1 ? 1 : k) * ck) / cq;
         if (k > most) k = most;
         if (q > most) q = most;
         aq = q < 1 ? 1 : (int)q;
