@@ -47,7 +47,7 @@ using namespace attn;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
-constexpr int kRowCache = 64;      // rows whose lengths a CTA keeps
+constexpr int kRowCache = 192;     // rows whose lengths a CTA keeps
 constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles (B = 128, ragged, e4m3: 1, 2, 3 of
                                   // them 56.2, 53.6, 53.7 us)
 constexpr int kSmemSM = 228 * 1024;   // shared memory of an SM
@@ -57,7 +57,7 @@ constexpr int kMaxCtas = 2;       // CTAs on an SM
 template <int D_, bool FP8_, bool SMALL_>
 struct Geo {
     static constexpr int D = D_, W = SMALL_ ? 4 : 8, THREADS = W * 32, CTAS = SMALL_ ? 2 : 1;
-    static constexpr int SMEM = kSmemSM / CTAS - 2048;         // (1 KB of a CTA is the system's; static shared memory)
+    static constexpr int SMEM = kSmemSM / CTAS - 3072;         // (1 KB of a CTA is the system's; static shared memory)
     static constexpr bool FP8 = FP8_;
     static constexpr int ROWB = FP8 ? D : 2 * D;               // bytes of a key
     static constexpr int SUBB = ROWB < 128 ? ROWB : 128;       // ... in sub-tiles of one swizzle span
@@ -307,14 +307,19 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     // the share: prefix sums of the rows' tiles, blockDim rows at a time (twice, if that is not all of them)
     const int heads = p.Hkv * p.RB;
     constexpr int nthr = (W + G::PRODUCERS) * 32, nwarp = nthr / 32;
-    const bool once = p.B <= nthr;
+    const bool once = p.B <= nthr, keep = p.B <= kRowCache && once;   // (keep: all rows' lengths, as they come in)
     Shares sh;
     unsigned start = 0;
     for (int pass = 0; pass < 2; ++pass) {
         unsigned run = 0;
         for (int base = 0; base < p.B; base += nthr) {
             const int b = base + tid;
-            const unsigned v = b < p.B ? (unsigned)((row_len<G>(p, b).tiles + kBlank) * heads) : 0;
+            unsigned v = 0;
+            if (b < p.B) {
+                const int pos = p.pos[b], n = clamp_new(p.n_new, b, p.T);
+                if (keep) row_cache[b] = make_int2(pos, n);
+                v = (unsigned)((row_len<G>(p, pos, n).tiles + kBlank) * heads);
+            }
             unsigned x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -352,11 +357,16 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     Walk<G> walk;
     walk.b = found_b;
     walk.rows = row_cache;
-    walk.row0 = found_b;
-    if (tid < kRowCache && found_b + tid < p.B)
-        row_cache[tid] = make_int2(p.pos[found_b + tid], clamp_new(p.n_new, found_b + tid, p.T));
-    __syncthreads();
-    walk.len = row_len<G>(p, walk.b);
+    walk.row0 = keep ? 0 : found_b;
+    if (!keep) {
+        if (tid < kRowCache && found_b + tid < p.B)
+            row_cache[tid] = make_int2(p.pos[found_b + tid], clamp_new(p.n_new, found_b + tid, p.T));
+        __syncthreads();
+    }
+    {
+        const int2 row = row_cache[found_b - walk.row0];
+        walk.len = row_len<G>(p, row.x, row.y);
+    }
     walk.slot = start;
     walk.left = (int)(sh.start(blockIdx.x + 1) - start);
     {
@@ -1022,6 +1032,15 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
     const int nrows = min(p.rows, p.R - r0);
     const int tid = threadIdx.x, col = tid % COLS, grp = tid / COLS;
     for (int r = blockIdx.y; r < nrows; r += gridDim.y) {
+        const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
+        const long long bt = (long long)b * p.T + t;
+        constexpr int OUTS = (D + THREADS - 1) / THREADS;
+        uint16_t gate[OUTS];   // (asked for before it is needed)
+#pragma unroll
+        for (int i = 0; i < OUTS; ++i) {
+            const int d = tid + i * THREADS;
+            gate[i] = p.gate.p != nullptr && d < D ? p.gate.p[bt * p.gate.ts + hq * p.gate.hs + d] : 0;
+        }
         // this group's parts, with a running maximum
         float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1064,7 +1083,10 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
             red_l[grp] = l;
         }
         __syncthreads();
-        for (int d = tid; d < D; d += THREADS) {
+#pragma unroll
+        for (int x = 0; x < OUTS; ++x) {
+            const int d = tid + x * THREADS;
+            if (d >= D) break;
             float top = -INFINITY, acc = 0.0f, total = 0.0f;
 #pragma unroll
             for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, red_m[i]);
@@ -1075,10 +1097,8 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
                 acc = fmaf(w, reinterpret_cast<const float *>(sums[i])[d], acc);
                 total = fmaf(w, red_l[i], total);
             }
-            const int rr = r0 + r, t = rr / p.G, hq = h * p.G + rr % p.G;
-            const long long bt = (long long)b * p.T + t;
             float y = total == 0.0f ? 0.0f : acc / total;
-            if (p.gate.p != nullptr) y *= sigmoid(bf16_to_f32(p.gate.p[bt * p.gate.ts + hq * p.gate.hs + d]));
+            if (p.gate.p != nullptr) y *= sigmoid(bf16_to_f32(gate[x]));
             p.out[(bt * p.Hq + hq) * D + d] = f32_to_bf16(y);
             if (d == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;
         }
