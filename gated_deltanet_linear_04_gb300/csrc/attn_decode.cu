@@ -5,7 +5,7 @@
 // running maximum: one pass over the keys and values, HBM-bound (16 flop per
 // byte for 8 query heads per key head, bf16).
 //
-// Work.  A unit is one (row b, key head h, block of at most 64 of its T * Hq/Hkv
+// Work.  A unit is one (row b, key head h, block of at most 32 of its T * Hq/Hkv
 // query rows); its keys come in tiles of KT (32 KB of keys, 32 KB of values).
 // The tiles of all units form one list (with a blank slot before each unit's
 // first tile, for what its start and end cost), cut into equal shares for one
@@ -27,10 +27,12 @@
 // a join at the end of each unit, held each tile three times as long and lost
 // 5 us at each unit's end: 69 against 61 us for B = 128, e4m3, 2048 keys.)
 // What it came to (16 query and 2 key heads of 256 channels): one row of 262144
-// keys in bf16 85.7 us, 6.3 TB/s of keys and values; B = 128, up to 4096 keys in
-// e4m3 53.6 us, 5.1 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
-// channels, bf16 58.5 us, 5.2 TB/s.  A tile takes the consumers about 3000
-// clocks with e4m3 (its conversions alone take 770 of them), the memory 2700.
+// keys in bf16 87 us, 6.2 TB/s of keys and values; B = 128, up to 4096 keys in
+// e4m3 52.4 us, 5.2 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
+// channels, bf16 57.5 us, 5.3 TB/s.  In between, a tile takes the consumers about
+// 3100 clocks (with e4m3 its conversions alone take 770 of them), the memory 2990;
+// the first data come after 5 us, and a unit's end and the next one's start cost
+// 4000 clocks more than a tile.
 //
 // Products.  mma.sync m16n8k16 with keys (then channels) as the 16 and query
 // rows as the 8: eight heads per key head fill n = 8 exactly, where a 128-row
@@ -106,7 +108,7 @@ struct Smem {
     static constexpr int s_only = G::SPLIT * rows * G::SSTR * 4, o_parts = (G::KSPL - 1) * rows * G::D * 4;
     static constexpr int s_bytes = s_only > o_parts ? s_only : o_parts;
     static constexpr int p_bytes = rows * G::PSTR * 2;
-    static constexpr int row_bytes = rows * 20;                // corr, qscale, (m, l), fin
+    static constexpr int row_bytes = rows * 16;                // corr, qscale, fin
     static constexpr int sc_bytes = G::FP8 ? 2 * G::KT : 0;    // a stage's scales
     static constexpr int fixed = q_bytes + s_bytes + p_bytes + row_bytes;
     static constexpr int pair = 2 * G::TILE + sc_bytes;        // a stage of both rings
@@ -152,6 +154,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// sigmoid(x), a factor of an f32 that is rounded to bf16 next: the hardware's
+// exponential and reciprocal are off by about 2^-21 (2^-17 at |x| = 80).
+__device__ __forceinline__ float gate_value(float x) { return rcp_fast(1.0f + exp_fast(-x)); }
 
 // The warp's largest value; a NaN is passed over.
 __device__ __forceinline__ float warp_max(float x) {
@@ -284,13 +290,14 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     constexpr bool QREG = NT <= 2;           // query operands in registers; else read from shared memory each time
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) uint64_t full_k[NST], full_v[NST], empty_k[NST], empty_v[NST];
-    __shared__ uint32_t bad_boxes[NST];
+    __shared__ uint32_t bad_boxes[NST], nan_tile;
     __shared__ unsigned warp_sum_sh[G::W + 4], found_off;
     __shared__ int found_b;
     __shared__ int2 row_cache[kRowCache];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
+        nan_tile = 0;
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full_k[i], G::PRODUCERS == 4 ? 3 : 1);
@@ -469,8 +476,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     float *sS = reinterpret_cast<float *>(smem + L::s);            // [SPLIT][rows][SSTR]
     uint16_t *sP = reinterpret_cast<uint16_t *>(smem + L::p);      // [rows][PSTR]
     float *corr = reinterpret_cast<float *>(smem + L::row), *qscale = corr + L::rows;
-    float2 *ml = reinterpret_cast<float2 *>(qscale + L::rows);
-    float *fin = reinterpret_cast<float *>(ml + L::rows);
+    float2 *fin = reinterpret_cast<float2 *>(qscale + L::rows);
     const uint32_t ring = smem_u32(smem);
     // ldmatrix rows and 16-byte chunks of this lane: matrix mi holds rows (mi & 1) * 8 .. and chunk + (mi >> 1)
     // (keys; e4m3 values), or rows (mi >> 1) * 8 .. and chunk + (mi & 1) (bf16 values)
@@ -510,6 +516,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
     int stv = 0;                      // the stage of the tile's values (st: of the next tile's keys), and their parity
     uint32_t phv = 0;
     bool first = true;
+    uint32_t tile_no = 0;
     // 8 channels of a query row per thread, asked for a unit ahead (where the registers allow it)
     constexpr bool EARLY = NT <= 2;
     constexpr int QV = (L::rows * (D / 8) + G::THREADS - 1) / G::THREADS;
@@ -693,6 +700,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
             const int key0 = (ta + i) * KT;
             const uint32_t bad = bad_next;
             const bool tail = bad != 0 || key0 + KT > all_see;
+            ++tile_no;
             consumer_sync<G::THREADS>();
 
             // softmax: weights of this warp's rows
@@ -774,6 +782,46 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 st = 0;
                 ph ^= 1;
             }
+            if (tail) {
+                // the values of slots that hold no key: zeros (a weight of 0 times whatever lies there is not 0), so that
+                // the products need no masks.  (They are read after the next barrier.)
+                if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
+                dead = __any_sync(0xffffffffu, dead);
+                unsigned char *const values = smem + stv * 2 * G::TILE + G::TILE;
+                auto chunk = [&](int key, int c) {   // 16 bytes of a key's value row, in any order
+                    return values + (key >> p.box_log2) * (boxrows * G::ROWB) + (c / (G::SUBB / 16)) * substride +
+                           (key & (boxrows - 1)) * G::SUBB + c % (G::SUBB / 16) * 16;
+                };
+                constexpr int CPR = G::ROWB / 16;
+                if (!dead && (bad != 0 || key0 + KT > len.keys)) {
+                    const int end = min(KT, ((int)len.keys - key0 + 31) & ~31);   // (the products stop there)
+#pragma unroll 1
+                    for (int x = tid; x < (i + 1 < n ? KT : end) * CPR; x += G::THREADS) {
+                        const int key = x / CPR;
+                        if (key0 + key >= len.keys || (bad >> (key >> p.box_log2) & 1) != 0)
+                            *reinterpret_cast<uint4 *>(chunk(key, x % CPR)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();   // (before the next fill of the stage)
+                }
+                // a NaN or infinity among the values that only later tokens see
+                if (!dead && p.T > 1) {
+                    bool nan = false;
+                    for (int key = max(all_see - key0, 0) + warp; key < KT && key0 + key < len.keys; key += W) {
+                        if (bad >> (key >> p.box_log2) & 1) continue;
+                        for (int x = lane; x < G::ROWB / 4; x += 32) {
+                            const uint32_t v = *reinterpret_cast<const uint32_t *>(chunk(key, x / 4) + x % 4 * 4);
+                            if (FP8) {
+                                const uint32_t y = v & 0x7f7f7f7fu;
+                                nan |= (y & 0xff) == 0x7f || (y & 0xff00) == 0x7f00 || (y & 0xff0000) == 0x7f0000 ||
+                                       (y >> 24) == 0x7f;
+                            } else {
+                                nan |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+                            }
+                        }
+                    }
+                    if (nan) nan_tile = tile_no;
+                }
+            }
             // usually both are there already: one look on the way to the barrier instead of two waits after it
             const bool more = i + 1 < n;
             const bool there = mbar_test(&full_v[stv], phv) && (!more || mbar_test(&full_k[st], ph));
@@ -808,7 +856,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
                         const int kb = kk + k2;
-                        // values of slots that hold no key are zeroed
+                        // masked: zeros for values that the token does not see
                         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
                         if (masked) {
 #pragma unroll
@@ -852,56 +900,36 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                     }
                 };
                 const int kk0 = o_part * G::KK;
-                if (!tail && more) {
+                // (a NaN that some tokens do not see: 0 times it is not 0)
+                const bool window = tail && p.T > 1 && *static_cast<volatile uint32_t *>(&nan_tile) == tile_no;
+                if (!window && more) {
                     scores();
 #pragma unroll
                     for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, false, 0, acc);
-                } else if (!tail) {
-#pragma unroll 2
-                    for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, false, 0, acc);
+                } else if (!window) {
+                    // (the last tile: blocks of 32 keys that hold none are left out)
+                    const int held = ((int)len.keys - key0 + 31) / 32 * 2;
+#pragma unroll
+                    for (int kk = 0; kk < G::KK; kk += 2) {
+                        if (kk0 + kk >= held) break;
+                        step(kk0 + kk, false, 0, acc);
+                    }
                 } else {
                     if (more) scores();
-                    // a NaN or infinity among the values that only later tokens see: 0 times it is not 0
-                    bool window = false;
-                    if (p.T > 1) {
-                        for (int key = max(all_see - key0, 0); key < KT && key0 + key < len.keys; ++key) {
-                            if (bad >> (key >> p.box_log2) & 1) continue;
-                            const unsigned char *row = smem + stv * 2 * G::TILE + G::TILE +
-                                                       (key >> p.box_log2) * (boxrows * G::ROWB) +
-                                                       (key & (boxrows - 1)) * G::SUBB;
-                            for (int x = lane; x < G::ROWB / 4; x += 32) {
-                                const uint32_t v = *reinterpret_cast<const uint32_t *>(
-                                    row + (x / (G::SUBB / 4)) * substride + (x % (G::SUBB / 4)) * 4);
-                                if (FP8) {
-                                    const uint32_t y = v & 0x7f7f7f7fu;
-                                    window |= (y & 0xff) == 0x7f || (y & 0xff00) == 0x7f00 ||
-                                              (y & 0xff0000) == 0x7f0000 || (y >> 24) == 0x7f;
-                                } else {
-                                    window |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+                    // one pass per token over the values it sees, the other rows' sums dropped
+                    for (int t = 0; t < len.n; ++t) {
+                        float one[G::DPW][NT][4] = {};
+                        const int see = (int)min(max(len.pos + t + 1, 0LL), len.keys);
+#pragma unroll 1
+                        for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, true, see, one);
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (((r0 + c * 8 + 2 * j + (e & 1)) * p.g_mul >> 16) == t) {
+#pragma unroll
+                                    for (int d = 0; d < G::DPW; ++d) acc[d][c][e] += one[d][c][e];
                                 }
-                            }
-                        }
-                        window = __any_sync(0xffffffffu, window);
-                    }
-                    if (!window) {
-#pragma unroll 1
-                        for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, true, (int)len.keys, acc);
-                    } else {
-                        // one pass per token over the values it sees, the other rows' sums dropped
-                        for (int t = 0; t < len.n; ++t) {
-                            float one[G::DPW][NT][4] = {};
-                            const int see = (int)min(max(len.pos + t + 1, 0LL), len.keys);
-#pragma unroll 1
-                            for (int kk = 0; kk < G::KK; kk += 2) step(kk0 + kk, true, see, one);
-#pragma unroll
-                            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (((r0 + c * 8 + 2 * j + (e & 1)) * p.g_mul >> 16) == t) {
-#pragma unroll
-                                        for (int d = 0; d < G::DPW; ++d) acc[d][c][e] += one[d][c][e];
-                                    }
-                        }
                     }
                 }
                 __syncwarp();
@@ -914,17 +942,39 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
             if (more) put_scores();
         }
 
-        // the unit's output, or this share's part of it
+        // the unit's output, or this share's part of it.  Lane c finishes row c of the warp: its factors (of a row that
+        // saw nothing: -1), log-sum-exp or part.
+        const bool whole = seg.whole();
+        const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+        {
+            float top = -INFINITY, sum = 0.0f, topv = 0.0f;
+            bool none = true;
 #pragma unroll
-        for (int c = 0; c < RPW; ++c) {
-            float sum = l[c];
+            for (int c = 0; c < RPW; ++c) {
+                float x = l[c];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0 && c * W + warp < L::rows) {
-                // (a token that is not there has no visible key; mv - m: the weighted sum in units of 2^m)
-                const bool none = lim[c] == 0 || m[c] == -INFINITY;
-                ml[c * W + warp] = make_float2(none ? -INFINITY : m[c], none ? 0.0f : sum);
-                fin[c * W + warp] = none ? 0.0f : FP8 ? ex2(mv[c] - m[c]) : 1.0f;
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane == c) {
+                    top = m[c];
+                    topv = mv[c];
+                    sum = x;
+                    none = lim[c] == 0 || m[c] == -INFINITY || x == 0.0f;   // (also a token that is not there)
+                }
+            }
+            const int r = lane * W + warp;
+            if (lane < RPW && r < nrows) {
+                // (mv - m: the weighted sum in units of 2^m)
+                fin[r] = make_float2(none ? -1.0f : FP8 ? ex2(topv - top) : 1.0f, whole ? rcp_fast(sum) : 1.0f);
+                if (none) {
+                    top = -INFINITY;
+                    sum = 0.0f;
+                }
+                if (!whole) {
+                    p.part_ml[(size_t)slot * p.rows + r] = make_float2(top, sum);
+                } else if (p.lse != nullptr) {
+                    const int rr = r0 + r, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
+                    p.lse[((long long)b * p.T + t) * p.Hq + hq] = (top + log2f(sum)) * kLn2;
+                }
             }
         }
         // the parts of O that went over other keys, joined in their order in S's place
@@ -950,8 +1000,6 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[d][c][e] += part(y, d, c, e);
         }
-        const bool whole = seg.whole();
-        const int slot = 2 * blockIdx.x + (first ? 0 : 1);
         if (o_part == 0) {
 #pragma unroll
             for (int c = 0; c < NT; ++c)
@@ -959,31 +1007,28 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 for (int x = 0; x < 2; ++x) {
                     const int r = c * 8 + 2 * j + x;
                     if (r >= nrows) continue;
-                    const float2 v = ml[r];
-                    const float f = fin[r];
+                    const float2 f = fin[r];
                     const int rr = r0 + r, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
                     const long long bt = (long long)b * p.T + t;
-                    const float inv = v.y == 0.0f ? 0.0f : 1.0f / v.y;
 #pragma unroll
                     for (int d = 0; d < G::DPW; ++d) {
                         // channels d0, d1 of this thread's two values
                         const int dt = (o_blk + d) * 16, d0 = FP8 ? dt + 2 * g : dt + g, d1 = FP8 ? d0 + 1 : d0 + 8;
                         float o0 = acc[d][c][x], o1 = acc[d][c][2 + x];
-                        if (v.y == 0.0f) o0 = o1 = 0.0f;           // (also of a token that is not there)
-                        o0 *= f;
-                        o1 *= f;
+                        o0 = f.x < 0.0f ? 0.0f : o0 * f.x;
+                        o1 = f.x < 0.0f ? 0.0f : o1 * f.x;
                         if (!whole) {
                             float *dst = p.part_o + ((size_t)slot * p.rows + r) * D;
                             dst[d0] = o0;
                             dst[d1] = o1;
                             continue;
                         }
-                        o0 *= inv;
-                        o1 *= inv;
+                        o0 = f.x < 0.0f ? 0.0f : o0 * f.y;   // (the reciprocal of no sum is an infinity)
+                        o1 = f.x < 0.0f ? 0.0f : o1 * f.y;
                         if (gated) {
                             const uint32_t z = EARLY ? gates[EARLY ? d : 0][EARLY ? c : 0][x] : gate_pair(r, d);
-                            o0 *= sigmoid(__uint_as_float(z << 16));
-                            o1 *= sigmoid(__uint_as_float(z & 0xffff0000u));
+                            o0 *= gate_value(__uint_as_float(z << 16));
+                            o1 *= gate_value(__uint_as_float(z & 0xffff0000u));
                         }
                         uint16_t *dst = p.out + (bt * p.Hq + hq) * D;
                         if (FP8) {
@@ -994,15 +1039,6 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                         }
                     }
                 }
-        }
-        if (tid < nrows) {
-            const float2 v = ml[tid];
-            if (!whole) {
-                p.part_ml[(size_t)slot * p.rows + tid] = v;
-            } else if (p.lse != nullptr) {
-                const int rr = r0 + tid, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
-                p.lse[((long long)b * p.T + t) * p.Hq + hq] = (v.x + log2f(v.y)) * kLn2;
-            }
         }
         if (ta == 0 && !whole && tid == 0) {
             // the unit goes on: its last tile lies in the share that holds that tile's slot
@@ -1098,17 +1134,20 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
                 total = fmaf(w, red_l[i], total);
             }
             float y = total == 0.0f ? 0.0f : acc / total;
-            if (p.gate.p != nullptr) y *= sigmoid(bf16_to_f32(gate[x]));
+            if (p.gate.p != nullptr) y *= gate_value(bf16_to_f32(gate[x]));
             p.out[(bt * p.Hq + hq) * D + d] = f32_to_bf16(y);
             if (d == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;
         }
     }
 }
 
-// Row blocks of a (b, h) and the query rows of one.
-void row_blocks(const AttnSizes &s, int most, int *blocks, int *rows) {
+// Row blocks of a (b, h) and the query rows of one.  (Blocks of 64 read the keys
+// once where two of 32 read them twice, but spill registers: B = 32, 64 rows, 4
+// key heads of 256 channels, e4m3, 2300 keys: 213 against 114 us.)
+void row_blocks(const AttnSizes &s, int *blocks, int *rows) {
+    constexpr int kMost = 32;
     const int R = s.T * (s.Hq / s.Hkv);
-    *blocks = (R + most - 1) / most;
+    *blocks = (R + kMost - 1) / kMost;
     *rows = (R + *blocks - 1) / *blocks;
 }
 
@@ -1119,8 +1158,8 @@ struct Workspace {
 };
 
 Workspace workspace(const AttnSizes &s) {
-    int blocks, rows;   // (the most rows of a unit with either cache format)
-    row_blocks(s, 64, &blocks, &rows);
+    int blocks, rows;
+    row_blocks(s, &blocks, &rows);
     const size_t ctas = (size_t)num_sms() * kMaxCtas, slots = 2 * ctas;
     Workspace w;
     w.o = 0;
@@ -1176,8 +1215,7 @@ cudaError_t launch_t(const Params &p0, cudaStream_t st) {
 template <int D, bool FP8>
 cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
     using G = Geo<D, FP8, false>;
-    constexpr int most = G::KT == 256 ? 32 : 64;   // query rows of a unit: S and P of a tile have to fit
-    row_blocks(s, most, &p.RB, &p.rows);
+    row_blocks(s, &p.RB, &p.rows);
     if constexpr (FP8 || D < 256) {
         // Short tables: a unit's start and end cost more than its keys, and two CTAs go through them side by side (B =
         // 128, 32 and 8 heads of 128 channels, e4m3: one tile of up to 128 keys 15.7 us, with 32 KB tiles 26.4; 300
@@ -1189,9 +1227,7 @@ cudaError_t launch_g(Params &p, const AttnSizes &s, cudaStream_t st) {
     }
     if (p.rows <= 8) return launch_t<G, 1>(p, st);
     if (p.rows <= 16) return launch_t<G, 2>(p, st);
-    if (p.rows <= 32) return launch_t<G, 4>(p, st);
-    if constexpr (most > 32) return launch_t<G, 8>(p, st);
-    return cudaErrorInvalidValue;
+    return launch_t<G, 4>(p, st);
 }
 
 template <int D>
