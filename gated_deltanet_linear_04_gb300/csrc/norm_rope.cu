@@ -74,9 +74,17 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], F &&f) {
 
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    if constexpr (LPR == 32) return __reduce_max_sync(0xffffffffu, x);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = LPR / 2; LPR < 32 && o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
+}
+
+// max(a, |b|, |c|), a >= 0; a NaN if one of them is
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Two f32 in one register pair.
@@ -267,8 +275,10 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
         const long long hop = RPW * in.hs;
 #pragma unroll
         for (int u = 0; u < ROWS; ++u) {
-            cp_async16(ring + u * RPW * D + lane * 8, src, u * RPW < rows);
-            if (u * RPW + RPW < rows) src += hop;
+            if (u * RPW < rows + sub) {   // (a row of the warp)
+                cp_async16(ring + u * RPW * D + lane * 8, src, u * RPW < rows);
+                if (u * RPW + RPW < rows) src += hop;
+            }
             if ((u + 1) % GROUP == 0) cp_async_commit();
         }
     }
@@ -361,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
                 continue;
             }
             float2 v[4];
-            uint32_t amax = 0;
+            float most = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 v[k] = parts(x.x[k]);
-                amax = max(amax, max(__float_as_uint(v[k].x) & 0x7fffffffu, __float_as_uint(v[k].y) & 0x7fffffffu));
+                most = max_abs(most, v[k].x, v[k].y);
             }
-            amax = row_max<LPR>(amax);
+            const uint32_t amax = row_max<LPR>(__float_as_uint(most));
             const uint32_t byte = e8m0_for(amax);
             const float inv = e8m0_inverse(byte);
             const float y[8] = {v[0].x * inv, v[0].y * inv, v[1].x * inv, v[1].y * inv,
