@@ -74,10 +74,13 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], F &&f) {
 
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t x) {
-    if constexpr (LPR == 32) return __reduce_max_sync(0xffffffffu, x);
+    if constexpr (LPR == 32) {
+        return __reduce_max_sync(0xffffffffu, x);
+    } else {
 #pragma unroll
-    for (int o = LPR / 2; LPR < 32 && o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+        for (int o = LPR / 2; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+    }
 }
 
 // max(a, |b|, |c|), a >= 0; a NaN if one of them is
