@@ -458,13 +458,11 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 id1 = id2;
             }
         }
-        // after a wait that gave up: let the copies in flight land before the CTA ends
-        if (dead) {
-            for (int i = 0; i < NST; ++i) {
-                if ((used >> i & 1) == 0) continue;
-                const uint32_t phase = i < st ? ph : ph ^ 1;   // the parity of stage i's last fill
-                for (uint32_t k = 0; k < kSpinLimit && !mbar_try_wait(&full[i], phase); ++k) {
-                }
+        // let the copies in flight land before the CTA ends (they have, but after a wait that gave up)
+        for (int i = 0; i < NST; ++i) {
+            if ((used >> i & 1) == 0) continue;
+            const uint32_t phase = i < st ? ph : ph ^ 1;   // the parity of stage i's last fill
+            for (uint32_t k = 0; k < kSpinLimit && !mbar_try_wait(&full[i], phase); ++k) {
             }
         }
         return;
@@ -774,10 +772,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                     *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
                 }
             }
-            if (FP8 && !dead) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty_k[st]);
-            }
+            const int scales = st;
             if (++st == NST) {
                 st = 0;
                 ph ^= 1;
@@ -824,11 +819,12 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
             }
             // usually both are there already: one look on the way to the barrier instead of two waits after it
             const bool more = i + 1 < n;
-            const bool there = mbar_test(&full_v[stv], phv) && (!more || mbar_test(&full_k[st], ph));
+            const bool v_there = mbar_test(&full_v[stv], phv), k_there = mbar_test(&full_k[st], ph);
             consumer_sync<G::THREADS>();
+            if (FP8 && !dead && lane == 0) mbar_arrive(&empty_k[scales]);
 
             // the next tile's scores and this one's O^T += V^T P^T, which do not wait for each other
-            if (!__all_sync(0xffffffffu, there)) {
+            if (!__all_sync(0xffffffffu, v_there && (k_there || !more))) {
                 if (!dead && !mbar_wait(&full_v[stv], phv, p.err)) dead = true;
                 dead = __any_sync(0xffffffffu, dead);
                 if (more) wait_keys();
