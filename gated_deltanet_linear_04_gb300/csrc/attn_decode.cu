@@ -7,12 +7,12 @@
 //
 // Work.  A unit is one (row b, key head h, block of at most 32 of its T * Hq/Hkv
 // query rows); its keys come in tiles of KT (32 KB of keys, 32 KB of values).
-// The tiles of all units form one list (with a blank slot before each unit's
-// first tile, for what its start and end cost), cut into equal shares for one
-// CTA per SM, so ragged batches and a single long row both fill the GPU; each
-// CTA finds its share from pos / n_new itself.  A unit that crosses shares leaves
-// partial results (m, sum, weighted sum) in the workspace, and a second kernel
-// joins them in share order.
+// The tiles of all units form one list (with blank slots before each unit's first
+// tile, for what its start and end cost), cut into equal shares for one CTA per
+// SM (two, with half the tile, for short tables), so ragged batches and a single
+// long row both fill the GPU; each CTA finds its share from pos / n_new itself.
+// A unit that crosses shares leaves partial results (m, sum, weighted sum) in the
+// workspace, and a second kernel joins them in share order.
 //
 // CTA.  Producer warps keep two rings (keys, values) filled with TMA box loads
 // (a box: the tokens of one page, or KT of them, 128-byte swizzled; a page
