@@ -27,9 +27,9 @@
 // a join at the end of each unit, held each tile three times as long and lost
 // 5 us at each unit's end: 69 against 61 us for B = 128, e4m3, 2048 keys.)
 // What it came to (16 query and 2 key heads of 256 channels): one row of 262144
-// keys in bf16 87 us, 6.2 TB/s of keys and values; B = 128, up to 4096 keys in
-// e4m3 52.4 us, 5.2 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
-// channels, bf16 57.5 us, 5.3 TB/s.  In between, a tile takes the consumers about
+// keys in bf16 86 us, 6.3 TB/s of keys and values; B = 128, up to 4096 keys in
+// e4m3 49.2 us, 5.5 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
+// channels, bf16 54.9 us, 5.5 TB/s.  (With every key in the L2 cache 41 and 47 us.)  In between, a tile takes the consumers about
 // 3100 clocks (with e4m3 its conversions alone take 770 of them), the memory 2990;
 // the first data come after 5 us, and a unit's end and the next one's start cost
 // 4000 clocks more than a tile.
@@ -171,6 +171,25 @@ __device__ __forceinline__ float2 e8m0_pair(uint32_t bytes) {
     uint32_t b;
     asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"((uint16_t)bytes));
     return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+
+// L2 policy of keys and values, which a call reads once (rows that share pages, at
+// about the same time): they go before what else the cache holds.  In calls one after
+// the other the ragged batch takes 50.2 instead of 53.0 us, windows 56.0 instead of
+// 58.7; after a flush of the cache there is no difference, nor with shared pages.
+__device__ __forceinline__ uint64_t read_once() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+
+// A box of a page's keys or values: row `row` on, all channels.
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int row, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %2}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(row), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
 }
 
 // Four e4m3 codes as two f16 pairs, exactly.
@@ -398,6 +417,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
         unsigned char *ring = role < 2 ? smem + (role == 0 ? 0 : G::TILE) : smem + L::sc + (role - 2) * KT;
         const int pitch = role < 2 ? 2 * G::TILE : 2 * KT;
         const uint8_t *scales = role == 2 ? p.c.ks : p.c.vs;
+        const uint64_t policy = read_once();
         uint32_t used = 0;
         // page numbers, asked for two tiles ahead, those of a unit's first two during the unit before
         auto boxes = [&](const Seg &u) { return (int)((u.len.keys + boxrows - 1) >> p.box_log2); };
@@ -438,7 +458,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                         const int row = ((id * p.Hkv + h) << p.c.shift) + ((box << p.box_log2) & (p.c.page - 1));
                         unsigned char *dst = ring + st * pitch + lane * bytes;
                         if (role < 2)
-                            tma_load_3d(dst, role == 0 ? &tm_k : &tm_v, 0, row, 0, &full[st]);
+                            load_box(dst, role == 0 ? &tm_k : &tm_v, row, &full[st], policy);
                         else
                             bulk_load(dst, scales + row, bytes, &full[st]);
                         if (all_scales && role == 0) {
