@@ -89,7 +89,7 @@ struct Params {
     uint16_t *out;
     float *lse;
     float *part_o;      // [2 * ctas][rows][D]
-    float2 *part_ml;    // [2 * ctas][rows]
+    float2 *part_ml;    // [2 * ctas][rows]: m and the sum, which is -1 where the row saw no key of the part
     int *meta;          // [ctas][3]: the unit that starts in the share and goes on (or -1), its last share, its slot
     unsigned *err;
     int B, T, Hq, Hkv, G, R;
@@ -607,6 +607,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
         // softmax state of this warp's rows
         float m[RPW], l[RPW], mv[RPW], rs[RPW];
         int lim[RPW];                 // visible keys, 0 for a row that is not there
+        uint32_t seen = 0;            // bit c: this lane saw a key of row c
 #pragma unroll
         for (int c = 0; c < RPW; ++c) {
             m[c] = mv[c] = -INFINITY;
@@ -718,6 +719,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
             const int key0 = (ta + i) * KT;
             const uint32_t bad = bad_next;
             const bool tail = bad != 0 || key0 + KT > all_see;
+            if (!tail) seen = ~0u;
             ++tile_no;
             consumer_sync<G::THREADS>();
 
@@ -761,6 +763,8 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                             if (!there || key0 + key + e >= lim[c]) {
                                 z[x][e] = -INFINITY;
                                 ve[x][e] = 0.0f;
+                            } else {
+                                seen |= 1u << c;
                             }
                     }
 #pragma unroll
@@ -772,7 +776,8 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 top = warp_max(top);
                 if (FP8) topv = warp_max(topv);
                 const float mn = fmaxf(m[c], top), mvn = FP8 ? fmaxf(mv[c], topv) : mn;
-                // (an infinite maximum only where nothing, or an infinity, was seen)
+                // (an infinite maximum only where nothing, an infinity or nothing but NaN was seen: the maxima pass
+                // over NaN, which the sum and the weights take up)
                 const float base = mn == -INFINITY ? 0.0f : mn, basev = mvn == -INFINITY ? 0.0f : mvn;
                 l[c] *= ex2(m[c] - base);
                 float f = FP8 ? ex2(mv[c] - basev) : ex2(m[c] - base);
@@ -959,12 +964,14 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
         }
 
         // the unit's output, or this share's part of it.  Lane c finishes row c of the warp: its factors (of a row that
-        // saw nothing: -1), log-sum-exp or part.
+        // saw nothing: -1), log-sum-exp or part.  What a row saw is counted and not read off its maximum, which is
+        // -inf after scores of NaN too: there the sum is NaN (after scores of -inf: 0, and the output 0 / 0).
         const bool whole = seg.whole();
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
         {
             float top = -INFINITY, sum = 0.0f, topv = 0.0f;
             bool none = true;
+            seen = __reduce_or_sync(0xffffffffu, seen);
 #pragma unroll
             for (int c = 0; c < RPW; ++c) {
                 float x = l[c];
@@ -974,19 +981,20 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                     top = m[c];
                     topv = mv[c];
                     sum = x;
-                    none = lim[c] == 0 || m[c] == -INFINITY || x == 0.0f;   // (also a token that is not there)
+                    none = lim[c] == 0 || (seen >> c & 1) == 0;   // (also a token that is not there)
                 }
             }
             const int r = lane * W + warp;
             if (lane < RPW && r < nrows) {
-                // (mv - m: the weighted sum in units of 2^m)
-                fin[r] = make_float2(none ? -1.0f : FP8 ? ex2(topv - top) : 1.0f, whole ? rcp_fast(sum) : 1.0f);
+                // (mv - m: the weighted sum in units of 2^m; without a maximum it is 0 or NaN in any units)
+                fin[r] = make_float2(none ? -1.0f : FP8 && top != -INFINITY ? ex2(topv - top) : 1.0f,
+                                     whole ? rcp_fast(sum) : 1.0f);
                 if (none) {
                     top = -INFINITY;
                     sum = 0.0f;
                 }
                 if (!whole) {
-                    p.part_ml[(size_t)slot * p.rows + r] = make_float2(top, sum);
+                    p.part_ml[(size_t)slot * p.rows + r] = make_float2(top, none ? -1.0f : sum);
                 } else if (p.lse != nullptr) {
                     const int rr = r0 + r, t = rr * p.g_mul >> 16, hq = h * p.G + rr - t * p.G;
                     p.lse[((long long)b * p.T + t) * p.Hq + hq] = (top + log2f(sum)) * kLn2;
@@ -1093,8 +1101,10 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
             const int d = tid + i * THREADS;
             gate[i] = p.gate.p != nullptr && d < D ? p.gate.p[bt * p.gate.ts + hq * p.gate.hs + d] : 0;
         }
-        // this group's parts, with a running maximum
+        // this group's parts, with a running maximum.  A part without a maximum has the weight 0: it saw nothing (its
+        // sums are -1 and 0), only scores of -inf (0 and 0) or only NaN (both NaN, and 0 times them is NaN).
         float m = -INFINITY, l = 0.0f;
+        bool seen = false;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int i0 = grp; i0 < n; i0 += GROUPS * UNROLL) {
             float2 v[UNROLL];
@@ -1103,7 +1113,7 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
             for (int k = 0; k < UNROLL; ++k) {
                 const int i = i0 + k * GROUPS;
                 const size_t slot = i == 0 ? first_slot : 2 * (c0 + i);
-                v[k] = make_float2(-INFINITY, 0.0f);
+                v[k] = make_float2(-INFINITY, -1.0f);
                 x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (i < n) {
                     v[k] = p.part_ml[slot * p.rows + r];
@@ -1118,8 +1128,8 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
             l *= f;
 #pragma unroll
             for (int k = 0; k < UNROLL; ++k) {
-                if (v[k].x == -INFINITY) continue;   // (a part in which the row saw nothing)
-                const float w = ex2(v[k].x - top);
+                seen |= !(v[k].y < 0.0f);
+                const float w = v[k].x == -INFINITY ? 0.0f : ex2(v[k].x - top);
                 l = fmaf(w, v[k].y, l);
                 o.x = fmaf(w, x[k].x, o.x);
                 o.y = fmaf(w, x[k].y, o.y);
@@ -1132,7 +1142,7 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
         sums[grp][col] = o;
         if (col == 0) {
             red_m[grp] = m;
-            red_l[grp] = l;
+            red_l[grp] = seen ? l : -1.0f;
         }
         __syncthreads();
 #pragma unroll
@@ -1140,16 +1150,17 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
             const int d = tid + x * THREADS;
             if (d >= D) break;
             float top = -INFINITY, acc = 0.0f, total = 0.0f;
+            bool any = false;
 #pragma unroll
             for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, red_m[i]);
 #pragma unroll
             for (int i = 0; i < GROUPS; ++i) {
-                if (red_m[i] == -INFINITY) continue;
-                const float w = ex2(red_m[i] - top);
+                any |= !(red_l[i] < 0.0f);
+                const float w = red_m[i] == -INFINITY ? 0.0f : ex2(red_m[i] - top);
                 acc = fmaf(w, reinterpret_cast<const float *>(sums[i])[d], acc);
                 total = fmaf(w, red_l[i], total);
             }
-            float y = total == 0.0f ? 0.0f : acc / total;
+            float y = any ? acc / total : 0.0f;
             if (p.gate.p != nullptr) y *= gate_value(bf16_to_f32(gate[x]));
             p.out[(bt * p.Hq + hq) * D + d] = f32_to_bf16(y);
             if (d == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;

@@ -537,7 +537,9 @@ GDN_API gdn_status gdn_kv_read(const gdn_attn_dims *dims, const gdn_kv_cache *ca
  *          order: equal calls give equal bits.
  * Scores and sums are f32.  Softmax weights are rounded to 16 bits for the
  * product with V.  Values and keys at positions that a token does not see do
- * not enter its results, whatever they hold. */
+ * not enter its results, whatever they hold; a NaN among the scores that it
+ * does see makes its output and lse NaN, and scores that are all -inf make its
+ * output NaN (0 / 0) and lse -inf. */
 GDN_API size_t gdn_attn_decode_workspace_size(const gdn_attn_dims *dims);
 GDN_API gdn_status gdn_attn_decode(const gdn_attn_dims *dims, const uint16_t *q, const gdn_kv_cache *cache,
                                    const int32_t *page_table, int32_t table_width, const int32_t *pos,
