@@ -1049,7 +1049,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                         }
                         o0 = f.x < 0.0f ? 0.0f : o0 * f.y;   // (the reciprocal of no sum is an infinity)
                         o1 = f.x < 0.0f ? 0.0f : o1 * f.y;
-                        if (gated) {
+                        if (gated && !(f.x < 0.0f)) {   // (the gate of a token that is not there may be NaN)
                             const uint32_t z = EARLY ? gates[EARLY ? d : 0][EARLY ? c : 0][x] : gate_pair(r, d);
                             o0 *= gate_value(__uint_as_float(z << 16));
                             o1 *= gate_value(__uint_as_float(z & 0xffff0000u));
@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(THREADS) attn_join_kernel(const Params p) {
                 total = fmaf(w, red_l[i], total);
             }
             float y = any ? acc / total : 0.0f;
-            if (p.gate.p != nullptr) y *= gate_value(bf16_to_f32(gate[x]));
+            if (any && p.gate.p != nullptr) y *= gate_value(bf16_to_f32(gate[x]));
             p.out[(bt * p.Hq + hq) * D + d] = f32_to_bf16(y);
             if (d == 0 && p.lse != nullptr) p.lse[bt * p.Hq + hq] = (top + log2f(total)) * kLn2;
         }

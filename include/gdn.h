@@ -526,7 +526,7 @@ GDN_API gdn_status gdn_kv_read(const gdn_attn_dims *dims, const gdn_kv_cache *ca
  * lse = log sum_j exp(s_j).
  *   q      bf16 [B, T, Hq, D] (in), dense: gdn_kv_append's q_out
  *   pos, n_new as gdn_kv_append; a token past n_new[b], or one that sees no
- *          key, gives zeros and lse = -inf
+ *          key, gives zeros and lse = -inf, whatever its gate holds
  *   gate   bf16 heads [B, T, Hq, D] or NULL: out is multiplied by
  *          sigmoid(gate), in f32 before its one rounding to bf16
  *   scale  of the scores (usually 1/sqrt(D)); finite
