@@ -785,17 +785,19 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 if (lane == 0) corr[r] = f;
                 m[c] = mn;
                 mv[c] = mvn;
+                float sum = 0.0f;   // of the tile: added to the running sum at once, or small weights drift beside a large one
 #pragma unroll
                 for (int x = 0; x < KT / 64; ++x) {
                     float w[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         w[e] = ex2(z[x][e] - base);
-                        l[c] += w[e];
+                        sum += w[e];
                         if (FP8) w[e] = ex2(z[x][e] + ve[x][e] - basev);
                     }
                     *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
                 }
+                l[c] += sum;
             }
             const int scales = st;
             if (++st == NST) {
