@@ -50,6 +50,10 @@ using namespace attn;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxStages = 4;
 constexpr int kRowCache = 192;     // rows whose lengths a CTA keeps
+// f16 softmax weights (e4m3 caches) are 2^14 at the largest: f16 ends at 2^16, and below 2^-14 it loses bits.  So a
+// weight is whole down to 2^-28 of the largest and lost only below 2^-39; with 1 as the largest, 2^-14 and 2^-25, a few
+// hundred thousand keys 17 nats below another lost a third of their share of the output.
+constexpr float kWeightBits = 14.0f, kWeightUnit = 1.0f / 16384;
 constexpr int kBlank = 2;         // blank slots of a unit in the list of tiles (B = 128, ragged, e4m3: 1, 2, 3 of
                                   // them 56.2, 53.6, 53.7 us)
 constexpr int kSmemSM = 228 * 1024;   // shared memory of an SM
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                     for (int e = 0; e < 2; ++e) {
                         w[e] = ex2(z[x][e] - base);
                         sum += w[e];
-                        if (FP8) w[e] = ex2(z[x][e] + ve[x][e] - basev);
+                        if (FP8) w[e] = ex2(z[x][e] + ve[x][e] - basev + kWeightBits);
                     }
                     *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
                 }
@@ -988,9 +992,10 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
             }
             const int r = lane * W + warp;
             if (lane < RPW && r < nrows) {
-                // (mv - m: the weighted sum in units of 2^m; without a maximum it is 0 or NaN in any units)
+                // (mv - m: the weighted sum in units of 2^m; without a maximum it is 0 or NaN in any units.  The second
+                // factor comes first: it takes the sum to the values' codes, the other one these to the values)
                 fin[r] = make_float2(none ? -1.0f : FP8 && top != -INFINITY ? ex2(topv - top) : 1.0f,
-                                     whole ? rcp_fast(sum) : 1.0f);
+                                     (whole ? rcp_fast(sum) : 1.0f) * (FP8 ? kWeightUnit : 1.0f));
                 if (none) {
                     top = -INFINITY;
                     sum = 0.0f;
@@ -1041,16 +1046,14 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                         // channels d0, d1 of this thread's two values
                         const int dt = (o_blk + d) * 16, d0 = FP8 ? dt + 2 * g : dt + g, d1 = FP8 ? d0 + 1 : d0 + 8;
                         float o0 = acc[d][c][x], o1 = acc[d][c][2 + x];
-                        o0 = f.x < 0.0f ? 0.0f : o0 * f.x;
-                        o1 = f.x < 0.0f ? 0.0f : o1 * f.x;
+                        o0 = f.x < 0.0f ? 0.0f : o0 * f.y * f.x;   // (the reciprocal of no sum is an infinity)
+                        o1 = f.x < 0.0f ? 0.0f : o1 * f.y * f.x;
                         if (!whole) {
                             float *dst = p.part_o + ((size_t)slot * p.rows + r) * D;
                             dst[d0] = o0;
                             dst[d1] = o1;
                             continue;
                         }
-                        o0 = f.x < 0.0f ? 0.0f : o0 * f.y;   // (the reciprocal of no sum is an infinity)
-                        o1 = f.x < 0.0f ? 0.0f : o1 * f.y;
                         if (gated && !(f.x < 0.0f)) {   // (the gate of a token that is not there may be NaN)
                             const uint32_t z = EARLY ? gates[EARLY ? d : 0][EARLY ? c : 0][x] : gate_pair(r, d);
                             o0 *= gate_value(__uint_as_float(z << 16));

@@ -54,3 +54,12 @@ def test_sum_of_one_key_before_many(attn, nats, place, rows, fp8):  # noqa: F811
     """The log-sum-exp: small terms on top of a large one do not drift."""
     _, _, err, tol = one_before_many(attn, nats, place, rows, fp8)
     assert torch.all(err <= tol), (float(err.max()), float(tol.max()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [1, 0])
+@pytest.mark.parametrize("nats,place", CASES)
+def test_output_of_one_key_before_many(attn, nats, place, rows, fp8):  # noqa: F811
+    """Each weight's rounding and the output's are at most half a step of bf16."""
+    err, tol, _, _ = one_before_many(attn, nats, place, rows, fp8)
+    assert torch.all(err <= tol), "off by %.3e more than %.3e" % (float((err - tol).max()), float(tol[..., 6].max()))
