@@ -609,12 +609,12 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 for (int c = 0; c < NT; ++c) qr[ks][c] = qf[((s_part * G::KS + ks) * NT + c) * 32 + lane];
         }
         // softmax state of this warp's rows
-        float m[RPW], l[RPW], mv[RPW], rs[RPW];
+        float m[RPW], l[RPW], dv[RPW], rs[RPW];   // dv: largest (score + value exponent), less m
         int lim[RPW];                 // visible keys, 0 for a row that is not there
         uint32_t seen = 0;            // bit c: this lane saw a key of row c
 #pragma unroll
         for (int c = 0; c < RPW; ++c) {
-            m[c] = mv[c] = -INFINITY;
+            m[c] = dv[c] = -INFINITY;
             l[c] = 0.0f;
             const int r = c * W + warp, t = (r0 + r) * p.g_mul >> 16;
             lim[c] = r < nrows && t < len.n ? (int)min(max(len.pos + t + 1, 0LL), len.keys) : 0;
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 const int r = c * W + warp;
                 if (r >= nrows) continue;
                 float z[KT / 64][2], ve[KT / 64][2];
-                float top = -INFINITY, topv = -INFINITY;
+                float top = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < KT / 64; ++x) {
                     const int key = x * 64 + 2 * lane;
@@ -772,32 +772,44 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                             }
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        top = fmaxf(top, z[x][e]);
-                        if (FP8) topv = fmaxf(topv, z[x][e] + ve[x][e]);
-                    }
+                    for (int e = 0; e < 2; ++e) top = fmaxf(top, z[x][e]);
                 }
-                top = warp_max(top);
-                if (FP8) topv = warp_max(topv);
-                const float mn = fmaxf(m[c], top), mvn = FP8 ? fmaxf(mv[c], topv) : mn;
+                const float mn = fmaxf(m[c], warp_max(top));
                 // (an infinite maximum only where nothing, an infinity or nothing but NaN was seen: the maxima pass
                 // over NaN, which the sum and the weights take up)
-                const float base = mn == -INFINITY ? 0.0f : mn, basev = mvn == -INFINITY ? 0.0f : mvn;
+                const float base = mn == -INFINITY ? 0.0f : mn;
                 l[c] *= ex2(m[c] - base);
-                float f = FP8 ? ex2(mv[c] - basev) : ex2(m[c] - base);
-                if (m[c] == -INFINITY && (!FP8 || mv[c] == -INFINITY)) f = 1.0f;   // (nothing to scale yet)
-                if (lane == 0) corr[r] = f;
+                float f, based = 0.0f;
+                if (FP8) {
+                    // the same of score + exponent, which start from the scores less their maximum: on a score of
+                    // 2^24 and more the exponent would be rounded away
+                    float topd = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < KT / 64; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            z[x][e] -= base;
+                            ve[x][e] += z[x][e];
+                            topd = fmaxf(topd, ve[x][e]);
+                        }
+                    const float d = dv[c] + (m[c] - base), dn = fmaxf(d, warp_max(topd));
+                    based = dn == -INFINITY ? 0.0f : dn;
+                    f = ex2(d - based);
+                    dv[c] = dn;
+                } else {
+                    f = ex2(m[c] - base);
+                }
+                if (lane == 0) corr[r] = f;   // (0 where nothing was seen yet: the sums are 0)
                 m[c] = mn;
-                mv[c] = mvn;
                 float sum = 0.0f;   // of the tile: added to the running sum at once, or small weights drift beside a large one
 #pragma unroll
                 for (int x = 0; x < KT / 64; ++x) {
                     float w[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        w[e] = ex2(z[x][e] - base);
+                        w[e] = ex2(FP8 ? z[x][e] : z[x][e] - base);
                         sum += w[e];
-                        if (FP8) w[e] = ex2(z[x][e] + ve[x][e] - basev + kWeightBits);
+                        if (FP8) w[e] = ex2(ve[x][e] - based + kWeightBits);
                     }
                     *reinterpret_cast<uint32_t *>(sP + r * G::PSTR + x * 64 + 2 * lane) = pack16<FP8>(w[0], w[1]);
                 }
@@ -975,7 +987,7 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
         const bool whole = seg.whole();
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
         {
-            float top = -INFINITY, sum = 0.0f, topv = 0.0f;
+            float top = -INFINITY, sum = 0.0f, topd = 0.0f;
             bool none = true;
             seen = __reduce_or_sync(0xffffffffu, seen);
 #pragma unroll
@@ -985,16 +997,16 @@ __global__ void __launch_bounds__((G::W + G::PRODUCERS) * 32, G::CTAS)
                 for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
                 if (lane == c) {
                     top = m[c];
-                    topv = mv[c];
+                    topd = dv[c];
                     sum = x;
                     none = lim[c] == 0 || (seen >> c & 1) == 0;   // (also a token that is not there)
                 }
             }
             const int r = lane * W + warp;
             if (lane < RPW && r < nrows) {
-                // (mv - m: the weighted sum in units of 2^m; without a maximum it is 0 or NaN in any units.  The second
+                // (2^dv: the weighted sum in units of 2^m; without a maximum it is 0 or NaN in any units.  The second
                 // factor comes first: it takes the sum to the values' codes, the other one these to the values)
-                fin[r] = make_float2(none ? -1.0f : FP8 && top != -INFINITY ? ex2(topv - top) : 1.0f,
+                fin[r] = make_float2(none ? -1.0f : FP8 && top != -INFINITY ? ex2(topd) : 1.0f,
                                      (whole ? rcp_fast(sum) : 1.0f) * (FP8 ? kWeightUnit : 1.0f));
                 if (none) {
                     top = -INFINITY;
