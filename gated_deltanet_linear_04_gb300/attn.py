@@ -87,13 +87,13 @@ def rope_freqs(inv_freq: torch.Tensor, device=None) -> torch.Tensor:
 
 
 class _CacheRecord(ctypes.Structure):
-    _fields_ = [("c", GdnKvCache), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
+    _fields_ = [("c", GdnKvCache), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("device", ctypes.c_int32)]
 
 
 class KVCache:
     """A paged cache: k, v [n_pages, Hkv, page_size, D] bf16, or float8_e4m3fn
-    with k_scale, v_scale [n_pages, Hkv, page_size] float8_e8m0fnu.  Checked
-    once here; the tensors must not be resized afterwards."""
+    with k_scale, v_scale [n_pages, Hkv, page_size] float8_e8m0fnu, all on one
+    device.  Checked once here; the tensors must not be resized afterwards."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
                  v_scale: Optional[torch.Tensor] = None):
@@ -112,9 +112,12 @@ class KVCache:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and t.shape != k.shape[:3]:
                 raise ValueError("KVCache: %s must have shape %s, got %s" % (name, tuple(k.shape[:3]), tuple(t.shape)))
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and t.device != k.device:
+                raise ValueError("KVCache: %s is on %s, k on %s" % (name, t.device, k.device))
         self._c = _CacheRecord(GdnKvCache(_ptr(k, k.dtype, "k"), _ptr(v, v.dtype, "v"), _ptr(k_scale, E8M0, "k_scale"),
                                           _ptr(v_scale, E8M0, "v_scale"), self.n_pages, self.page_size, int(fp8)),
-                               self.Hkv, self.D)
+                               self.Hkv, self.D, k.device.index if k.is_cuda and k.numel() else -1)
 
     @classmethod
     def empty(cls, dims, n_pages: int, page_size: int, dtype=BF16, device="cuda") -> "KVCache":

@@ -26,10 +26,11 @@ namespace {
 
 PyObject *g_error = nullptr;   // gdn.GdnError
 
-// attn.KVCache's record: the ABI's struct, and the heads and channels its pages were made for.
+// attn.KVCache's record: the ABI's struct, the heads and channels its pages were made for, and the device that they
+// are on (-1: no pages).
 struct Cache {
     gdn_kv_cache c;
-    int32_t Hkv, D;
+    int32_t Hkv, D, device;
 };
 
 // A Python exception is set.
@@ -83,7 +84,10 @@ struct Call {
 
     void placed(const at::Tensor &t, const char *name) {
         if (!t.is_cuda()) raise(PyExc_ValueError, std::string(name) + " must be a CUDA tensor");
-        const int d = t.device().index();
+        placed(t.device().index(), name);
+    }
+
+    void placed(int d, const char *name) {
         if (device < 0) device = d;
         if (d != device) raise(PyExc_ValueError, std::string(name) + " is on another device than the tensors before it");
     }
@@ -255,6 +259,7 @@ Pages page_args(Call &c, const gdn_attn_dims &d, PyObject *cache, PyObject *tabl
         raise(PyExc_ValueError, std::string(c.where) + ": the cache holds " + std::to_string(k->Hkv) + " heads of " +
                                     std::to_string(k->D) + " channels, the dims say " + std::to_string(d.Hkv) + " of " +
                                     std::to_string(d.D));
+    if (k->device >= 0) c.placed(k->device, "the cache");
     const at::Tensor &t = c.tensor(table, at::kInt, "page_table");
     if (t.dim() != 2 || t.size(0) != d.B || t.size(1) > 0x7fffffff)
         raise(PyExc_ValueError, std::string(c.where) + ": page_table must have shape (" + std::to_string(d.B) +
