@@ -408,19 +408,38 @@ def gdn_abi_version() -> int:
 # ---------------------------------------------------------------------------
 # allocating conveniences
 # ---------------------------------------------------------------------------
+
+def _empty(shape, dtype, device, stream, scratch=False):
+    """An output or scratch of a call on `stream`.  For a given stream it comes
+    from that stream's own pool (a block of the current stream's may still be
+    in use by work queued there, which the call does not wait for), and the
+    current stream, on which the caller will use an output, is recorded."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    handle = _stream(stream) or 0
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.numel() and not scratch:
+        t.record_stream(current)
+    return t
+
+
 def conv_update(dims, qkv, conv_w, conv_state=None, mask=None, stream=None):
     """Returns (q, k, v); conv_state (if given) is updated in place."""
     dev = qkv.device
-    q = torch.empty((dims.B, dims.T, dims.Hk, dims.Dk), dtype=BF16, device=dev)
-    k = torch.empty_like(q)
-    v = torch.empty((dims.B, dims.T, dims.Hv, dims.Dv), dtype=BF16, device=dev)
+    q = _empty((dims.B, dims.T, dims.Hk, dims.Dk), BF16, dev, stream)
+    k = _empty(q.shape, BF16, dev, stream)
+    v = _empty((dims.B, dims.T, dims.Hv, dims.Dv), BF16, dev, stream)
     gdn_conv_update(dims, qkv, conv_w, conv_state, mask, q, k, v, stream)
     return q, k, v
 
 
 def gating(dims, a, b, A_log, dt_bias, stream=None):
-    g = torch.empty((dims.B, dims.T, dims.Hv), dtype=F32, device=a.device)
-    beta = torch.empty_like(g)
+    g = _empty((dims.B, dims.T, dims.Hv), F32, a.device, stream)
+    beta = _empty(g.shape, F32, a.device, stream)
     gdn_gating(dims, a, b, A_log, dt_bias, g, beta, stream)
     return g, beta
 
@@ -441,7 +460,7 @@ def shard_rows(B: int, world: int, rank: int):
 
 def recurrent_decode(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, row_mask=None, stream=None):
     """One token; conv_state and state are updated in place.  Returns y [B, Hv, Dv]."""
-    y = torch.empty((dims.B, dims.Hv, dims.Dv), dtype=BF16, device=qkv.device)
+    y = _empty((dims.B, dims.Hv, dims.Dv), BF16, qkv.device, stream)
     gdn_recurrent_decode(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, row_mask, y, stream)
     return y
 
@@ -455,7 +474,7 @@ def recurrent_decode_host_steps(dims, qkv_h, a_h, b_h, conv_w, conv_state, A_log
     if y_h is None:
         y_h = torch.empty((n, dims.B, dims.Hv, dims.Dv), dtype=BF16).pin_memory()
     if staging is None:
-        staging = torch.empty(gdn_decode_host_staging_size(dims), dtype=torch.uint8, device=conv_state.device)
+        staging = _empty(gdn_decode_host_staging_size(dims), torch.uint8, conv_state.device, stream, scratch=True)
     gdn_recurrent_decode_host_steps(dims, n, qkv_h, a_h, b_h, y_h, conv_w, conv_state, A_log, dt_bias, state,
                                     row_mask, staging, stream)
     return y_h
@@ -464,7 +483,7 @@ def recurrent_decode_host_steps(dims, qkv_h, a_h, b_h, conv_w, conv_state, A_log
 def decode_window(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, keep=None, stream=None):
     """dims.T tokens per row; conv_state and state advance by keep[b] (default
     all) tokens in place.  Returns y [B, T, Hv, Dv]."""
-    y = torch.empty((dims.B, dims.T, dims.Hv, dims.Dv), dtype=BF16, device=qkv.device)
+    y = _empty((dims.B, dims.T, dims.Hv, dims.Dv), BF16, qkv.device, stream)
     gdn_decode_window(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, keep, y, stream)
     return y
 
@@ -475,13 +494,13 @@ def prefill(dims, q, k, v, g, beta, state_in=None, mask=None, chunk=0, state_out
     for is passed (row order for masked batches; the two-pass chunked form
     for few heads); the results are the same either way."""
     dev = q.device
-    y = torch.empty((dims.B, dims.T, dims.Hv, dims.Dv), dtype=BF16, device=dev)
+    y = _empty((dims.B, dims.T, dims.Hv, dims.Dv), BF16, dev, stream)
     if state_out is None:
-        state_out = torch.empty((dims.B, dims.Hv, dims.Dv, dims.Dk), dtype=F32, device=dev)
+        state_out = _empty((dims.B, dims.Hv, dims.Dv, dims.Dk), F32, dev, stream)
     ws = None
     if use_workspace:
         nws = gdn_prefill_workspace_size(dims, chunk)
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws > 0 else None
+        ws = _empty(nws, torch.uint8, dev, stream, scratch=True) if nws > 0 else None
     gdn_prefill(dims, q, k, v, g, beta, state_in, state_out, mask, y, chunk, ws, stream)
     return y, state_out
 
@@ -489,7 +508,7 @@ def prefill(dims, q, k, v, g, beta, state_in=None, mask=None, chunk=0, state_out
 def recurrent_decode_gated(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, z, norm_w, norm_eps=1e-6,
                            row_mask=None, stream=None):
     """One token with the gated norm fused; returns out [B, Hv, Dv]."""
-    out = torch.empty((dims.B, dims.Hv, dims.Dv), dtype=BF16, device=qkv.device)
+    out = _empty((dims.B, dims.Hv, dims.Dv), BF16, qkv.device, stream)
     gdn_recurrent_decode_gated(dims, qkv, conv_w, conv_state, a, b, A_log, dt_bias, state, row_mask, z, norm_w,
                                norm_eps, out, stream)
     return out
@@ -499,11 +518,11 @@ def prefill_gated(dims, q, k, v, g, beta, z, norm_w, norm_eps=1e-6, state_in=Non
                   state_out=None, stream=None):
     """Returns (out, state_out), out the gated norm of y."""
     dev = q.device
-    out = torch.empty((dims.B, dims.T, dims.Hv, dims.Dv), dtype=BF16, device=dev)
+    out = _empty((dims.B, dims.T, dims.Hv, dims.Dv), BF16, dev, stream)
     if state_out is None:
-        state_out = torch.empty((dims.B, dims.Hv, dims.Dv, dims.Dk), dtype=F32, device=dev)
+        state_out = _empty((dims.B, dims.Hv, dims.Dv, dims.Dk), F32, dev, stream)
     nws = gdn_prefill_workspace_size(dims, chunk)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws > 0 else None
+    ws = _empty(nws, torch.uint8, dev, stream, scratch=True) if nws > 0 else None
     gdn_prefill_gated(dims, q, k, v, g, beta, state_in, state_out, mask, z, norm_w, norm_eps, out, chunk, ws, stream)
     return out, state_out
 
@@ -516,16 +535,16 @@ def prefill_backward(dims, q, k, v, g, beta, dy, state_in=None, mask=None, dstat
         raise ValueError("prefill_backward: chunk must be 0 or 64")
     dev = q.device
     B, T = dims.B, dims.T
-    out = {"dq": torch.empty((B, T, dims.Hk, dims.Dk), dtype=F32, device=dev),
-           "dk": torch.empty((B, T, dims.Hk, dims.Dk), dtype=F32, device=dev),
-           "dv": torch.empty((B, T, dims.Hv, dims.Dv), dtype=F32, device=dev),
-           "dg": torch.empty((B, T, dims.Hv), dtype=F32, device=dev),
-           "dbeta": torch.empty((B, T, dims.Hv), dtype=F32, device=dev),
-           "dstate_in": torch.empty((B, dims.Hv, dims.Dv, dims.Dk), dtype=F32, device=dev)}
+    out = {"dq": _empty((B, T, dims.Hk, dims.Dk), F32, dev, stream),
+           "dk": _empty((B, T, dims.Hk, dims.Dk), F32, dev, stream),
+           "dv": _empty((B, T, dims.Hv, dims.Dv), F32, dev, stream),
+           "dg": _empty((B, T, dims.Hv), F32, dev, stream),
+           "dbeta": _empty((B, T, dims.Hv), F32, dev, stream),
+           "dstate_in": _empty((B, dims.Hv, dims.Dv, dims.Dk), F32, dev, stream)}
     size_fn, call = ((gdn_prefill_backward_chunked_workspace_size, gdn_prefill_backward_chunked) if chunk
                      else (gdn_prefill_backward_workspace_size, gdn_prefill_backward))
     nws = size_fn(dims)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws > 0 else None
+    ws = _empty(nws, torch.uint8, dev, stream, scratch=True) if nws > 0 else None
     call(dims, q, k, v, g, beta, state_in, mask, dy, dstate_out, out["dq"], out["dk"], out["dv"], out["dg"],
          out["dbeta"], out["dstate_in"], ws, stream)
     return out
@@ -533,15 +552,15 @@ def prefill_backward(dims, q, k, v, g, beta, dy, state_in=None, mask=None, dstat
 
 def rmsnorm_gated(dims, y, z, norm_w, norm_eps=1e-6, stream=None):
     """Returns out = bf16(silu(z) * w * rms_normalize(y)) shaped like y."""
-    out = torch.empty_like(y)
+    out = _empty(y.shape, y.dtype, y.device, stream)
     gdn_rmsnorm_gated(dims, y, z, norm_w, norm_eps, out, stream)
     return out
 
 
 def prefill_vec(dims, q, k, v, g_vec, beta, state_in=None, mask=None, stream=None):
     """Vectorized gating (g_vec [B, T, Hv, Dk]); returns (y, state_out)."""
-    y = torch.empty((dims.B, dims.T, dims.Hv, dims.Dv), dtype=BF16, device=q.device)
-    state_out = torch.empty((dims.B, dims.Hv, dims.Dv, dims.Dk), dtype=F32, device=q.device)
+    y = _empty((dims.B, dims.T, dims.Hv, dims.Dv), BF16, q.device, stream)
+    state_out = _empty((dims.B, dims.Hv, dims.Dv, dims.Dk), F32, q.device, stream)
     gdn_prefill_vec(dims, q, k, v, g_vec, beta, state_in, state_out, mask, y, stream)
     return y, state_out
 
