@@ -26,20 +26,31 @@
 // their way.  (Warps that take whole tiles on their own, with all channels and
 // a join at the end of each unit, held each tile three times as long and lost
 // 5 us at each unit's end: 69 against 61 us for B = 128, e4m3, 2048 keys.)
-// What it came to (16 query and 2 key heads of 256 channels): one row of 262144
-// keys in bf16 86 us, 6.3 TB/s of keys and values; B = 128, up to 4096 keys in
-// e4m3 49.2 us, 5.5 TB/s; B = 32, windows of 4 tokens, 32 and 8 heads of 128
-// channels, bf16 54.9 us, 5.5 TB/s.  (With every key in the L2 cache 41 and 47 us.)  In between, a tile takes the consumers about
-// 3100 clocks (with e4m3 its conversions alone take 770 of them), the memory 2990;
-// the first data come after 5 us, and a unit's end and the next one's start cost
-// 4000 clocks more than a tile.
+// What it came to (16 query and 2 key heads of 256 channels; calls in a host loop
+// over fresh inputs): one row of 262144 keys in bf16 86.5 us, 6.2 TB/s of keys and
+// values; B = 128, up to 4096 keys in e4m3 51.0 us, 5.3 TB/s; B = 32, windows of 4
+// tokens, 32 and 8 heads of 128 channels, bf16 56.7 us, 5.3 TB/s.  (With every key in
+// the L2 cache the last two take 41 and 47 us.)  In between, a tile takes the consumers
+// about 3100 clocks (with e4m3 its conversions alone take 770 of them), the memory 2990;
+// the first data come after 5 us, and a unit's end and the next one's start cost 4000
+// clocks more than a tile.
 //
-// Products.  mma.sync m16n8k16 with keys (then channels) as the 16 and query
-// rows as the 8: eight heads per key head fill n = 8 exactly, where a 128-row
-// tcgen05 tile would hold 8 rows of use, and the tensor work is far from the
-// bound.  e4m3 codes are turned into f16 pairs on the way from shared memory to
-// the operand (exactly); their scales go to the scores (keys) and into the
-// exponent of the weights (values).
+// Products.  mma.sync m16n8k16 with keys (then channels) as the 16 and query rows
+// as the 8, which eight heads per key head fill exactly.  With up to 8 rows the
+// products are far from the bound, and tcgen05 (128 keys by the rows, as full as
+// these) would only add the way through tensor memory in front of the softmax.  With
+// 32 and more rows they are the bound (B = 32, up to 4095 keys, 16 and 2 heads of 256,
+// bf16: 8, 32 and 64 rows 31, 50 and 79 us): there these products are what holds the
+// kernel back.  e4m3 codes are turned into f16 pairs on the way from shared memory to
+// the operand (exactly); their scales go to the scores (keys) and into the exponent of
+// the weights (values).
+//
+// Weights are rounded to the 16 bits of the operand beside them: f16 with e4m3 values,
+// bf16 with bf16 values.  bf16 weights leave the output 0.0020 from the 64-bit result
+// (2-norm) where its own rounding alone is 0.0017.  A high and a low bf16 part of each
+// gives 0.0017 for twice the products: one row of 262144 keys 86.5 -> 86.7 us, windows
+// of 16 rows 56.7 -> 58.7, 32 rows 49.7 -> 53.1, 64 rows of 128 channels 76 -> 87; one
+// part was kept.
 #include "attn.cuh"
 
 namespace gdn {
@@ -179,7 +190,7 @@ __device__ __forceinline__ float2 e8m0_pair(uint32_t bytes) {
 
 // L2 policy of keys and values, which a call reads once (rows that share pages, at
 // about the same time): they go before what else the cache holds.  In calls one after
-// the other the ragged batch takes 50.2 instead of 53.0 us, windows 56.0 instead of
+// the other the ragged batch took 50.2 instead of 53.0 us, windows 56.0 instead of
 // 58.7; after a flush of the cache there is no difference, nor with shared pages.
 __device__ __forceinline__ uint64_t read_once() {
     uint64_t policy;

@@ -3,7 +3,7 @@
 // the row's power of two): HBM-bound.  A warp takes one token: its page is
 // looked up once, then up to ROWS * RPW key rows and the value rows beside
 // them are asked for before the first is written (eight channels a lane).
-// B = 8, up to 4093 positions of 2 heads of 256 channels from e4m3 (92 MB): 13.5 us.
+// B = 8, up to 4093 positions of 2 heads of 256 channels from e4m3 (92 MB): 16.5 us.
 #include <type_traits>
 
 #include "attn.cuh"

@@ -22,8 +22,8 @@
 //     each head row is y = rstd (x A + x' B), x' the partners.
 //   - four rows' sums go over the lanes together; arithmetic goes two channels
 //     at a time (f32x2 instructions).
-// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): 27.4 us forward (a plain
-// copy of as much takes 23.5), 42.9 backward (227 MB).  Steps on the way: a warp per
+// At B = 1, T = 8192, 16 + 2 heads of 256 channels (151 MB): 27.9 us forward (a plain
+// copy of as much takes 23.5), 43.6 backward (227 MB).  Steps on the way: a warp per
 // head row 89 us; four rows a warp, into registers, partners by shuffle, sincospi
 // 31.4 (164 instructions a row, most of them a token's angles and addresses).
 #include "attn.cuh"
@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
     }
 }
 
-// dw = the CTAs' shares, every eighth one by one thread, then those sums in
-// order.  Blocks: (q or k, 32 channels).
+// dw = the CTAs' shares: 32 threads per channel, each sums every 32nd of them, then
+// their sums are added in order.  Blocks: (q or k, 32 channels).
 __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *partial, int nq, int n, int D, float *dwq,
                                                           float *dwk) {
     __shared__ float sum[32][33];

@@ -536,8 +536,8 @@ GDN_API gdn_status gdn_kv_read(const gdn_attn_dims *dims, const gdn_kv_cache *ca
  *          length is split over several CTAs.  They are joined in a fixed
  *          order: equal calls give equal bits.
  * Scores and sums are f32.  Softmax weights are rounded to 16 bits for the
- * product with V: bf16, or with an e4m3 cache f16 (weights below 2^-39 of the
- * largest are 0).  Values and keys at positions that a token does not see do
+ * product with V: bf16, or with an e4m3 cache f16 (those that, times their
+ * value's scale, are below 2^-39 of the largest such product are 0).  Values and keys at positions that a token does not see do
  * not enter its results, whatever they hold; a NaN among the scores that it
  * does see makes its output and lse NaN, and scores that are all -inf make its
  * output NaN (0 / 0) and lse -inf. */
