@@ -184,6 +184,16 @@ def gdn_attn_decode(dims, q, cache, page_table, pos, n_new, gate, scale, out, ls
                         _handle(stream))
 
 
+def gdn_attn_prefill_workspace_size(dims, q_rows, k_rows) -> int:
+    return int(lib().gdn_attn_prefill_workspace_size(ctypes.byref(_dims(dims)), int(q_rows), int(k_rows)))
+
+
+def gdn_attn_prefill(dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, workspace, stream=None):
+    _given("gdn_attn_prefill", out=out, workspace=workspace)
+    c = _dims(dims)
+    _bind().attn_prefill(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, False, workspace, _handle(stream))
+
+
 # ---------------------------------------------------------------------------
 # allocating conveniences
 # ---------------------------------------------------------------------------
@@ -224,3 +234,15 @@ def attn_decode(dims, q, cache, page_table, pos, n_new=None, gate=None, scale=No
     return _bind().attn_decode(_at(c), q, _at(cache._c), page_table, pos, n_new, gate,
                                dims.D ** -0.5 if scale is None else scale, None, None, bool(return_lse), workspace,
                                _handle(stream))
+
+
+def attn_prefill(dims, q, k, v, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=None, scale=None, return_lse=False,
+                 workspace=None, stream=None):
+    """Causal attention of dims.B whole prompts, or of new tokens after a kept
+    prefix; the last query of a sequence sees its last key.  q [B, T, Hq, D] and
+    k, v [B, Tk, Hkv, D] with lengths n_q, n_k (None: all), or packed: q [N, Hq,
+    D] with offsets cu_q [B + 1], k, v [M, Hkv, D] with cu_k (None: cu_q).  Returns
+    out shaped as q, or (out, lse)."""
+    c = _dims(dims)
+    return _bind().attn_prefill(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, dims.D ** -0.5 if scale is None else scale,
+                                None, None, bool(return_lse), workspace, _handle(stream))

@@ -239,6 +239,7 @@ const char *gdn_status_string(gdn_status status) {
         case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: size outside the supported set";
         case GDN_ERR_CUDA: return "GDN_ERR_CUDA: a CUDA call failed";
         case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT: a bounded device wait gave up";
+        case GDN_ERR_BAD_OFFSETS: return "GDN_ERR_BAD_OFFSETS: offsets of packed sequences decrease or leave their buffer";
         case GDN_ERR_BAD_PAGE: return "GDN_ERR_BAD_PAGE: a cache position had no valid page";
         default: return "GDN_ERR_UNKNOWN";
     }
@@ -627,7 +628,8 @@ gdn_status gdn_device_status(gdn_stream stream) {
     if (host != 0) {
         const unsigned zero = 0;
         if (cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return GDN_ERR_CUDA;
-        return (host & ~(unsigned)gdn::kErrBadPage) == 0 ? GDN_ERR_BAD_PAGE : GDN_ERR_TIMEOUT;
+        if ((host & ~(unsigned)(gdn::kErrBadPage | gdn::kErrBadOffsets)) != 0) return GDN_ERR_TIMEOUT;
+        return (host & gdn::kErrBadOffsets) != 0 ? GDN_ERR_BAD_OFFSETS : GDN_ERR_BAD_PAGE;
     }
     return GDN_OK;
 }

@@ -53,6 +53,29 @@ bool ok_norm(const AttnSizes &s, const float *wq, const float *wk, const uint64_
     return ok(freqs, (size_t)s.Drot);
 }
 
+// [rows, H, D] views of a prompt: tensor maps take no stride of 0.
+gdn_status check_rows(const HeadsIn &h, long long rows, int H) {
+    if (!ok_heads(h, (size_t)rows)) return GDN_ERR_INVALID_ARG;
+    const long long most = 1LL << 39;   // (elements: a tensor map's strides are below 2^40 bytes)
+    if ((rows > 1 && (h.ts == 0 || h.ts >= most)) || (H > 1 && (h.hs == 0 || h.hs >= most))) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+gdn_status check_prompt(const gdn_attn_dims *d, int64_t q_rows, int64_t k_rows, PromptSizes *out) {
+    AttnSizes s;
+    const gdn_status st = check(d, &s);
+    if (st != GDN_OK) return st;
+    if (q_rows < 0 || k_rows < 0) return GDN_ERR_INVALID_ARG;
+    if (q_rows > 0x7fff0000LL || k_rows > 0x7fff0000LL) return GDN_ERR_UNSUPPORTED;
+    *out = PromptSizes{s.B, s.Hq, s.Hkv, s.D, q_rows, k_rows};
+    return GDN_OK;
+}
+
+bool ok_sequences(const PromptSizes &s, const PromptSeqs &q) {
+    if (!ok(q.cu_q, 0, 4) || !ok(q.cu_k, 0, 4) || !ok(q.n_q, 0, 4) || !ok(q.n_k, 0, 4)) return false;
+    return s.B == 0 || ((q.cu_q != nullptr || s.Nq % s.B == 0) && (q.cu_k != nullptr || s.Nk % s.B == 0));
+}
+
 gdn_status from(cudaError_t e) {
     if (e == cudaSuccess) return GDN_OK;
     return e == cudaErrorNotSupported ? GDN_ERR_UNSUPPORTED : GDN_ERR_CUDA;
@@ -189,6 +212,39 @@ gdn_status gdn_attn_decode(const gdn_attn_dims *dims, const uint16_t *q, const g
     if (err == nullptr) return GDN_ERR_CUDA;
     return gdn::from(gdn::launch_attn_decode(s, q, c, pos, n_new, hg, scale, out, lse, workspace, err,
                                              (cudaStream_t)stream));
+}
+
+size_t gdn_attn_prefill_workspace_size(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows) {
+    gdn::PromptSizes s;
+    if (gdn::check_prompt(dims, q_rows, k_rows, &s) != GDN_OK) return 0;
+    return gdn::attn_prefill_workspace(s);
+}
+
+gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows, const uint16_t *q,
+                            int64_t q_token_stride, int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                            int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride, int64_t v_head_stride,
+                            const int32_t *cu_q, const int32_t *cu_k, const int32_t *n_q, const int32_t *n_k,
+                            const uint16_t *gate, int64_t gate_token_stride, int64_t gate_head_stride, float scale,
+                            uint16_t *out, float *lse, void *workspace, size_t ws_bytes, gdn_stream stream) {
+    gdn::PromptSizes s;
+    gdn_status st = gdn::check_prompt(dims, q_rows, k_rows, &s);
+    if (st != GDN_OK) return st;
+    const HeadsIn hq{q, q_token_stride, q_head_stride}, hk{k, k_token_stride, k_head_stride},
+        hv{v, v_token_stride, v_head_stride}, hg{gate, gate_token_stride, gate_head_stride};
+    const gdn::PromptSeqs seqs{cu_q, cu_k, n_q, n_k};
+    st = gdn::check_rows(hq, s.Nq, s.Hq);
+    if (st == GDN_OK) st = gdn::check_rows(hk, s.Nk, s.Hkv);
+    if (st == GDN_OK) st = gdn::check_rows(hv, s.Nk, s.Hkv);
+    if (st == GDN_OK && gate != nullptr) st = gdn::check_rows(hg, s.Nq, s.Hq);
+    if (st != GDN_OK) return st;
+    if (!gdn::ok_sequences(s, seqs) || !gdn::ok(out, (size_t)s.Nq) || !gdn::ok(lse, 0, 4) || !isfinite(scale))
+        return GDN_ERR_INVALID_ARG;
+    if (s.Nq == 0 || s.B == 0) return GDN_OK;
+    if (!gdn::ok(workspace, 1) || ws_bytes < gdn::attn_prefill_workspace(s)) return GDN_ERR_INVALID_ARG;
+    unsigned *err = gdn::device_error_word();
+    if (err == nullptr) return GDN_ERR_CUDA;
+    return gdn::from(gdn::launch_attn_prefill(s, hq, hk, hv, seqs, hg, scale, out, lse, workspace, err,
+                                              (cudaStream_t)stream));
 }
 
 }  // extern "C"

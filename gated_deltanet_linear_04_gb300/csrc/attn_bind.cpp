@@ -131,6 +131,32 @@ struct Call {
         return {static_cast<const uint16_t *>(t.data_ptr()), ts, hs};
     }
 
+    // the rows of a prompt: [B, T, H, D] as above, or packed [N, H, D]
+    struct Rows {
+        Heads h;
+        int64_t n, t;      // rows; tokens of a slot, or -1 if packed
+    };
+    Rows rows(PyObject *o, const gdn_attn_dims &d, int64_t H, const char *name) {
+        const at::Tensor &t = tensor(o, at::kBFloat16, name);
+        if (t.dim() == 4) {
+            gdn_attn_dims e = d;
+            e.T = (int32_t)t.size(1);
+            if (t.size(1) > 0x7fffffff) raise(PyExc_ValueError, std::string(name) + ": too many tokens");
+            return {heads(o, e, H, name), (int64_t)d.B * t.size(1), t.size(1)};
+        }
+        if (t.dim() != 3)
+            raise(PyExc_ValueError, std::string(name) + " must have shape (B, T, heads, D), or (N, heads, D) with offsets, got " +
+                                        show(t.sizes()));
+        shaped(t, {t.size(0), H, d.D}, name);
+        if (t.numel() == 0) return {{nullptr, 0, 0}, t.size(0), -1};
+        const int64_t ts = t.size(0) > 1 ? t.stride(0) : 0, hs = H > 1 ? t.stride(1) : 0;
+        if (t.stride(2) != 1 || ts % 8 != 0 || hs % 8 != 0)
+            raise(PyExc_ValueError, std::string(name) + " must have dense channels and token and head strides that are "
+                                                        "multiples of 8, got strides " + show(t.strides()));
+        placed(t, name);
+        return {{static_cast<const uint16_t *>(t.data_ptr()), ts, hs}, t.size(0), -1};
+    }
+
     // the stream of the call: the given handle, else torch's current one
     cudaStream_t stream() {
         if (device < 0) device = c10::cuda::current_device();
@@ -376,6 +402,75 @@ PyObject *attn_decode(PyObject *const *a) {
     return lse.defined() && a[10] == Py_True ? pair(out, lse) : THPVariable_Wrap(out);
 }
 
+// A prompt's queries, keys and values with their sequences.
+struct Prompt {
+    Call::Rows q, k, v;
+    const int32_t *cu_q, *cu_k, *n_q, *n_k;
+
+    Prompt(Call &c, const gdn_attn_dims &d, PyObject *qo, PyObject *ko, PyObject *vo, PyObject *cuq, PyObject *cuk,
+           PyObject *nq, PyObject *nk) {
+        q = c.rows(qo, d, d.Hq, "q");
+        k = c.rows(ko, d, d.Hkv, "k");
+        v = c.rows(vo, d, d.Hkv, "v");
+        if (q.t >= 0 && q.t != d.T)
+            raise(PyExc_ValueError, "q must have shape (B, T, heads, D) of the dims, got " + std::to_string(q.t) + " tokens");
+        if (v.n != k.n || v.t != k.t) raise(PyExc_ValueError, "k and v must have the same shape");
+        if ((q.t < 0) != (cuq != Py_None))
+            raise(PyExc_ValueError, q.t < 0 ? "packed q needs cu_q" : "cu_q goes with packed q (N, heads, D)");
+        if (k.t < 0 && cuk == Py_None) {
+            if (cuq == Py_None) raise(PyExc_ValueError, "packed k needs cu_k");
+            cuk = cuq;
+        } else if (k.t >= 0 && cuk != Py_None) {
+            raise(PyExc_ValueError, "cu_k goes with packed k (N, heads, D)");
+        }
+        cu_q = index_arg(c, cuq, (int64_t)d.B + 1, "cu_q", true);
+        cu_k = index_arg(c, cuk, (int64_t)d.B + 1, "cu_k", true);
+        n_q = index_arg(c, nq, d.B, "n_q", true);
+        n_k = index_arg(c, nk, d.B, "n_k", true);
+    }
+    // a tensor of q's rows
+    at::Tensor like_q(Call &c, PyObject *o, const gdn_attn_dims &d, const char *name) const {
+        return q.t >= 0 ? c.output(o, at::kBFloat16, {d.B, d.T, d.Hq, d.D}, name)
+                        : c.output(o, at::kBFloat16, {q.n, d.Hq, d.D}, name);
+    }
+};
+
+double number(PyObject *o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Raised();
+    return x;
+}
+
+Call::Heads gate_arg(Call &c, const gdn_attn_dims &d, const Prompt &p, PyObject *o) {
+    if (o == Py_None) return {nullptr, 0, 0};
+    const Call::Rows g = c.rows(o, d, d.Hq, "gate");
+    if (g.n != p.q.n || g.t != p.q.t) raise(PyExc_ValueError, "gate must have q's shape");
+    return g.h;
+}
+
+// (dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, want_lse, workspace, stream) -> out or (out, lse)
+PyObject *attn_prefill(PyObject *const *a) {
+    const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
+    Call c("gdn_attn_prefill", a[14]);
+    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+    const Call::Heads gate = gate_arg(c, d, p, a[8]);
+    const double scale = number(a[9]);
+    const at::Tensor out = p.like_q(c, a[10], d, "out");
+    at::Tensor lse;
+    Scratch ws;
+    if (a[12] == Py_True || a[11] != Py_None)
+        lse = p.q.t >= 0 ? c.output(a[11], at::kFloat, {d.B, d.T, d.Hq}, "lse")
+                         : c.output(a[11], at::kFloat, {p.q.n, d.Hq}, "lse");
+    if (a[13] != Py_None)
+        ws.given(c, a[13]);
+    else if (p.q.n > 0 && d.B > 0)
+        ws.make(c, gdn_attn_prefill_workspace_size(&d, p.q.n, p.k.n));
+    c.done(gdn_attn_prefill(&d, p.q.n, p.k.n, p.q.h.p, p.q.h.ts, p.q.h.hs, p.k.h.p, p.k.h.ts, p.k.h.hs, p.v.h.p, p.v.h.ts,
+                            p.v.h.hs, p.cu_q, p.cu_k, p.n_q, p.n_k, gate.p, gate.ts, gate.hs, (float)scale, bf16(out),
+                            lse.defined() ? f32(lse) : nullptr, ws.p, ws.bytes, (gdn_stream)c.stream()));
+    return lse.defined() && a[12] == Py_True ? pair(out, lse) : THPVariable_Wrap(out);
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -399,7 +494,7 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(qk_norm_rope, 11), ENTRY(qk_norm_rope_backward, 16), ENTRY(kv_append, 13),
-                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13),
+                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13), ENTRY(attn_prefill, 15),
                          {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_attn_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

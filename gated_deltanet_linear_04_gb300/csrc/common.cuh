@@ -8,12 +8,13 @@
 
 namespace gdn {
 
-// Error word bits: kernels whose bounded waits give up, and cache positions
-// without a valid page.
+// Error word bits: kernels whose bounded waits give up, cache positions
+// without a valid page, and offsets of packed sequences that are not in order.
 enum : unsigned {
     kErrMbarTimeout = 1u,
     kErrMmaTimeout = 2u,
     kErrBadPage = 4u,
+    kErrBadOffsets = 8u,
 };
 
 // Spin limit of every bounded wait: try_wait suspends for a hardware-chosen

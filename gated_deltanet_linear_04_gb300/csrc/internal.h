@@ -215,4 +215,38 @@ cudaError_t launch_attn_decode(const AttnSizes &s, const uint16_t *q, const Page
                                const int32_t *n_new, const HeadsIn &gate, float scale, uint16_t *out, float *lse,
                                void *ws, unsigned *err, cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// Whole prompts (prompt_*.cu; attn_api.cu validates)
+// ---------------------------------------------------------------------------
+namespace prompt {
+struct List;
+}
+
+struct PromptSizes {
+    int B, Hq, Hkv, D;
+    long long Nq, Nk;   // rows of the buffers of queries and of keys
+};
+
+// The sequences' offsets and lengths (device; layouts in gdn.h).
+struct PromptSeqs {
+    const int32_t *cu_q, *cu_k, *n_q, *n_k;
+};
+
+// A list of work: tiles of `tile` tokens of queries (or keys) that meet the
+// others in steps of `step`; for `ctas` CTAs with shares of `least` steps or more.
+struct PromptList {
+    bool keys;
+    int tile, step, ctas, least;
+};
+
+size_t prompt_list_bytes(const PromptSizes &s, const PromptList &l);
+prompt::List prompt_list_at(const PromptSizes &s, const PromptList &l, void *ws);
+cudaError_t launch_prompt_plan(const PromptSizes &s, const PromptSeqs &q, const PromptList *lists, int n, void *const *ws,
+                               unsigned *err, cudaStream_t st);
+
+size_t attn_prefill_workspace(const PromptSizes &s);
+cudaError_t launch_attn_prefill(const PromptSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                                const PromptSeqs &seqs, const HeadsIn &gate, float scale, uint16_t *out, float *lse,
+                                void *ws, unsigned *err, cudaStream_t st);
+
 }  // namespace gdn

@@ -1,0 +1,728 @@
+// Causal attention of whole prompts: out = softmax(scale Q K^T) V, query heads
+// in groups on one key head, sequences of different lengths, each aligned at
+// its end (the last query sees the last key), with the layer's sigmoid gate
+// and the log-sum-exp.
+//
+// One pass over the keys of a tile with the running maximum m and sum l of the
+// softmax: P = 2^(scale' S - m), O += P V.  m is taken up only when a row's
+// maximum has grown by more than 8 (in powers of two; P stays below 2^8, exact
+// in f32 sums and as precise in bf16 as below 1), so that the accumulators are
+// hardly ever rescaled.  P is rounded to bf16 for its product (as the values
+// are bf16; the sum l takes the unrounded P).
+//
+// 4 D operations per seen (query head, key): bound by the tensor cores.
+//   - Rows of a tile are G query heads of one key head and 128 / G tokens.  Keys
+//     and values come by TMA in tiles of 128 into a ring of 128-byte-swizzled
+//     stages; S = Q K^T and O are accumulated in tensor memory, P goes back
+//     there as the A operand of its product.
+//   - One warp loads, one thread issues the products, the others do the
+//     softmax.  Up to 128 channels: two tiles of 128 rows at a time share the
+//     keys, one warpgroup each, so that one's softmax runs beside the other's
+//     products.  256 channels: O alone takes half of the tensor memory; one
+//     tile, two buffers of S, the next step's scores beside this one's softmax.
+//   - All tiles of all sequences and key heads are one list of steps, cut into
+//     equal shares for one CTA per SM (prompt.cuh): no SM waits for the longest
+//     tile, and a few rows with many keys use all of them.
+#include "prompt_row.cuh"
+#include "umma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace prompt;
+
+constexpr int kKeys = 128;             // of a step
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kRaise = 8.0f;         // powers of two that a row's maximum may grow by before m follows
+
+template <int D_>
+struct Geo {
+    static constexpr int D = D_;
+    static constexpr int TILES = D <= 128 ? 2 : 1;
+    static constexpr int SUB = 128 * 128;                  // bytes of 128 rows of 64 channels
+    static constexpr int QTILE = D / 64 * SUB;
+    // a stage of the ring: 64 channels of 128 keys, or all channels of VK values
+    static constexpr int STAGE = SUB, STAGES = 9, PER_STEP = D / 64, VK = 128 * 64 / D;
+    static constexpr int WARPS = 4 * TILES;                // softmax
+    static constexpr int THREADS = 32 * (WARPS + 2);
+    static constexpr int GROUP = 32;                       // channels that a warp turns into rows at a time
+    static constexpr int TURN = 32 * GROUP * 2;            // bytes for that, of a warp
+    static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + WARPS * TURN + 1024;
+    static constexpr int S_COL = TILES * D;                // two buffers of 128 columns
+};
+
+struct Params {
+    List list;
+    HeadsIn q, k, v, gate;
+    uint16_t *out;
+    float *lse;
+    float *part_o;     // [slot][D / 4][rows][4]
+    float2 *part_ml;   // [slot][rows]
+    unsigned *err;
+    int Hq, Hkv, G, tpt;   // tpt: tokens of a tile
+    float scale, scale2;   // scale2: in powers of two
+};
+
+struct Bars {
+    uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2];
+};
+
+// Waits of one role: after one that gave up, none waits any more.
+struct Waits {
+    unsigned *err;
+    bool dead = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, err)) dead = true;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Writes a row's results, or what is known of it if others hold the rest.
+struct RowOut {
+    long long at;        // (token, head) in out and lse
+    bool mine, valid;    // a row of the sequence's slot; one that holds a token
+    int keys;            // that it sees
+    const uint16_t *gate;
+};
+
+template <int D>
+__device__ __forceinline__ RowOut row_out(const Params &p, const Unit &u, int head, int tile, int r) {
+    const int t = r / p.G, g = r - t * p.G, tok = tile * p.tpt + t;
+    RowOut o;
+    o.mine = t < p.tpt && tok < u.slot_a;
+    o.valid = t < p.tpt && tok < u.n_a;
+    o.keys = o.valid ? max(u.lim0 + tok, 0) : 0;
+    const long long n = (long long)u.a0 + tok;
+    const int h = head * p.G + g;
+    o.at = n * p.Hq + h;
+    o.gate = p.gate.p == nullptr || !o.valid ? nullptr : p.gate.p + n * p.gate.ts + h * p.gate.hs;
+    return o;
+}
+
+// Where a lane stands when a warp writes (or reads) its 32 rows as rows: four
+// lanes to 64 bytes of a row, rows 8 k + lane / 4.
+struct RowsOut {
+    uint16_t *out[4];
+    const uint16_t *gate[4];
+};
+
+template <int D>
+__device__ __forceinline__ RowsOut rows_out(const Params &p, const RowOut &o) {
+    const int lane = threadIdx.x & 31;
+    RowsOut r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int src = 8 * k + (lane >> 2);
+        const long long at = __shfl_sync(0xffffffffu, o.at, src);
+        const bool mine = __shfl_sync(0xffffffffu, (int)o.mine, src);
+        const unsigned long long g = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o.gate), src);
+        r.out[k] = mine ? p.out + at * D + (lane & 3) * 8 : nullptr;
+        r.gate[k] = g != 0 ? reinterpret_cast<const uint16_t *>(g) + (lane & 3) * 8 : nullptr;
+    }
+    return r;
+}
+
+// Byte offset of 16 bytes (chunk 0..3) of a row in a warp's 32 x 64 bytes: no
+// two of the eight lanes of a phase, by rows or by chunks, meet in a bank.
+__device__ __forceinline__ int turn_at(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); }
+
+struct GateGroup {
+    uint4 v[4];
+};
+
+__device__ __forceinline__ GateGroup ask_gate(const RowsOut &r, int d) {
+    GateGroup g;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        g.v[k] = r.gate[k] != nullptr ? *reinterpret_cast<const uint4 *>(r.gate[k] + d) : make_uint4(0, 0, 0, 0);
+    return g;
+}
+
+// 32 channels from d of the warp's rows: lane i's x of row i scaled, gated,
+// rounded, written.
+__device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, const RowOut &o, bool gated,
+                                            const GateGroup &gate, int d, const float *x, float f) {
+    const int lane = threadIdx.x & 31;
+    if (gated) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4 *>(turn + turn_at(8 * k + (lane >> 2), lane & 3)) = gate.v[k];
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(turn + turn_at(lane, i));
+        float y[8];
+        if (gated) {
+            float g[8];
+            attn::unpack8(*at, g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k] * f * rcp_fast(1.0f + exp_fast(-g[k]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k] * f;
+        }
+        const uint4 w = attn::pack8(y);
+        *at = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (r.out[k] != nullptr)
+            *reinterpret_cast<uint4 *>(r.out[k] + d) =
+                *reinterpret_cast<const uint4 *>(turn + turn_at(8 * k + (lane >> 2), lane & 3));
+    __syncwarp();
+}
+
+// The warp's rows that are not finite once more, by the definition.
+template <int D>
+__device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, const Unit &u, int head, bool bad, int d0,
+                                          int d1) {
+    unsigned todo = __ballot_sync(0xffffffffu, bad && o.mine && o.keys > 0);
+    while (todo != 0) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const long long at = __shfl_sync(0xffffffffu, o.at, src);
+        const int keys = __shfl_sync(0xffffffffu, o.keys, src);
+        const long long n = at / p.Hq;
+        const int h = (int)(at - n * p.Hq);
+        exact_row<D>(p.q.p + n * p.q.ts + h * p.q.hs, p.k.p + u.b0 * p.k.ts + head * p.k.hs, p.k.ts,
+                     p.v.p + u.b0 * p.v.ts + head * p.v.hs, p.v.ts, keys, p.scale,
+                     p.gate.p == nullptr ? nullptr : p.gate.p + n * p.gate.ts + h * p.gate.hs, p.out + at * D, d0, d1);
+    }
+}
+
+template <int D_>
+__global__ void __launch_bounds__(Geo<D_>::THREADS, 1)
+prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                      const __grid_constant__ CUtensorMap v_map, const Params p) {
+    using G = Geo<D_>;
+    constexpr int D = D_;
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    __shared__ uint32_t tmem_slot;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = smem + G::TILES * G::QTILE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        umma::tmem_alloc(&tmem_slot, 512);
+        umma::tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < G::STAGES; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.o_done[i], 1);
+            mbar_init(&bars.o_free[i], 4);
+        }
+        fence_mbar_init();
+    }
+    // rows of a tile that no token has (128 is no multiple of G): zeros, never written again
+    for (int i = threadIdx.x; i < G::TILES * (D / 64) * (128 - p.tpt * p.G) * 8; i += G::THREADS) {
+        const int c = i & 7, r = i >> 3, rows = 128 - p.tpt * p.G;
+        *reinterpret_cast<uint4 *>(smem + r / rows * G::SUB + (p.tpt * p.G + r % rows) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    attn::grid_dep_enter();
+
+    // The barrier and its phase for a step's product with the values.  A wait for a phase is sound if the one before it is
+    // over: one tile has two in turn, as its next scores come before its values; a step's scores, once they are there,
+    // say that the values two steps back (with two tiles: one step back) are through.
+    auto o_done = [&](int tile, int step) { return &bars.o_done[G::TILES == 2 ? tile : step & 1]; };
+    auto o_phase = [&](int step) { return (uint32_t)(G::TILES == 2 ? step & 1 : (step >> 1) & 1); };
+
+    Walk w;
+    const bool any = w.begin(p.list, blockIdx.x, p.Hkv);
+    if (any && warp == G::WARPS) {
+        // ---- loads
+        if (lane == 0) {
+            prefetch_tmap(&q_map);
+            prefetch_tmap(&k_map);
+            prefetch_tmap(&v_map);
+            Waits wait{p.err};
+            int stage = 0, units = 0;
+            uint32_t phase = 0;
+            auto next_stage = [&]() -> uint8_t * {
+                wait(&bars.empty[stage], phase ^ 1);
+                if (!wait.dead) mbar_expect_tx(&bars.full[stage], G::STAGE);
+                return ring + stage * G::STAGE;
+            };
+            auto stage_done = [&] {
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            };
+            auto load_keys = [&](int head, int token) {
+                for (int c = 0; c < G::PER_STEP; ++c) {
+                    uint8_t *dst = next_stage();
+                    if (!wait.dead) tma_load_3d(dst, &k_map, c * 64, head, token, &bars.full[stage]);
+                    stage_done();
+                }
+            };
+            auto load_values = [&](int head, int token) {
+                for (int c = 0; c < G::PER_STEP; ++c) {
+                    uint8_t *dst = next_stage();
+                    if (!wait.dead)
+                        for (int i = 0; i < D / 64; ++i)
+                            tma_load_3d(dst + i * (G::VK * 128), &v_map, i * 64, head, token + c * G::VK, &bars.full[stage]);
+                    stage_done();
+                }
+            };
+            auto load_q = [&](const Walk &x) {
+                wait(&bars.q_free, (units & 1) ^ 1);
+                ++units;
+                if (wait.dead) return;
+                mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
+                for (int t = 0; t < G::TILES; ++t)
+                    for (int i = 0; i < D / 64; ++i)
+                        tma_load_3d(smem + t * G::QTILE + i * G::SUB, &q_map, i * 64, x.head * p.G, x.u.a0 + t * p.tpt,
+                                    &bars.q_full);
+            };
+            Walk x = w;   // the keys' walk, a step ahead of the values'
+            int j = x.first;
+            bool more = true;
+            auto load_k = [&] {
+                if (j == x.last) {
+                    more = x.next();
+                    if (!more) return;
+                    j = x.first;
+                }
+                if (j == x.first) load_q(x);
+                load_keys(x.head, x.u.b0 + j * kKeys);
+                ++j;
+            };
+            load_k();
+            do {
+                for (int i = w.first; i < w.last; ++i) {
+                    if (G::TILES == 1 && more) load_k();
+                    load_values(w.head, w.u.b0 + i * kKeys);
+                    if (G::TILES == 2 && more) load_k();
+                }
+            } while (w.next());
+            if (wait.dead)   // let the copies in flight land
+                for (int i = 0; i < G::STAGES; ++i) mbar_try_wait(&bars.full[i], 0);
+        }
+    } else if (any && warp == G::WARPS + 1) {
+        // ---- products.  The whole warp goes through the loop, so that operands stay uniform; one lane issues.
+        Waits wait{p.err};
+        const bool leader = lane == 0;
+        const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+        int stage = 0, units = 0, step = 0;
+        uint32_t phase = 0;
+        constexpr uint32_t id_s = umma::idesc(128, 128, umma::kFmtBF16);
+        constexpr uint32_t id_o = umma::idesc(128, D, umma::kFmtBF16) | umma::kBTransposed;
+        const uint64_t d_ring = umma::desc_sw128(smem_u32(ring)), d_q = umma::desc_sw128(smem_u32(smem));
+        const uint64_t d_values = umma::desc_sw128_mn(smem_u32(ring), G::VK * 128);
+        auto take = [&](int s, uint32_t ph) {
+            wait(&bars.full[s], ph);
+            umma::fence_after_sync();
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (leader) umma::mma_commit(bar);
+        };
+        auto pass = [&](int &s, uint32_t &ph) {
+            if (++s == G::STAGES) {
+                s = 0;
+                ph ^= 1;
+            }
+        };
+        // the scores of 64 channels, in stage s, of tile t into buffer buf
+        auto scores = [&](int t, int buf, int c, int s) {
+            const uint64_t a = d_q + (uint32_t)((t * G::QTILE + c * G::SUB) >> 4), b = d_ring + (uint32_t)(s * (G::STAGE >> 4));
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma::mma_bf16(base + G::S_COL + buf * 128, a + k * 2, b + k * 2, id_s, c > 0 || k > 0);
+            }
+        };
+        // the product of VK of P's keys with their values, in stage s
+        auto values = [&](int t, int buf, int c, int s, bool acc) {
+            const uint64_t b = d_values + (uint32_t)(s * (G::STAGE >> 4));
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < G::VK / 16; ++k)
+                    umma::mma_bf16_tmem_a(base + t * D, base + G::S_COL + buf * 128 + c * (G::VK / 2) + k * 8,
+                                          b + k * (2048 >> 4), id_o, acc || c > 0 || k > 0);
+            }
+        };
+        Walk x = w;
+        int j = x.first, qstep = 0;
+        bool more = true;
+        auto enter = [&]() -> bool {   // the next step's scores
+            if (j == x.last) {
+                more = x.next();
+                if (!more) return false;
+                j = x.first;
+            }
+            if (j == x.first) wait(&bars.q_full, units++ & 1);
+            return true;
+        };
+        auto leave = [&] {
+            ++j;
+            ++qstep;
+            if (j == x.last) commit(&bars.q_free);
+        };
+        auto all_scores = [&] {   // (256 channels, and the first step)
+            if (!enter()) return;
+            for (int c = 0; c < G::PER_STEP; ++c) {
+                take(stage, phase);
+                for (int t = 0; t < G::TILES; ++t) scores(t, G::TILES == 1 ? qstep & 1 : t, c, stage);
+                commit(&bars.empty[stage]);
+                pass(stage, phase);
+            }
+            if (G::TILES == 1) {
+                commit(&bars.s_full[qstep & 1]);
+            } else {
+                commit(&bars.s_full[0]);
+                commit(&bars.s_full[1]);
+            }
+            leave();
+        };
+        all_scores();
+        int done = 0;   // units whose values are through
+        do {
+            for (int i = w.first; i < w.last; ++i, ++step) {
+                const bool acc = i > w.first;
+                if (G::TILES == 1) {
+                    if (more) all_scores();
+                    wait(&bars.p_full[step & 1], (step >> 1) & 1);
+                    if (!acc && done > 0) wait(&bars.o_free[0], (done - 1) & 1);
+                    for (int c = 0; c < G::PER_STEP; ++c) {
+                        take(stage, phase);
+                        values(0, step & 1, c, stage, acc);
+                        commit(&bars.empty[stage]);
+                        pass(stage, phase);
+                    }
+                    commit(o_done(0, step));
+                } else {
+                    // each tile: this step's values, then the next step's scores (into the buffer that P has left)
+                    bool next = more;
+                    int sv = stage, sk = stage;
+                    uint32_t pv = phase, pk = phase;
+                    for (int c = 0; c < G::PER_STEP; ++c) pass(sk, pk);
+                    for (int t = 0; t < 2; ++t) {
+                        wait(&bars.p_full[t], step & 1);
+                        if (!acc && done > 0) wait(&bars.o_free[t], (done - 1) & 1);
+                        umma::fence_after_sync();
+                        int s = sv;
+                        uint32_t ph = pv;
+                        for (int c = 0; c < G::PER_STEP; ++c) {
+                            if (t == 0) take(s, ph);
+                            values(t, t, c, s, acc);
+                            if (t == 1) commit(&bars.empty[s]);
+                            pass(s, ph);
+                        }
+                        commit(o_done(t, step));
+                        if (t == 0 && next) next = enter();
+                        if (next) {
+                            s = sk;
+                            ph = pk;
+                            for (int c = 0; c < G::PER_STEP; ++c) {
+                                if (t == 0) take(s, ph);
+                                scores(t, t, c, s);
+                                if (t == 1) commit(&bars.empty[s]);
+                                pass(s, ph);
+                            }
+                            commit(&bars.s_full[t]);
+                            if (t == 1) {
+                                stage = s;
+                                phase = ph;
+                                leave();
+                            }
+                        } else if (t == 1) {
+                            stage = sk;
+                            phase = pk;
+                        }
+                    }
+                }
+            }
+            ++done;
+        } while (w.next());
+        // every product is through before the tensor memory goes back
+        for (int i = G::TILES == 1 && step > 1 ? step - 2 : step - 1; i < step; ++i)
+            for (int t = 0; t < G::TILES; ++t) wait(o_done(t, i), o_phase(i));
+    } else if (any) {
+        // ---- softmax and results
+        const int tile = G::TILES == 2 ? warp >> 2 : 0, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D;
+        uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
+        Waits wait{p.err};
+        int step = 0;
+        do {
+            const RowOut o = row_out<D>(p, w.u, w.head, tile, r);
+            float m = -INFINITY, l = 0.0f;   // m: of the scores in powers of two
+            for (int i = w.first; i < w.last; ++i, ++step) {
+                const int buf = G::TILES == 2 ? tile : step & 1;
+                const uint32_t s_at = lanes + G::S_COL + buf * 128;
+                wait(&bars.s_full[buf], G::TILES == 2 ? step & 1 : (step >> 1) & 1);
+                umma::fence_after_sync();
+                float s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_at + c * 32, s[c]);
+                umma::tmem_ld_wait();
+                const int lim = o.keys - i * kKeys;
+                if (p.scale2 < 0.0f) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[c][k] = -s[c][k];
+                }
+                if (__any_sync(0xffffffffu, lim < kKeys)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[c][k] = c * 32 + k < lim ? s[c][k] : -INFINITY;
+                }
+                float top[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = s[c][0];
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) top[c] = fmaxf(top[c], s[c][k]);
+                }
+                const float f2 = fabsf(p.scale2);
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f2;
+                const bool raise = most > m + kRaise;   // (m = -infinity: the first that is seen)
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float m1 = raise ? most : m, f = raise ? (m == -INFINITY ? 0.0f : ex2(m - m1)) : 1.0f;
+                    m = m1;
+                    l *= f;
+                    if (i > w.first) {
+                        if (G::TILES == 1) {
+                            wait(o_done(0, step - 1), o_phase(step - 1));   // (two tiles: their scores came after it)
+                            umma::fence_after_sync();
+                        }
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float x[32];
+                            umma::tmem_ld32(o_at + c * 32, x);
+                            umma::tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] *= f;
+                            umma::tmem_st32(o_at + c * 32, x);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    float pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float e[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            e[z] = ex2(fmaf(s[c + k / 16][2 * (k % 16) + z], f2, -base));
+                            sum[c / 2 * 2 + z] += e[z];
+                        }
+                        pk[k] = __uint_as_float(attn::pack2(e[0], e[1]));
+                    }
+                    umma::tmem_st32(s_at + c * 16, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                umma::tmem_st_wait();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[buf]);
+            }
+            // the unit's results
+            const bool whole = w.whole(), gated = p.gate.p != nullptr;
+            const int slot = w.slot(blockIdx.x);
+            const float f = 1.0f / l;
+            float check = 0.0f;
+            constexpr int BATCH = D / 32 < 4 ? D / 32 : 4;   // groups whose gates are asked for at once
+            GateGroup gates[BATCH];
+            const RowsOut rows = rows_out<D>(p, o);
+            auto ask = [&](int b) {
+                if (!gated || !whole) return;
+#pragma unroll
+                for (int c = 0; c < BATCH; ++c) gates[c] = ask_gate(rows, (b * BATCH + c) * 32);
+            };
+            ask(0);
+            wait(o_done(tile, step - 1), o_phase(step - 1));
+            umma::fence_after_sync();
+#pragma unroll
+            for (int b = 0; b < D / 32 / BATCH; ++b) {
+                if (b > 0) ask(b);
+#pragma unroll
+                for (int cc = 0; cc < BATCH; ++cc) {
+                    const int c = b * BATCH + cc;
+                    float x[32];
+                    umma::tmem_ld32(o_at + c * 32, x);
+                    umma::tmem_ld_wait();
+                    if (c == D / 32 - 1) {
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.o_free[tile]);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
+                        write_group(turn, rows, o, gated, gates[cc], c * 32, x, f);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
+                                      ((size_t)slot * (D / 4) + c * 8) * (G::TILES * 128) + tile * 128 + r;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[(size_t)k * (G::TILES * 128)] =
+                                make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    }
+                }
+            }
+            if (whole) {
+                if (p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+                mend_rows<D>(p, o, w.u, w.head, check != 0.0f, 0, D);
+            } else {
+                p.part_ml[(size_t)slot * (G::TILES * 128) + tile * 128 + r] = make_float2(m, l);
+            }
+        } while (w.next());
+        umma::fence_before_sync();
+    }
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 0) umma::tmem_dealloc(tmem, 512);
+}
+
+// A split unit's parts joined: 32 channels of 128 rows a block.
+template <int D>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ctas) {
+    constexpr int ROWS = Geo<D>::TILES * 128;
+    __shared__ __align__(16) uint8_t turn[4][Geo<D>::TURN];
+    attn::grid_dep_enter();
+    const Parts parts = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
+    if (parts.n == 0) return;
+    const int tile = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32), r = threadIdx.x, row = tile * 128 + r;
+    const RowOut o = row_out<D>(p, parts.u, parts.head, tile, r);
+    const RowsOut rows = rows_out<D>(p, o);
+    const GateGroup gate = ask_gate(rows, c * 32);
+    float m = -INFINITY, l = 0.0f, x[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+    for (int i = 0; i < parts.n; ++i) {
+        const size_t slot = 2 * (size_t)(blockIdx.x + i) + (i == 0 ? 1 : 0);
+        const float2 ml = p.part_ml[slot * ROWS + row];
+        const float4 *src = reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + c * 8) * ROWS + row;
+        const float top = fmaxf(m, ml.x), f = m == top ? 1.0f : ex2(m - top), g = ml.x == top ? 1.0f : ex2(ml.x - top);
+        m = top;
+        l = l * f + ml.y * g;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 v = src[(size_t)k * ROWS];
+            x[4 * k] = x[4 * k] * f + v.x * g;
+            x[4 * k + 1] = x[4 * k + 1] * f + v.y * g;
+            x[4 * k + 2] = x[4 * k + 2] * f + v.z * g;
+            x[4 * k + 3] = x[4 * k + 3] * f + v.w * g;
+        }
+    }
+    const float f = 1.0f / l;
+    float check = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
+    write_group(turn[threadIdx.x >> 5], rows, o, p.gate.p != nullptr, gate, c * 32, x, f);
+    if (c == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+    mend_rows<D>(p, o, parts.u, parts.head, check != 0.0f, c * 32, c * 32 + 32);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int tiles_of(int D) { return D <= 128 ? 2 : 1; }
+
+PromptList list_of(const PromptSizes &s) {
+    const int tpt = 128 / (s.Hq / s.Hkv);
+    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4};
+}
+
+struct Workspace {
+    size_t o, ml, total;
+};
+
+Workspace workspace(const PromptSizes &s) {
+    Workspace w;
+    const size_t rows = 2 * (size_t)num_sms() * tiles_of(s.D) * 128;
+    w.o = prompt_list_bytes(s, list_of(s));
+    w.ml = w.o + up256(rows * s.D * sizeof(float));
+    w.total = w.ml + up256(rows * sizeof(float2));
+    return w;
+}
+
+// [rows, H, D] as (channels, heads, tokens) in boxes of 64 channels.
+bool heads_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_heads, int box_tokens) {
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows};
+    const uint64_t strides[2] = {(uint64_t)(H > 1 ? x.hs : D) * 2, (uint64_t)(rows > 1 ? x.ts : (long long)H * D) * 2};
+    const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_tokens};
+    return encode_tmap_strided(map, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D>
+cudaError_t launch_d(const PromptSizes &s, Params &p, cudaStream_t st) {
+    using G = Geo<D>;
+    static unsigned long long done = 0;
+    cudaError_t e = set_max_smem(done, prompt_forward_kernel<D>, G::SMEM);
+    if (e != cudaSuccess) return e;
+    CUtensorMap q, k, v;
+    // (no keys: nothing of what is loaded counts, but a map needs a tensor)
+    const bool none = s.Nk == 0;
+    const HeadsIn dummy{p.q.p, 0, 0};
+    if (!heads_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) ||
+        !heads_map(&k, none ? dummy : p.k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, 1, kKeys) ||
+        !heads_map(&v, none ? dummy : p.v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, 1, G::VK))
+        return cudaErrorInvalidValue;
+    const int ctas = num_sms();
+    e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, p);
+    if (e != cudaSuccess) return e;
+    return DependentLaunch(dim3(ctas - 1, G::TILES * (D / 32)), dim3(128), 0, st)(prompt_join_kernel<D>, p, ctas);
+}
+
+}  // namespace
+
+size_t attn_prefill_workspace(const PromptSizes &s) { return workspace(s).total; }
+
+cudaError_t launch_attn_prefill(const PromptSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                                const PromptSeqs &seqs, const HeadsIn &gate, float scale, uint16_t *out, float *lse,
+                                void *ws, unsigned *err, cudaStream_t st) {
+    const PromptList list = list_of(s);
+    const Workspace w = workspace(s);
+    char *base = static_cast<char *>(ws);
+    cudaError_t e = launch_prompt_plan(s, seqs, &list, 1, &ws, err, st);
+    if (e != cudaSuccess) return e;
+    Params p = {};
+    p.list = prompt_list_at(s, list, ws);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.gate = gate;
+    p.out = out;
+    p.lse = lse;
+    p.part_o = reinterpret_cast<float *>(base + w.o);
+    p.part_ml = reinterpret_cast<float2 *>(base + w.ml);
+    p.err = err;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.G = s.Hq / s.Hkv;
+    p.tpt = 128 / p.G;
+    p.scale = scale;
+    p.scale2 = scale * kLog2e;
+    if (s.D == 64) return launch_d<64>(s, p, st);
+    if (s.D == 128) return launch_d<128>(s, p, st);
+    return launch_d<256>(s, p, st);
+}
+
+}  // namespace gdn

@@ -33,7 +33,18 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t smem_addr) {
     return d;
 }
 
+// ... and the K-stride of an operand whose rows are not its K: tiles of R rows
+// (K) x 64 bf16 (M or N), swizzled as above; 8-row groups 1024 B apart (stride
+// byte offset), tiles of the next 64 M or N `tile_bytes` apart (leading byte
+// offset).  16 rows of K further: 2048 B.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t smem_addr, uint32_t tile_bytes) {
+    return (desc_sw128(smem_addr) & ~((uint64_t)0x3FFFu << 16)) | ((uint64_t)(tile_bytes >> 4) << 16);
+}
+
 enum : uint32_t { kFmtBF16 = 1u, kFmtTF32 = 2u };
+
+// Added to an instruction descriptor: B's rows are its K (desc_sw128_mn).
+constexpr uint32_t kBTransposed = 1u << 16;
 
 // Instruction descriptor: dense, f32 accumulator, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t fmt) {
@@ -95,6 +106,16 @@ __device__ __forceinline__ void mma_tf32_tmem_a(uint32_t d_tmem, uint32_t a_tmem
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)acc)
+        : "memory");
+}
+
+// bf16 with the A operand read from tensor memory (two bf16 of K per column).
+__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)acc)
         : "memory");
 }

@@ -21,7 +21,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libgdn.so")
 
-GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, GDN_ERR_BAD_PAGE = range(6)
+GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, GDN_ERR_BAD_PAGE, GDN_ERR_BAD_OFFSETS = \
+    range(7)
 
 # batch rows gdn_prefill_noalloc accepts (GDN_NOALLOC_MAX_ROWS in gdn.h)
 GDN_NOALLOC_MAX_ROWS = 4096
@@ -56,6 +57,8 @@ _P = ctypes.c_void_p
 _HEADS = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64]      # pointer, token stride, head stride
 _ATTN = [ctypes.POINTER(GdnAttnDims)]
 _CACHE = [ctypes.POINTER(GdnKvCache), _P, ctypes.c_int32]       # cache, page table, its width
+_ROWS = _ATTN + [ctypes.c_int64] * 2
+
 _SIGS = {
     "gdn_conv_update": (ctypes.c_int, [ctypes.POINTER(GdnDims), _P, _P, _P, _P, _P, _P, _P, _P]),
     "gdn_gating": (ctypes.c_int, [ctypes.POINTER(GdnDims), _P, _P, _P, _P, _P, _P, _P]),
@@ -87,6 +90,9 @@ _SIGS = {
     "gdn_attn_decode_workspace_size": (ctypes.c_size_t, _ATTN),
     "gdn_attn_decode": (ctypes.c_int, _ATTN + [_P] + _CACHE + [_P] * 2 + _HEADS + [ctypes.c_float] + [_P] * 3 +
                         [ctypes.c_size_t, _P]),
+    "gdn_attn_prefill_workspace_size": (ctypes.c_size_t, _ROWS),
+    "gdn_attn_prefill": (ctypes.c_int, _ROWS + _HEADS * 3 + [_P] * 4 + _HEADS + [ctypes.c_float] + [_P] * 3 +
+                         [ctypes.c_size_t, _P]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_device_status": (ctypes.c_int, [_P]),
     "gdn_selftest_timeout": (ctypes.c_int, [_P]),

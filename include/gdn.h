@@ -67,7 +67,8 @@ typedef enum gdn_status {
     GDN_ERR_UNSUPPORTED = 2,   /* a size outside the supported set above */
     GDN_ERR_CUDA = 3,          /* a CUDA launch or attribute call failed */
     GDN_ERR_TIMEOUT = 4,       /* a bounded on-device wait gave up (see gdn_device_status) */
-    GDN_ERR_BAD_PAGE = 5       /* a cache position had no valid page (see gdn_device_status) */
+    GDN_ERR_BAD_PAGE = 5,      /* a cache position had no valid page (see gdn_device_status) */
+    GDN_ERR_BAD_OFFSETS = 6    /* offsets of packed sequences not in order (see gdn_device_status) */
 } gdn_status;
 
 /* Problem sizes: the fields of GatedDeltaConfig (mlex gated_delta.rs) plus the
@@ -393,9 +394,10 @@ GDN_API const char *gdn_status_string(gdn_status status);
  * word, which a kernel sets when one of its bounded waits (on an mbarrier or
  * a tensor-core commit) gives up, or when a position of a paged cache has no
  * page (a page-table entry outside [0, n_pages), a negative position, or one
- * past the table).  Returns GDN_OK, GDN_ERR_TIMEOUT (also when both kinds
- * were recorded), GDN_ERR_BAD_PAGE, or GDN_ERR_CUDA if the synchronisation
- * itself failed. */
+ * past the table), or when the offsets of packed sequences decrease or leave
+ * their buffer.  Returns GDN_OK, GDN_ERR_TIMEOUT (whatever else was recorded),
+ * GDN_ERR_BAD_OFFSETS (also when a bad page was recorded), GDN_ERR_BAD_PAGE, or
+ * GDN_ERR_CUDA if the synchronisation itself failed. */
 GDN_API gdn_status gdn_device_status(gdn_stream stream);
 
 /* Self-test of the failure path: launches a kernel whose bounded wait (on an
@@ -547,6 +549,53 @@ GDN_API gdn_status gdn_attn_decode(const gdn_attn_dims *dims, const uint16_t *q,
                                    const int32_t *n_new, const uint16_t *gate, int64_t gate_token_stride,
                                    int64_t gate_head_stride, float scale, uint16_t *out, float *lse, void *workspace,
                                    size_t ws_bytes, gdn_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Whole prompts
+ * ------------------------------------------------------------------------
+ * Causal attention of dims->B sequences of different lengths, queries and keys
+ * from buffers of q_rows and k_rows tokens.  Sequence s holds the tokens
+ * cu_q[s] .. cu_q[s + 1] - 1 of the queries' buffer (its slot) and cu_k[s] ..
+ * cu_k[s + 1] - 1 of the keys'; of these the first n_q[s] and n_k[s] (clamped to
+ * the slot) are there, the others are padding.  The last query sees the last
+ * key: query t sees the keys 0 .. t + (keys - queries), so that keys before the
+ * queries' own are a kept prefix; a query that sees no key gives zeros and lse =
+ * -inf.  dims->T and dims->Drot are not used (but must be valid).
+ *   cu_q, cu_k i32 [B + 1] or NULL: slots of q_rows / B (k_rows / B) tokens, which
+ *          must be whole numbers.  Offsets that decrease or leave the buffer are
+ *          found on the device: the call then writes nothing and the device
+ *          error word records GDN_ERR_BAD_OFFSETS.
+ *   n_q, n_k i32 [B] or NULL (the whole slots)
+ * Padding of a slot gives zeros (and lse = -inf); rows of the outputs in no slot
+ * are left as they were.  What lies in keys and values that a query does not
+ * see, in padding and in no slot does not enter its results, whatever it is.
+ *
+ * Inputs marked "heads" are [rows, H, D] views as above (element (n, h, d) at
+ * ptr[n*token_stride + h*head_stride + d]); here a stride of 0 over more than
+ * one token or head gives GDN_ERR_UNSUPPORTED, as do more than 2^31 - 2^16 rows. */
+
+/* Per query row: s_j = scale q.k_j, out = softmax(s) V, lse = log sum_j exp(s_j).
+ *   q      bf16 heads [q_rows, Hq, D];  k, v bf16 heads [k_rows, Hkv, D] (in)
+ *   gate   bf16 heads [q_rows, Hq, D] or NULL: out is multiplied by
+ *          sigmoid(gate), in f32 before its one rounding to bf16
+ *   scale  of the scores (usually 1/sqrt(D)); finite
+ *   out    bf16 [q_rows, Hq, D] (out);  lse f32 [q_rows, Hq] (out) or NULL
+ *   workspace  device scratch of gdn_attn_prefill_workspace_size() bytes on the
+ *          device that runs the call: the work list, and the partial results
+ *          of tiles that are split over several CTAs.  They are joined in a
+ *          fixed order: equal calls give equal bits.
+ * Scores, sums and accumulators are f32; softmax weights are rounded to bf16 for
+ * the product with V.  A NaN or +inf among the scores that a query sees makes
+ * its output and lse NaN; scores that are all -inf make its output NaN (0 / 0)
+ * and lse -inf. */
+GDN_API size_t gdn_attn_prefill_workspace_size(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows);
+GDN_API gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows, const uint16_t *q,
+                                    int64_t q_token_stride, int64_t q_head_stride, const uint16_t *k,
+                                    int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
+                                    const int32_t *cu_k, const int32_t *n_q, const int32_t *n_k, const uint16_t *gate,
+                                    int64_t gate_token_stride, int64_t gate_head_stride, float scale, uint16_t *out,
+                                    float *lse, void *workspace, size_t ws_bytes, gdn_stream stream);
 
 /* ABI version of this header (incremented on any signature change). */
 GDN_API int gdn_abi_version(void);
