@@ -233,10 +233,11 @@ struct PromptSeqs {
 };
 
 // A list of work: tiles of `tile` tokens of queries (or keys) that meet the
-// others in steps of `step`; for `ctas` CTAs with shares of `least` steps or more.
+// others in steps of `step`; for `ctas` CTAs with shares of `least` steps or
+// more; `blank`: the steps' time that a tile's start and end take.
 struct PromptList {
     bool keys;
-    int tile, step, ctas, least;
+    int tile, step, ctas, least, blank;
 };
 
 size_t prompt_list_bytes(const PromptSizes &s, const PromptList &l);

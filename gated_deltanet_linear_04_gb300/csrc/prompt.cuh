@@ -6,8 +6,10 @@
 // are rows of one tile, row t * G + g, so that keys are read once for all of
 // them; or 128 keys) with the tokens of the other kind that it has to meet, in
 // steps of a fixed number.  The units of all sequences, once for each key head,
-// are one list of steps; every CTA takes an equal share of it.  A unit that
-// crosses shares leaves partial results, which a second kernel joins in order.
+// are one list of steps, each unit with a few blank ones before its own, which
+// stand for the time that its start and end take; every CTA takes an equal
+// share of the list.  A unit whose steps cross shares leaves partial results,
+// which a second kernel joins in order.
 #pragma once
 
 #include "attn.cuh"
@@ -21,20 +23,20 @@ struct __align__(16) Unit {
     int lim0;              // queries: keys that the first token sees.  keys: key j of the tile is seen by token i of
                            // the b's if j <= lim0 + i
     int steps, pad;
-    long long pre;         // steps of the units before
+    long long pre;         // steps of the units before, blank ones among them
     long long pad2;
 };
 
 struct Start {             // where a CTA's share begins
     int head, unit;
-    long long offset;      // steps into the unit
+    long long offset;      // steps into the unit, blank ones first
 };
 
 struct Header {
     long long steps;       // of one key head
     long long share;       // of a CTA
-    int units, pad;
-    long long pad2;
+    int units, blank;      // blank steps of a unit
+    long long pad;
 };
 
 // One list in the workspace: header, shares (CTAs), units.
@@ -74,26 +76,44 @@ __device__ __forceinline__ Seq load_seq(const Sequences &p, int s) {
 // A CTA's way through its share.
 struct Walk {
     const Unit *units;
-    int n_units, heads;
+    int n_units, heads, blank;
     long long left;        // steps of the share after the current unit's
     int head, unit, first, last;   // the current unit's steps first .. last - 1
     Unit u;
+    int4 ahead[2];         // the next unit, asked for early
 
-    __device__ __forceinline__ bool open(int at) {
-        if (left <= 0) return false;
-        const int4 *p = reinterpret_cast<const int4 *>(units + unit);
-        const int4 x = p[0], y = p[1];
-        u.a0 = x.x;
-        u.n_a = x.y;
-        u.slot_a = x.z;
-        u.b0 = x.w;
-        u.n_b = y.x;
-        u.lim0 = y.y;
-        u.steps = y.z;
-        first = at;
-        last = (long long)(u.steps - at) <= left ? u.steps : at + (int)left;
-        left -= last - first;
-        return true;
+    // the unit's steps from `at` (blank ones counted); units of which the share holds only blank steps are passed over
+    __device__ __forceinline__ bool open(long long at) {
+        while (left > 0) {
+            const int4 x = ahead[0], y = ahead[1];
+            ask(unit + 1 == n_units ? 0 : unit + 1);
+            u.a0 = x.x;
+            u.n_a = x.y;
+            u.slot_a = x.z;
+            u.b0 = x.w;
+            u.n_b = y.x;
+            u.lim0 = y.y;
+            u.steps = y.z;
+            const long long whole = (long long)u.steps + blank - at, n = whole < left ? whole : left;
+            first = at > blank ? (int)(at - blank) : 0;
+            last = at + n > blank ? (int)(at + n - blank) : 0;
+            left -= n;
+            if (last > first) return true;
+            advance();
+            at = 0;
+        }
+        return false;
+    }
+    __device__ __forceinline__ void ask(int i) {
+        const int4 *p = reinterpret_cast<const int4 *>(units + i);
+        ahead[0] = p[0];
+        ahead[1] = p[1];
+    }
+    __device__ __forceinline__ void advance() {
+        if (++unit == n_units) {
+            unit = 0;
+            ++head;
+        }
     }
     __device__ __forceinline__ bool begin(const List &l, int cta, int heads_) {
         const Header h = *l.header;
@@ -102,17 +122,24 @@ struct Walk {
         if (left <= 0) return false;
         units = l.unit;
         n_units = h.units;
+        blank = h.blank;
         heads = heads_;
         const Start s = l.start[cta];
         head = s.head;
         unit = s.unit;
-        return open((int)s.offset);
+        ask(unit);
+        return open(s.offset);
+    }
+    // the same values in every lane, and known to be (for loops of a whole warp)
+    __device__ __forceinline__ void uniform() {
+        first = __shfl_sync(0xffffffffu, first, 0);
+        last = __shfl_sync(0xffffffffu, last, 0);
+        head = __shfl_sync(0xffffffffu, head, 0);
+        u.a0 = __shfl_sync(0xffffffffu, u.a0, 0);
+        u.b0 = __shfl_sync(0xffffffffu, u.b0, 0);
     }
     __device__ __forceinline__ bool next() {
-        if (++unit == n_units) {
-            unit = 0;
-            ++head;
-        }
+        advance();
         return open(0);
     }
     __device__ __forceinline__ bool whole() const { return first == 0 && last == u.steps; }
@@ -134,13 +161,31 @@ __device__ __forceinline__ Parts parts_from(const List &l, int cta, int ctas, in
     const long long total = h.steps * heads, x1 = h.share * (cta + 1);
     if (cta + 1 >= ctas || x1 >= total) return r;
     const Start s = l.start[cta + 1];
-    if (s.offset == 0 || s.offset > h.share) return r;   // (begins there, or before this share)
+    const long long mine = s.offset - h.blank;   // steps before x1
+    if (mine <= 0 || mine > h.share) return r;   // (begins after x1, or before this share)
     r.u = l.unit[s.unit];
     r.head = s.head;
-    const long long end = x1 - s.offset + r.u.steps;
+    const long long end = x1 - s.offset + h.blank + r.u.steps;
     r.n = (int)((end - 1) / h.share) - cta + 1;
     return r;
 }
+
+// Waits of a CTA's roles: after one that gave up, none waits any more (`dead`,
+// in shared memory).  False: not there.
+struct Waits {
+    unsigned *err;
+    volatile int *dead;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        for (uint32_t i = 0; i < kSpinLimit; ++i) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if (*dead) return false;
+        }
+        atomicOr(err, kErrMbarTimeout);
+        *dead = 1;
+        return false;
+    }
+};
 
 }  // namespace prompt
 }  // namespace gdn

@@ -42,13 +42,14 @@ struct Geo {
     static constexpr int SUB = 128 * 128;                  // bytes of 128 rows of 64 channels
     static constexpr int QTILE = D / 64 * SUB;
     // a stage of the ring: 64 channels of 128 keys, or all channels of VK values
-    static constexpr int STAGE = SUB, STAGES = 9, PER_STEP = D / 64, VK = 128 * 64 / D;
-    static constexpr int WARPS = 4 * TILES;                // softmax
+    static constexpr int STAGE = SUB, STAGES = D == 256 ? 9 : 8, PER_STEP = D / 64, VK = 128 * 64 / D;
+    static constexpr int HALVES = 2 / TILES;               // warpgroups that share a tile's softmax
+    static constexpr int WARPS = 8;
     static constexpr int THREADS = 32 * (WARPS + 2);
-    static constexpr int GROUP = 32;                       // channels that a warp turns into rows at a time
-    static constexpr int TURN = 32 * GROUP * 2;            // bytes for that, of a warp
+    static constexpr int TURN = 32 * 32;                   // bytes in which a warp turns 16 channels of its rows into rows
     static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + WARPS * TURN + 1024;
     static constexpr int S_COL = TILES * D;                // two buffers of 128 columns
+    static_assert(SMEM + 6144 <= 227 * 1024, "");
 };
 
 struct Params {
@@ -65,21 +66,74 @@ struct Params {
 
 struct Bars {
     uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2];
-};
-
-// Waits of one role: after one that gave up, none waits any more.
-struct Waits {
-    unsigned *err;
-    bool dead = false;
-    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, err)) dead = true;
-    }
+    float most[2][2][128];   // [step parity][half][row]: what the halves of a row tell each other
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two f32 in one register pair.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2_of(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// The two warpgroups of a tile meet.
+__device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Scores that are not to be seen (from `lim` on) are -infinity.
+__device__ __forceinline__ void hide(float (&s)[32], int lim) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[k] = k < lim ? s[k] : -INFINITY;
+}
+
+__device__ __forceinline__ float largest(const float (&x)[32]) {
+    float a = max3(x[0], x[1], x[2]), b = max3(x[16], x[17], x[18]);
+#pragma unroll
+    for (int k = 3; k < 15; k += 2) {
+        a = max3(a, x[k], x[k + 1]);
+        b = max3(b, x[16 + k], x[17 + k]);
+    }
+    return max3(a, b, fmaxf(x[15], x[31]));
+}
+
+// e = 2^(s mul + add) of 32 scores, their sum added to `sum`, as bf16 pairs.
+__device__ __forceinline__ void weights(const float (&s)[32], F2 mul, F2 add, F2 &sum, float *pk) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float2 x = parts(fma2(f2_of(s[2 * k], s[2 * k + 1]), mul, add));
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        sum = add2(sum, f2_of(e.x, e.y));
+        pk[k] = __uint_as_float(attn::pack2(e.x, e.y));
+    }
 }
 
 // Writes a row's results, or what is known of it if others hold the rest.
@@ -104,11 +158,11 @@ __device__ __forceinline__ RowOut row_out(const Params &p, const Unit &u, int he
     return o;
 }
 
-// Where a lane stands when a warp writes (or reads) its 32 rows as rows: four
-// lanes to 64 bytes of a row, rows 8 k + lane / 4.
+// Where a lane stands when a warp writes (or reads) its 32 rows as rows: two
+// lanes to 32 bytes of a row, rows 16 k + lane / 2.
 struct RowsOut {
-    uint16_t *out[4];
-    const uint16_t *gate[4];
+    uint16_t *out[2];
+    const uint16_t *gate[2];
 };
 
 template <int D>
@@ -116,67 +170,74 @@ __device__ __forceinline__ RowsOut rows_out(const Params &p, const RowOut &o) {
     const int lane = threadIdx.x & 31;
     RowsOut r;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int src = 8 * k + (lane >> 2);
+    for (int k = 0; k < 2; ++k) {
+        const int src = 16 * k + (lane >> 1);
         const long long at = __shfl_sync(0xffffffffu, o.at, src);
         const bool mine = __shfl_sync(0xffffffffu, (int)o.mine, src);
         const unsigned long long g = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o.gate), src);
-        r.out[k] = mine ? p.out + at * D + (lane & 3) * 8 : nullptr;
-        r.gate[k] = g != 0 ? reinterpret_cast<const uint16_t *>(g) + (lane & 3) * 8 : nullptr;
+        r.out[k] = mine ? p.out + at * D + (lane & 1) * 8 : nullptr;
+        r.gate[k] = g != 0 ? reinterpret_cast<const uint16_t *>(g) + (lane & 1) * 8 : nullptr;
     }
     return r;
 }
 
-// Byte offset of 16 bytes (chunk 0..3) of a row in a warp's 32 x 64 bytes: no
+// Byte offset of 16 bytes (chunk 0 or 1) of a row in a warp's 32 x 32 bytes: no
 // two of the eight lanes of a phase, by rows or by chunks, meet in a bank.
-__device__ __forceinline__ int turn_at(int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); }
+__device__ __forceinline__ int turn_at(int row, int chunk) { return row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4); }
 
-struct GateGroup {
-    uint4 v[4];
+// The gates of 32 channels of the warp's rows, as they are read.
+struct Gates {
+    uint4 v[2][2];
 };
 
-__device__ __forceinline__ GateGroup ask_gate(const RowsOut &r, int d) {
-    GateGroup g;
+__device__ __forceinline__ Gates ask_gates(const RowsOut &r, int d) {
+    Gates g;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        g.v[k] = r.gate[k] != nullptr ? *reinterpret_cast<const uint4 *>(r.gate[k] + d) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            g.v[i][k] = r.gate[k] != nullptr ? *reinterpret_cast<const uint4 *>(r.gate[k] + d + 16 * i) : make_uint4(0, 0, 0, 0);
     return g;
 }
 
 // 32 channels from d of the warp's rows: lane i's x of row i scaled, gated,
 // rounded, written.
-__device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, const RowOut &o, bool gated,
-                                            const GateGroup &gate, int d, const float *x, float f) {
+__device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, const RowOut &o, bool gated, const Gates &gates,
+                                            int d, const float *x, float f) {
     const int lane = threadIdx.x & 31;
-    if (gated) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4 *>(turn + turn_at(8 * k + (lane >> 2), lane & 3)) = gate.v[k];
+    for (int h = 0; h < 2; ++h) {
+        if (gated) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4 *>(turn + turn_at(16 * k + (lane >> 1), lane & 1)) = gates.v[h][k];
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint4 *at = reinterpret_cast<uint4 *>(turn + turn_at(lane, i));
+            const float *xs = x + 16 * h + 8 * i;
+            float y[8];
+            if (gated) {
+                float g[8];
+                attn::unpack8(*at, g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = xs[k] * f * rcp_fast(1.0f + exp_fast(-g[k]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = xs[k] * f;
+            }
+            const uint4 w = attn::pack8(y);
+            *at = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (r.out[k] != nullptr)
+                *reinterpret_cast<uint4 *>(r.out[k] + d + 16 * h) =
+                    *reinterpret_cast<const uint4 *>(turn + turn_at(16 * k + (lane >> 1), lane & 1));
         __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint4 *at = reinterpret_cast<uint4 *>(turn + turn_at(lane, i));
-        float y[8];
-        if (gated) {
-            float g[8];
-            attn::unpack8(*at, g);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k] * f * rcp_fast(1.0f + exp_fast(-g[k]));
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k] * f;
-        }
-        const uint4 w = attn::pack8(y);
-        *at = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (r.out[k] != nullptr)
-            *reinterpret_cast<uint4 *>(r.out[k] + d) =
-                *reinterpret_cast<const uint4 *>(turn + turn_at(8 * k + (lane >> 2), lane & 3));
-    __syncwarp();
 }
 
 // The warp's rows that are not finite once more, by the definition.
@@ -206,15 +267,17 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *ring = smem + G::TILES * G::QTILE;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (warp == 0) {
         umma::tmem_alloc(&tmem_slot, 512);
         umma::tmem_relinquish();
     }
     if (threadIdx.x == 32) {
+        dead = 0;
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
@@ -223,9 +286,9 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         mbar_init(&bars.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.p_full[i], 4 * G::HALVES);
             mbar_init(&bars.o_done[i], 1);
-            mbar_init(&bars.o_free[i], 4);
+            mbar_init(&bars.o_free[i], 4 * G::HALVES);
         }
         fence_mbar_init();
     }
@@ -247,82 +310,85 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     auto o_done = [&](int tile, int step) { return &bars.o_done[G::TILES == 2 ? tile : step & 1]; };
     auto o_phase = [&](int step) { return (uint32_t)(G::TILES == 2 ? step & 1 : (step >> 1) & 1); };
 
+    const Waits wait{p.err, &dead};
     Walk w;
     const bool any = w.begin(p.list, blockIdx.x, p.Hkv);
     if (any && warp == G::WARPS) {
-        // ---- loads
-        if (lane == 0) {
+        // ---- loads.  The whole warp goes through the loop, as for the products.
+        if (umma::elect_one()) {
             prefetch_tmap(&q_map);
             prefetch_tmap(&k_map);
             prefetch_tmap(&v_map);
-            Waits wait{p.err};
-            int stage = 0, units = 0;
-            uint32_t phase = 0;
-            auto next_stage = [&]() -> uint8_t * {
-                wait(&bars.empty[stage], phase ^ 1);
-                if (!wait.dead) mbar_expect_tx(&bars.full[stage], G::STAGE);
-                return ring + stage * G::STAGE;
-            };
-            auto stage_done = [&] {
-                if (++stage == G::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            };
-            auto load_keys = [&](int head, int token) {
-                for (int c = 0; c < G::PER_STEP; ++c) {
-                    uint8_t *dst = next_stage();
-                    if (!wait.dead) tma_load_3d(dst, &k_map, c * 64, head, token, &bars.full[stage]);
-                    stage_done();
-                }
-            };
-            auto load_values = [&](int head, int token) {
-                for (int c = 0; c < G::PER_STEP; ++c) {
-                    uint8_t *dst = next_stage();
-                    if (!wait.dead)
-                        for (int i = 0; i < D / 64; ++i)
-                            tma_load_3d(dst + i * (G::VK * 128), &v_map, i * 64, head, token + c * G::VK, &bars.full[stage]);
-                    stage_done();
-                }
-            };
-            auto load_q = [&](const Walk &x) {
-                wait(&bars.q_free, (units & 1) ^ 1);
-                ++units;
-                if (wait.dead) return;
-                mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
-                for (int t = 0; t < G::TILES; ++t)
-                    for (int i = 0; i < D / 64; ++i)
-                        tma_load_3d(smem + t * G::QTILE + i * G::SUB, &q_map, i * 64, x.head * p.G, x.u.a0 + t * p.tpt,
-                                    &bars.q_full);
-            };
-            Walk x = w;   // the keys' walk, a step ahead of the values'
-            int j = x.first;
-            bool more = true;
-            auto load_k = [&] {
-                if (j == x.last) {
-                    more = x.next();
-                    if (!more) return;
-                    j = x.first;
-                }
-                if (j == x.first) load_q(x);
-                load_keys(x.head, x.u.b0 + j * kKeys);
-                ++j;
-            };
-            load_k();
-            do {
-                for (int i = w.first; i < w.last; ++i) {
-                    if (G::TILES == 1 && more) load_k();
-                    load_values(w.head, w.u.b0 + i * kKeys);
-                    if (G::TILES == 2 && more) load_k();
-                }
-            } while (w.next());
-            if (wait.dead)   // let the copies in flight land
-                for (int i = 0; i < G::STAGES; ++i) mbar_try_wait(&bars.full[i], 0);
         }
+        int stage = 0, units = 0;
+        uint32_t phase = 0;
+        auto stage_done = [&] {
+            if (++stage == G::STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        auto load_keys = [&](int head, int token) {
+#pragma unroll
+            for (int c = 0; c < G::PER_STEP; ++c) {
+                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                    mbar_expect_tx(&bars.full[stage], G::STAGE);
+                    tma_load_4d(ring + stage * G::STAGE, &k_map, 0, token, c, head, &bars.full[stage]);
+                }
+                stage_done();
+            }
+        };
+        auto load_values = [&](int head, int token) {
+#pragma unroll
+            for (int c = 0; c < G::PER_STEP; ++c) {
+                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                    mbar_expect_tx(&bars.full[stage], G::STAGE);
+                    tma_load_4d(ring + stage * G::STAGE, &v_map, 0, token + c * G::VK, 0, head, &bars.full[stage]);
+                }
+                stage_done();
+            }
+        };
+        auto load_q = [&](int head, int token) {
+            const bool free = wait(&bars.q_free, (units & 1) ^ 1);
+            ++units;
+            if (free && umma::elect_one()) {
+                mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
+#pragma unroll
+                for (int t = 0; t < G::TILES; ++t)
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        tma_load_3d(smem + t * G::QTILE + i * G::SUB, &q_map, i * 64, head * p.G, token + t * p.tpt,
+                                    &bars.q_full);
+            }
+        };
+        w.uniform();
+        Walk x = w;   // the keys' walk, a step ahead of the values'
+        int j = x.first;
+        bool more = true;
+        auto load_k = [&] {
+            if (j == x.last) {
+                more = __any_sync(0xffffffffu, x.next());
+                if (!more) return;
+                x.uniform();
+                j = x.first;
+            }
+            if (j == x.first) load_q(x.head, x.u.a0);
+            load_keys(x.head, x.u.b0 + j * kKeys);
+            ++j;
+        };
+        load_k();
+        do {
+            w.uniform();
+            for (int i = w.first; i < w.last; ++i) {
+                if (G::TILES == 1 && more) load_k();
+                load_values(w.head, w.u.b0 + i * kKeys);
+                if (G::TILES == 2 && more) load_k();
+            }
+        } while (__any_sync(0xffffffffu, w.next()));
+        if (dead)   // let the copies in flight land
+            for (int i = 0; i < G::STAGES; ++i) mbar_try_wait(&bars.full[i], 0);
     } else if (any && warp == G::WARPS + 1) {
         // ---- products.  The whole warp goes through the loop, so that operands stay uniform; one lane issues.
-        Waits wait{p.err};
-        const bool leader = lane == 0;
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
         int stage = 0, units = 0, step = 0;
         uint32_t phase = 0;
@@ -334,9 +400,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             wait(&bars.full[s], ph);
             umma::fence_after_sync();
         };
-        auto commit = [&](uint64_t *bar) {
-            if (leader) umma::mma_commit(bar);
-        };
+        auto commit = [&](uint64_t *bar) { umma::warp_mma_commit(bar); };
         auto pass = [&](int &s, uint32_t &ph) {
             if (++s == G::STAGES) {
                 s = 0;
@@ -346,29 +410,25 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         // the scores of 64 channels, in stage s, of tile t into buffer buf
         auto scores = [&](int t, int buf, int c, int s) {
             const uint64_t a = d_q + (uint32_t)((t * G::QTILE + c * G::SUB) >> 4), b = d_ring + (uint32_t)(s * (G::STAGE >> 4));
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma::mma_bf16(base + G::S_COL + buf * 128, a + k * 2, b + k * 2, id_s, c > 0 || k > 0);
-            }
+            umma::warp_mma_bf16_k64(base + G::S_COL + buf * 128, a, b, id_s, c > 0);
         };
         // the product of VK of P's keys with their values, in stage s
         auto values = [&](int t, int buf, int c, int s, bool acc) {
             const uint64_t b = d_values + (uint32_t)(s * (G::STAGE >> 4));
-            if (leader) {
 #pragma unroll
-                for (int k = 0; k < G::VK / 16; ++k)
-                    umma::mma_bf16_tmem_a(base + t * D, base + G::S_COL + buf * 128 + c * (G::VK / 2) + k * 8,
-                                          b + k * (2048 >> 4), id_o, acc || c > 0 || k > 0);
-            }
+            for (int k = 0; k < G::VK / 32; ++k)
+                umma::warp_mma_bf16_tmem_a_k32(base + t * D, base + G::S_COL + buf * 128 + c * (G::VK / 2) + k * 16,
+                                               b + k * (4096 >> 4), id_o, acc || c > 0 || k > 0);
         };
+        w.uniform();
         Walk x = w;
         int j = x.first, qstep = 0;
         bool more = true;
         auto enter = [&]() -> bool {   // the next step's scores
             if (j == x.last) {
-                more = x.next();
+                more = __any_sync(0xffffffffu, x.next());
                 if (!more) return false;
+                x.uniform();
                 j = x.first;
             }
             if (j == x.first) wait(&bars.q_full, units++ & 1);
@@ -398,6 +458,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         all_scores();
         int done = 0;   // units whose values are through
         do {
+            w.uniform();
             for (int i = w.first; i < w.last; ++i, ++step) {
                 const bool acc = i > w.first;
                 if (G::TILES == 1) {
@@ -454,51 +515,65 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
             }
             ++done;
-        } while (w.next());
+        } while (__any_sync(0xffffffffu, w.next()));
         // every product is through before the tensor memory goes back
         for (int i = G::TILES == 1 && step > 1 ? step - 2 : step - 1; i < step; ++i)
             for (int t = 0; t < G::TILES; ++t) wait(o_done(t, i), o_phase(i));
     } else if (any) {
-        // ---- softmax and results
-        const int tile = G::TILES == 2 ? warp >> 2 : 0, r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D;
+        // ---- softmax and results.  One tile: two warpgroups, each with half of a step's keys and half of the channels;
+        // the scores stay in registers.  Two tiles: a warpgroup each; the scores are read twice, for their maximum and for
+        // the weights (128 of them in registers do not leave room for the rest).
+        constexpr bool ALONE = G::HALVES == 1;
+        constexpr int COLS = 128 / G::HALVES, DH = D / G::HALVES;
+        const int tile = ALONE ? warp >> 2 : 0, half = ALONE ? 0 : warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D + half * DH;
         uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
-        Waits wait{p.err};
+        const float f2 = fabsf(p.scale2);
+        const bool negative = p.scale2 < 0.0f;
         int step = 0;
         do {
             const RowOut o = row_out<D>(p, w.u, w.head, tile, r);
-            float m = -INFINITY, l = 0.0f;   // m: of the scores in powers of two
+            const bool whole = w.whole(), gated = p.gate.p != nullptr && whole;
+            float m = -INFINITY, l = 0.0f;   // m: of the scores in powers of two; l: of this half's keys
+            if (gated && o.gate != nullptr)   // (on its way to L2 before it is needed)
+                for (int d = half * DH; d < (half + 1) * DH; d += 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(o.gate + d));
             for (int i = w.first; i < w.last; ++i, ++step) {
                 const int buf = G::TILES == 2 ? tile : step & 1;
                 const uint32_t s_at = lanes + G::S_COL + buf * 128;
                 wait(&bars.s_full[buf], G::TILES == 2 ? step & 1 : (step >> 1) & 1);
                 umma::fence_after_sync();
-                float s[4][32];
+                const int lim = o.keys - i * kKeys - half * 64;
+                const bool masked = __any_sync(0xffffffffu, lim < COLS);
+                auto scores_of = [&](float (&s)[32], int c) {   // (after the load)
+                    if (negative) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) umma::tmem_ld32(s_at + c * 32, s[c]);
+                        for (int k = 0; k < 32; ++k) s[k] = -s[k];
+                    }
+                    if (masked) hide(s, lim - c * 32);
+                };
+                float s[2][32], most;
+                umma::tmem_ld32(s_at + half * 64, s[0]);
+                umma::tmem_ld32(s_at + half * 64 + 32, s[1]);
                 umma::tmem_ld_wait();
-                const int lim = o.keys - i * kKeys;
-                if (p.scale2 < 0.0f) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[c][k] = -s[c][k];
+                scores_of(s[0], 0);
+                scores_of(s[1], 1);
+                most = fmaxf(largest(s[0]), largest(s[1]));
+                if (ALONE) {
+                    float x[2][32];
+                    umma::tmem_ld32(s_at + 64, x[0]);
+                    umma::tmem_ld32(s_at + 96, x[1]);
+                    umma::tmem_ld_wait();
+                    scores_of(x[0], 2);
+                    scores_of(x[1], 3);
+                    most = max3(most, largest(x[0]), largest(x[1]));
+                } else {
+                    float *ex = bars.most[step & 1][0];
+                    ex[half * 128 + r] = most;
+                    pair_sync();   // (both halves have read their scores: P may go where they were)
+                    most = fmaxf(ex[r], ex[128 + r]);
                 }
-                if (__any_sync(0xffffffffu, lim < kKeys)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[c][k] = c * 32 + k < lim ? s[c][k] : -INFINITY;
-                }
-                float top[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    top[c] = s[c][0];
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) top[c] = fmaxf(top[c], s[c][k]);
-                }
-                const float f2 = fabsf(p.scale2);
-                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f2;
+                most *= f2;
                 const bool raise = most > m + kRaise;   // (m = -infinity: the first that is seen)
                 if (__any_sync(0xffffffffu, raise)) {
                     const float m1 = raise ? most : m, f = raise ? (m == -INFINITY ? 0.0f : ex2(m - m1)) : 1.0f;
@@ -509,8 +584,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                             wait(o_done(0, step - 1), o_phase(step - 1));   // (two tiles: their scores came after it)
                             umma::fence_after_sync();
                         }
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+                        for (int c = 0; c < DH / 32; ++c) {
                             float x[32];
                             umma::tmem_ld32(o_at + c * 32, x);
                             umma::tmem_ld_wait();
@@ -520,79 +595,83 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    float pk[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float e[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            e[z] = ex2(fmaf(s[c + k / 16][2 * (k % 16) + z], f2, -base));
-                            sum[c / 2 * 2 + z] += e[z];
-                        }
-                        pk[k] = __uint_as_float(attn::pack2(e[0], e[1]));
-                    }
-                    umma::tmem_st32(s_at + c * 16, pk);
+                const float base = m == -INFINITY ? 0.0f : -m;
+                const F2 mul = f2_of(f2, f2), add = f2_of(base, base);
+                F2 sum[2] = {f2_of(0.0f, 0.0f), f2_of(0.0f, 0.0f)};
+                float pk[32];
+                weights(s[0], mul, add, sum[0], pk);
+                weights(s[1], mul, add, sum[1], pk + 16);
+                umma::tmem_st32(s_at + half * 32, pk);
+                if (ALONE) {   // (P of the first 64 keys lies over their scores only)
+                    umma::tmem_ld32(s_at + 64, s[0]);
+                    umma::tmem_ld32(s_at + 96, s[1]);
+                    umma::tmem_ld_wait();
+                    scores_of(s[0], 2);
+                    scores_of(s[1], 3);
+                    weights(s[0], mul, add, sum[0], pk);
+                    weights(s[1], mul, add, sum[1], pk + 16);
+                    umma::tmem_st32(s_at + 32, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 t = parts(add2(sum[0], sum[1]));
+                l += t.x + t.y;
                 umma::tmem_st_wait();
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[buf]);
             }
             // the unit's results
-            const bool whole = w.whole(), gated = p.gate.p != nullptr;
             const int slot = w.slot(blockIdx.x);
-            const float f = 1.0f / l;
             float check = 0.0f;
-            constexpr int BATCH = D / 32 < 4 ? D / 32 : 4;   // groups whose gates are asked for at once
-            GateGroup gates[BATCH];
+            if (!ALONE) {
+                float *ex = bars.most[step & 1][0];
+                ex[half * 128 + r] = l;
+                pair_sync();
+                l = ex[r] + ex[128 + r];
+            }
+            const float f = 1.0f / l;
             const RowsOut rows = rows_out<D>(p, o);
-            auto ask = [&](int b) {
-                if (!gated || !whole) return;
-#pragma unroll
-                for (int c = 0; c < BATCH; ++c) gates[c] = ask_gate(rows, (b * BATCH + c) * 32);
-            };
-            ask(0);
+            Gates gates[2];
+            if (gated) {
+                gates[0] = ask_gates(rows, half * DH);
+                gates[1] = ask_gates(rows, half * DH + 32);
+            }
             wait(o_done(tile, step - 1), o_phase(step - 1));
             umma::fence_after_sync();
+            // (not unrolled: the code would be fetched anew for every tile)
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+                const int d = half * DH + c * 32;
+                float x[32];
+                umma::tmem_ld32(o_at + c * 32, x);
+                umma::tmem_ld_wait();
+                if (c == DH / 32 - 1) {
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.o_free[tile]);
+                }
+                if (whole) {
 #pragma unroll
-            for (int b = 0; b < D / 32 / BATCH; ++b) {
-                if (b > 0) ask(b);
+                    for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
+                    const Gates now = gates[0];
+                    gates[0] = gates[1];
+                    if (gated && c + 2 < DH / 32) gates[1] = ask_gates(rows, d + 64);
+                    write_group(turn, rows, o, gated, now, d, x, f);
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
+                                  ((size_t)slot * (D / 4) + d / 4) * (G::TILES * 128) + tile * 128 + r;
 #pragma unroll
-                for (int cc = 0; cc < BATCH; ++cc) {
-                    const int c = b * BATCH + cc;
-                    float x[32];
-                    umma::tmem_ld32(o_at + c * 32, x);
-                    umma::tmem_ld_wait();
-                    if (c == D / 32 - 1) {
-                        umma::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.o_free[tile]);
-                    }
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
-                        write_group(turn, rows, o, gated, gates[cc], c * 32, x, f);
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
-                                      ((size_t)slot * (D / 4) + c * 8) * (G::TILES * 128) + tile * 128 + r;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[(size_t)k * (G::TILES * 128)] =
-                                make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        dst[(size_t)k * (G::TILES * 128)] =
+                            make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
             }
             if (whole) {
-                if (p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-                mend_rows<D>(p, o, w.u, w.head, check != 0.0f, 0, D);
-            } else {
+                if (half == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+                mend_rows<D>(p, o, w.u, w.head, check != 0.0f, half * DH, (half + 1) * DH);
+            } else if (half == 0) {
                 p.part_ml[(size_t)slot * (G::TILES * 128) + tile * 128 + r] = make_float2(m, l);
             }
+            if (!ALONE) pair_sync();   // (the exchange's readers)
         } while (w.next());
         umma::fence_before_sync();
     }
@@ -607,16 +686,16 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ct
     constexpr int ROWS = Geo<D>::TILES * 128;
     __shared__ __align__(16) uint8_t turn[4][Geo<D>::TURN];
     attn::grid_dep_enter();
-    const Parts parts = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
-    if (parts.n == 0) return;
+    const Parts part = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
+    if (part.n == 0) return;
     const int tile = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32), r = threadIdx.x, row = tile * 128 + r;
-    const RowOut o = row_out<D>(p, parts.u, parts.head, tile, r);
+    const RowOut o = row_out<D>(p, part.u, part.head, tile, r);
     const RowsOut rows = rows_out<D>(p, o);
-    const GateGroup gate = ask_gate(rows, c * 32);
+    const Gates gates = ask_gates(rows, c * 32);
     float m = -INFINITY, l = 0.0f, x[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] = 0.0f;
-    for (int i = 0; i < parts.n; ++i) {
+    for (int i = 0; i < part.n; ++i) {
         const size_t slot = 2 * (size_t)(blockIdx.x + i) + (i == 0 ? 1 : 0);
         const float2 ml = p.part_ml[slot * ROWS + row];
         const float4 *src = reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + c * 8) * ROWS + row;
@@ -636,9 +715,9 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ct
     float check = 0.0f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
-    write_group(turn[threadIdx.x >> 5], rows, o, p.gate.p != nullptr, gate, c * 32, x, f);
+    write_group(turn[threadIdx.x >> 5], rows, o, p.gate.p != nullptr, gates, c * 32, x, f);
     if (c == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-    mend_rows<D>(p, o, parts.u, parts.head, check != 0.0f, c * 32, c * 32 + 32);
+    mend_rows<D>(p, o, part.u, part.head, check != 0.0f, c * 32, c * 32 + 32);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -647,7 +726,7 @@ int tiles_of(int D) { return D <= 128 ? 2 : 1; }
 
 PromptList list_of(const PromptSizes &s) {
     const int tpt = 128 / (s.Hq / s.Hkv);
-    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4};
+    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4, 2};
 }
 
 struct Workspace {
@@ -663,12 +742,23 @@ Workspace workspace(const PromptSizes &s) {
     return w;
 }
 
-// [rows, H, D] as (channels, heads, tokens) in boxes of 64 channels.
-bool heads_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_heads, int box_tokens) {
+long long head_stride(const HeadsIn &x, int H, int D) { return H > 1 ? x.hs : D; }
+long long token_stride(const HeadsIn &x, long long rows, int H, int D) { return rows > 1 ? x.ts : (long long)H * D; }
+
+// [rows, H, D] as (64 channels, heads, tokens): boxes of one tile's rows.
+bool queries_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_heads, int box_tokens) {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows};
-    const uint64_t strides[2] = {(uint64_t)(H > 1 ? x.hs : D) * 2, (uint64_t)(rows > 1 ? x.ts : (long long)H * D) * 2};
+    const uint64_t strides[2] = {(uint64_t)head_stride(x, H, D) * 2, (uint64_t)token_stride(x, rows, H, D) * 2};
     const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_tokens};
     return encode_tmap_strided(map, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ... as (64 channels, tokens, groups of 64 channels, heads): boxes of one head's tokens, groups one after the other.
+bool keys_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_tokens, int box_groups) {
+    const uint64_t dims[4] = {64, (uint64_t)rows, (uint64_t)(D / 64), (uint64_t)H};
+    const uint64_t strides[3] = {(uint64_t)token_stride(x, rows, H, D) * 2, 128, (uint64_t)head_stride(x, H, D) * 2};
+    const uint32_t box[4] = {64, (uint32_t)box_tokens, (uint32_t)box_groups, 1};
+    return encode_tmap_strided(map, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D>
@@ -681,9 +771,9 @@ cudaError_t launch_d(const PromptSizes &s, Params &p, cudaStream_t st) {
     // (no keys: nothing of what is loaded counts, but a map needs a tensor)
     const bool none = s.Nk == 0;
     const HeadsIn dummy{p.q.p, 0, 0};
-    if (!heads_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) ||
-        !heads_map(&k, none ? dummy : p.k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, 1, kKeys) ||
-        !heads_map(&v, none ? dummy : p.v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, 1, G::VK))
+    if (!queries_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) ||
+        !keys_map(&k, none ? dummy : p.k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kKeys, 1) ||
+        !keys_map(&v, none ? dummy : p.v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, G::VK, D / 64))
         return cudaErrorInvalidValue;
     const int ctas = num_sms();
     e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, p);

@@ -19,7 +19,7 @@ struct ListParams {
     int *seq_first;    // [B + 1]: a sequence's first unit
     int keys;          // tiles of keys, steps of queries; or the other way round
     int tile, step;    // tokens
-    int ctas, heads, least;   // least: steps of a share
+    int ctas, heads, least, blank;   // least: steps of a share
 };
 
 struct PlanParams {
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
             unit = make_unit(load_seq(p.s, s), (int)u - (B <= kCached ? first_cached[s] : l.seq_first[s]), l);
         }
         long long sum;
-        unit.pre = total + block_scan((long long)unit.steps, sums, sum);
+        unit.pre = total + block_scan(u < units ? (long long)unit.steps + l.blank : 0, sums, sum);
         if (u < units) {
             l.unit[u] = unit;
             if (u < kCached) cached[u] = unit.pre;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
     const long long all = total * l.heads;
     long long share = (all + l.ctas - 1) / l.ctas;
     if (share < l.least) share = l.least;
-    if (tid == 0) *l.header = Header{total, share, (int)units, 0, 0};
+    if (tid == 0) *l.header = Header{total, share, (int)units, l.blank, 0};
     for (int c = tid; c < l.ctas; c += kThreads) {
         const long long x = share * c;
         if (x >= all) break;
@@ -192,7 +192,7 @@ cudaError_t launch_prompt_plan(const PromptSizes &s, const PromptSeqs &q, const 
         const List a = prompt_list_at(s, l, ws[i]);
         char *end = static_cast<char *>(ws[i]) + prompt_list_bytes(s, l) - up256(sizeof(int) * ((size_t)s.B + 1));
         p.l[i] = ListParams{a.header, a.start, a.unit, reinterpret_cast<int *>(end), l.keys ? 1 : 0, l.tile, l.step,
-                            l.ctas, s.Hkv, l.least};
+                            l.ctas, s.Hkv, l.least, l.blank};
     }
     return DependentLaunch(dim3(n), dim3(kThreads), 0, st)(prompt_plan_kernel, p);
 }

@@ -79,6 +79,55 @@ __device__ __forceinline__ void fence_after_sync() {
 }
 
 // ---------------------------------------------------------------------------
+// Issue by a whole warp: one lane is elected inside each block, so the code
+// around it stays convergent and operands stay in uniform registers.  (Issued
+// under a test of the lane number, each product costs the issuing thread some
+// 85 cycles, more than an M = N = 128 product takes.)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+#define GDN_UMMA_WARP_BEGIN                                                                            \
+    "{\n\t.reg .pred w, p, t;\n\t.reg .b64 b;\n\telect.sync _|w, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t" \
+    "setp.eq.b32 t, 0, 0;\n\t"
+
+// K = 64 (four instructions) of A and B in one 128-byte-swizzled tile each.
+__device__ __forceinline__ void warp_mma_bf16_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(GDN_UMMA_WARP_BEGIN
+                 ".reg .b64 a;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                 "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                 "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+                 : "memory");
+}
+
+// K = 32 of A in tensor memory (16 columns) and a transposed B (rows of K).
+__device__ __forceinline__ void warp_mma_bf16_tmem_a_k32(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(GDN_UMMA_WARP_BEGIN
+                 ".reg .b32 a;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 128;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void warp_mma_commit(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred w;\n\telect.sync _|w, 0xffffffff;\n\t"
+        "@w tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // MMA issue (one thread) and completion
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, bool acc) {
