@@ -194,6 +194,21 @@ def gdn_attn_prefill(dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse,
     _bind().attn_prefill(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, False, workspace, _handle(stream))
 
 
+def gdn_attn_prefill_backward_workspace_size(dims, q_rows, k_rows, gated) -> int:
+    return int(lib().gdn_attn_prefill_backward_workspace_size(ctypes.byref(_dims(dims)), int(q_rows), int(k_rows),
+                                                              int(bool(gated))))
+
+
+def gdn_attn_prefill_backward(dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, dout, dq, dk, dv, dgate,
+                              workspace, stream=None):
+    _given("gdn_attn_prefill_backward", dq=dq, dk=dk, dv=dv, workspace=workspace)
+    if gate is not None:
+        _given("gdn_attn_prefill_backward", dgate=dgate)
+    c = _dims(dims)
+    _bind().attn_prefill_backward(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, dout, dq, dk, dv, dgate,
+                                  workspace, _handle(stream))
+
+
 # ---------------------------------------------------------------------------
 # allocating conveniences
 # ---------------------------------------------------------------------------
@@ -246,3 +261,14 @@ def attn_prefill(dims, q, k, v, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=N
     c = _dims(dims)
     return _bind().attn_prefill(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, dims.D ** -0.5 if scale is None else scale,
                                 None, None, bool(return_lse), workspace, _handle(stream))
+
+
+def attn_prefill_backward(dims, q, k, v, out, lse, dout, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=None, scale=None,
+                          workspace=None, stream=None):
+    """Gradients of attn_prefill, from its inputs, its results out and lse, and
+    the gradient of out; returns a dict dq, dk, dv and, with a gate, dgate (bf16)."""
+    c = _dims(dims)
+    dq, dk, dv, dgate = _bind().attn_prefill_backward(
+        _at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, dims.D ** -0.5 if scale is None else scale, out, lse, dout, None, None,
+        None, None, workspace, _handle(stream))
+    return {"dq": dq, "dk": dk, "dv": dv} if dgate is None else {"dq": dq, "dk": dk, "dv": dv, "dgate": dgate}

@@ -71,6 +71,14 @@ gdn_status check_prompt(const gdn_attn_dims *d, int64_t q_rows, int64_t k_rows, 
     return GDN_OK;
 }
 
+gdn_status check_prompt_heads(const PromptSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v, const HeadsIn &gate) {
+    gdn_status st = check_rows(q, s.Nq, s.Hq);
+    if (st == GDN_OK) st = check_rows(k, s.Nk, s.Hkv);
+    if (st == GDN_OK) st = check_rows(v, s.Nk, s.Hkv);
+    if (st == GDN_OK && gate.p != nullptr) st = check_rows(gate, s.Nq, s.Hq);
+    return st;
+}
+
 bool ok_sequences(const PromptSizes &s, const PromptSeqs &q) {
     if (!ok(q.cu_q, 0, 4) || !ok(q.cu_k, 0, 4) || !ok(q.n_q, 0, 4) || !ok(q.n_k, 0, 4)) return false;
     return s.B == 0 || ((q.cu_q != nullptr || s.Nq % s.B == 0) && (q.cu_k != nullptr || s.Nk % s.B == 0));
@@ -232,10 +240,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, int64_t k
     const HeadsIn hq{q, q_token_stride, q_head_stride}, hk{k, k_token_stride, k_head_stride},
         hv{v, v_token_stride, v_head_stride}, hg{gate, gate_token_stride, gate_head_stride};
     const gdn::PromptSeqs seqs{cu_q, cu_k, n_q, n_k};
-    st = gdn::check_rows(hq, s.Nq, s.Hq);
-    if (st == GDN_OK) st = gdn::check_rows(hk, s.Nk, s.Hkv);
-    if (st == GDN_OK) st = gdn::check_rows(hv, s.Nk, s.Hkv);
-    if (st == GDN_OK && gate != nullptr) st = gdn::check_rows(hg, s.Nq, s.Hq);
+    st = gdn::check_prompt_heads(s, hq, hk, hv, hg);
     if (st != GDN_OK) return st;
     if (!gdn::ok_sequences(s, seqs) || !gdn::ok(out, (size_t)s.Nq) || !gdn::ok(lse, 0, 4) || !isfinite(scale))
         return GDN_ERR_INVALID_ARG;
@@ -245,6 +250,43 @@ gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, int64_t k
     if (err == nullptr) return GDN_ERR_CUDA;
     return gdn::from(gdn::launch_attn_prefill(s, hq, hk, hv, seqs, hg, scale, out, lse, workspace, err,
                                               (cudaStream_t)stream));
+}
+
+size_t gdn_attn_prefill_backward_workspace_size(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows, int32_t gated) {
+    gdn::PromptSizes s;
+    if (gdn::check_prompt(dims, q_rows, k_rows, &s) != GDN_OK) return 0;
+    return gdn::attn_prefill_backward_workspace(s, gated != 0);
+}
+
+gdn_status gdn_attn_prefill_backward(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows, const uint16_t *q,
+                                     int64_t q_token_stride, int64_t q_head_stride, const uint16_t *k,
+                                     int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
+                                     int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
+                                     const int32_t *cu_k, const int32_t *n_q, const int32_t *n_k, const uint16_t *gate,
+                                     int64_t gate_token_stride, int64_t gate_head_stride, float scale,
+                                     const uint16_t *out, const float *lse, const uint16_t *dout, uint16_t *dq,
+                                     uint16_t *dk, uint16_t *dv, uint16_t *dgate, void *workspace, size_t ws_bytes,
+                                     gdn_stream stream) {
+    gdn::PromptSizes s;
+    gdn_status st = gdn::check_prompt(dims, q_rows, k_rows, &s);
+    if (st != GDN_OK) return st;
+    const HeadsIn hq{q, q_token_stride, q_head_stride}, hk{k, k_token_stride, k_head_stride},
+        hv{v, v_token_stride, v_head_stride}, hg{gate, gate_token_stride, gate_head_stride};
+    const gdn::PromptSeqs seqs{cu_q, cu_k, n_q, n_k};
+    st = gdn::check_prompt_heads(s, hq, hk, hv, hg);
+    if (st != GDN_OK) return st;
+    const size_t nq = (size_t)s.Nq, nk = (size_t)s.Nk;
+    if (!gdn::ok_sequences(s, seqs) || !gdn::ok(out, nq) || !gdn::ok(lse, nq, 4) || !gdn::ok(dout, nq) ||
+        !gdn::ok(dq, nq) || !gdn::ok(dk, nk) || !gdn::ok(dv, nk) || !isfinite(scale))
+        return GDN_ERR_INVALID_ARG;
+    if (gate != nullptr ? !gdn::ok(dgate, nq) : dgate != nullptr) return GDN_ERR_INVALID_ARG;
+    if ((nq == 0 && nk == 0) || s.B == 0) return GDN_OK;
+    if (!gdn::ok(workspace, 1) || ws_bytes < gdn::attn_prefill_backward_workspace(s, gate != nullptr))
+        return GDN_ERR_INVALID_ARG;
+    unsigned *err = gdn::device_error_word();
+    if (err == nullptr) return GDN_ERR_CUDA;
+    return gdn::from(gdn::launch_attn_prefill_backward(s, hq, hk, hv, seqs, hg, scale, out, lse, dout, dq, dk, dv, dgate,
+                                                       workspace, err, (cudaStream_t)stream));
 }
 
 }  // extern "C"

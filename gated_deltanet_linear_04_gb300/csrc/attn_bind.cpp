@@ -428,6 +428,16 @@ struct Prompt {
         n_q = index_arg(c, nq, d.B, "n_q", true);
         n_k = index_arg(c, nk, d.B, "n_k", true);
     }
+    at::Tensor like_k(Call &c, PyObject *o, const gdn_attn_dims &d, const char *name) const {
+        return k.t >= 0 ? c.output(o, at::kBFloat16, {d.B, k.t, d.Hkv, d.D}, name)
+                        : c.output(o, at::kBFloat16, {k.n, d.Hkv, d.D}, name);
+    }
+    // a dense input of q's rows
+    void *dense_q(Call &c, PyObject *o, const gdn_attn_dims &d, at::ScalarType type, bool channels, const char *name) const {
+        if (channels)
+            return q.t >= 0 ? c.dense(o, type, {d.B, d.T, d.Hq, d.D}, name) : c.dense(o, type, {q.n, d.Hq, d.D}, name);
+        return q.t >= 0 ? c.dense(o, type, {d.B, d.T, d.Hq}, name) : c.dense(o, type, {q.n, d.Hq}, name);
+    }
     // a tensor of q's rows
     at::Tensor like_q(Call &c, PyObject *o, const gdn_attn_dims &d, const char *name) const {
         return q.t >= 0 ? c.output(o, at::kBFloat16, {d.B, d.T, d.Hq, d.D}, name)
@@ -471,6 +481,40 @@ PyObject *attn_prefill(PyObject *const *a) {
     return lse.defined() && a[12] == Py_True ? pair(out, lse) : THPVariable_Wrap(out);
 }
 
+// (dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, dout, dq, dk, dv, dgate, workspace, stream)
+// -> (dq, dk, dv, dgate or None)
+PyObject *attn_prefill_backward(PyObject *const *a) {
+    const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
+    Call c("gdn_attn_prefill_backward", a[18]);
+    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+    const Call::Heads gate = gate_arg(c, d, p, a[8]);
+    const bool gated = a[8] != Py_None;
+    const double scale = number(a[9]);
+    const auto *out = static_cast<uint16_t *>(p.dense_q(c, a[10], d, at::kBFloat16, true, "out"));
+    const auto *lse = static_cast<float *>(p.dense_q(c, a[11], d, at::kFloat, false, "lse"));
+    const auto *dout = static_cast<uint16_t *>(p.dense_q(c, a[12], d, at::kBFloat16, true, "dout"));
+    if (!gated && a[16] != Py_None) raise(PyExc_ValueError, "dgate goes with gate");
+    const at::Tensor dq = p.like_q(c, a[13], d, "dq"), dk = p.like_k(c, a[14], d, "dk"), dv = p.like_k(c, a[15], d, "dv");
+    at::Tensor dgate;
+    if (gated) dgate = p.like_q(c, a[16], d, "dgate");
+    Scratch ws;
+    if (a[17] != Py_None)
+        ws.given(c, a[17]);
+    else if ((p.q.n > 0 || p.k.n > 0) && d.B > 0)
+        ws.make(c, gdn_attn_prefill_backward_workspace_size(&d, p.q.n, p.k.n, gated));
+    c.done(gdn_attn_prefill_backward(&d, p.q.n, p.k.n, p.q.h.p, p.q.h.ts, p.q.h.hs, p.k.h.p, p.k.h.ts, p.k.h.hs, p.v.h.p,
+                                     p.v.h.ts, p.v.h.hs, p.cu_q, p.cu_k, p.n_q, p.n_k, gate.p, gate.ts, gate.hs,
+                                     (float)scale, out, lse, dout, bf16(dq), bf16(dk), bf16(dv),
+                                     gate.p != nullptr ? bf16(dgate) : nullptr, ws.p, ws.bytes, (gdn_stream)c.stream()));
+    PyObject *t = PyTuple_New(4);
+    if (t == nullptr) throw Raised();
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(dq));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(dk));
+    PyTuple_SET_ITEM(t, 2, THPVariable_Wrap(dv));
+    PyTuple_SET_ITEM(t, 3, gated ? THPVariable_Wrap(dgate) : Py_NewRef(Py_None));
+    return t;
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -494,7 +538,7 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(qk_norm_rope, 11), ENTRY(qk_norm_rope_backward, 16), ENTRY(kv_append, 13),
-                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13), ENTRY(attn_prefill, 15),
+                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13), ENTRY(attn_prefill, 15), ENTRY(attn_prefill_backward, 19),
                          {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_attn_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -250,4 +250,10 @@ cudaError_t launch_attn_prefill(const PromptSizes &s, const HeadsIn &q, const He
                                 const PromptSeqs &seqs, const HeadsIn &gate, float scale, uint16_t *out, float *lse,
                                 void *ws, unsigned *err, cudaStream_t st);
 
+size_t attn_prefill_backward_workspace(const PromptSizes &s, bool gated);
+cudaError_t launch_attn_prefill_backward(const PromptSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                                         const PromptSeqs &seqs, const HeadsIn &gate, float scale, const uint16_t *out,
+                                         const float *lse, const uint16_t *dout, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                                         uint16_t *dgate, void *ws, unsigned *err, cudaStream_t st);
+
 }  // namespace gdn

@@ -1,0 +1,893 @@
+// Gradients of a prompt's attention (prompt_fwd.cu).  With P = exp(scale S -
+// lse), dO the output's gradient (times the gate), delta = rowsum(dO O):
+//   dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = scale dS K,  dK = scale dS^T Q,  dgate = dout out (1 - sigmoid(gate)).
+// P and dS are rounded to bf16 for their products, as the other operands are.
+//
+// 10 D operations per seen (query head, key) are needed: bound by the tensor
+// cores.  Here a tile of 128 rows (queries of a key head's group, or keys) stays
+// in a CTA and the others pass by in steps of 64 rows: one kernel accumulates
+// dQ, others dK and dV, so that every sum is in a fixed order in one
+// accumulator, without atomics; S and dP are computed twice (14 D; with 256
+// channels, where dK and dV do not fit the tensor memory together, S three
+// times: 16 D).
+//   - The resident rows are A operands in tensor memory (with 256 channels the
+//     second one lies in shared memory): a product of 128 x 64 with both
+//     operands in shared memory takes 48 clocks for 32 clocks' work (measured),
+//     with A in tensor memory 32.
+//   - A step: S and dP into tensor memory; two warpgroups take 32 columns each
+//     into registers, which frees them for the next step at once, and leave P and
+//     dS as bf16 in shared memory, the A operands of the accumulating products.
+//   - The lists, shares and joins are those of the forward pass (prompt.cuh).
+#include "prompt.cuh"
+#include "umma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace prompt;
+
+enum { kDQ, kDKV, kDK, kDV };
+
+constexpr int kRows = 64;   // of a step
+
+template <int D_, int KIND_>
+struct Geo {
+    static constexpr int D = D_, KIND = KIND_;
+    static constexpr bool KEYS = KIND != kDQ;                       // the resident rows are keys
+    static constexpr bool HAS_DP = KIND != kDV, HAS_P = KIND == kDKV || KIND == kDV;   // dP needed; P accumulated
+    static constexpr int ACCS = (HAS_DP ? 1 : 0) + (HAS_P ? 1 : 0);
+    static constexpr bool A2_SMEM = D == 256 && HAS_DP;
+    static constexpr int A1_COL = ACCS * D, A2_COL = A1_COL + D / 2, S_COL = HAS_DP && !A2_SMEM ? A2_COL + D / 2 : A2_COL;
+    static_assert(S_COL + 128 <= 512, "");
+    static constexpr int SUB = kRows * 128;                         // bytes of 64 rows of 64 channels
+    static constexpr int STAGE = D / 64 * SUB;
+    static constexpr int N1 = D == 256 ? (KIND == kDV ? 2 : 3) : 4, N2 = D == 256 ? (KIND == kDV ? 3 : 1) : 4;
+    static constexpr int XTILE = 128 * 128, XT = ACCS, XB = A2_SMEM ? 1 : 2;   // 128 rows of 64 bf16; tiles; buffers
+    static constexpr int A2_BYTES = A2_SMEM ? 128 * D * 2 : 0;
+    static constexpr int WARPS = 8, TURN = 32 * 32;
+    static constexpr int THREADS = 32 * (WARPS + 2 + (KEYS ? 1 : 0));
+    static constexpr int X_AT = A2_BYTES, RING1 = X_AT + XB * XT * XTILE, RING2 = RING1 + N1 * STAGE,
+                         TURN_AT = RING2 + N2 * STAGE, SMEM = TURN_AT + WARPS * TURN + 1024;
+    static_assert(SMEM + 4608 <= 227 * 1024, "");
+};
+
+constexpr int kStats = 4;   // steps of row statistics in shared memory
+
+struct Params {
+    List list;
+    HeadsIn a1, a2;          // the resident rows
+    const uint16_t *out, *dout;
+    HeadsIn q, k, v, d_o;    // for rows that are done once more
+    float scale, scale2;
+    const float *lse;
+    float *delta;
+    uint16_t *acc_out[2];
+    float *part;             // [slot][acc][D / 4][128][4]
+    unsigned *err;
+    int Hq, Hkv, G, tile, tps;   // tile: tokens of a resident tile; tps: of a step
+};
+
+struct Bars {
+    uint64_t full1[4], empty1[4], full2[4], empty2[4], a_full, s_full, s_free, x_full[2], x_free[2], acc_done, acc_free;
+    uint64_t stats_full[kStats], stats_free[kStats];
+};
+
+struct Stats {
+    float nlse[kRows], delta[kRows];   // -lse in powers of two (-infinity: no such row)
+    int token[kRows];
+};
+
+struct RowOut {
+    long long at;       // (token, head) of the outputs
+    long long token;
+    int head;
+    bool mine, valid;
+};
+
+template <class G>
+__device__ __forceinline__ RowOut row_out(const Params &p, const Unit &u, int head, int r) {
+    RowOut o;
+    const int t = G::KEYS ? r : r / p.G;
+    o.head = G::KEYS ? head : head * p.G + r - t * p.G;
+    o.mine = t < p.tile && t < u.slot_a;
+    o.valid = t < p.tile && t < u.n_a;
+    o.token = (long long)u.a0 + t;
+    o.at = o.token * (G::KEYS ? p.Hkv : p.Hq) + o.head;
+    return o;
+}
+
+// ---------------------------------------------------------------------------
+// rows by the definition (results that are not finite: what lies in unseen
+// slots must not have entered)
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void lane_row(const HeadsIn &h, long long n, int head, float (&x)[D / 32]) {
+    constexpr int N = D / 32;
+    const uint16_t *q = h.p + n * h.ts + head * h.hs + (threadIdx.x & 31) * N;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(q)[i];
+        x[2 * i] = __uint_as_float(w << 16);
+        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ float row_dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) t = fmaf(a[i], b[i], t);
+    return warp_sum(t);
+}
+
+// One row's dQ (KEYS false: query (token, head), over `n` keys from `first`) or
+// dK / dV (key (token, head), over the queries of `n` tokens from `first`, of
+// which the token i sees it if row <= lim0 + i); channels d0 .. d1 - 1.
+template <int D, bool KEYS>
+__device__ __noinline__ void exact_row(const Params &p, long long token, int head, int first, int n, int row, int lim0,
+                                       bool of_p, uint16_t *out, int d0, int d1) {
+    constexpr int N = D / 32;
+    const int lane = threadIdx.x & 31;
+    float a1[N], a2[N], acc[N];
+    lane_row<D>(p.a1, token, head, a1);
+    if (!KEYS || !of_p) lane_row<D>(p.a2, token, head, a2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    const int heads = KEYS ? p.G : 1;
+    for (int i = 0; i < n; ++i) {
+        if (KEYS && row > lim0 + i) continue;
+        for (int g = 0; g < heads; ++g) {
+            const long long q_token = KEYS ? (long long)first + i : token, k_token = KEYS ? token : (long long)first + i;
+            const int qh = KEYS ? head * p.G + g : head, kh = KEYS ? head : head / p.G;
+            float x[N], y[N];
+            lane_row<D>(KEYS ? p.q : p.k, KEYS ? q_token : k_token, KEYS ? qh : kh, x);
+            const float w = expf(row_dot<D>(a1, x) * p.scale - p.lse[q_token * p.Hq + qh]);
+            lane_row<D>(KEYS ? p.d_o : p.v, KEYS ? q_token : k_token, KEYS ? qh : kh, y);
+            if (KEYS && of_p) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) acc[c] = fmaf(w, y[c], acc[c]);
+            } else {
+                const float ds = w * (row_dot<D>(a2, y) - p.delta[q_token * p.Hq + qh]);
+#pragma unroll
+                for (int c = 0; c < N; ++c) acc[c] = fmaf(ds, x[c], acc[c]);
+            }
+        }
+    }
+    const float f = KEYS && of_p ? 1.0f : p.scale;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int d = lane * N + c;
+        if (d >= d0 && d < d1) out[d] = f32_to_bf16(acc[c] * f);
+    }
+}
+
+template <class G>
+__device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, const Unit &u, int row, bool of_p, bool bad,
+                                          uint16_t *out, int d0, int d1) {
+    unsigned todo = __ballot_sync(0xffffffffu, bad && o.mine && o.valid);
+    while (todo != 0) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const long long token = __shfl_sync(0xffffffffu, o.token, src), at = __shfl_sync(0xffffffffu, o.at, src);
+        const int head = __shfl_sync(0xffffffffu, o.head, src), r = __shfl_sync(0xffffffffu, row, src);
+        const int n = G::KEYS ? u.n_b : max(u.lim0 + (int)(token - u.a0), 0);
+        exact_row<G::D, G::KEYS>(p, token, head, u.b0, n, r, u.lim0, of_p, out + at * G::D, d0, d1);
+    }
+}
+
+// 32 channels from d of the warp's rows, scaled and rounded (0 for rows that
+// are padding).
+template <int D>
+__device__ __forceinline__ void write_group(uint8_t *turn, uint16_t *const (&rows)[2], bool valid, int d, const float *x,
+                                            float f) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[16 * h + 8 * i + k] * f;
+            const uint4 w = attn::pack8(y);
+            *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = valid ? w : make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (rows[k] != nullptr)
+                *reinterpret_cast<uint4 *>(rows[k] + d + 16 * h) =
+                    *reinterpret_cast<const uint4 *>(turn + turn_at(16 * k + (lane >> 1), lane & 1));
+        __syncwarp();
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void rows_out(const RowOut &o, uint16_t *out, uint16_t *(&rows)[2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int src = 16 * k + (lane >> 1);
+        const long long at = __shfl_sync(0xffffffffu, o.at, src);
+        const bool mine = __shfl_sync(0xffffffffu, (int)o.mine, src);
+        rows[k] = mine ? out + at * D + (lane & 1) * 8 : nullptr;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the pass
+// ---------------------------------------------------------------------------
+template <class G>
+__global__ void __launch_bounds__(G::THREADS, 1)
+prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const Params p) {
+    constexpr int D = G::D;
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
+    __shared__ __align__(16) Stats stats[G::KEYS ? kStats : 1];
+    __shared__ float swap[G::KEYS ? 1 : 256];   // deltas of a tile of one step: [half][row]
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        umma::tmem_alloc(&tmem_slot, 512);
+        umma::tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        dead = 0;
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.full1[i], 1);
+            mbar_init(&bars.empty1[i], 1);
+            mbar_init(&bars.full2[i], 1);
+            mbar_init(&bars.empty2[i], 1);
+        }
+        mbar_init(&bars.a_full, 8);
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.s_free, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.x_full[i], 8);
+            mbar_init(&bars.x_free[i], 1);
+        }
+        mbar_init(&bars.acc_done, 1);
+        mbar_init(&bars.acc_free, 8);
+        for (int i = 0; i < kStats; ++i) {
+            mbar_init(&bars.stats_full[i], 1);
+            mbar_init(&bars.stats_free[i], 8);
+        }
+        fence_mbar_init();
+    }
+    if (G::KEYS) {   // rows of a step that no token has: zeros, never written again
+        const int used = p.tps * p.G, rows = kRows - used;
+        for (int i = threadIdx.x; i < (G::N1 + G::N2) * (D / 64) * rows * 8; i += G::THREADS) {
+            const int c = i & 7, r = i >> 3;
+            *reinterpret_cast<uint4 *>(smem + G::RING1 + r / rows * G::SUB + (used + r % rows) * 128 + c * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+    }
+    fence_proxy_async_smem();
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    attn::grid_dep_enter();
+
+    const Waits wait{p.err, &dead};
+    Walk w;
+    const bool any = w.begin(p.list, blockIdx.x, p.Hkv);
+    if (any && warp == G::WARPS) {
+        // ---- loads
+        if (umma::elect_one()) {
+            prefetch_tmap(&map1);
+            prefetch_tmap(&map2);
+        }
+        int s1 = 0, s2 = 0;
+        uint32_t ph1 = 0, ph2 = 0;
+        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int head, int token) {
+            if (G::KEYS) {
+                mbar_expect_tx(bar, (uint32_t)(D * 2 * p.tps * p.G));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) tma_load_3d(dst + i * G::SUB, map, i * 64, head * p.G, token, bar);
+            } else {
+                mbar_expect_tx(bar, G::STAGE);
+                tma_load_4d(dst, map, 0, token, 0, head, bar);
+            }
+        };
+        do {
+            w.uniform();
+            for (int i = w.first; i < w.last; ++i) {
+                const int token = w.u.b0 + i * p.tps;
+                if (wait(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
+                    load(&map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token);
+                if (++s1 == G::N1) {
+                    s1 = 0;
+                    ph1 ^= 1;
+                }
+                if (wait(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
+                    load(&map2, smem + G::RING2 + s2 * G::STAGE, &bars.full2[s2], w.head, token);
+                if (++s2 == G::N2) {
+                    s2 = 0;
+                    ph2 ^= 1;
+                }
+            }
+        } while (__any_sync(0xffffffffu, w.next()));
+        if (dead)   // let the copies in flight land
+            for (int i = 0; i < 4; ++i) {
+                mbar_try_wait(&bars.full1[i], 0);
+                mbar_try_wait(&bars.full2[i], 0);
+            }
+    } else if (any && warp == G::WARPS + 1) {
+        // ---- products
+        const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), at = smem_u32(smem);
+        constexpr uint32_t id_s = umma::idesc(128, kRows, umma::kFmtBF16);
+        constexpr uint32_t id_a = umma::idesc(128, D, umma::kFmtBF16) | umma::kBTransposed;
+        const uint64_t d_b1 = umma::desc_sw128(at + G::RING1), d_b2 = umma::desc_sw128(at + G::RING2);
+        const uint64_t d_t1 = umma::desc_sw128_mn(at + G::RING1, G::SUB), d_t2 = umma::desc_sw128_mn(at + G::RING2, G::SUB);
+        const uint64_t d_x = umma::desc_sw128(at + G::X_AT), d_a2 = umma::desc_sw128(at);
+        int s1 = 0, s2 = 0, t1 = 0, t2 = 0, step = 0, units = 0, done = 0;   // s: of the scores, t: of the accumulating products
+        uint32_t ph1 = 0, ph2 = 0;
+        bool acc = false, last = false;
+        // the products into the accumulators of the step before
+        auto accumulate = [&](int x) {
+            const int xb = x % G::XB;
+            wait(&bars.x_full[xb], (x / G::XB) & 1);
+            if (!acc && done > 0) wait(&bars.acc_free, (done - 1) & 1);
+            umma::fence_after_sync();
+            const uint64_t a = d_x + (uint32_t)(xb * G::XT * (G::XTILE >> 4));
+            if (G::HAS_DP) {
+                umma::warp_mma_bf16_k64_bt(base, a, d_t1 + (uint32_t)(t1 * (G::STAGE >> 4)), id_a, acc);
+                umma::warp_mma_commit(&bars.empty1[t1]);
+                if (++t1 == G::N1) t1 = 0;
+            }
+            if (G::HAS_P) {
+                umma::warp_mma_bf16_k64_bt(base + (G::HAS_DP ? D : 0), a + (G::HAS_DP ? G::XTILE >> 4 : 0),
+                                           d_t2 + (uint32_t)(t2 * (G::STAGE >> 4)), id_a, acc);
+                umma::warp_mma_commit(&bars.empty2[t2]);
+                if (++t2 == G::N2) t2 = 0;
+            }
+            umma::warp_mma_commit(&bars.x_free[xb]);
+            acc = true;
+            if (last) {
+                umma::warp_mma_commit(&bars.acc_done);
+                ++done;
+                acc = false;
+            }
+        };
+        do {
+            w.uniform();
+            wait(&bars.a_full, units++ & 1);
+            for (int i = w.first; i < w.last; ++i, ++step) {
+                if (step > 0) wait(&bars.s_free, (step - 1) & 1);
+                wait(&bars.full1[s1], ph1);
+                umma::fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    umma::warp_mma_bf16_tmem_a_k64(base + G::S_COL, base + G::A1_COL + c * 32,
+                                                   d_b1 + (uint32_t)((s1 * G::STAGE + c * G::SUB) >> 4), id_s, c > 0);
+                if (!G::HAS_DP) umma::warp_mma_commit(&bars.empty1[s1]);
+                if (++s1 == G::N1) {
+                    s1 = 0;
+                    ph1 ^= 1;
+                }
+                wait(&bars.full2[s2], ph2);
+                umma::fence_after_sync();
+                if (G::HAS_DP) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint64_t b = d_b2 + (uint32_t)((s2 * G::STAGE + c * G::SUB) >> 4);
+                        if (G::A2_SMEM)
+                            umma::warp_mma_bf16_k64(base + G::S_COL + 64, d_a2 + (uint32_t)(c * ((128 * 128) >> 4)), b, id_s, c > 0);
+                        else
+                            umma::warp_mma_bf16_tmem_a_k64(base + G::S_COL + 64, base + G::A2_COL + c * 32, b, id_s, c > 0);
+                    }
+                    if (!G::HAS_P) umma::warp_mma_commit(&bars.empty2[s2]);
+                }
+                if (++s2 == G::N2) {
+                    s2 = 0;
+                    ph2 ^= 1;
+                }
+                umma::warp_mma_commit(&bars.s_full);
+                if (step > 0) accumulate(step - 1);
+                last = i + 1 == w.last;
+            }
+        } while (__any_sync(0xffffffffu, w.next()));
+        accumulate(step - 1);
+        wait(&bars.acc_done, (done - 1) & 1);   // every product is through before the tensor memory goes back
+    } else if (G::KEYS && any && warp == G::WARPS + 2) {
+        // ---- the statistics of the rows that pass by
+        int st = 0;
+        uint32_t ph = 0;
+        int t[2], g[2];
+        for (int k = 0; k < 2; ++k) {
+            t[k] = (lane + 32 * k) / p.G;
+            g[k] = lane + 32 * k - t[k] * p.G;
+        }
+        do {
+            for (int i = w.first; i < w.last; ++i) {
+                float nlse[2], delta[2];
+                int token[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int x = i * p.tps + t[k];
+                    const bool there = t[k] < p.tps && x < w.u.n_b;
+                    const long long at = ((long long)w.u.b0 + x) * p.Hq + w.head * p.G + g[k];
+                    nlse[k] = there ? -kLog2e * p.lse[at] : -INFINITY;
+                    delta[k] = there && G::HAS_DP ? p.delta[at] : 0.0f;
+                    token[k] = there ? x : -0x40000000;
+                }
+                wait(&bars.stats_free[st], ph ^ 1);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    stats[st].nlse[lane + 32 * k] = nlse[k];
+                    stats[st].delta[lane + 32 * k] = delta[k];
+                    stats[st].token[lane + 32 * k] = token[k];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.stats_full[st]);
+                if (++st == kStats) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        } while (w.next());
+    } else if (any && warp < G::WARPS) {
+        // ---- P and dS, and the results
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        uint8_t *turn = smem + G::TURN_AT + warp * G::TURN;
+        // the resident rows: the first half of the warps brings A1, the second A2
+        auto load_resident = [&](const RowOut &o) {
+            if (half == 0 || G::HAS_DP) {
+                const HeadsIn &h = half == 0 ? p.a1 : p.a2;
+                const uint4 *src = reinterpret_cast<const uint4 *>(h.p + o.token * h.ts + o.head * h.hs);
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = o.valid ? src[c * 8 + k] : make_uint4(0, 0, 0, 0);
+                    if (half == 1 && G::A2_SMEM) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4 *>(smem + c * 128 * 128 + umma::sw128(r, k * 16)) = x[k];
+                    } else {
+                        float y[32];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            y[4 * k] = __uint_as_float(x[k].x);
+                            y[4 * k + 1] = __uint_as_float(x[k].y);
+                            y[4 * k + 2] = __uint_as_float(x[k].z);
+                            y[4 * k + 3] = __uint_as_float(x[k].w);
+                        }
+                        umma::tmem_st32(lanes + (half == 0 ? G::A1_COL : G::A2_COL) + c * 32, y);
+                    }
+                }
+                umma::tmem_st_wait();
+                fence_proxy_async_smem();
+            }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.a_full);
+        };
+        RowOut o = row_out<G>(p, w.u, w.head, r);
+        load_resident(o);
+        int step = 0, st = 0, units = 0;
+        uint32_t ph = 0;
+        bool more = true;
+        while (more) {
+            float nlse = -INFINITY, delta = 0.0f;
+            int keys = 0;
+            if (!G::KEYS && o.valid) {
+                keys = max(w.u.lim0 + (int)(o.token - w.u.a0), 0);
+                if (keys > 0) {
+                    nlse = -kLog2e * p.lse[o.at];
+                    delta = p.delta[o.at];
+                }
+            }
+            for (int i = w.first; i < w.last; ++i, ++step) {
+                float s[32], dp[32];
+                wait(&bars.s_full, step & 1);
+                umma::fence_after_sync();
+                umma::tmem_ld32(lanes + G::S_COL + half * 32, s);
+                if (G::HAS_DP) umma::tmem_ld32(lanes + G::S_COL + 64 + half * 32, dp);
+                umma::tmem_ld_wait();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.s_free);
+                const Stats *x = nullptr;
+                if (G::KEYS) {
+                    wait(&bars.stats_full[st], ph);
+                    x = &stats[st];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 n = *reinterpret_cast<const float4 *>(&x->nlse[half * 32 + k]);
+                        s[k] = ex2(fmaf(s[k], p.scale2, n.x));
+                        s[k + 1] = ex2(fmaf(s[k + 1], p.scale2, n.y));
+                        s[k + 2] = ex2(fmaf(s[k + 2], p.scale2, n.z));
+                        s[k + 3] = ex2(fmaf(s[k + 3], p.scale2, n.w));
+                    }
+                    // (not all keys seen by the step's first token, or rows behind the last token)
+                    const bool masked = w.u.lim0 + i * p.tps < 127 || (i + 1) * p.tps > w.u.n_b;
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const int4 n = *reinterpret_cast<const int4 *>(&x->token[half * 32 + k]);
+                            const int tok[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                if (r > w.u.lim0 + tok[z]) {
+                                    s[k + z] = 0.0f;
+                                    if (G::HAS_DP) dp[k + z] = 0.0f;
+                                }
+                        }
+                    }
+                } else {
+                    const int lim = keys - i * kRows - half * 32;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = ex2(fmaf(s[k], p.scale2, nlse));
+                    if (__any_sync(0xffffffffu, lim < 32)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (k >= lim) s[k] = dp[k] = 0.0f;
+                    }
+                    if (w.u.steps == 1) {
+                        // all of a row's keys at hand: its delta from P and dP themselves (the output's rounding to bf16 is
+                        // too coarse for rows of few keys), also for the kernels that come after
+                        float t = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) t = fmaf(s[k], dp[k], t);
+                        swap[half * 128 + r] = t;
+                        asm volatile("bar.sync 1, 256;" ::: "memory");
+                        delta = swap[r] + swap[128 + r];
+                        asm volatile("bar.sync 1, 256;" ::: "memory");
+                        if (half == 0 && o.valid) p.delta[o.at] = delta;
+                    }
+                }
+                const int xb = step % G::XB;
+                if (step >= G::XB) wait(&bars.x_free[xb], (step / G::XB - 1) & 1);
+                uint8_t *xs = smem + G::X_AT + xb * G::XT * G::XTILE;
+                auto put = [&](uint8_t *tile, const float (&v)[32]) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float y[8] = {v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3],
+                                            v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7]};
+                        *reinterpret_cast<uint4 *>(tile + umma::sw128(r, half * 64 + c * 16)) = attn::pack8(y);
+                    }
+                };
+                if (G::HAS_P) put(xs + (G::HAS_DP ? G::XTILE : 0), s);
+                if (G::HAS_DP) {
+                    if (G::KEYS) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 n = *reinterpret_cast<const float4 *>(&x->delta[half * 32 + k]);
+                            s[k] *= dp[k] - n.x;
+                            s[k + 1] *= dp[k + 1] - n.y;
+                            s[k + 2] *= dp[k + 2] - n.z;
+                            s[k + 3] *= dp[k + 3] - n.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] *= dp[k] - delta;
+                    }
+                    put(xs, s);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.x_full[xb]);
+                    if (G::KEYS) mbar_arrive(&bars.stats_free[st]);
+                }
+                if (G::KEYS && ++st == kStats) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            // the next tile's resident rows, then this one's results
+            Walk y = w;
+            more = y.next();
+            RowOut next = o;
+            if (more) {
+                next = row_out<G>(p, y.u, y.head, r);
+                load_resident(next);
+            }
+            const bool whole = w.whole();
+            const int slot = w.slot(blockIdx.x);
+            const bool valid = o.valid && (!G::KEYS || w.u.n_b > 0) && (G::KEYS || keys > 0);
+            wait(&bars.acc_done, units & 1);
+            umma::fence_after_sync();
+#pragma unroll 1
+            for (int a = 0; a < G::ACCS; ++a) {
+                const bool of_p = a == 1 || !G::HAS_DP;
+                const float f = of_p ? 1.0f : p.scale;
+                float check = 0.0f;
+                uint16_t *rows[2];
+                rows_out<D>(o, p.acc_out[a], rows);
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    const int d = half * (D / 2) + c * 32;
+                    float v[32];
+                    umma::tmem_ld32(lanes + a * D + d, v);
+                    umma::tmem_ld_wait();
+                    if (a == G::ACCS - 1 && c == D / 64 - 1) {
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.acc_free);
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) check = fmaf(v[k], 0.0f, check);
+                        write_group<D>(turn, rows, valid, d, v, f);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part) +
+                                      (((size_t)slot * G::ACCS + a) * (D / 4) + d / 4) * 128 + r;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[(size_t)k * 128] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                }
+                if (whole)
+                    mend_rows<G>(p, o, w.u, r, of_p, valid && check != 0.0f, p.acc_out[a], half * (D / 2),
+                                 (half + 1) * (D / 2));
+            }
+            ++units;
+            w = y;
+            o = next;
+        }
+        umma::fence_before_sync();
+    }
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == 0) umma::tmem_dealloc(tmem, 512);
+}
+
+// A split tile's parts added up: 32 channels of 128 rows a block.
+template <class G>
+__global__ void __launch_bounds__(128) prompt_backward_join_kernel(const Params p, int ctas) {
+    constexpr int D = G::D;
+    __shared__ __align__(16) uint8_t turn[4][G::TURN];
+    attn::grid_dep_enter();
+    const Parts part = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
+    if (part.n == 0) return;
+    const int a = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32), r = threadIdx.x;
+    const RowOut o = row_out<G>(p, part.u, part.head, r);
+    uint16_t *rows[2];
+    rows_out<D>(o, p.acc_out[a], rows);
+    float x[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = 0.0f;
+    for (int i = 0; i < part.n; ++i) {
+        const size_t slot = 2 * (size_t)(blockIdx.x + i) + (i == 0 ? 1 : 0);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part) + ((slot * G::ACCS + a) * (D / 4) + c * 8) * 128 + r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 v = src[(size_t)k * 128];
+            x[4 * k] += v.x;
+            x[4 * k + 1] += v.y;
+            x[4 * k + 2] += v.z;
+            x[4 * k + 3] += v.w;
+        }
+    }
+    const bool of_p = a == 1 || !G::HAS_DP;
+    float check = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) check = fmaf(x[k], 0.0f, check);
+    const bool valid = o.valid && (G::KEYS || part.u.lim0 + (int)(o.token - part.u.a0) > 0);
+    write_group<D>(turn[threadIdx.x >> 5], rows, valid, c * 32, x, of_p ? 1.0f : p.scale);
+    mend_rows<G>(p, o, part.u, r, of_p, valid && check != 0.0f, p.acc_out[a], c * 32, c * 32 + 32);
+}
+
+// ---------------------------------------------------------------------------
+// before the passes: delta = rowsum(dout out), and with a gate dO = dout
+// sigmoid(gate), rounded to bf16 for the products, and the gate's own gradient.
+// Memory-bound; a group of D / 8 lanes takes a row.
+// ---------------------------------------------------------------------------
+struct PrepareParams {
+    List list;
+    const uint16_t *out, *dout;
+    HeadsIn gate;
+    uint16_t *d_o, *dgate;
+    float *delta;
+    const int32_t *cu_q;
+    int Hq, Hkv, G, tile, B;
+    long long Nq;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams p) {
+    constexpr int LPR = D / 8, RPB = 256 / LPR;
+    const int sub = threadIdx.x / LPR, d = threadIdx.x % LPR * 8;
+    attn::grid_dep_enter();
+    const Header h = *p.list.header;
+    const long long units = (long long)h.units * p.Hkv;
+    const bool gated = p.gate.p != nullptr;
+    for (long long x = blockIdx.x; x < units; x += gridDim.x) {
+        const int head = (int)(x / h.units);
+        const Unit u = p.list.unit[x - (long long)head * h.units];
+        for (int r0 = 0; r0 < p.tile * p.G; r0 += RPB) {
+            const int r = r0 + sub, t = r / p.G, hq = head * p.G + r - t * p.G;
+            const bool mine = r < p.tile * p.G && t < u.slot_a;
+            const long long n = (long long)u.a0 + t, at = n * p.Hq + hq;
+            uint4 z = make_uint4(0, 0, 0, 0), zg = z;
+            float sum = 0.0f;
+            if (mine && t < u.n_a) {
+                float a[8], b[8];
+                attn::unpack8(*reinterpret_cast<const uint4 *>(p.dout + at * D + d), a);
+                attn::unpack8(*reinterpret_cast<const uint4 *>(p.out + at * D + d), b);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum = fmaf(a[k], b[k], sum);
+                if (gated) {
+                    float g[8], y[8];
+                    attn::unpack8(*reinterpret_cast<const uint4 *>(p.gate.p + n * p.gate.ts + hq * p.gate.hs + d), g);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float e = exp_fast(-g[k]), sg = rcp_fast(1.0f + e);
+                        y[k] = a[k] * sg;
+                        a[k] *= b[k] * (e < INFINITY ? e * sg : 1.0f);   // 1 - sigmoid
+                    }
+                    z = attn::pack8(y);
+                    zg = attn::pack8(a);
+                }
+            }
+            if (gated && mine) {
+                *reinterpret_cast<uint4 *>(p.d_o + at * D + d) = z;
+                *reinterpret_cast<uint4 *>(p.dgate + at * D + d) = zg;
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, LPR);
+            if (d == 0 && mine) p.delta[at] = sum;
+        }
+    }
+    // rows behind the last sequence, which its last steps may bring along: finite
+    if (gated && p.cu_q != nullptr && h.units > 0 && blockIdx.x == 0) {
+        const long long end = p.cu_q[p.B], most = end + kRows < p.Nq ? end + kRows : p.Nq;
+        for (long long i = threadIdx.x; i < (most - end) * p.Hq * (D / 8); i += 256)
+            reinterpret_cast<uint4 *>(p.d_o + end * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+PromptList q_list(const PromptSizes &s) {
+    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, 2};
+}
+
+PromptList k_list(const PromptSizes &s) {
+    return PromptList{true, 128, kRows / (s.Hq / s.Hkv), num_sms(), 4, 2};
+}
+
+struct Workspace {
+    size_t k, d_o, delta, part[3], total;
+};
+
+Workspace workspace(const PromptSizes &s, bool gated) {
+    Workspace w;
+    const size_t part = up256(2 * (size_t)num_sms() * 128 * s.D * sizeof(float));
+    w.k = prompt_list_bytes(s, q_list(s));
+    w.delta = w.k + prompt_list_bytes(s, k_list(s));
+    w.d_o = w.delta + up256((size_t)s.Nq * s.Hq * sizeof(float));
+    w.part[0] = w.d_o + (gated ? up256((size_t)s.Nq * s.Hq * s.D * 2) : 0);
+    w.part[1] = w.part[0] + part;
+    w.part[2] = w.part[1] + part;      // (up to 128 channels: the second half of dK and dV's)
+    w.total = w.part[2] + part;
+    return w;
+}
+
+template <class G>
+cudaError_t launch_pass(const CUtensorMap &m1, const CUtensorMap &m2, const Params &p, cudaStream_t st) {
+    static unsigned long long done = 0;
+    cudaError_t e = set_max_smem(done, prompt_backward_kernel<G>, G::SMEM);
+    if (e != cudaSuccess) return e;
+    return DependentLaunch(dim3(num_sms()), dim3(G::THREADS), G::SMEM, st)(prompt_backward_kernel<G>, m1, m2, p);
+}
+
+template <class G>
+cudaError_t launch_join(const Params &p, cudaStream_t st) {
+    const int ctas = num_sms();
+    return DependentLaunch(dim3(ctas - 1, G::ACCS * (G::D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<G>, p, ctas);
+}
+
+template <int D>
+cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                     const HeadsIn &gate, const uint16_t *out, const float *lse, const uint16_t *dout, float scale, uint16_t *dq,
+                     uint16_t *dk, uint16_t *dv, uint16_t *dgate, char *ws, unsigned *err, cudaStream_t st) {
+    const bool gated = gate.p != nullptr;
+    const Workspace w = workspace(s, gated);
+    const PromptList lists[2] = {q_list(s), k_list(s)};
+    void *const at[2] = {ws, ws + w.k};
+    cudaError_t e = launch_prompt_plan(s, seqs, lists, 2, at, err, st);
+    if (e != cudaSuccess) return e;
+    const int G = s.Hq / s.Hkv;
+    uint16_t *d_o = gated ? reinterpret_cast<uint16_t *>(ws + w.d_o) : nullptr;
+    PrepareParams r = {};
+    r.list = prompt_list_at(s, lists[0], at[0]);
+    r.out = out;
+    r.dout = dout;
+    r.gate = gate;
+    r.d_o = d_o;
+    r.dgate = dgate;
+    r.delta = reinterpret_cast<float *>(ws + w.delta);
+    r.cu_q = seqs.cu_q;
+    r.Hq = s.Hq;
+    r.Hkv = s.Hkv;
+    r.G = G;
+    r.tile = lists[0].tile;
+    r.B = s.B;
+    r.Nq = s.Nq;
+    const long long most = ((s.Nq + r.tile - 1) / r.tile + s.B) * s.Hkv, fill = 8LL * num_sms();
+    if (s.Nq > 0) e = DependentLaunch(dim3((unsigned)(most < fill ? most : fill)), dim3(256), 0, st)(prompt_prepare_kernel<D>, r);
+    if (e != cudaSuccess) return e;
+
+    const HeadsIn g{gated ? d_o : dout, (long long)s.Hq * D, D};
+    const bool none = s.Nk == 0;   // (no keys, or no queries: nothing of what is loaded counts, but a map needs a tensor)
+    const bool no_q = s.Nq == 0;
+    const HeadsIn dummy{no_q ? k.p : q.p, 0, 0};
+    CUtensorMap mq, mg, mk, mv;
+    const int tps = lists[1].step;
+    if (!queries_map(&mq, no_q ? dummy : q, no_q ? 1 : s.Nq, no_q ? 1 : s.Hq, D, G, tps) ||
+        !queries_map(&mg, no_q ? dummy : g, no_q ? 1 : s.Nq, no_q ? 1 : s.Hq, D, G, tps) ||
+        !keys_map(&mk, none ? dummy : k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kRows, D / 64) ||
+        !keys_map(&mv, none ? dummy : v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kRows, D / 64))
+        return cudaErrorInvalidValue;
+    Params p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.d_o = g;
+    p.scale = scale;
+    p.scale2 = scale * kLog2e;
+    p.lse = lse;
+    p.delta = r.delta;
+    p.err = err;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.G = G;
+    auto part = [&](int i) { return reinterpret_cast<float *>(ws + w.part[i]); };
+
+    Params pq = p;
+    pq.list = r.list;
+    pq.a1 = q;
+    pq.a2 = g;
+    pq.acc_out[0] = dq;
+    pq.part = part(0);
+    pq.tile = lists[0].tile;
+    pq.tps = kRows;
+    Params pk = p;
+    pk.list = prompt_list_at(s, lists[1], at[1]);
+    pk.a1 = k;
+    pk.a2 = v;
+    pk.part = part(1);
+    pk.tile = 128;
+    pk.tps = tps;
+    if (!no_q) e = launch_pass<Geo<D, kDQ>>(mk, mv, pq, st);
+    if (e == cudaSuccess && !no_q) e = launch_join<Geo<D, kDQ>>(pq, st);
+    if (e != cudaSuccess || none) return e;
+    if constexpr (D == 256) {
+        Params pv = pk;
+        pk.acc_out[0] = dk;
+        pv.acc_out[0] = dv;
+        pv.part = part(2);
+        e = launch_pass<Geo<D, kDK>>(mq, mg, pk, st);
+        if (e == cudaSuccess) e = launch_pass<Geo<D, kDV>>(mq, mg, pv, st);
+        if (e == cudaSuccess) e = launch_join<Geo<D, kDK>>(pk, st);
+        if (e == cudaSuccess) e = launch_join<Geo<D, kDV>>(pv, st);
+    } else {
+        pk.acc_out[0] = dk;
+        pk.acc_out[1] = dv;
+        e = launch_pass<Geo<D, kDKV>>(mq, mg, pk, st);
+        if (e == cudaSuccess) e = launch_join<Geo<D, kDKV>>(pk, st);
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t attn_prefill_backward_workspace(const PromptSizes &s, bool gated) { return workspace(s, gated).total; }
+
+cudaError_t launch_attn_prefill_backward(const PromptSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
+                                         const PromptSeqs &seqs, const HeadsIn &gate, float scale, const uint16_t *out,
+                                         const float *lse, const uint16_t *dout, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                                         uint16_t *dgate, void *ws, unsigned *err, cudaStream_t st) {
+    char *base = static_cast<char *>(ws);
+    if (s.D == 64) return launch_d<64>(s, seqs, q, k, v, gate, out, lse, dout, scale, dq, dk, dv, dgate, base, err, st);
+    if (s.D == 128) return launch_d<128>(s, seqs, q, k, v, gate, out, lse, dout, scale, dq, dk, dv, dgate, base, err, st);
+    return launch_d<256>(s, seqs, q, k, v, gate, out, lse, dout, scale, dq, dk, dv, dgate, base, err, st);
+}
+
+}  // namespace gdn

@@ -32,7 +32,6 @@ namespace {
 using namespace prompt;
 
 constexpr int kKeys = 128;             // of a step
-constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kRaise = 8.0f;         // powers of two that a row's maximum may grow by before m follows
 
 template <int D_>
@@ -69,40 +68,9 @@ struct Bars {
     float most[2][2][128];   // [step parity][half][row]: what the halves of a row tell each other
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Two f32 in one register pair.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 f2_of(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 parts(F2 x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 
@@ -180,10 +148,6 @@ __device__ __forceinline__ RowsOut rows_out(const Params &p, const RowOut &o) {
     }
     return r;
 }
-
-// Byte offset of 16 bytes (chunk 0 or 1) of a row in a warp's 32 x 32 bytes: no
-// two of the eight lanes of a phase, by rows or by chunks, meet in a bank.
-__device__ __forceinline__ int turn_at(int row, int chunk) { return row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4); }
 
 // The gates of 32 channels of the warp's rows, as they are read.
 struct Gates {
@@ -720,8 +684,6 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ct
     mend_rows<D>(p, o, part.u, part.head, check != 0.0f, c * 32, c * 32 + 32);
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 int tiles_of(int D) { return D <= 128 ? 2 : 1; }
 
 PromptList list_of(const PromptSizes &s) {
@@ -740,25 +702,6 @@ Workspace workspace(const PromptSizes &s) {
     w.ml = w.o + up256(rows * s.D * sizeof(float));
     w.total = w.ml + up256(rows * sizeof(float2));
     return w;
-}
-
-long long head_stride(const HeadsIn &x, int H, int D) { return H > 1 ? x.hs : D; }
-long long token_stride(const HeadsIn &x, long long rows, int H, int D) { return rows > 1 ? x.ts : (long long)H * D; }
-
-// [rows, H, D] as (64 channels, heads, tokens): boxes of one tile's rows.
-bool queries_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_heads, int box_tokens) {
-    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)rows};
-    const uint64_t strides[2] = {(uint64_t)head_stride(x, H, D) * 2, (uint64_t)token_stride(x, rows, H, D) * 2};
-    const uint32_t box[3] = {64, (uint32_t)box_heads, (uint32_t)box_tokens};
-    return encode_tmap_strided(map, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// ... as (64 channels, tokens, groups of 64 channels, heads): boxes of one head's tokens, groups one after the other.
-bool keys_map(CUtensorMap *map, const HeadsIn &x, long long rows, int H, int D, int box_tokens, int box_groups) {
-    const uint64_t dims[4] = {64, (uint64_t)rows, (uint64_t)(D / 64), (uint64_t)H};
-    const uint64_t strides[3] = {(uint64_t)token_stride(x, rows, H, D) * 2, 128, (uint64_t)head_stride(x, H, D) * 2};
-    const uint32_t box[4] = {64, (uint32_t)box_tokens, (uint32_t)box_groups, 1};
-    return encode_tmap_strided(map, x.p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D>

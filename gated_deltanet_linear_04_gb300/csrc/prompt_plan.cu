@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
     }
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 }  // namespace
+
+using prompt::up256;
 
 size_t prompt_list_bytes(const PromptSizes &s, const PromptList &l) {
     const long long rows = l.keys ? s.Nk : s.Nq;

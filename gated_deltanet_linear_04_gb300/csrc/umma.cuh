@@ -109,6 +109,36 @@ __device__ __forceinline__ void warp_mma_bf16_k64(uint32_t d, uint64_t a, uint64
                  : "memory");
 }
 
+// ... of A in tensor memory (32 columns) and B in one tile.
+__device__ __forceinline__ void warp_mma_bf16_tmem_a_k64(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(GDN_UMMA_WARP_BEGIN
+                 ".reg .b32 a;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+                 "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+                 "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+                 : "memory");
+}
+
+// ... of A in one tile and 64 rows (K) of a transposed B.
+__device__ __forceinline__ void warp_mma_bf16_k64_bt(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+    asm volatile(GDN_UMMA_WARP_BEGIN
+                 ".reg .b64 a;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                 "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 128;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                 "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 256;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+                 "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 384;\n\t"
+                 "@w tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+                 : "memory");
+}
+
 // K = 32 of A in tensor memory (16 columns) and a transposed B (rows of K).
 __device__ __forceinline__ void warp_mma_bf16_tmem_a_k32(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
     asm volatile(GDN_UMMA_WARP_BEGIN

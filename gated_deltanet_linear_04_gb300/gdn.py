@@ -93,6 +93,9 @@ _SIGS = {
     "gdn_attn_prefill_workspace_size": (ctypes.c_size_t, _ROWS),
     "gdn_attn_prefill": (ctypes.c_int, _ROWS + _HEADS * 3 + [_P] * 4 + _HEADS + [ctypes.c_float] + [_P] * 3 +
                          [ctypes.c_size_t, _P]),
+    "gdn_attn_prefill_backward_workspace_size": (ctypes.c_size_t, _ROWS + [ctypes.c_int32]),
+    "gdn_attn_prefill_backward": (ctypes.c_int, _ROWS + _HEADS * 3 + [_P] * 4 + _HEADS + [ctypes.c_float] + [_P] * 8 +
+                                  [ctypes.c_size_t, _P]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_device_status": (ctypes.c_int, [_P]),
     "gdn_selftest_timeout": (ctypes.c_int, [_P]),

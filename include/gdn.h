@@ -597,6 +597,36 @@ GDN_API gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, i
                                     int64_t gate_token_stride, int64_t gate_head_stride, float scale, uint16_t *out,
                                     float *lse, void *workspace, size_t ws_bytes, gdn_stream stream);
 
+/* Its gradients.  P = exp(s - lse), dO = dout sigmoid(gate), delta = sum of dO O
+ * over a row's channels:  dv = P^T dO;  dS = P (dO v^T - delta);  dq = scale dS k;
+ * dk = scale dS^T q, both summed over the query heads of a key head;
+ * dgate = dout out (1 - sigmoid(gate)).
+ *   q, k, v, cu_q, cu_k, n_q, n_k, gate, scale  as above (the forward inputs)
+ *   out    bf16 [q_rows, Hq, D], lse f32 [q_rows, Hq] (in): the forward results
+ *   dout   bf16 [q_rows, Hq, D] (in), dense
+ *   dq     bf16 [q_rows, Hq, D], dk, dv bf16 [k_rows, Hkv, D] (out), dense: they
+ *          feed bf16 products, so they are rounded once here
+ *   dgate  bf16 [q_rows, Hq, D] (out); NULL when gate is
+ *   workspace  device scratch of gdn_attn_prefill_backward_workspace_size()
+ *          bytes (gated: whether there is a gate) on the device that runs the
+ *          call: work lists, delta, dO and partial sums
+ * P and dS are rounded to bf16 for their products, dO too where there is a gate;
+ * delta is taken from out, for queries that see no more than 64 keys mostly from
+ * P and dP themselves, where out's rounding would be too coarse.  Sums are f32 in
+ * a fixed order: equal calls give equal bits.  Padding gives zeros, rows in no
+ * slot are left as they were; a query that sees no key has no gradient. */
+GDN_API size_t gdn_attn_prefill_backward_workspace_size(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows,
+                                                        int32_t gated);
+GDN_API gdn_status gdn_attn_prefill_backward(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows, const uint16_t *q,
+                                             int64_t q_token_stride, int64_t q_head_stride, const uint16_t *k,
+                                             int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
+                                             int64_t v_token_stride, int64_t v_head_stride, const int32_t *cu_q,
+                                             const int32_t *cu_k, const int32_t *n_q, const int32_t *n_k,
+                                             const uint16_t *gate, int64_t gate_token_stride, int64_t gate_head_stride,
+                                             float scale, const uint16_t *out, const float *lse, const uint16_t *dout,
+                                             uint16_t *dq, uint16_t *dk, uint16_t *dv, uint16_t *dgate, void *workspace,
+                                             size_t ws_bytes, gdn_stream stream);
+
 /* ABI version of this header (incremented on any signature change). */
 GDN_API int gdn_abi_version(void);
 
