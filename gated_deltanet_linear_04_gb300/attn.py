@@ -86,6 +86,20 @@ def rope_freqs(inv_freq: torch.Tensor, device=None) -> torch.Tensor:
     return torch.tensor([b - 2 ** 64 if b >= 2 ** 63 else b for b in bits], dtype=I64, device=dev)
 
 
+def rope_axes(sections, cyclic: bool = False, device=None) -> torch.Tensor:
+    """The axis of each rotated pair (u8 [sum of sections]): sections[i] pairs
+    turn with axis i, one axis after the other, or in turn (0, 1, 2, 0, 1, ...;
+    an axis whose pairs are used up is passed over)."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 8 or min(left) < 0:
+        raise ValueError("rope_axes: 1 to 8 sections of 0 or more pairs, got %s" % (left,))
+    if not cyclic:
+        pairs = [i for i, n in enumerate(left) for _ in range(n)]
+    else:
+        pairs = [i for k in range(max(left)) for i, n in enumerate(left) if k < n]
+    return torch.tensor(pairs, dtype=U8, device=device)
+
+
 class _CacheRecord(ctypes.Structure):
     _fields_ = [("c", GdnKvCache), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("device", ctypes.c_int32)]
 
@@ -184,6 +198,29 @@ def gdn_attn_decode(dims, q, cache, page_table, pos, n_new, gate, scale, out, ls
                         _handle(stream))
 
 
+def gdn_qk_norm_rope_axes(dims, q, k, wq, wk, freqs, axes, pos, mask, q_out, k_out, stream=None):
+    _given("gdn_qk_norm_rope_axes", q_out=q_out, k_out=k_out)
+    c = _dims(dims)
+    _bind().qk_norm_rope_axes(_at(c), q, k, wq, wk, freqs, axes, pos, mask, q_out, k_out, _handle(stream))
+
+
+def gdn_qk_norm_rope_axes_backward(dims, q, k, wq, wk, freqs, axes, pos, mask, dq_out, dk_out, dq, dk, dwq, dwk, workspace,
+                                   stream=None):
+    _given("gdn_qk_norm_rope_axes_backward", dq=dq, dk=dk)
+    if wq is not None:
+        _given("gdn_qk_norm_rope_axes_backward", dwq=dwq, dwk=dwk, workspace=workspace)
+    c = _dims(dims)
+    _bind().qk_norm_rope_axes_backward(_at(c), q, k, wq, wk, freqs, axes, pos, mask, dq_out, dk_out, dq, dk, dwq, dwk,
+                                       workspace, _handle(stream))
+
+
+def gdn_kv_append_axes(dims, q, k, v, wq, wk, freqs, axes, rope_pos, cache, page_table, pos, n_new, q_out, stream=None):
+    _given("gdn_kv_append_axes", q_out=q_out)
+    c = _dims(dims)
+    _bind().kv_append_axes(_at(c), q, k, v, wq, wk, freqs, axes, rope_pos, _at(cache._c), page_table, pos, n_new, q_out,
+                           _handle(stream))
+
+
 def gdn_attn_prefill_workspace_size(dims, q_rows, k_rows) -> int:
     return int(lib().gdn_attn_prefill_workspace_size(ctypes.byref(_dims(dims)), int(q_rows), int(k_rows)))
 
@@ -249,6 +286,29 @@ def attn_decode(dims, q, cache, page_table, pos, n_new=None, gate=None, scale=No
     return _bind().attn_decode(_at(c), q, _at(cache._c), page_table, pos, n_new, gate,
                                dims.D ** -0.5 if scale is None else scale, None, None, bool(return_lse), workspace,
                                _handle(stream))
+
+
+def qk_norm_rope_axes(dims, q, k, wq, wk, freqs, axes, pos, mask=None, stream=None):
+    """qk_norm_rope with pos [axes, B, T], each pair turning with its own axis
+    (axes: rope_axes); returns (q_out, k_out)."""
+    c = _dims(dims)
+    return _bind().qk_norm_rope_axes(_at(c), q, k, wq, wk, freqs, axes, pos, mask, None, None, _handle(stream))
+
+
+def qk_norm_rope_axes_backward(dims, q, k, wq, wk, freqs, axes, pos, dq_out, dk_out, mask=None, stream=None):
+    """Gradients of qk_norm_rope_axes, as qk_norm_rope_backward's."""
+    c = _dims(dims)
+    dq, dk, dwq, dwk = _bind().qk_norm_rope_axes_backward(_at(c), q, k, wq, wk, freqs, axes, pos, mask, dq_out, dk_out, None,
+                                                          None, None, None, None, _handle(stream))
+    return {"dq": dq, "dk": dk} if dwq is None else {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
+
+
+def kv_append_axes(dims, q, k, v, wq, wk, freqs, axes, rope_pos, cache, page_table, pos, n_new=None, stream=None):
+    """kv_append with rotary positions rope_pos [axes, B, T]; pos [B] says where
+    in the cache the new tokens go."""
+    c = _dims(dims)
+    return _bind().kv_append_axes(_at(c), q, k, v, wq, wk, freqs, axes, rope_pos, _at(cache._c), page_table, pos, n_new, None,
+                                  _handle(stream))
 
 
 def attn_prefill(dims, q, k, v, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=None, scale=None, return_lse=False,

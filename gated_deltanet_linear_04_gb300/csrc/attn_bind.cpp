@@ -305,6 +305,23 @@ PyObject *pair(const at::Tensor &a, const at::Tensor &b) {
     return t;
 }
 
+// Positions on several axes: (axes u8 [Drot / 2], pos i32 [n, B, T]).
+struct Axes {
+    const uint8_t *axis;
+    int32_t n;
+    const int32_t *pos;
+
+    Axes(Call &c, const gdn_attn_dims &d, PyObject *axes, PyObject *pos, const char *name) {
+        axis = static_cast<uint8_t *>(c.dense(axes, at::kByte, {d.Drot / 2}, "axes"));
+        const at::Tensor &t = c.tensor(pos, at::kInt, name);
+        if (t.dim() != 3 || t.size(0) < 1 || t.size(0) > 8)
+            raise(PyExc_ValueError, std::string(name) + " must have shape (axes, B, T) with 1 to 8 axes, got " + show(t.sizes()));
+        c.shaped(t, {t.size(0), d.B, d.T}, name);
+        n = (int32_t)t.size(0);
+        this->pos = static_cast<int32_t *>(c.address(t, name));
+    }
+};
+
 // (dims, q, k, wq, wk, freqs, pos, mask, q_out, k_out, stream) -> (q_out, k_out)
 PyObject *qk_norm_rope(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
@@ -316,6 +333,22 @@ PyObject *qk_norm_rope(PyObject *const *a) {
     const at::Tensor qo = c.output(a[8], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
     const at::Tensor ko = c.output(a[9], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "k_out");
     c.done(gdn_qk_norm_rope(&d, q.p, q.ts, q.hs, k.p, k.ts, k.hs, n.wq, n.wk, n.freqs, pos, mask, bf16(qo), bf16(ko),
+                            (gdn_stream)c.stream()));
+    return pair(qo, ko);
+}
+
+// (dims, q, k, wq, wk, freqs, axes, pos, mask, q_out, k_out, stream) -> (q_out, k_out)
+PyObject *qk_norm_rope_axes(PyObject *const *a) {
+    const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
+    Call c("gdn_qk_norm_rope_axes", a[11]);
+    const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k");
+    const Norm n = norm_args(c, d, a[3], a[4], a[5]);
+    const Axes x(c, d, a[6], a[7], "pos");
+    const auto *mask = static_cast<uint8_t *>(c.dense(a[8], at::kByte, {d.B, d.T}, "mask", true));
+    const at::Tensor qo = c.output(a[9], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
+    const at::Tensor ko = c.output(a[10], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "k_out");
+    c.done(gdn_qk_norm_rope_axes(&d, q.p, q.ts, q.hs, k.p, k.ts, k.hs, n.wq, n.wk, n.freqs, x.axis, x.n,
+                                 x.pos, mask, bf16(qo), bf16(ko),
                             (gdn_stream)c.stream()));
     return pair(qo, ko);
 }
@@ -353,6 +386,39 @@ PyObject *qk_norm_rope_backward(PyObject *const *a) {
     return t;
 }
 
+// (dims, q, k, wq, wk, freqs, axes, pos, mask, dq_out, dk_out, dq, dk, dwq, dwk, workspace, stream) -> (dq, dk, dwq, dwk)
+PyObject *qk_norm_rope_axes_backward(PyObject *const *a) {
+    const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
+    Call c("gdn_qk_norm_rope_axes_backward", a[16]);
+    const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k");
+    const Norm n = norm_args(c, d, a[3], a[4], a[5]);
+    const Axes x(c, d, a[6], a[7], "pos");
+    const auto *mask = static_cast<uint8_t *>(c.dense(a[8], at::kByte, {d.B, d.T}, "mask", true));
+    const auto *dqo = static_cast<uint16_t *>(c.dense(a[9], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "dq_out"));
+    const auto *dko = static_cast<uint16_t *>(c.dense(a[10], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "dk_out"));
+    const at::Tensor dq = c.output(a[11], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "dq");
+    const at::Tensor dk = c.output(a[12], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "dk");
+    at::Tensor dwq, dwk;
+    Scratch ws;
+    if (n.wq != nullptr || a[13] != Py_None) dwq = c.output(a[13], at::kFloat, {d.D}, "dwq");
+    if (n.wk != nullptr || a[14] != Py_None) dwk = c.output(a[14], at::kFloat, {d.D}, "dwk");
+    if (a[15] != Py_None)
+        ws.given(c, a[15]);
+    else if (n.wq != nullptr)
+        ws.make(c, gdn_qk_norm_rope_backward_workspace_size(&d));
+    c.done(gdn_qk_norm_rope_axes_backward(&d, q.p, q.ts, q.hs, k.p, k.ts, k.hs, n.wq, n.wk, n.freqs, x.axis, x.n, x.pos, mask, dqo, dko,
+                                     bf16(dq), bf16(dk), dwq.defined() ? f32(dwq) : nullptr,
+                                     dwk.defined() ? f32(dwk) : nullptr, ws.p, ws.bytes,
+                                     (gdn_stream)c.stream()));
+    PyObject *t = PyTuple_New(4);
+    if (t == nullptr) throw Raised();
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(dq));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(dk));
+    PyTuple_SET_ITEM(t, 2, dwq.defined() ? THPVariable_Wrap(dwq) : Py_NewRef(Py_None));
+    PyTuple_SET_ITEM(t, 3, dwk.defined() ? THPVariable_Wrap(dwk) : Py_NewRef(Py_None));
+    return t;
+}
+
 // (dims, q, k, v, wq, wk, freqs, cache, page_table, pos, n_new, q_out, stream) -> q_out
 PyObject *kv_append(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
@@ -363,6 +429,22 @@ PyObject *kv_append(PyObject *const *a) {
     const int32_t *pos = index_arg(c, a[9], d.B, "pos"), *n_new = index_arg(c, a[10], d.B, "n_new", true);
     const at::Tensor qo = c.output(a[11], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
     c.done(gdn_kv_append(&d, q.p, q.ts, q.hs, k.p, k.ts, k.hs, v.p, v.ts, v.hs, n.wq, n.wk, n.freqs, pg.c, pg.table,
+                         pg.width, pos, n_new, bf16(qo), (gdn_stream)c.stream()));
+    return THPVariable_Wrap(qo);
+}
+
+// (dims, q, k, v, wq, wk, freqs, axes, rope_pos, cache, page_table, pos, n_new, q_out, stream) -> q_out
+PyObject *kv_append_axes(PyObject *const *a) {
+    const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
+    Call c("gdn_kv_append_axes", a[14]);
+    const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k"), v = c.heads(a[3], d, d.Hkv, "v");
+    const Norm n = norm_args(c, d, a[4], a[5], a[6]);
+    const Axes x(c, d, a[7], a[8], "rope_pos");
+    const Pages pg = page_args(c, d, a[9], a[10]);
+    const int32_t *pos = index_arg(c, a[11], d.B, "pos"), *n_new = index_arg(c, a[12], d.B, "n_new", true);
+    const at::Tensor qo = c.output(a[13], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
+    c.done(gdn_kv_append_axes(&d, q.p, q.ts, q.hs, k.p, k.ts, k.hs, v.p, v.ts, v.hs, n.wq, n.wk, n.freqs,
+                              x.axis, x.n, x.pos, pg.c, pg.table,
                          pg.width, pos, n_new, bf16(qo), (gdn_stream)c.stream()));
     return THPVariable_Wrap(qo);
 }
@@ -515,6 +597,24 @@ PyObject *attn_prefill_backward(PyObject *const *a) {
     return t;
 }
 
+// (target, draft, tokens, u, n, tokens_out, keep, stream) -> (tokens_out, keep)
+PyObject *spec_verify(PyObject *const *a) {
+    Call c("gdn_spec_verify", a[7]);
+    const at::Tensor &t = c.tensor(a[0], at::kFloat, "target");
+    if (t.dim() != 3 || t.size(1) < 1 || t.size(0) > 0x7fffffff || t.size(1) > 0x7fffffff || t.size(2) > 0x7fffffff)
+        raise(PyExc_ValueError, "target must have shape (B, T + 1, V), got " + show(t.sizes()));
+    const int64_t B = t.size(0), T = t.size(1) - 1, V = t.size(2);
+    const auto *target = static_cast<float *>(c.address(t, "target"));
+    const auto *draft = static_cast<float *>(c.dense(a[1], at::kFloat, {B, T, V}, "draft", true));
+    const auto *tokens = static_cast<int32_t *>(c.dense(a[2], at::kInt, {B, T}, "tokens"));
+    const auto *u = static_cast<float *>(c.dense(a[3], at::kFloat, {B, T + 1}, "u"));
+    const int32_t *n = index_arg(c, a[4], B, "n", true);
+    const at::Tensor out = c.output(a[5], at::kInt, {B, T + 1}, "tokens_out"), keep = c.output(a[6], at::kInt, {B}, "keep");
+    c.done(gdn_spec_verify((int32_t)B, (int32_t)T, (int32_t)V, target, draft, tokens, u, n, static_cast<int32_t *>(data(out)),
+                           static_cast<int32_t *>(data(keep)), (gdn_stream)c.stream()));
+    return pair(out, keep);
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -538,7 +638,8 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(qk_norm_rope, 11), ENTRY(qk_norm_rope_backward, 16), ENTRY(kv_append, 13),
-                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13), ENTRY(attn_prefill, 15), ENTRY(attn_prefill_backward, 19),
+                         ENTRY(kv_read, 8), ENTRY(attn_decode, 13), ENTRY(qk_norm_rope_axes, 12), ENTRY(qk_norm_rope_axes_backward, 17),
+                         ENTRY(kv_append_axes, 15), ENTRY(spec_verify, 8), ENTRY(attn_prefill, 15), ENTRY(attn_prefill_backward, 19),
                          {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_attn_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

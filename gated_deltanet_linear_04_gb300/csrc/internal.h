@@ -181,6 +181,13 @@ struct HeadsIn {
     long long ts, hs;
 };
 
+// Positions on several axes: pos [n][B, T], and each pair's axis (device).
+struct AxesIn {
+    const uint8_t *axis = nullptr;   // null: one axis
+    int n = 0;
+    const int32_t *pos = nullptr;
+};
+
 // A paged cache with the rows' page table (layouts in gdn.h).
 struct PagedCache {
     void *k, *v;
@@ -193,19 +200,19 @@ struct PagedCache {
 
 cudaError_t launch_qk_norm_rope(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
                                 const float *wk, const uint64_t *freqs, const int32_t *pos, const uint8_t *mask,
-                                uint16_t *q_out, uint16_t *k_out, cudaStream_t st);
+                                uint16_t *q_out, uint16_t *k_out, cudaStream_t st, const AxesIn &axes = AxesIn());
 
 size_t qk_norm_rope_backward_workspace(const AttnSizes &s);
 cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
                                          const float *wk, const uint64_t *freqs, const int32_t *pos,
                                          const uint8_t *mask, const uint16_t *dq_out, const uint16_t *dk_out,
                                          uint16_t *dq, uint16_t *dk, float *dwq, float *dwk, void *ws,
-                                         cudaStream_t st);
+                                         cudaStream_t st, const AxesIn &axes = AxesIn());
 
 cudaError_t launch_kv_append(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
                              const float *wq, const float *wk, const uint64_t *freqs, const PagedCache &c,
                              const int32_t *pos, const int32_t *n_new, uint16_t *q_out, unsigned *err,
-                             cudaStream_t st);
+                             cudaStream_t st, const AxesIn &axes = AxesIn());
 
 cudaError_t launch_kv_read(const AttnSizes &s, const PagedCache &c, const int32_t *start, const int32_t *n,
                            uint16_t *k_out, uint16_t *v_out, unsigned *err, cudaStream_t st);
@@ -255,5 +262,8 @@ cudaError_t launch_attn_prefill_backward(const PromptSizes &s, const HeadsIn &q,
                                          const PromptSeqs &seqs, const HeadsIn &gate, float scale, const uint16_t *out,
                                          const float *lse, const uint16_t *dout, uint16_t *dq, uint16_t *dk, uint16_t *dv,
                                          uint16_t *dgate, void *ws, unsigned *err, cudaStream_t st);
+
+cudaError_t launch_spec_verify(int B, int T, int V, const float *target, const float *draft, const int32_t *tokens,
+                               const float *u, const int32_t *n, int32_t *tokens_out, int32_t *keep, cudaStream_t st);
 
 }  // namespace gdn

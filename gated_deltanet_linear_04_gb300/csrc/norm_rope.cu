@@ -39,7 +39,7 @@ struct RowParams {
     HeadsIn q, k, v;
     const float *wq, *wk;
     const uint64_t *freqs;
-    const int32_t *pos;     // dense: [B, T]; append: [B]
+    const int32_t *pos;     // dense: [B, T], null with several axes; append: [B]
     const uint8_t *mask;
     const int32_t *n_new;
     const uint16_t *dq_out, *dk_out;
@@ -47,6 +47,7 @@ struct RowParams {
     float *partial;            // backward: [2][gridDim.x][D]
     PagedCache c;
     unsigned *err;
+    AxesIn axes;               // of a pair's position, if there are several
     int B, T, Hq, Hkv, R;
     int cq, ck;                // parts of a token's heads: of q, of k (and of v)
     int aq, ak;                // backward: CTAs of a part of q, of k
@@ -172,13 +173,18 @@ __device__ __forceinline__ F2 partners(const Row &x, int k) {
 // a = cos and b = the sine with the sign of the channel's place in its pair
 // (`back`: of the opposite turn) of the lane's channels at a position; 1 and 0
 // for channels that do not turn.  The warp computes the angles together, into
-// its table; four entries behind them hold (1, 0).
+// its table; four entries behind them hold (1, 0).  With several axes a pair
+// turns by the token's position on its own.
 template <bool INTER>
-__device__ __forceinline__ void lane_angles(const RowParams &p, float2 *table, const Pieces &pc, long long pos,
-                                            bool back, Row &a, Row &b) {
+__device__ __forceinline__ void lane_angles(const RowParams &p, float2 *table, const Pieces &pc, unsigned bt,
+                                            long long pos, bool back, Row &a, Row &b) {
     const int lane = threadIdx.x & 31, half = p.R / 2;
     __syncwarp();   // (the previous token's readers)
-    for (int i = lane; i < half; i += 32) rope_angle(pos, p.freqs[i], table[i].x, table[i].y);
+    for (int i = lane; i < half; i += 32) {
+        long long at = pos;
+        if (p.axes.axis != nullptr) at = p.axes.pos[(long long)min((int)p.axes.axis[i], p.axes.n - 1) * p.B * p.T + bt];
+        rope_angle(at, p.freqs[i], table[i].x, table[i].y);
+    }
     if (lane < 4) table[half + lane] = make_float2(1.0f, 0.0f);
     __syncwarp();
     const float sg = back ? -1.0f : 1.0f;
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
     } else if (!on) {
         return;
     }
-    const long long pos = MODE == kDense ? p.pos[bt] : (long long)p.pos[b] + t;
+    const long long pos = MODE == kDense ? (p.pos != nullptr ? p.pos[bt] : 0) : (long long)p.pos[b] + t;
     long long at = -1;   // the cache row of head h0
     if (MODE != kDense && !isq) {
         at = cache_row(p.c, p.Hkv, p.c.table + (long long)b * p.c.width, pos, 0);
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
     Row A, B;
     const float *wp = isq ? p.wq : p.wk;
     const bool norm = !isv && wp != nullptr;
-    if (!isv) lane_angles<INTER>(p, tables[warp], pc, pos, false, A, B);
+    if (!isv) lane_angles<INTER>(p, tables[warp], pc, bt, pos, false, A, B);
     if (norm) {
         const Row w = load_weights(wp, pc);
 #pragma unroll
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
             continue;
         }
         Row a, b;
-        lane_angles<INTER>(p, tables[warp], pc, p.pos[bt], true, a, b);
+        lane_angles<INTER>(p, tables[warp], pc, bt, p.pos != nullptr ? p.pos[bt] : 0, true, a, b);
         cp_async_wait<1>();
         __syncwarp();
         const uint16_t *src = ring + stage * STAGE + sub * D;
@@ -646,8 +652,9 @@ struct BackwardGrid {
 
 cudaError_t launch_qk_norm_rope(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
                                 const float *wk, const uint64_t *freqs, const int32_t *pos, const uint8_t *mask,
-                                uint16_t *q_out, uint16_t *k_out, cudaStream_t st) {
+                                uint16_t *q_out, uint16_t *k_out, cudaStream_t st, const AxesIn &axes) {
     RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
+    p.axes = axes;
     p.mask = mask;
     p.q_out = q_out;
     p.k_out = k_out;
@@ -657,8 +664,9 @@ cudaError_t launch_qk_norm_rope(const AttnSizes &s, const HeadsIn &q, const Head
 cudaError_t launch_kv_append(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
                              const float *wq, const float *wk, const uint64_t *freqs, const PagedCache &c,
                              const int32_t *pos, const int32_t *n_new, uint16_t *q_out, unsigned *err,
-                             cudaStream_t st) {
+                             cudaStream_t st, const AxesIn &axes) {
     RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
+    p.axes = axes;
     p.v = v;
     p.c = c;
     p.n_new = n_new;
@@ -676,8 +684,9 @@ cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, c
                                          const float *wk, const uint64_t *freqs, const int32_t *pos,
                                          const uint8_t *mask, const uint16_t *dq_out, const uint16_t *dk_out,
                                          uint16_t *dq, uint16_t *dk, float *dwq, float *dwk, void *ws,
-                                         cudaStream_t st) {
+                                         cudaStream_t st, const AxesIn &axes) {
     RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
+    p.axes = axes;
     p.mask = mask;
     p.dq_out = dq_out;
     p.dk_out = dk_out;

@@ -1,0 +1,232 @@
+// Drafted tokens against the target's probabilities, from given random
+// numbers.  A drafted token x stands while u q(x) < p(x) (that is, with the
+// probability min(1, p / q)); the token after the last one that stands is drawn
+// from what the target has above the draft, max(p - q, 0), or from the target's
+// next row where all stand: the first token whose cumulative sum is above u
+// times the whole.  Tokens so kept and drawn are distributed as the target's.
+//
+// Two numbers are read for each drafted token; then one row of V probabilities
+// (two where a token fell) per batch row: HBM-bound.  A row is spread over a
+// cluster of CTAs, each warp has a contiguous piece and sums it; the sums meet
+// in distributed shared memory, and the warp whose piece holds the drawn token
+// goes over its piece once more.
+//
+// Sums are 64-bit integers in units of 2^-60: exact whatever their order, so
+// that a token does not depend on how a row is split.  Probabilities from 2^-37
+// on enter exactly, smaller ones rounded to the unit.
+//
+// B = 128, V = 131072: see the table of cases; one row of 32003: a launch and a
+// chain of five loads.
+#include <cooperative_groups.h>
+
+#include "attn.cuh"
+
+namespace gdn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kAhead = 8, kMostCtas = 8;
+
+struct Params {
+    const float *target, *draft, *u;
+    const int32_t *tokens, *n;
+    int32_t *out, *keep;
+    int T, V;
+};
+
+using Sum = unsigned long long;
+
+// A probability in units of 2^-60 (NaN and below 0: 0; above 1: 1).
+__device__ __forceinline__ Sum fixed(float p) {
+    Sum r;
+    asm("cvt.rni.u64.f32 %0, %1;" : "=l"(r) : "f"(fminf(p, 1.0f) * 0x1p60f));
+    return p == p ? r : 0ull;
+}
+
+// What is drawn from: p, or p above q, or p without one token.
+struct Rest {
+    const float *p, *q;
+    int without;
+    __device__ __forceinline__ Sum operator()(int i) const {
+        const Sum a = i == without ? 0ull : fixed(p[i]);
+        if (q == nullptr) return a;
+        const Sum b = fixed(q[i]);
+        return a > b ? a - b : 0ull;
+    }
+};
+
+__device__ __forceinline__ Sum warp_total(Sum v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The largest integer not above u * total, below total: a cumulative sum is
+// above u * total if it is above this.
+__device__ __forceinline__ Sum threshold(float u, Sum total) {
+    if (!(u > 0.0f)) return 0ull;
+    if (u >= 1.0f) return total - 1;
+    const uint32_t bits = __float_as_uint(u);
+    const int e = (int)(bits >> 23);
+    const Sum m = e == 0 ? bits : (bits & 0x7fffffu) | 0x800000u;
+    const int s = 150 - (e == 0 ? 1 : e);   // u = m 2^-s, s >= 24
+    const Sum hi = __umul64hi(m, total), lo = m * total;
+    if (s < 64) return (hi << (64 - s)) | (lo >> s);
+    return s < 128 ? hi >> (s - 64) : 0ull;
+}
+
+__global__ void __launch_bounds__(kThreads) spec_verify_kernel(const Params p) {
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ Sum sums[kMostCtas][kWarps];   // of all warps of the row's CTAs
+    __shared__ int stands;
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long b = blockIdx.x / ctas;
+    const int T = p.T, V = p.V;
+    attn::grid_dep_enter();
+    const float *target = p.target + b * (T + 1) * V, *draft = p.draft == nullptr ? nullptr : p.draft + b * T * V;
+    const int32_t *tokens = p.tokens + b * T;
+    const int n = p.n == nullptr ? T : min(max(p.n[b], 0), T);
+    if (warp == 0) {
+        int a = 0;
+        for (int t0 = 0; t0 < n; t0 += 32) {
+            const int t = t0 + lane;
+            bool ok = false;
+            if (t < n) {
+                const int x = tokens[t];
+                if (x >= 0 && x < V) {
+                    const float q = draft == nullptr ? 1.0f : draft[(long long)t * V + x];
+                    // (both sides exact in 64 bits)
+                    ok = (double)p.u[b * (T + 1) + t] * (double)q < (double)target[(long long)t * V + x];
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            const int run = __ffs(~m) - 1;   // (-1: all 32)
+            a += run < 0 ? 32 : run;
+            if (run >= 0) break;
+        }
+        if (lane == 0) stands = a < n ? a : n;
+    }
+    __syncthreads();
+    const int a = stands;
+    if (rank == 0) {
+        for (int t = threadIdx.x; t <= T; t += kThreads)
+            if (t != a) p.out[b * (T + 1) + t] = t < a ? tokens[t] : -1;
+        if (threadIdx.x == 0) p.keep[b] = a + 1;
+    }
+    Rest rest{target + (long long)a * V, a < n && draft != nullptr ? draft + (long long)a * V : nullptr,
+              a < n && draft == nullptr ? tokens[a] : -1};
+    // the warp's piece: whole lines of 32
+    const int pieces = ctas * kWarps, piece = rank * kWarps + warp;
+    const int each = (int)((((long long)V + 31) / 32 + pieces - 1) / pieces) * 32;
+    const int first = (int)min((long long)piece * each, (long long)V), last = (int)min((long long)first + each, (long long)V);
+    Sum total = 0, before = 0, mine = 0;
+    for (int round = 0; round < 2; ++round) {
+        Sum s = 0;
+        int i = first + lane;
+        for (; i + (kAhead - 1) * 32 < last; i += kAhead * 32) {
+            if (rest.q != nullptr) {
+                float x[kAhead], y[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    x[k] = __ldcs(rest.p + i + k * 32);
+                    y[k] = __ldcs(rest.q + i + k * 32);
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const Sum f = fixed(x[k]), g = fixed(y[k]);
+                    s += f > g ? f - g : 0ull;
+                }
+            } else {
+                float x[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) x[k] = __ldcs(rest.p + i + k * 32);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) s += i + k * 32 == rest.without ? 0ull : fixed(x[k]);
+            }
+        }
+        for (; i < last; i += 32) s += rest(i);
+        mine = warp_total(s);
+        if (lane < ctas) *cluster.map_shared_rank(&sums[rank][warp], lane) = mine;
+        cluster.sync();
+        total = before = 0;
+        for (int k = lane; k < pieces; k += 32) {
+            const Sum v = sums[k / kWarps][k % kWarps];
+            total += v;
+            if (k < piece) before += v;
+        }
+        total = warp_total(total);
+        before = warp_total(before);
+        cluster.sync();   // (the sums' readers, and no CTA leaves before its sums are written)
+        if (total != 0 || (rest.q == nullptr && rest.without < 0)) break;
+        rest.q = nullptr;   // nothing above the draft: the target itself
+        rest.without = -1;
+    }
+    int32_t *to = p.out + b * (T + 1) + a;
+    if (total == 0) {
+        if (piece == 0 && lane == 0) *to = 0;
+        return;
+    }
+    const Sum x = threshold(p.u[b * (T + 1) + T], total);
+    if (x < before || x >= before + mine) return;
+    // this piece: a contiguous part a lane, then the part's tokens
+    const int part = each / 32, p0 = first + lane * part;
+    Sum s = 0;
+    for (int i = p0; i < min(p0 + part, last); ++i) s += rest(i);
+    Sum upto = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    Sum c = before + upto - s;
+    if (x < c || x >= c + s) return;
+    for (int i = p0; i < min(p0 + part, last); ++i) {
+        c += rest(i);
+        if (c > x) {
+            *to = i;
+            return;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_spec_verify(int B, int T, int V, const float *target, const float *draft, const int32_t *tokens,
+                               const float *u, const int32_t *n, int32_t *tokens_out, int32_t *keep, cudaStream_t st) {
+    const Params p{target, draft, u, tokens, n, tokens_out, keep, T, V};
+    // two CTAs an SM or more, no more than a piece of 256 tokens for each warp
+    int ctas = 1;
+    while (ctas < kMostCtas && (long long)B * ctas < 4LL * num_sms() && (long long)ctas * 2 * kWarps * 256 <= V + 8191) ctas *= 2;
+    if ((long long)B * ctas > 0x7fffffffLL) return cudaErrorNotSupported;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(B * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, spec_verify_kernel, p);
+}
+
+}  // namespace gdn
+
+extern "C" gdn_status gdn_spec_verify(int32_t B, int32_t T, int32_t V, const float *target, const float *draft,
+                                      const int32_t *tokens, const float *u, const int32_t *n, int32_t *tokens_out,
+                                      int32_t *keep, gdn_stream stream) {
+    auto ok = [](const void *p, bool needed) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && (!needed || p != nullptr); };
+    if (B < 0 || T < 0 || V <= 0) return GDN_ERR_INVALID_ARG;
+    if (T > 1023 || V > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    const bool some = B > 0;
+    if (!ok(target, some) || !ok(draft, false) || !ok(tokens, some && T > 0) || !ok(u, some) || !ok(n, false) ||
+        !ok(tokens_out, some) || !ok(keep, some))
+        return GDN_ERR_INVALID_ARG;
+    if (!some) return GDN_OK;
+    const cudaError_t e = gdn::launch_spec_verify(B, T, V, target, draft, tokens, u, n, tokens_out, keep, (cudaStream_t)stream);
+    return e == cudaSuccess ? GDN_OK : e == cudaErrorNotSupported ? GDN_ERR_UNSUPPORTED : GDN_ERR_CUDA;
+}

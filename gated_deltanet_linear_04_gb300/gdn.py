@@ -90,6 +90,11 @@ _SIGS = {
     "gdn_attn_decode_workspace_size": (ctypes.c_size_t, _ATTN),
     "gdn_attn_decode": (ctypes.c_int, _ATTN + [_P] + _CACHE + [_P] * 2 + _HEADS + [ctypes.c_float] + [_P] * 3 +
                         [ctypes.c_size_t, _P]),
+    "gdn_qk_norm_rope_axes": (ctypes.c_int, _ATTN + _HEADS * 2 + [_P] * 4 + [ctypes.c_int32] + [_P] * 5),
+    "gdn_qk_norm_rope_axes_backward": (ctypes.c_int, _ATTN + _HEADS * 2 + [_P] * 4 + [ctypes.c_int32] + [_P] * 9 +
+                                       [ctypes.c_size_t, _P]),
+    "gdn_kv_append_axes": (ctypes.c_int, _ATTN + _HEADS * 3 + [_P] * 4 + [ctypes.c_int32, _P] + _CACHE + [_P] * 4),
+    "gdn_spec_verify": (ctypes.c_int, [ctypes.c_int32] * 3 + [_P] * 8),
     "gdn_attn_prefill_workspace_size": (ctypes.c_size_t, _ROWS),
     "gdn_attn_prefill": (ctypes.c_int, _ROWS + _HEADS * 3 + [_P] * 4 + _HEADS + [ctypes.c_float] + [_P] * 3 +
                          [ctypes.c_size_t, _P]),

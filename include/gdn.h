@@ -513,6 +513,36 @@ GDN_API gdn_status gdn_kv_append(const gdn_attn_dims *dims, const uint16_t *q, i
                                  const gdn_kv_cache *cache, const int32_t *page_table, int32_t table_width,
                                  const int32_t *pos, const int32_t *n_new, uint16_t *q_out, gdn_stream stream);
 
+/* gdn_qk_norm_rope, its gradients and gdn_kv_append with positions on several axes
+ * (the time, height and width of an image's or a video's patches): pair i turns
+ * by the token's position on axis axes[i].
+ *   axes   u8 [Drot/2] (in): values from n_axes on count as n_axes - 1; not NULL
+ *          when Drot > 0
+ *   n_axes 1..8
+ *   pos    i32 [n_axes, B, T] (in): the position of every token on every axis;
+ *          rope_pos likewise, beside gdn_kv_append's pos, which says where in
+ *          the cache the tokens go
+ * Everything else as above; one axis gives the same bits. */
+GDN_API gdn_status gdn_qk_norm_rope_axes(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                         int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                         int64_t k_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
+                                         const uint8_t *axes, int32_t n_axes, const int32_t *pos, const uint8_t *mask,
+                                         uint16_t *q_out, uint16_t *k_out, gdn_stream stream);
+GDN_API gdn_status gdn_qk_norm_rope_axes_backward(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                                  int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                                  int64_t k_head_stride, const float *wq, const float *wk,
+                                                  const uint64_t *freqs, const uint8_t *axes, int32_t n_axes,
+                                                  const int32_t *pos, const uint8_t *mask, const uint16_t *dq_out,
+                                                  const uint16_t *dk_out, uint16_t *dq, uint16_t *dk, float *dwq,
+                                                  float *dwk, void *workspace, size_t ws_bytes, gdn_stream stream);
+GDN_API gdn_status gdn_kv_append_axes(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                                      int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                      int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
+                                      int64_t v_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
+                                      const uint8_t *axes, int32_t n_axes, const int32_t *rope_pos,
+                                      const gdn_kv_cache *cache, const int32_t *page_table, int32_t table_width,
+                                      const int32_t *pos, const int32_t *n_new, uint16_t *q_out, gdn_stream stream);
+
 /* Positions start[b] .. start[b] + T - 1 of every row read back as bf16 (of an
  * e4m3 cache exactly: code * 2^e is a bf16 value, but where it underflows).
  *   start  i32 [B] (in);  n i32 [B] or NULL (= T): steps from n[b] on are zeros
@@ -626,6 +656,36 @@ GDN_API gdn_status gdn_attn_prefill_backward(const gdn_attn_dims *dims, int64_t 
                                              float scale, const uint16_t *out, const float *lse, const uint16_t *dout,
                                              uint16_t *dq, uint16_t *dk, uint16_t *dv, uint16_t *dgate, void *workspace,
                                              size_t ws_bytes, gdn_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens
+ * ------------------------------------------------------------------------
+ * Which of a row's drafted tokens stand, and the token after them, by given
+ * random numbers, so that what comes out is distributed as the target's own:
+ * drafted token x_t stands while all before it do and u_t q_t(x_t) < p_t(x_t).
+ * With a of n standing, the next token is drawn from max(p_a - q_a, 0) (from p_a
+ * itself where that is all zeros), or for a = n from p_n: the first token whose
+ * cumulative sum is above u_T times the whole row's.  (a = the accepted tokens of
+ * a window of gdn_decode_window or gdn_attn_decode that held the last token and
+ * the drafts: a + 1 of its tokens are kept.)
+ *   target f32 [B, T + 1, V] (in): the target's probabilities p_0 .. p_T
+ *   draft  f32 [B, T, V] or NULL: the draft's q_0 .. q_(T-1); NULL: tokens from a
+ *          lookup, certain to the draft (q = 1 at the token, 0 elsewhere)
+ *   tokens i32 [B, T] (in): a token outside [0, V) does not stand
+ *   u      f32 [B, T + 1] (in): in [0, 1); the last one draws the next token,
+ *          whatever n is
+ *   n      i32 [B] or NULL (= T): drafted tokens of a row, clamped to [0, T]
+ *   tokens_out i32 [B, T + 1] (out): the standing tokens, the next one, then -1
+ *   keep   i32 [B] (out): a + 1, the tokens of tokens_out that are there and
+ *          gdn_decode_window's keep
+ * 0 <= T <= 1023, 1 <= V <= 2^24, else GDN_ERR_UNSUPPORTED.  Rows are dense and
+ * need only 4-byte alignment.  Probabilities count as their nearest value in [0,
+ * 1] (NaN as 0); a row's sum must be below 16, else its token is some token in
+ * [0, V).  A row of zeros draws token 0.  Comparisons are exact, sums are exact
+ * in units of 2^-60: equal calls give equal tokens. */
+GDN_API gdn_status gdn_spec_verify(int32_t B, int32_t T, int32_t V, const float *target, const float *draft,
+                                   const int32_t *tokens, const float *u, const int32_t *n, int32_t *tokens_out,
+                                   int32_t *keep, gdn_stream stream);
 
 /* ABI version of this header (incremented on any signature change). */
 GDN_API int gdn_abi_version(void);
