@@ -56,6 +56,7 @@ bool ok_norm(const AttnSizes &s, const float *wq, const float *wk, const uint64_
 // [rows, H, D] views of a prompt: tensor maps take no stride of 0.
 gdn_status check_rows(const HeadsIn &h, long long rows, int H) {
     if (!ok_heads(h, (size_t)rows)) return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
     const long long most = 1LL << 39;   // (elements: a tensor map's strides are below 2^40 bytes)
     if ((rows > 1 && (h.ts == 0 || h.ts >= most)) || (H > 1 && (h.hs == 0 || h.hs >= most))) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

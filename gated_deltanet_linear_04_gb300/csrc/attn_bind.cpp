@@ -100,6 +100,11 @@ struct Call {
         return address(t, name);
     }
 
+    // its type and shape alone (what is wrong with them is said before where it is)
+    void sized(PyObject *o, at::ScalarType type, Shape want, const char *name, bool optional = false) {
+        if (!optional || o != Py_None) shaped(tensor(o, type, name), want, name);
+    }
+
     void *address(const at::Tensor &t, const char *name) {
         if (t.numel() == 0) return nullptr;
         placed(t, name);
@@ -144,9 +149,6 @@ struct Call {
             if (t.size(1) > 0x7fffffff) raise(PyExc_ValueError, std::string(name) + ": too many tokens");
             return {heads(o, e, H, name), (int64_t)d.B * t.size(1), t.size(1)};
         }
-        if (t.dim() != 3)
-            raise(PyExc_ValueError, std::string(name) + " must have shape (B, T, heads, D), or (N, heads, D) with offsets, got " +
-                                        show(t.sizes()));
         shaped(t, {t.size(0), H, d.D}, name);
         if (t.numel() == 0) return {{nullptr, 0, 0}, t.size(0), -1};
         const int64_t ts = t.size(0) > 1 ? t.stride(0) : 0, hs = H > 1 ? t.stride(1) : 0;
@@ -312,12 +314,13 @@ struct Axes {
     const int32_t *pos;
 
     Axes(Call &c, const gdn_attn_dims &d, PyObject *axes, PyObject *pos, const char *name) {
-        axis = static_cast<uint8_t *>(c.dense(axes, at::kByte, {d.Drot / 2}, "axes"));
+        c.sized(axes, at::kByte, {d.Drot / 2}, "axes");
         const at::Tensor &t = c.tensor(pos, at::kInt, name);
         if (t.dim() != 3 || t.size(0) < 1 || t.size(0) > 8)
             raise(PyExc_ValueError, std::string(name) + " must have shape (axes, B, T) with 1 to 8 axes, got " + show(t.sizes()));
         c.shaped(t, {t.size(0), d.B, d.T}, name);
         n = (int32_t)t.size(0);
+        axis = static_cast<uint8_t *>(c.dense(axes, at::kByte, {d.Drot / 2}, "axes"));
         this->pos = static_cast<int32_t *>(c.address(t, name));
     }
 };
@@ -341,9 +344,9 @@ PyObject *qk_norm_rope(PyObject *const *a) {
 PyObject *qk_norm_rope_axes(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
     Call c("gdn_qk_norm_rope_axes", a[11]);
+    const Axes x(c, d, a[6], a[7], "pos");
     const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k");
     const Norm n = norm_args(c, d, a[3], a[4], a[5]);
-    const Axes x(c, d, a[6], a[7], "pos");
     const auto *mask = static_cast<uint8_t *>(c.dense(a[8], at::kByte, {d.B, d.T}, "mask", true));
     const at::Tensor qo = c.output(a[9], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
     const at::Tensor ko = c.output(a[10], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "k_out");
@@ -390,9 +393,9 @@ PyObject *qk_norm_rope_backward(PyObject *const *a) {
 PyObject *qk_norm_rope_axes_backward(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
     Call c("gdn_qk_norm_rope_axes_backward", a[16]);
+    const Axes x(c, d, a[6], a[7], "pos");
     const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k");
     const Norm n = norm_args(c, d, a[3], a[4], a[5]);
-    const Axes x(c, d, a[6], a[7], "pos");
     const auto *mask = static_cast<uint8_t *>(c.dense(a[8], at::kByte, {d.B, d.T}, "mask", true));
     const auto *dqo = static_cast<uint16_t *>(c.dense(a[9], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "dq_out"));
     const auto *dko = static_cast<uint16_t *>(c.dense(a[10], at::kBFloat16, {d.B, d.T, d.Hkv, d.D}, "dk_out"));
@@ -437,9 +440,9 @@ PyObject *kv_append(PyObject *const *a) {
 PyObject *kv_append_axes(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
     Call c("gdn_kv_append_axes", a[14]);
+    const Axes x(c, d, a[7], a[8], "rope_pos");
     const auto q = c.heads(a[1], d, d.Hq, "q"), k = c.heads(a[2], d, d.Hkv, "k"), v = c.heads(a[3], d, d.Hkv, "v");
     const Norm n = norm_args(c, d, a[4], a[5], a[6]);
-    const Axes x(c, d, a[7], a[8], "rope_pos");
     const Pages pg = page_args(c, d, a[9], a[10]);
     const int32_t *pos = index_arg(c, a[11], d.B, "pos"), *n_new = index_arg(c, a[12], d.B, "n_new", true);
     const at::Tensor qo = c.output(a[13], at::kBFloat16, {d.B, d.T, d.Hq, d.D}, "q_out");
@@ -489,22 +492,51 @@ struct Prompt {
     Call::Rows q, k, v;
     const int32_t *cu_q, *cu_k, *n_q, *n_k;
 
+    // rows, and tokens of a slot or -1 if packed
+    struct Extent {
+        int64_t n, t;
+        Extent(Call &c, PyObject *o, const gdn_attn_dims &d, int64_t H, const char *name) {
+            const at::Tensor &x = c.tensor(o, at::kBFloat16, name);
+            if (x.dim() == 4) {
+                c.shaped(x, {d.B, x.size(1), H, d.D}, name);
+                n = d.B * x.size(1);
+                t = x.size(1);
+            } else if (x.dim() == 3) {
+                c.shaped(x, {x.size(0), H, d.D}, name);
+                n = x.size(0);
+                t = -1;
+            } else {
+                raise(PyExc_ValueError, std::string(name) + " must have shape (B, T, heads, D), or (N, heads, D) with offsets, got " +
+                                            show(x.sizes()));
+            }
+        }
+    };
+
     Prompt(Call &c, const gdn_attn_dims &d, PyObject *qo, PyObject *ko, PyObject *vo, PyObject *cuq, PyObject *cuk,
-           PyObject *nq, PyObject *nk) {
+           PyObject *nq, PyObject *nk, PyObject *gate) {
+        const Extent eq(c, qo, d, d.Hq, "q"), ek(c, ko, d, d.Hkv, "k"), ev(c, vo, d, d.Hkv, "v");
+        if (eq.t >= 0 && eq.t != d.T)
+            raise(PyExc_ValueError, "q must have shape (B, T, heads, D) of the dims, got " + std::to_string(eq.t) + " tokens");
+        if (ev.n != ek.n || ev.t != ek.t) raise(PyExc_ValueError, "k and v must have the same shape");
+        if ((eq.t < 0) != (cuq != Py_None))
+            raise(PyExc_ValueError, eq.t < 0 ? "packed q needs cu_q" : "cu_q goes with packed q (N, heads, D)");
+        if (ek.t < 0 && cuk == Py_None) {
+            if (cuq == Py_None) raise(PyExc_ValueError, "packed k needs cu_k");
+            cuk = cuq;
+        } else if (ek.t >= 0 && cuk != Py_None) {
+            raise(PyExc_ValueError, "cu_k goes with packed k (N, heads, D)");
+        }
+        c.sized(cuq, at::kInt, {(int64_t)d.B + 1}, "cu_q", true);
+        c.sized(cuk, at::kInt, {(int64_t)d.B + 1}, "cu_k", true);
+        c.sized(nq, at::kInt, {d.B}, "n_q", true);
+        c.sized(nk, at::kInt, {d.B}, "n_k", true);
+        if (gate != Py_None) {
+            const Extent eg(c, gate, d, d.Hq, "gate");
+            if (eg.n != eq.n || eg.t != eq.t) raise(PyExc_ValueError, "gate must have q's shape");
+        }
         q = c.rows(qo, d, d.Hq, "q");
         k = c.rows(ko, d, d.Hkv, "k");
         v = c.rows(vo, d, d.Hkv, "v");
-        if (q.t >= 0 && q.t != d.T)
-            raise(PyExc_ValueError, "q must have shape (B, T, heads, D) of the dims, got " + std::to_string(q.t) + " tokens");
-        if (v.n != k.n || v.t != k.t) raise(PyExc_ValueError, "k and v must have the same shape");
-        if ((q.t < 0) != (cuq != Py_None))
-            raise(PyExc_ValueError, q.t < 0 ? "packed q needs cu_q" : "cu_q goes with packed q (N, heads, D)");
-        if (k.t < 0 && cuk == Py_None) {
-            if (cuq == Py_None) raise(PyExc_ValueError, "packed k needs cu_k");
-            cuk = cuq;
-        } else if (k.t >= 0 && cuk != Py_None) {
-            raise(PyExc_ValueError, "cu_k goes with packed k (N, heads, D)");
-        }
         cu_q = index_arg(c, cuq, (int64_t)d.B + 1, "cu_q", true);
         cu_k = index_arg(c, cuk, (int64_t)d.B + 1, "cu_k", true);
         n_q = index_arg(c, nq, d.B, "n_q", true);
@@ -533,19 +565,17 @@ double number(PyObject *o) {
     return x;
 }
 
-Call::Heads gate_arg(Call &c, const gdn_attn_dims &d, const Prompt &p, PyObject *o) {
+Call::Heads gate_arg(Call &c, const gdn_attn_dims &d, PyObject *o) {
     if (o == Py_None) return {nullptr, 0, 0};
-    const Call::Rows g = c.rows(o, d, d.Hq, "gate");
-    if (g.n != p.q.n || g.t != p.q.t) raise(PyExc_ValueError, "gate must have q's shape");
-    return g.h;
+    return c.rows(o, d, d.Hq, "gate").h;
 }
 
 // (dims, q, k, v, cu_q, cu_k, n_q, n_k, gate, scale, out, lse, want_lse, workspace, stream) -> out or (out, lse)
 PyObject *attn_prefill(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
     Call c("gdn_attn_prefill", a[14]);
-    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
-    const Call::Heads gate = gate_arg(c, d, p, a[8]);
+    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]);
+    const Call::Heads gate = gate_arg(c, d, a[8]);
     const double scale = number(a[9]);
     const at::Tensor out = p.like_q(c, a[10], d, "out");
     at::Tensor lse;
@@ -568,8 +598,8 @@ PyObject *attn_prefill(PyObject *const *a) {
 PyObject *attn_prefill_backward(PyObject *const *a) {
     const gdn_attn_dims &d = *at_address<gdn_attn_dims>(a[0]);
     Call c("gdn_attn_prefill_backward", a[18]);
-    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
-    const Call::Heads gate = gate_arg(c, d, p, a[8]);
+    const Prompt p(c, d, a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]);
+    const Call::Heads gate = gate_arg(c, d, a[8]);
     const bool gated = a[8] != Py_None;
     const double scale = number(a[9]);
     const auto *out = static_cast<uint16_t *>(p.dense_q(c, a[10], d, at::kBFloat16, true, "out"));
@@ -604,6 +634,10 @@ PyObject *spec_verify(PyObject *const *a) {
     if (t.dim() != 3 || t.size(1) < 1 || t.size(0) > 0x7fffffff || t.size(1) > 0x7fffffff || t.size(2) > 0x7fffffff)
         raise(PyExc_ValueError, "target must have shape (B, T + 1, V), got " + show(t.sizes()));
     const int64_t B = t.size(0), T = t.size(1) - 1, V = t.size(2);
+    c.sized(a[1], at::kFloat, {B, T, V}, "draft", true);
+    c.sized(a[2], at::kInt, {B, T}, "tokens");
+    c.sized(a[3], at::kFloat, {B, T + 1}, "u");
+    c.sized(a[4], at::kInt, {B}, "n", true);
     const auto *target = static_cast<float *>(c.address(t, "target"));
     const auto *draft = static_cast<float *>(c.dense(a[1], at::kFloat, {B, T, V}, "draft", true));
     const auto *tokens = static_cast<int32_t *>(c.dense(a[2], at::kInt, {B, T}, "tokens"));

@@ -492,8 +492,10 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         const int tile = ALONE ? warp >> 2 : 0, half = ALONE ? 0 : warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D + half * DH;
         uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
-        const float f2 = fabsf(p.scale2);
-        const bool negative = p.scale2 < 0.0f;
+        // (the scores' maximum is taken before the scale: a negative one turns them round; one of 0 would make NaN of the
+        // -infinity of those that are not seen)
+        const float turn_by = p.scale2 < 0.0f ? -1.0f : 0.0f, f2 = p.scale2 == 0.0f ? 1.0f : fabsf(p.scale2);
+        const bool turned = !(p.scale2 > 0.0f);
         int step = 0;
         do {
             const RowOut o = row_out<D>(p, w.u, w.head, tile, r);
@@ -510,9 +512,9 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 const int lim = o.keys - i * kKeys - half * 64;
                 const bool masked = __any_sync(0xffffffffu, lim < COLS);
                 auto scores_of = [&](float (&s)[32], int c) {   // (after the load)
-                    if (negative) {
+                    if (turned) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = -s[k];
+                        for (int k = 0; k < 32; ++k) s[k] *= turn_by;
                     }
                     if (masked) hide(s, lim - c * 32);
                 };
