@@ -744,12 +744,15 @@ __global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams
     }
 }
 
+// A tile's start and end in steps (T = 8192: 2 1888 us, 6 1640, 9 1570, 12 1575; packed, 128 channels: 523, 463, 459, 463).
+constexpr int kBlank = 9;
+
 PromptList q_list(const PromptSizes &s) {
-    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, 2};
+    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, kBlank};
 }
 
 PromptList k_list(const PromptSizes &s) {
-    return PromptList{true, 128, kRows / (s.Hq / s.Hkv), num_sms(), 4, 2};
+    return PromptList{true, 128, kRows / (s.Hq / s.Hkv), num_sms(), 4, kBlank};
 }
 
 struct Workspace {

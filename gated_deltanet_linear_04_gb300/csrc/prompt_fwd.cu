@@ -690,7 +690,9 @@ int tiles_of(int D) { return D <= 128 ? 2 : 1; }
 
 PromptList list_of(const PromptSizes &s) {
     const int tpt = 128 / (s.Hq / s.Hkv);
-    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4, 2};
+    // A tile's start and end in steps (T = 8192, 256 channels: 2 481 us, 4 380, 6 351, 8 355; packed, 128 channels: 2 445,
+    // 4 460, 6 468: with two tiles one's end runs beside the other's steps).
+    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4, s.D == 256 ? 6 : 2};
 }
 
 struct Workspace {

@@ -13,7 +13,7 @@
 //
 // Sums are 64-bit integers in units of 2^-60: exact whatever their order, so
 // that a token does not depend on how a row is split.  Probabilities from 2^-37
-// on enter exactly, smaller ones rounded to the unit.
+// on enter exactly, of smaller ones whole units.
 //
 // B = 128, V = 131072: see the table of cases; one row of 32003: a launch and a
 // chain of five loads.
@@ -26,7 +26,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kAhead = 8, kMostCtas = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kAhead = 8, kBatch = 32 * kAhead, kMostCtas = 8;
 
 struct Params {
     const float *target, *draft, *u;
@@ -37,29 +37,37 @@ struct Params {
 
 using Sum = unsigned long long;
 
-// A probability in units of 2^-60 (NaN and below 0: 0; above 1: 1).
+// A probability within [0, 1].
+__device__ __forceinline__ float clamped(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }   // (NaN: 0)
+
+// ... in units of 2^-60, what is below them cut off: its 24 bits shifted to their place.  (A conversion to 64-bit
+// integers takes this GPU's few double-precision units: with it the largest case took 73 us.)
 __device__ __forceinline__ Sum fixed(float p) {
-    Sum r;
-    asm("cvt.rni.u64.f32 %0, %1;" : "=l"(r) : "f"(fminf(p, 1.0f) * 0x1p60f));
-    return p == p ? r : 0ull;
+    const uint32_t b = __float_as_uint(p);
+    return ((Sum)((b & 0x7fffffu) | 0x800000u) << 37) >> min(127u - (b >> 23), 63u);
 }
 
 // What is drawn from: p, or p above q, or p without one token.
 struct Rest {
     const float *p, *q;
     int without;
-    __device__ __forceinline__ Sum operator()(int i) const {
-        const Sum a = i == without ? 0ull : fixed(p[i]);
-        if (q == nullptr) return a;
-        const Sum b = fixed(q[i]);
-        return a > b ? a - b : 0ull;
-    }
 };
 
 __device__ __forceinline__ Sum warp_total(Sum v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// The sum of the lanes before.
+__device__ __forceinline__ Sum warp_before(Sum v) {
+    Sum s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum y = __shfl_up_sync(0xffffffffu, s, o);
+        if ((threadIdx.x & 31) >= o) s += y;
+    }
+    return s - v;
 }
 
 // The largest integer not above u * total, below total: a cumulative sum is
@@ -76,7 +84,7 @@ __device__ __forceinline__ Sum threshold(float u, Sum total) {
     return s < 128 ? hi >> (s - 64) : 0ull;
 }
 
-__global__ void __launch_bounds__(kThreads) spec_verify_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p) {
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Sum sums[kMostCtas][kWarps];   // of all warps of the row's CTAs
     __shared__ int stands;
@@ -116,37 +124,45 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const Params p) {
     }
     Rest rest{target + (long long)a * V, a < n && draft != nullptr ? draft + (long long)a * V : nullptr,
               a < n && draft == nullptr ? tokens[a] : -1};
-    // the warp's piece: whole lines of 32
+    // the warp's piece, in up to 32 chunks of whole batches; lane c remembers chunk c's sum
     const int pieces = ctas * kWarps, piece = rank * kWarps + warp;
-    const int each = (int)((((long long)V + 31) / 32 + pieces - 1) / pieces) * 32;
-    const int first = (int)min((long long)piece * each, (long long)V), last = (int)min((long long)first + each, (long long)V);
-    Sum total = 0, before = 0, mine = 0;
-    for (int round = 0; round < 2; ++round) {
-        Sum s = 0;
-        int i = first + lane;
-        for (; i + (kAhead - 1) * 32 < last; i += kAhead * 32) {
-            if (rest.q != nullptr) {
-                float x[kAhead], y[kAhead];
+    const int batches = (V + kBatch - 1) / kBatch, each = (batches + pieces - 1) / pieces;
+    const int chunk = (each + 31) / 32 * kBatch;
+    const long long start = (long long)piece * each * kBatch;
+    const int first = (int)min(start, (long long)V), last = (int)min(start + (long long)each * kBatch, (long long)V);
+    // the batch of 32 x kAhead tokens from i: token i + 32 k + lane in v[k]
+    auto batch = [&](int i, Sum (&v)[kAhead]) {
+        float x[kAhead], y[kAhead];
+        const bool full = i + kBatch <= last;
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    x[k] = __ldcs(rest.p + i + k * 32);
-                    y[k] = __ldcs(rest.q + i + k * 32);
-                }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const Sum f = fixed(x[k]), g = fixed(y[k]);
-                    s += f > g ? f - g : 0ull;
-                }
-            } else {
-                float x[kAhead];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) x[k] = __ldcs(rest.p + i + k * 32);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) s += i + k * 32 == rest.without ? 0ull : fixed(x[k]);
-            }
+        for (int k = 0; k < kAhead; ++k) {
+            const int at = i + k * 32 + lane;
+            const bool there = full || at < last;
+            x[k] = there ? rest.p[at] : 0.0f;
+            y[k] = there && rest.q != nullptr ? rest.q[at] : 0.0f;
         }
-        for (; i < last; i += 32) s += rest(i);
-        mine = warp_total(s);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float p1 = i + k * 32 + lane == rest.without ? 0.0f : clamped(x[k]);
+            v[k] = fixed(p1);
+            if (rest.q != nullptr) v[k] -= fixed(fminf(p1, clamped(y[k])));   // p - min(p, q)
+        }
+    };
+    Sum total = 0, before = 0, mine = 0, of_chunk = 0;
+    for (int round = 0; round < 2; ++round) {
+        of_chunk = 0;
+        for (int c = 0, i = first; i < last; ++c) {
+            Sum s = 0;
+            for (const int end = min(i + chunk, last); i < end; i += kBatch) {
+                Sum v[kAhead];
+                batch(i, v);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) s += v[k];
+            }
+            s = warp_total(s);
+            if (lane == c) of_chunk = s;
+        }
+        mine = warp_total(of_chunk);
         if (lane < ctas) *cluster.map_shared_rank(&sums[rank][warp], lane) = mine;
         cluster.sync();
         total = before = 0;
@@ -169,23 +185,23 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const Params p) {
     }
     const Sum x = threshold(p.u[b * (T + 1) + T], total);
     if (x < before || x >= before + mine) return;
-    // this piece: a contiguous part a lane, then the part's tokens
-    const int part = each / 32, p0 = first + lane * part;
-    Sum s = 0;
-    for (int i = p0; i < min(p0 + part, last); ++i) s += rest(i);
-    Sum upto = s;
+    // this piece: the chunk, then the batch's lines of 32, then the lane
+    Sum c = before + warp_before(of_chunk);
+    const int hit = __ffs(__ballot_sync(0xffffffffu, x >= c && x < c + of_chunk)) - 1;
+    c = __shfl_sync(0xffffffffu, c, hit);
+    const int end = min(first + (hit + 1) * chunk, last);
+    for (int i = first + hit * chunk; i < end; i += kBatch) {
+        Sum v[kAhead];
+        batch(i, v);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Sum y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-    }
-    Sum c = before + upto - s;
-    if (x < c || x >= c + s) return;
-    for (int i = p0; i < min(p0 + part, last); ++i) {
-        c += rest(i);
-        if (c > x) {
-            *to = i;
-            return;
+        for (int k = 0; k < kAhead; ++k) {
+            const Sum line = warp_total(v[k]);
+            if (x < c + line) {
+                const Sum upto = c + warp_before(v[k]);
+                if (x >= upto && x < upto + v[k]) *to = i + k * 32 + lane;
+                return;
+            }
+            c += line;
         }
     }
 }
@@ -195,9 +211,10 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const Params p) {
 cudaError_t launch_spec_verify(int B, int T, int V, const float *target, const float *draft, const int32_t *tokens,
                                const float *u, const int32_t *n, int32_t *tokens_out, int32_t *keep, cudaStream_t st) {
     const Params p{target, draft, u, tokens, n, tokens_out, keep, T, V};
-    // two CTAs an SM or more, no more than a piece of 256 tokens for each warp
-    int ctas = 1;
-    while (ctas < kMostCtas && (long long)B * ctas < 4LL * num_sms() && (long long)ctas * 2 * kWarps * 256 <= V + 8191) ctas *= 2;
+    // one wave of two CTAs an SM, a batch for every warp at least
+    const int room = 2 * num_sms() / B, full = (V + kWarps * kBatch - 1) / (kWarps * kBatch);
+    int ctas = room < full ? room : full;
+    ctas = ctas < 1 ? 1 : ctas > kMostCtas ? kMostCtas : ctas;
     if ((long long)B * ctas > 0x7fffffffLL) return cudaErrorNotSupported;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
