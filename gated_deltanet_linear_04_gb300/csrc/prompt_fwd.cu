@@ -42,8 +42,8 @@ struct Geo {
     static constexpr int QTILE = D / 64 * SUB;
     // a stage of the ring: 64 channels of 128 keys, or all channels of VK values
     static constexpr int STAGE = SUB, STAGES = D == 256 ? 9 : 8, PER_STEP = D / 64, VK = 128 * 64 / D;
-    static constexpr int HALVES = 2 / TILES;               // warpgroups that share a tile's softmax
-    static constexpr int WARPS = 8;
+    static constexpr int HALVES = 2;                       // warpgroups that share a tile's softmax: 64 keys of a step each
+    static constexpr int WARPS = 4 * HALVES * TILES;
     static constexpr int THREADS = 32 * (WARPS + 2);
     static constexpr int TURN = 32 * 32;                   // bytes in which a warp turns 16 channels of its rows into rows
     static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + WARPS * TURN + 1024;
@@ -65,7 +65,7 @@ struct Params {
 
 struct Bars {
     uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2];
-    float most[2][2][128];   // [step parity][half][row]: what the halves of a row tell each other
+    float most[2][2][2][128];   // [tile][step parity][half][row]: what the halves of a row tell each other
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -75,7 +75,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // The two warpgroups of a tile meet.
-__device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void pair_sync(int tile) {
+    if (tile == 0)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+    else
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+}
 
 // Scores that are not to be seen (from `lim` on) are -infinity.
 __device__ __forceinline__ void hide(float (&s)[32], int lim) {
@@ -381,8 +386,10 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             const uint64_t b = d_values + (uint32_t)(s * (G::STAGE >> 4));
 #pragma unroll
             for (int k = 0; k < G::VK / 32; ++k)
-                umma::warp_mma_bf16_tmem_a_k32(base + t * D, base + G::S_COL + buf * 128 + c * (G::VK / 2) + k * 16,
-                                               b + k * (4096 >> 4), id_o, acc || c > 0 || k > 0);
+                // (P of 64 keys lies over the first half of their scores)
+                umma::warp_mma_bf16_tmem_a_k32(
+                    base + t * D, base + G::S_COL + buf * 128 + (c * G::VK + k * 32) / 64 * 64 + (c * G::VK + k * 32) % 64 / 2,
+                    b + k * (4096 >> 4), id_o, acc || c > 0 || k > 0);
         };
         w.uniform();
         Walk x = w;
@@ -484,12 +491,12 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         for (int i = G::TILES == 1 && step > 1 ? step - 2 : step - 1; i < step; ++i)
             for (int t = 0; t < G::TILES; ++t) wait(o_done(t, i), o_phase(i));
     } else if (any) {
-        // ---- softmax and results.  One tile: two warpgroups, each with half of a step's keys and half of the channels;
-        // the scores stay in registers.  Two tiles: a warpgroup each; the scores are read twice, for their maximum and for
-        // the weights (128 of them in registers do not leave room for the rest).
-        constexpr bool ALONE = G::HALVES == 1;
-        constexpr int COLS = 128 / G::HALVES, DH = D / G::HALVES;
-        const int tile = ALONE ? warp >> 2 : 0, half = ALONE ? 0 : warp >> 2, r = (warp & 3) * 32 + lane;
+        // ---- softmax and results.  Two warpgroups a tile, each with half of a step's keys and half of the channels.  One
+        // tile: the scores stay in registers.  Two tiles, sixteen warps with 96 registers: they are read twice, for their
+        // maximum and for the weights.
+        constexpr bool TWICE = G::TILES == 2;
+        constexpr int COLS = 64, DH = D / 2;
+        const int tile = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D + half * DH;
         uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
         // (the scores' maximum is taken before the scale: a negative one turns them round; one of 0 would make NaN of the
@@ -518,27 +525,28 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                     }
                     if (masked) hide(s, lim - c * 32);
                 };
-                float s[2][32], most;
-                umma::tmem_ld32(s_at + half * 64, s[0]);
-                umma::tmem_ld32(s_at + half * 64 + 32, s[1]);
-                umma::tmem_ld_wait();
-                scores_of(s[0], 0);
-                scores_of(s[1], 1);
-                most = fmaxf(largest(s[0]), largest(s[1]));
-                if (ALONE) {
-                    float x[2][32];
-                    umma::tmem_ld32(s_at + 64, x[0]);
-                    umma::tmem_ld32(s_at + 96, x[1]);
+                float s[TWICE ? 1 : 2][32], most;
+                if (TWICE) {
+                    umma::tmem_ld32(s_at + half * 64, s[0]);
                     umma::tmem_ld_wait();
-                    scores_of(x[0], 2);
-                    scores_of(x[1], 3);
-                    most = max3(most, largest(x[0]), largest(x[1]));
+                    scores_of(s[0], 0);
+                    most = largest(s[0]);
+                    umma::tmem_ld32(s_at + half * 64 + 32, s[0]);
+                    umma::tmem_ld_wait();
+                    scores_of(s[0], 1);
+                    most = fmaxf(most, largest(s[0]));
                 } else {
-                    float *ex = bars.most[step & 1][0];
-                    ex[half * 128 + r] = most;
-                    pair_sync();   // (both halves have read their scores: P may go where they were)
-                    most = fmaxf(ex[r], ex[128 + r]);
+                    umma::tmem_ld32(s_at + half * 64, s[0]);
+                    umma::tmem_ld32(s_at + half * 64 + 32, s[TWICE ? 0 : 1]);
+                    umma::tmem_ld_wait();
+                    scores_of(s[0], 0);
+                    scores_of(s[TWICE ? 0 : 1], 1);
+                    most = fmaxf(largest(s[0]), largest(s[TWICE ? 0 : 1]));
                 }
+                float *ex = bars.most[tile][step & 1][0];
+                ex[half * 128 + r] = most;
+                pair_sync(tile);
+                most = fmaxf(ex[r], ex[128 + r]);
                 most *= f2;
                 const bool raise = most > m + kRaise;   // (m = -infinity: the first that is seen)
                 if (__any_sync(0xffffffffu, raise)) {
@@ -564,19 +572,21 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 const float base = m == -INFINITY ? 0.0f : -m;
                 const F2 mul = f2_of(f2, f2), add = f2_of(base, base);
                 F2 sum[2] = {f2_of(0.0f, 0.0f), f2_of(0.0f, 0.0f)};
-                float pk[32];
-                weights(s[0], mul, add, sum[0], pk);
-                weights(s[1], mul, add, sum[1], pk + 16);
-                umma::tmem_st32(s_at + half * 32, pk);
-                if (ALONE) {   // (P of the first 64 keys lies over their scores only)
-                    umma::tmem_ld32(s_at + 64, s[0]);
-                    umma::tmem_ld32(s_at + 96, s[1]);
+                if (TWICE) {
+                    float pk[16];
+                    // (the second half is still there, first: P of the first lies over its own scores only)
+                    weights(s[0], mul, add, sum[1], pk);
+                    umma::tmem_ld32(s_at + half * 64, s[0]);
                     umma::tmem_ld_wait();
-                    scores_of(s[0], 2);
-                    scores_of(s[1], 3);
+                    umma::tmem_st16(s_at + half * 64 + 16, pk);
+                    scores_of(s[0], 0);
                     weights(s[0], mul, add, sum[0], pk);
-                    weights(s[1], mul, add, sum[1], pk + 16);
-                    umma::tmem_st32(s_at + 32, pk);
+                    umma::tmem_st16(s_at + half * 64, pk);
+                } else {
+                    float pk[32];
+                    weights(s[0], mul, add, sum[0], pk);
+                    weights(s[TWICE ? 0 : 1], mul, add, sum[1], pk + 16);
+                    umma::tmem_st32(s_at + half * 64, pk);
                 }
                 const float2 t = parts(add2(sum[0], sum[1]));
                 l += t.x + t.y;
@@ -588,18 +598,16 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             // the unit's results
             const int slot = w.slot(blockIdx.x);
             float check = 0.0f;
-            if (!ALONE) {
-                float *ex = bars.most[step & 1][0];
-                ex[half * 128 + r] = l;
-                pair_sync();
-                l = ex[r] + ex[128 + r];
-            }
+            float *ex = bars.most[tile][step & 1][0];
+            ex[half * 128 + r] = l;
+            pair_sync(tile);
+            l = ex[r] + ex[128 + r];
             const float f = 1.0f / l;
             const RowsOut rows = rows_out<D>(p, o);
             Gates gates[2];
             if (gated) {
                 gates[0] = ask_gates(rows, half * DH);
-                gates[1] = ask_gates(rows, half * DH + 32);
+                if (DH > 32) gates[1] = ask_gates(rows, half * DH + 32);
             }
             wait(o_done(tile, step - 1), o_phase(step - 1));
             umma::fence_after_sync();
@@ -637,7 +645,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             } else if (half == 0) {
                 p.part_ml[(size_t)slot * (G::TILES * 128) + tile * 128 + r] = make_float2(m, l);
             }
-            if (!ALONE) pair_sync();   // (the exchange's readers)
+            pair_sync(tile);   // (the exchange's readers)
         } while (w.next());
         umma::fence_before_sync();
     }
