@@ -171,19 +171,24 @@ __device__ __forceinline__ Parts parts_from(const List &l, int cta, int ctas, in
 }
 
 // Waits of a CTA's roles: after one that gave up, none waits any more (`dead`,
-// in shared memory).  False: not there.
+// in shared memory).  False: not there.  The loop is out of line: it would be
+// in the code some twenty times, and a tile's start and end run through code
+// that has to be fetched anew.
+__device__ __noinline__ inline bool wait_long(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *dead) {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*dead) return false;
+    }
+    atomicOr(err, kErrMbarTimeout);
+    *dead = 1;
+    return false;
+}
+
 struct Waits {
     unsigned *err;
     volatile int *dead;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
-        for (uint32_t i = 0; i < kSpinLimit; ++i) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if (*dead) return false;
-        }
-        atomicOr(err, kErrMbarTimeout);
-        *dead = 1;
-        return false;
+        return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_long(bar, parity, err, dead);
     }
 };
 

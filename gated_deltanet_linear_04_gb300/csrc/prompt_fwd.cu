@@ -297,63 +297,58 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 phase ^= 1;
             }
         };
-        auto load_keys = [&](int head, int token) {
-#pragma unroll
-            for (int c = 0; c < G::PER_STEP; ++c) {
-                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
-                    mbar_expect_tx(&bars.full[stage], G::STAGE);
-                    tma_load_4d(ring + stage * G::STAGE, &k_map, 0, token, c, head, &bars.full[stage]);
-                }
-                stage_done();
-            }
-        };
-        auto load_values = [&](int head, int token) {
-#pragma unroll
-            for (int c = 0; c < G::PER_STEP; ++c) {
-                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
-                    mbar_expect_tx(&bars.full[stage], G::STAGE);
-                    tma_load_4d(ring + stage * G::STAGE, &v_map, 0, token + c * G::VK, 0, head, &bars.full[stage]);
-                }
-                stage_done();
-            }
-        };
-        auto load_q = [&](int head, int token) {
-            const bool free = wait(&bars.q_free, (units & 1) ^ 1);
-            ++units;
-            if (free && umma::elect_one()) {
-                mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
-#pragma unroll
-                for (int t = 0; t < G::TILES; ++t)
-#pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
-                        tma_load_3d(smem + t * G::QTILE + i * G::SUB, &q_map, i * 64, head * p.G, token + t * p.tpt,
-                                    &bars.q_full);
-            }
-        };
+        // one loop: the keys of step n and the values of step n - 1, in the order of their products
         w.uniform();
-        Walk x = w;   // the keys' walk, a step ahead of the values'
-        int j = x.first;
+        Walk x = w;   // the keys' walk
+        int j = x.first, i = w.first;
         bool more = true;
-        auto load_k = [&] {
-            if (j == x.last) {
+        auto load_values = [&] {
+#pragma unroll 1
+            for (int c = 0; c < G::PER_STEP; ++c) {
+                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                    mbar_expect_tx(&bars.full[stage], G::STAGE);
+                    tma_load_4d(ring + stage * G::STAGE, &v_map, 0, w.u.b0 + i * kKeys + c * G::VK, 0, w.head, &bars.full[stage]);
+                }
+                stage_done();
+            }
+            ++i;
+        };
+        for (int n = 0;; ++n) {
+            if (G::TILES == 2 && n > 0) load_values();
+            if (more && j == x.last) {
                 more = __any_sync(0xffffffffu, x.next());
-                if (!more) return;
                 x.uniform();
                 j = x.first;
             }
-            if (j == x.first) load_q(x.head, x.u.a0);
-            load_keys(x.head, x.u.b0 + j * kKeys);
-            ++j;
-        };
-        load_k();
-        do {
-            w.uniform();
-            for (int i = w.first; i < w.last; ++i) {
-                if (G::TILES == 1 && more) load_k();
-                load_values(w.head, w.u.b0 + i * kKeys);
-                if (G::TILES == 2 && more) load_k();
+            if (more) {
+                if (j == x.first) {
+                    const bool free = wait(&bars.q_free, (units & 1) ^ 1);
+                    ++units;
+                    if (free && umma::elect_one()) {
+                        mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
+#pragma unroll 1
+                        for (int c = 0; c < G::TILES * (D / 64); ++c)
+                            tma_load_3d(smem + c * G::SUB, &q_map, c % (D / 64) * 64, x.head * p.G,
+                                        x.u.a0 + c / (D / 64) * p.tpt, &bars.q_full);
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < G::PER_STEP; ++c) {
+                    if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                        mbar_expect_tx(&bars.full[stage], G::STAGE);
+                        tma_load_4d(ring + stage * G::STAGE, &k_map, 0, x.u.b0 + j * kKeys, c, x.head, &bars.full[stage]);
+                    }
+                    stage_done();
+                }
+                ++j;
             }
-        } while (__any_sync(0xffffffffu, w.next()));
+            if (G::TILES == 1 && n > 0) load_values();
+            if (n > 0 && i == w.last) {
+                if (!__any_sync(0xffffffffu, w.next())) break;
+                w.uniform();
+                i = w.first;
+            }
+        }
         if (dead)   // let the copies in flight land
             for (int i = 0; i < G::STAGES; ++i) mbar_try_wait(&bars.full[i], 0);
     } else if (any && warp == G::WARPS + 1) {
@@ -391,102 +386,80 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                     base + t * D, base + G::S_COL + buf * 128 + (c * G::VK + k * 32) / 64 * 64 + (c * G::VK + k * 32) % 64 / 2,
                     b + k * (4096 >> 4), id_o, acc || c > 0 || k > 0);
         };
+        // one loop: the scores of step n and the values of step n - 1.  One tile: the scores first, into the other buffer.
+        // Two tiles: each tile's values, then its scores into the buffer that P has left.
         w.uniform();
         Walk x = w;
-        int j = x.first, qstep = 0;
+        int j = x.first, i = w.first, done = 0;   // done: tiles whose values are through
         bool more = true;
-        auto enter = [&]() -> bool {   // the next step's scores
-            if (j == x.last) {
+        for (int n = 0;; ++n) {
+            const int s0 = stage;
+            const uint32_t ph0 = phase;
+            int sk = stage;             // the stages of the scores: first, or behind those of the values
+            uint32_t pk = phase;
+            if (G::TILES == 2 && n > 0)
+                for (int c = 0; c < G::PER_STEP; ++c) pass(sk, pk);
+            if (more && j == x.last) {
                 more = __any_sync(0xffffffffu, x.next());
-                if (!more) return false;
                 x.uniform();
                 j = x.first;
             }
-            if (j == x.first) wait(&bars.q_full, units++ & 1);
-            return true;
-        };
-        auto leave = [&] {
-            ++j;
-            ++qstep;
-            if (j == x.last) commit(&bars.q_free);
-        };
-        auto all_scores = [&] {   // (256 channels, and the first step)
-            if (!enter()) return;
-            for (int c = 0; c < G::PER_STEP; ++c) {
-                take(stage, phase);
-                for (int t = 0; t < G::TILES; ++t) scores(t, G::TILES == 1 ? qstep & 1 : t, c, stage);
-                commit(&bars.empty[stage]);
-                pass(stage, phase);
-            }
-            if (G::TILES == 1) {
-                commit(&bars.s_full[qstep & 1]);
-            } else {
-                commit(&bars.s_full[0]);
-                commit(&bars.s_full[1]);
-            }
-            leave();
-        };
-        all_scores();
-        int done = 0;   // units whose values are through
-        do {
-            w.uniform();
-            for (int i = w.first; i < w.last; ++i, ++step) {
-                const bool acc = i > w.first;
-                if (G::TILES == 1) {
-                    if (more) all_scores();
-                    wait(&bars.p_full[step & 1], (step >> 1) & 1);
-                    if (!acc && done > 0) wait(&bars.o_free[0], (done - 1) & 1);
-                    for (int c = 0; c < G::PER_STEP; ++c) {
-                        take(stage, phase);
-                        values(0, step & 1, c, stage, acc);
-                        commit(&bars.empty[stage]);
-                        pass(stage, phase);
-                    }
-                    commit(o_done(0, step));
-                } else {
-                    // each tile: this step's values, then the next step's scores (into the buffer that P has left)
-                    bool next = more;
-                    int sv = stage, sk = stage;
-                    uint32_t pv = phase, pk = phase;
-                    for (int c = 0; c < G::PER_STEP; ++c) pass(sk, pk);
-                    for (int t = 0; t < 2; ++t) {
-                        wait(&bars.p_full[t], step & 1);
-                        if (!acc && done > 0) wait(&bars.o_free[t], (done - 1) & 1);
-                        umma::fence_after_sync();
-                        int s = sv;
-                        uint32_t ph = pv;
-                        for (int c = 0; c < G::PER_STEP; ++c) {
-                            if (t == 0) take(s, ph);
-                            values(t, t, c, s, acc);
-                            if (t == 1) commit(&bars.empty[s]);
-                            pass(s, ph);
-                        }
-                        commit(o_done(t, step));
-                        if (t == 0 && next) next = enter();
-                        if (next) {
-                            s = sk;
-                            ph = pk;
-                            for (int c = 0; c < G::PER_STEP; ++c) {
-                                if (t == 0) take(s, ph);
-                                scores(t, t, c, s);
-                                if (t == 1) commit(&bars.empty[s]);
-                                pass(s, ph);
-                            }
-                            commit(&bars.s_full[t]);
-                            if (t == 1) {
-                                stage = s;
-                                phase = ph;
-                                leave();
-                            }
-                        } else if (t == 1) {
-                            stage = sk;
-                            phase = pk;
-                        }
-                    }
+            int sv = s0;                // ... of the values
+            uint32_t pv = ph0;
+            if (G::TILES == 1 && more)
+                for (int c = 0; c < G::PER_STEP; ++c) pass(sv, pv);
+            auto do_scores = [&](int t) {
+                if (j == x.first && t == 0) wait(&bars.q_full, units++ & 1);
+                const int buf = G::TILES == 1 ? n & 1 : t;
+                int s = sk;
+                uint32_t ph = pk;
+#pragma unroll 1
+                for (int c = 0; c < G::PER_STEP; ++c) {
+                    if (t == 0) take(s, ph);
+                    scores(t, buf, c, s);
+                    if (t == G::TILES - 1) commit(&bars.empty[s]);
+                    pass(s, ph);
                 }
+                commit(&bars.s_full[buf]);
+                if (t == G::TILES - 1 && j + 1 == x.last) commit(&bars.q_free);
+            };
+#pragma unroll 1
+            for (int t = 0; t < G::TILES; ++t) {
+                if (G::TILES == 1 && more) do_scores(0);
+                if (n > 0) {
+                    const bool acc = i > w.first;
+                    const int buf = G::TILES == 1 ? step & 1 : t;
+                    wait(&bars.p_full[buf], o_phase(step));
+                    if (!acc && done > 0) wait(&bars.o_free[t], (done - 1) & 1);
+                    umma::fence_after_sync();
+                    int s = sv;
+                    uint32_t ph = pv;
+#pragma unroll 1
+                    for (int c = 0; c < G::PER_STEP; ++c) {
+                        if (t == 0) take(s, ph);
+                        values(t, buf, c, s, acc);
+                        if (t == G::TILES - 1) commit(&bars.empty[s]);
+                        pass(s, ph);
+                    }
+                    commit(o_done(t, step));
+                }
+                if (G::TILES == 2 && more) do_scores(t);
             }
-            ++done;
-        } while (__any_sync(0xffffffffu, w.next()));
+            if (n > 0)
+                for (int c = 0; c < G::PER_STEP; ++c) pass(stage, phase);
+            if (more) {
+                for (int c = 0; c < G::PER_STEP; ++c) pass(stage, phase);
+                ++j;
+            }
+            if (n == 0) continue;
+            ++step;
+            if (++i == w.last) {
+                ++done;
+                if (!__any_sync(0xffffffffu, w.next())) break;
+                w.uniform();
+                i = w.first;
+            }
+        }
         // every product is through before the tensor memory goes back
         for (int i = G::TILES == 1 && step > 1 ? step - 2 : step - 1; i < step; ++i)
             for (int t = 0; t < G::TILES; ++t) wait(o_done(t, i), o_phase(i));
@@ -499,10 +472,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         const int tile = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D + half * DH;
         uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
-        // (the scores' maximum is taken before the scale: a negative one turns them round; one of 0 would make NaN of the
-        // -infinity of those that are not seen)
-        const float turn_by = p.scale2 < 0.0f ? -1.0f : 0.0f, f2 = p.scale2 == 0.0f ? 1.0f : fabsf(p.scale2);
-        const bool turned = !(p.scale2 > 0.0f);
+        const float f2 = p.scale2;
         int step = 0;
         do {
             const RowOut o = row_out<D>(p, w.u, w.head, tile, r);
@@ -519,10 +489,6 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 const int lim = o.keys - i * kKeys - half * 64;
                 const bool masked = __any_sync(0xffffffffu, lim < COLS);
                 auto scores_of = [&](float (&s)[32], int c) {   // (after the load)
-                    if (turned) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] *= turn_by;
-                    }
                     if (masked) hide(s, lim - c * 32);
                 };
                 float s[TWICE ? 1 : 2][32], most;
@@ -654,6 +620,32 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
 
+// Every row by the definition: for scales that are not positive, whose scores'
+// order the passes above would have to turn round.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_rows_kernel(const Params p) {
+    attn::grid_dep_enter();
+    const Header h = *p.list.header;
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)Geo<D>::TILES * 128, all = rows * h.units * p.Hkv;
+    for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < all; x += (long long)gridDim.x * 8) {
+        const int head = (int)(x / (rows * h.units)), r = (int)(x % rows);
+        const Unit u = p.list.unit[x / rows % h.units];
+        const RowOut o = row_out<D>(p, u, head, r / 128, r % 128);
+        if (!o.mine) continue;
+        float lse = -INFINITY;
+        if (o.keys > 0) {
+            const long long n = o.at / p.Hq;
+            const int hq = (int)(o.at - n * p.Hq);
+            lse = exact_row<D>(p.q.p + n * p.q.ts + hq * p.q.hs, p.k.p + u.b0 * p.k.ts + head * p.k.hs, p.k.ts,
+                               p.v.p + u.b0 * p.v.ts + head * p.v.hs, p.v.ts, o.keys, p.scale, o.gate, p.out + o.at * D, 0, D);
+        } else {
+            for (int d = lane; d < D; d += 32) p.out[o.at * D + d] = 0;
+        }
+        if (lane == 0 && p.lse != nullptr) p.lse[o.at] = lse;
+    }
+}
+
 // A split unit's parts joined: 32 channels of 128 rows a block.
 template <int D>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ctas) {
@@ -719,6 +711,7 @@ Workspace workspace(const PromptSizes &s) {
 template <int D>
 cudaError_t launch_d(const PromptSizes &s, Params &p, cudaStream_t st) {
     using G = Geo<D>;
+    if (!(p.scale > 0.0f)) return DependentLaunch(dim3(8 * num_sms()), dim3(256), 0, st)(prompt_rows_kernel<D>, p);
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, prompt_forward_kernel<D>, G::SMEM);
     if (e != cudaSuccess) return e;

@@ -29,11 +29,12 @@ __device__ __forceinline__ float row_dot(const float (&a)[D / 32], const float (
     return warp_sum(t);
 }
 
-// out[d0 .. d1) of the row that sees the first `keys` keys at k, v (> 0).
+// out[d0 .. d1) of the row that sees the first `keys` keys at k, v (> 0);
+// returns its lse.
 template <int D>
-__device__ __noinline__ void exact_row(const uint16_t *q, const uint16_t *k, long long k_ts, const uint16_t *v,
+__device__ __noinline__ float exact_row(const uint16_t *q, const uint16_t *k, long long k_ts, const uint16_t *v,
                                        long long v_ts, int keys, float scale, const uint16_t *gate, uint16_t *out, int d0,
-                                       int d1) {
+                                        int d1) {
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31;
     float qx[N], o[N], l = 0.0f, m = -INFINITY;
@@ -63,6 +64,7 @@ __device__ __noinline__ void exact_row(const uint16_t *q, const uint16_t *k, lon
         if (gate != nullptr) y *= sigmoid(bf16_to_f32(gate[d]));
         out[d] = f32_to_bf16(y);
     }
+    return m + logf(l);
 }
 
 }  // namespace prompt
