@@ -182,22 +182,23 @@ __device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, con
                 *reinterpret_cast<uint4 *>(turn + turn_at(16 * k + (lane >> 1), lane & 1)) = gates.v[h][k];
             __syncwarp();
         }
+        float y[2][8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            uint4 *at = reinterpret_cast<uint4 *>(turn + turn_at(lane, i));
             const float *xs = x + 16 * h + 8 * i;
-            float y[8];
             if (gated) {
-                float g[8];
-                attn::unpack8(*at, g);
+                attn::unpack8(*reinterpret_cast<const uint4 *>(turn + turn_at(lane, i)), y[i]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = xs[k] * f * rcp_fast(1.0f + exp_fast(-g[k]));
+                for (int k = 0; k < 8; ++k) y[i][k] = xs[k] * f * rcp_fast(1.0f + exp_fast(-y[i][k]));
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = xs[k] * f;
+                for (int k = 0; k < 8; ++k) y[i][k] = xs[k] * f;
             }
-            const uint4 w = attn::pack8(y);
-            *at = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = attn::pack8(y[i]);
+            *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
 #pragma unroll
