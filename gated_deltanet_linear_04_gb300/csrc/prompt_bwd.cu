@@ -15,7 +15,7 @@
 //     second one lies in shared memory): a product of 128 x 64 with both
 //     operands in shared memory takes 48 clocks for 32 clocks' work (measured),
 //     with A in tensor memory 32.
-//   - A step: S and dP into tensor memory; two warpgroups take 32 columns each
+//   - A step: S and dP into tensor memory; two warpgroups take every other step
 //     into registers, which frees them for the next step at once, and leave P and
 //     dS as bf16 in shared memory, the A operands of the accumulating products.
 //   - The lists, shares and joins are those of the forward pass (prompt.cuh).
@@ -42,13 +42,19 @@ struct Geo {
     static_assert(S_COL + 128 <= 512, "");
     static constexpr int SUB = kRows * 128;                         // bytes of 64 rows of 64 channels
     static constexpr int STAGE = D / 64 * SUB;
-    static constexpr int N1 = D == 256 ? (KIND == kDV ? 2 : 3) : 4, N2 = D == 256 ? (KIND == kDV ? 3 : 1) : 4;
+    // the second ring: whole steps, or with 256 channels, where no second one has room, 64 channels at a time
+    static constexpr int N1 = D == 256 ? (KIND == kDV ? 2 : 3) : 4;
+    static constexpr int STAGE2 = A2_SMEM ? SUB : STAGE, N2 = A2_SMEM ? 5 : D == 256 ? 3 : 4, PER_STEP2 = STAGE / STAGE2;
     static constexpr int XTILE = 128 * 128, XT = ACCS, XB = A2_SMEM ? 1 : 2;   // 128 rows of 64 bf16; tiles; buffers
     static constexpr int A2_BYTES = A2_SMEM ? 128 * D * 2 : 0;
     static constexpr int WARPS = 8, TURN = 32 * 32;
+    // two warpgroups: every other step each, the products of a step two steps later; or half of every step's columns each
+    static constexpr bool TURNS = D <= 128 && KIND == kDQ;
+    static constexpr int LATER = TURNS ? 2 : 1, COLS = TURNS ? 64 : 32, ROWS_WARPS = TURNS ? 4 : 8;
     static constexpr int THREADS = 32 * (WARPS + 2 + (KEYS ? 1 : 0));
     static constexpr int X_AT = A2_BYTES, RING1 = X_AT + XB * XT * XTILE, RING2 = RING1 + N1 * STAGE,
-                         TURN_AT = RING2 + N2 * STAGE, SMEM = TURN_AT + WARPS * TURN + 1024;
+                         SMEM = RING2 + N2 * STAGE2 + 1024;
+    static_assert(WARPS * TURN <= XTILE, "");   // (results are turned into rows where P and dS lay)
     static_assert(SMEM + 4608 <= 227 * 1024, "");
 };
 
@@ -69,12 +75,14 @@ struct Params {
 };
 
 struct Bars {
-    uint64_t full1[4], empty1[4], full2[4], empty2[4], a_full, s_full, s_free, x_full[2], x_free[2], acc_done, acc_free;
+    uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free;
     uint64_t stats_full[kStats], stats_free[kStats];
 };
 
+// (s_full and x_free: of even and odd steps.  A wait for a phase is sound if the one before it is over, and each warpgroup
+// waits for every other step only.)
 struct Stats {
-    float nlse[kRows], delta[kRows];   // -lse in powers of two (-infinity: no such row)
+    float nlse[kRows], delta[kRows];   // -lse in powers of two (-infinity: no such row); -delta
     int token[kRows];
 };
 
@@ -217,6 +225,9 @@ __device__ __forceinline__ void rows_out(const RowOut &o, uint16_t *out, uint16_
 // ---------------------------------------------------------------------------
 // the pass
 // ---------------------------------------------------------------------------
+// The warps that hold rows meet.
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
 template <class G>
 __global__ void __launch_bounds__(G::THREADS, 1)
 prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const Params p) {
@@ -226,7 +237,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     __shared__ __align__(16) Stats stats[G::KEYS ? kStats : 1];
-    __shared__ float swap[G::KEYS ? 1 : 256];   // deltas of a tile of one step: [half][row]
+    __shared__ float swap[G::KEYS || G::TURNS ? 1 : 256];   // deltas of a tile of one step: [half][row]
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -236,30 +247,32 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     }
     if (threadIdx.x == 32) {
         dead = 0;
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&bars.full1[i], 1);
-            mbar_init(&bars.empty1[i], 1);
+        for (int i = 0; i < 5; ++i) {
+            if (i < 4) {
+                mbar_init(&bars.full1[i], 1);
+                mbar_init(&bars.empty1[i], 1);
+            }
             mbar_init(&bars.full2[i], 1);
             mbar_init(&bars.empty2[i], 1);
         }
-        mbar_init(&bars.a_full, 8);
-        mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.s_free, 8);
+        mbar_init(&bars.a_full, G::WARPS);
+        mbar_init(&bars.s_free, G::ROWS_WARPS);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.x_full[i], 8);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.x_full[i], G::ROWS_WARPS);
             mbar_init(&bars.x_free[i], 1);
         }
         mbar_init(&bars.acc_done, 1);
-        mbar_init(&bars.acc_free, 8);
+        mbar_init(&bars.acc_free, G::WARPS);
         for (int i = 0; i < kStats; ++i) {
             mbar_init(&bars.stats_full[i], 1);
-            mbar_init(&bars.stats_free[i], 8);
+            mbar_init(&bars.stats_free[i], G::ROWS_WARPS);
         }
         fence_mbar_init();
     }
     if (G::KEYS) {   // rows of a step that no token has: zeros, never written again
         const int used = p.tps * p.G, rows = kRows - used;
-        for (int i = threadIdx.x; i < (G::N1 + G::N2) * (D / 64) * rows * 8; i += G::THREADS) {
+        for (int i = threadIdx.x; i < (G::N1 * G::STAGE + G::N2 * G::STAGE2) / G::SUB * rows * 8; i += G::THREADS) {
             const int c = i & 7, r = i >> 3;
             *reinterpret_cast<uint4 *>(smem + G::RING1 + r / rows * G::SUB + (used + r % rows) * 128 + c * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -283,14 +296,14 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         }
         int s1 = 0, s2 = 0;
         uint32_t ph1 = 0, ph2 = 0;
-        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int head, int token) {
+        // `subs` groups of 64 channels from group `sub`
+        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int head, int token, int sub, int subs) {
             if (G::KEYS) {
-                mbar_expect_tx(bar, (uint32_t)(D * 2 * p.tps * p.G));
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) tma_load_3d(dst + i * G::SUB, map, i * 64, head * p.G, token, bar);
+                mbar_expect_tx(bar, (uint32_t)(subs * 128 * p.tps * p.G));
+                for (int i = 0; i < subs; ++i) tma_load_3d(dst + i * G::SUB, map, (sub + i) * 64, head * p.G, token, bar);
             } else {
-                mbar_expect_tx(bar, G::STAGE);
-                tma_load_4d(dst, map, 0, token, 0, head, bar);
+                mbar_expect_tx(bar, (uint32_t)(subs * G::SUB));
+                tma_load_4d(dst, map, 0, token, sub, head, bar);
             }
         };
         do {
@@ -298,22 +311,25 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
                 if (wait(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
-                    load(&map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token);
+                    load(&map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
                 if (++s1 == G::N1) {
                     s1 = 0;
                     ph1 ^= 1;
                 }
-                if (wait(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
-                    load(&map2, smem + G::RING2 + s2 * G::STAGE, &bars.full2[s2], w.head, token);
-                if (++s2 == G::N2) {
-                    s2 = 0;
-                    ph2 ^= 1;
+#pragma unroll 1
+                for (int c = 0; c < G::PER_STEP2; ++c) {
+                    if (wait(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
+                        load(&map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c, G::STAGE2 / G::SUB);
+                    if (++s2 == G::N2) {
+                        s2 = 0;
+                        ph2 ^= 1;
+                    }
                 }
             }
         } while (__any_sync(0xffffffffu, w.next()));
         if (dead)   // let the copies in flight land
-            for (int i = 0; i < 4; ++i) {
-                mbar_try_wait(&bars.full1[i], 0);
+            for (int i = 0; i < 5; ++i) {
+                if (i < 4) mbar_try_wait(&bars.full1[i], 0);
                 mbar_try_wait(&bars.full2[i], 0);
             }
     } else if (any && warp == G::WARPS + 1) {
@@ -326,9 +342,10 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         const uint64_t d_x = umma::desc_sw128(at + G::X_AT), d_a2 = umma::desc_sw128(at);
         int s1 = 0, s2 = 0, t1 = 0, t2 = 0, step = 0, units = 0, done = 0;   // s: of the scores, t: of the accumulating products
         uint32_t ph1 = 0, ph2 = 0;
-        bool acc = false, last = false;
-        // the products into the accumulators of the step before
-        auto accumulate = [&](int x) {
+        bool acc = false;
+        int waiting = 0;   // steps whose accumulating products are still to come
+        // the products of step x into the accumulators
+        auto accumulate = [&](int x, bool last) {
             const int xb = x % G::XB;
             wait(&bars.x_full[xb], (x / G::XB) & 1);
             if (!acc && done > 0) wait(&bars.acc_free, (done - 1) & 1);
@@ -341,11 +358,11 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             }
             if (G::HAS_P) {
                 umma::warp_mma_bf16_k64_bt(base + (G::HAS_DP ? D : 0), a + (G::HAS_DP ? G::XTILE >> 4 : 0),
-                                           d_t2 + (uint32_t)(t2 * (G::STAGE >> 4)), id_a, acc);
+                                           d_t2 + (uint32_t)(t2 * (G::STAGE2 >> 4)), id_a, acc);
                 umma::warp_mma_commit(&bars.empty2[t2]);
                 if (++t2 == G::N2) t2 = 0;
             }
-            umma::warp_mma_commit(&bars.x_free[xb]);
+            umma::warp_mma_commit(&bars.x_free[x & 1]);
             acc = true;
             if (last) {
                 umma::warp_mma_commit(&bars.acc_done);
@@ -353,7 +370,8 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 acc = false;
             }
         };
-        do {
+        bool more = true;
+        while (more) {
             w.uniform();
             wait(&bars.a_full, units++ & 1);
             for (int i = w.first; i < w.last; ++i, ++step) {
@@ -369,29 +387,41 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     s1 = 0;
                     ph1 ^= 1;
                 }
-                wait(&bars.full2[s2], ph2);
-                umma::fence_after_sync();
-                if (G::HAS_DP) {
+#pragma unroll 1
+                for (int h = 0; h < G::PER_STEP2; ++h) {
+                    wait(&bars.full2[s2], ph2);
+                    umma::fence_after_sync();
+                    if (G::HAS_DP) {
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const uint64_t b = d_b2 + (uint32_t)((s2 * G::STAGE + c * G::SUB) >> 4);
-                        if (G::A2_SMEM)
-                            umma::warp_mma_bf16_k64(base + G::S_COL + 64, d_a2 + (uint32_t)(c * ((128 * 128) >> 4)), b, id_s, c > 0);
-                        else
-                            umma::warp_mma_bf16_tmem_a_k64(base + G::S_COL + 64, base + G::A2_COL + c * 32, b, id_s, c > 0);
+                        for (int c = 0; c < G::STAGE2 / G::SUB; ++c) {
+                            const uint64_t b = d_b2 + (uint32_t)((s2 * G::STAGE2 + c * G::SUB) >> 4);
+                            if (G::A2_SMEM)
+                                umma::warp_mma_bf16_k64(base + G::S_COL + 64, d_a2 + (uint32_t)(h * ((128 * 128) >> 4)), b, id_s,
+                                                        h > 0);
+                            else
+                                umma::warp_mma_bf16_tmem_a_k64(base + G::S_COL + 64, base + G::A2_COL + c * 32, b, id_s, c > 0);
+                        }
+                        if (!G::HAS_P) umma::warp_mma_commit(&bars.empty2[s2]);
                     }
-                    if (!G::HAS_P) umma::warp_mma_commit(&bars.empty2[s2]);
+                    if (++s2 == G::N2) {
+                        s2 = 0;
+                        ph2 ^= 1;
+                    }
                 }
-                if (++s2 == G::N2) {
-                    s2 = 0;
-                    ph2 ^= 1;
+                umma::warp_mma_commit(&bars.s_full[step & 1]);
+                ++waiting;
+                // (of this tile: with products two steps later those of the last tile are through, see below)
+                if (waiting > G::LATER) {
+                    accumulate(step - G::LATER, G::LATER == 1 && i == w.first);
+                    --waiting;
                 }
-                umma::warp_mma_commit(&bars.s_full);
-                if (step > 0) accumulate(step - 1);
-                last = i + 1 == w.last;
             }
-        } while (__any_sync(0xffffffffu, w.next()));
-        accumulate(step - 1);
+            more = __any_sync(0xffffffffu, w.next());
+            // One step later: the next tile's first scores come before this one's last products.  Two: not, as their rows'
+            // warps would wait for these before they take the scores.
+            if (G::LATER > 1 || !more)
+                for (; waiting > 0; --waiting) accumulate(step - waiting, waiting == 1);
+        }
         wait(&bars.acc_done, (done - 1) & 1);   // every product is through before the tensor memory goes back
     } else if (G::KEYS && any && warp == G::WARPS + 2) {
         // ---- the statistics of the rows that pass by
@@ -412,7 +442,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     const bool there = t[k] < p.tps && x < w.u.n_b;
                     const long long at = ((long long)w.u.b0 + x) * p.Hq + w.head * p.G + g[k];
                     nlse[k] = there ? -kLog2e * p.lse[at] : -INFINITY;
-                    delta[k] = there && G::HAS_DP ? p.delta[at] : 0.0f;
+                    delta[k] = there && G::HAS_DP ? -p.delta[at] : 0.0f;
                     token[k] = there ? x : -0x40000000;
                 }
                 wait(&bars.stats_free[st], ph ^ 1);
@@ -432,38 +462,37 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         } while (w.next());
     } else if (any && warp < G::WARPS) {
         // ---- P and dS, and the results
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane, col0 = G::TURNS ? 0 : half * 32;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        uint8_t *turn = smem + G::TURN_AT + warp * G::TURN;
-        // the resident rows: the first half of the warps brings A1, the second A2
+        uint8_t *turn = smem + G::X_AT + warp * G::TURN;
+        // the resident rows: half of the warps brings A1, half A2
         auto load_resident = [&](const RowOut &o) {
-            if (half == 0 || G::HAS_DP) {
-                const HeadsIn &h = half == 0 ? p.a1 : p.a2;
-                const uint4 *src = reinterpret_cast<const uint4 *>(h.p + o.token * h.ts + o.head * h.hs);
+            const bool second = G::HAS_DP && half == 1;
+            const HeadsIn &h = second ? p.a2 : p.a1;
+            const uint4 *src = reinterpret_cast<const uint4 *>(h.p + o.token * h.ts + o.head * h.hs);
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    uint4 x[8];
+            for (int c = G::HAS_DP ? 0 : half; c < D / 64; c += G::HAS_DP ? 1 : 2) {
+                uint4 x[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = o.valid ? src[c * 8 + k] : make_uint4(0, 0, 0, 0);
-                    if (half == 1 && G::A2_SMEM) {
+                for (int k = 0; k < 8; ++k) x[k] = o.valid ? src[c * 8 + k] : make_uint4(0, 0, 0, 0);
+                if (second && G::A2_SMEM) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4 *>(smem + c * 128 * 128 + umma::sw128(r, k * 16)) = x[k];
-                    } else {
-                        float y[32];
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(smem + c * 128 * 128 + umma::sw128(r, k * 16)) = x[k];
+                } else {
+                    float y[32];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            y[4 * k] = __uint_as_float(x[k].x);
-                            y[4 * k + 1] = __uint_as_float(x[k].y);
-                            y[4 * k + 2] = __uint_as_float(x[k].z);
-                            y[4 * k + 3] = __uint_as_float(x[k].w);
-                        }
-                        umma::tmem_st32(lanes + (half == 0 ? G::A1_COL : G::A2_COL) + c * 32, y);
+                    for (int k = 0; k < 8; ++k) {
+                        y[4 * k] = __uint_as_float(x[k].x);
+                        y[4 * k + 1] = __uint_as_float(x[k].y);
+                        y[4 * k + 2] = __uint_as_float(x[k].z);
+                        y[4 * k + 3] = __uint_as_float(x[k].w);
                     }
+                    umma::tmem_st32(lanes + (second ? G::A2_COL : G::A1_COL) + c * 32, y);
                 }
-                umma::tmem_st_wait();
-                fence_proxy_async_smem();
             }
+            umma::tmem_st_wait();
+            fence_proxy_async_smem();
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.a_full);
@@ -484,103 +513,119 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 }
             }
             for (int i = w.first; i < w.last; ++i, ++step) {
-                float s[32], dp[32];
-                wait(&bars.s_full, step & 1);
+                const int xb = step % G::XB, stat = st;
+                const uint32_t stat_phase = ph;
+                if (G::KEYS && ++st == kStats) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                if (G::TURNS && (step & 1) != half) continue;   // (the other warpgroup's)
+                constexpr int PARTS = G::COLS / 32;
+                float s[PARTS][32], dp[PARTS][32];
+                wait(&bars.s_full[step & 1], (step >> 1) & 1);
                 umma::fence_after_sync();
-                umma::tmem_ld32(lanes + G::S_COL + half * 32, s);
-                if (G::HAS_DP) umma::tmem_ld32(lanes + G::S_COL + 64 + half * 32, dp);
+#pragma unroll
+                for (int c = 0; c < PARTS; ++c) umma::tmem_ld32(lanes + G::S_COL + col0 + c * 32, s[c]);
+                if (G::HAS_DP)
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c) umma::tmem_ld32(lanes + G::S_COL + 64 + col0 + c * 32, dp[c]);
                 umma::tmem_ld_wait();
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.s_free);
-                const Stats *x = nullptr;
+                const Stats *x = &stats[G::KEYS ? stat : 0];
+                // P of two scores; dS of two weights, by -delta
+                auto weigh = [&](float *v, F2 n) {
+                    const float2 e = parts(fma2(f2_of(v[0], v[1]), f2_of(p.scale2, p.scale2), n));
+                    v[0] = ex2(e.x);
+                    v[1] = ex2(e.y);
+                };
+                auto slope = [&](float *v, const float *d, F2 n) {
+                    const float2 e = parts(mul2(f2_of(v[0], v[1]), add2(f2_of(d[0], d[1]), n)));
+                    v[0] = e.x;
+                    v[1] = e.y;
+                };
                 if (G::KEYS) {
-                    wait(&bars.stats_full[st], ph);
-                    x = &stats[st];
+                    wait(&bars.stats_full[stat], stat_phase);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 n = *reinterpret_cast<const float4 *>(&x->nlse[half * 32 + k]);
-                        s[k] = ex2(fmaf(s[k], p.scale2, n.x));
-                        s[k + 1] = ex2(fmaf(s[k + 1], p.scale2, n.y));
-                        s[k + 2] = ex2(fmaf(s[k + 2], p.scale2, n.z));
-                        s[k + 3] = ex2(fmaf(s[k + 3], p.scale2, n.w));
+                    for (int k = 0; k < G::COLS; k += 4) {
+                        const float4 n = *reinterpret_cast<const float4 *>(&x->nlse[col0 + k]);
+                        weigh(&s[k / 32][k % 32], f2_of(n.x, n.y));
+                        weigh(&s[k / 32][k % 32 + 2], f2_of(n.z, n.w));
                     }
                     // (not all keys seen by the step's first token, or rows behind the last token)
-                    const bool masked = w.u.lim0 + i * p.tps < 127 || (i + 1) * p.tps > w.u.n_b;
-                    if (masked) {
+                    if (w.u.lim0 + i * p.tps < 127 || (i + 1) * p.tps > w.u.n_b) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const int4 n = *reinterpret_cast<const int4 *>(&x->token[half * 32 + k]);
+                        for (int k = 0; k < G::COLS; k += 4) {
+                            const int4 n = *reinterpret_cast<const int4 *>(&x->token[col0 + k]);
                             const int tok[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
                             for (int z = 0; z < 4; ++z)
                                 if (r > w.u.lim0 + tok[z]) {
-                                    s[k + z] = 0.0f;
-                                    if (G::HAS_DP) dp[k + z] = 0.0f;
+                                    s[k / 32][k % 32 + z] = 0.0f;
+                                    if (G::HAS_DP) dp[k / 32][k % 32 + z] = 0.0f;
                                 }
                         }
                     }
                 } else {
-                    const int lim = keys - i * kRows - half * 32;
+                    const int lim = keys - i * kRows - col0;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = ex2(fmaf(s[k], p.scale2, nlse));
-                    if (__any_sync(0xffffffffu, lim < 32)) {
+                    for (int k = 0; k < G::COLS; k += 2) weigh(&s[k / 32][k % 32], f2_of(nlse, nlse));
+                    if (__any_sync(0xffffffffu, lim < G::COLS)) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (k >= lim) s[k] = dp[k] = 0.0f;
+                        for (int k = 0; k < G::COLS; ++k)
+                            if (k >= lim) s[k / 32][k % 32] = dp[k / 32][k % 32] = 0.0f;
                     }
                     if (w.u.steps == 1) {
                         // all of a row's keys at hand: its delta from P and dP themselves (the output's rounding to bf16 is
                         // too coarse for rows of few keys), also for the kernels that come after
-                        float t = 0.0f;
+                        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) t = fmaf(s[k], dp[k], t);
-                        swap[half * 128 + r] = t;
-                        asm volatile("bar.sync 1, 256;" ::: "memory");
-                        delta = swap[r] + swap[128 + r];
-                        asm volatile("bar.sync 1, 256;" ::: "memory");
-                        if (half == 0 && o.valid) p.delta[o.at] = delta;
+                        for (int k = 0; k < G::COLS; ++k) t[k & 3] = fmaf(s[k / 32][k % 32], dp[k / 32][k % 32], t[k & 3]);
+                        delta = (t[0] + t[1]) + (t[2] + t[3]);
+                        if (!G::TURNS) {
+                            swap[half * 128 + r] = delta;
+                            meet();
+                            delta = swap[r] + swap[128 + r];
+                            meet();
+                        }
+                        if (o.valid && (G::TURNS || half == 0)) p.delta[o.at] = delta;
                     }
                 }
-                const int xb = step % G::XB;
-                if (step >= G::XB) wait(&bars.x_free[xb], (step / G::XB - 1) & 1);
+                if (step >= G::XB) wait(&bars.x_free[(step - G::XB) & 1], ((step - G::XB) >> 1) & 1);
                 uint8_t *xs = smem + G::X_AT + xb * G::XT * G::XTILE;
-                auto put = [&](uint8_t *tile, const float (&v)[32]) {
+                auto put = [&](uint8_t *tile) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float y[8] = {v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3],
-                                            v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7]};
-                        *reinterpret_cast<uint4 *>(tile + umma::sw128(r, half * 64 + c * 16)) = attn::pack8(y);
+                    for (int c = 0; c < G::COLS / 8; ++c) {
+                        const float *v = &s[c / 4][c % 4 * 8];
+                        const float y[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+                        *reinterpret_cast<uint4 *>(tile + umma::sw128(r, col0 * 2 + c * 16)) = attn::pack8(y);
                     }
                 };
-                if (G::HAS_P) put(xs + (G::HAS_DP ? G::XTILE : 0), s);
+                if (G::HAS_P) put(xs + (G::HAS_DP ? G::XTILE : 0));
                 if (G::HAS_DP) {
                     if (G::KEYS) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 n = *reinterpret_cast<const float4 *>(&x->delta[half * 32 + k]);
-                            s[k] *= dp[k] - n.x;
-                            s[k + 1] *= dp[k + 1] - n.y;
-                            s[k + 2] *= dp[k + 2] - n.z;
-                            s[k + 3] *= dp[k + 3] - n.w;
+                        for (int k = 0; k < G::COLS; k += 4) {
+                            const float4 n = *reinterpret_cast<const float4 *>(&x->delta[col0 + k]);
+                            slope(&s[k / 32][k % 32], &dp[k / 32][k % 32], f2_of(n.x, n.y));
+                            slope(&s[k / 32][k % 32 + 2], &dp[k / 32][k % 32 + 2], f2_of(n.z, n.w));
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] *= dp[k] - delta;
+                        for (int k = 0; k < G::COLS; k += 2)
+                            slope(&s[k / 32][k % 32], &dp[k / 32][k % 32], f2_of(-delta, -delta));
                     }
-                    put(xs, s);
+                    put(xs);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars.x_full[xb]);
-                    if (G::KEYS) mbar_arrive(&bars.stats_free[st]);
-                }
-                if (G::KEYS && ++st == kStats) {
-                    st = 0;
-                    ph ^= 1;
+                    if (G::KEYS) mbar_arrive(&bars.stats_free[stat]);
                 }
             }
+            if (G::TURNS) meet();   // (the next rows go where the other warpgroup's last step has its own)
             // the next tile's resident rows, then this one's results
             Walk y = w;
             more = y.next();
@@ -598,24 +643,19 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             for (int a = 0; a < G::ACCS; ++a) {
                 const bool of_p = a == 1 || !G::HAS_DP;
                 const float f = of_p ? 1.0f : p.scale;
-                float check = 0.0f;
                 uint16_t *rows[2];
                 rows_out<D>(o, p.acc_out[a], rows);
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    const int d = half * (D / 2) + c * 32;
+                for (int d = half * 32; d < D; d += 64) {
                     float v[32];
                     umma::tmem_ld32(lanes + a * D + d, v);
                     umma::tmem_ld_wait();
-                    if (a == G::ACCS - 1 && c == D / 64 - 1) {
-                        umma::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.acc_free);
-                    }
                     if (whole) {
+                        float check = 0.0f;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) check = fmaf(v[k], 0.0f, check);
                         write_group<D>(turn, rows, valid, d, v, f);
+                        mend_rows<G>(p, o, w.u, r, of_p, valid && check != 0.0f, p.acc_out[a], d, d + 32);
                     } else {
                         float4 *dst = reinterpret_cast<float4 *>(p.part) +
                                       (((size_t)slot * G::ACCS + a) * (D / 4) + d / 4) * 128 + r;
@@ -624,10 +664,11 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                             dst[(size_t)k * 128] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                     }
                 }
-                if (whole)
-                    mend_rows<G>(p, o, w.u, r, of_p, valid && check != 0.0f, p.acc_out[a], half * (D / 2),
-                                 (half + 1) * (D / 2));
             }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_free);
+            meet();   // (the next P and dS go where rows were turned)
             ++units;
             w = y;
             o = next;
@@ -639,15 +680,13 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
 
-// A split tile's parts added up: 32 channels of 128 rows a block.
+// Split tiles' parts added up: 32 channels of 128 rows a block.
 template <class G>
-__global__ void __launch_bounds__(128) prompt_backward_join_kernel(const Params p, int ctas) {
+__device__ __forceinline__ void join_parts(const Params &p, int ctas, int slice, uint8_t (&turn)[4][G::TURN]) {
     constexpr int D = G::D;
-    __shared__ __align__(16) uint8_t turn[4][G::TURN];
-    attn::grid_dep_enter();
     const Parts part = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
     if (part.n == 0) return;
-    const int a = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32), r = threadIdx.x;
+    const int a = slice / (D / 32), c = slice % (D / 32), r = threadIdx.x;
     const RowOut o = row_out<G>(p, part.u, part.head, r);
     uint16_t *rows[2];
     rows_out<D>(o, p.acc_out[a], rows);
@@ -673,6 +712,23 @@ __global__ void __launch_bounds__(128) prompt_backward_join_kernel(const Params 
     const bool valid = o.valid && (G::KEYS || part.u.lim0 + (int)(o.token - part.u.a0) > 0);
     write_group<D>(turn[threadIdx.x >> 5], rows, valid, c * 32, x, of_p ? 1.0f : p.scale);
     mend_rows<G>(p, o, part.u, r, of_p, valid && check != 0.0f, p.acc_out[a], c * 32, c * 32 + 32);
+}
+
+// All three (dQ, dK, dV): blockIdx.y is the accumulator and its channels.
+template <int D>
+__global__ void __launch_bounds__(128) prompt_backward_join_kernel(const Params q, const Params k, const Params v, int ctas) {
+    __shared__ __align__(16) uint8_t turn[4][Geo<D, kDQ>::TURN];
+    attn::grid_dep_enter();
+    const int slice = blockIdx.y;
+    if (slice < D / 32) {
+        join_parts<Geo<D, kDQ>>(q, ctas, slice, turn);
+    } else if constexpr (D <= 128) {
+        join_parts<Geo<D, kDKV>>(k, ctas, slice - D / 32, turn);
+    } else if (slice < 2 * (D / 32)) {
+        join_parts<Geo<D, kDK>>(k, ctas, slice - D / 32, turn);
+    } else {
+        join_parts<Geo<D, kDV>>(v, ctas, slice - 2 * (D / 32), turn);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -780,12 +836,6 @@ cudaError_t launch_pass(const CUtensorMap &m1, const CUtensorMap &m2, const Para
     return DependentLaunch(dim3(num_sms()), dim3(G::THREADS), G::SMEM, st)(prompt_backward_kernel<G>, m1, m2, p);
 }
 
-template <class G>
-cudaError_t launch_join(const Params &p, cudaStream_t st) {
-    const int ctas = num_sms();
-    return DependentLaunch(dim3(ctas - 1, G::ACCS * (G::D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<G>, p, ctas);
-}
-
 template <int D>
 cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn &q, const HeadsIn &k, const HeadsIn &v,
                      const HeadsIn &gate, const uint16_t *out, const float *lse, const uint16_t *dout, float scale, uint16_t *dq,
@@ -826,7 +876,7 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     if (!queries_map(&mq, no_q ? dummy : q, no_q ? 1 : s.Nq, no_q ? 1 : s.Hq, D, G, tps) ||
         !queries_map(&mg, no_q ? dummy : g, no_q ? 1 : s.Nq, no_q ? 1 : s.Hq, D, G, tps) ||
         !keys_map(&mk, none ? dummy : k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kRows, D / 64) ||
-        !keys_map(&mv, none ? dummy : v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kRows, D / 64))
+        !keys_map(&mv, none ? dummy : v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kRows, Geo<D, kDQ>::STAGE2 / Geo<D, kDQ>::SUB))
         return cudaErrorInvalidValue;
     Params p = {};
     p.q = q;
@@ -858,25 +908,23 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     pk.part = part(1);
     pk.tile = 128;
     pk.tps = tps;
+    Params pv = pk;
+    pk.acc_out[0] = dk;
+    pk.acc_out[1] = dv;
+    pv.acc_out[0] = dv;
+    pv.part = part(2);
     if (!no_q) e = launch_pass<Geo<D, kDQ>>(mk, mv, pq, st);
-    if (e == cudaSuccess && !no_q) e = launch_join<Geo<D, kDQ>>(pq, st);
-    if (e != cudaSuccess || none) return e;
     if constexpr (D == 256) {
-        Params pv = pk;
-        pk.acc_out[0] = dk;
-        pv.acc_out[0] = dv;
-        pv.part = part(2);
-        e = launch_pass<Geo<D, kDK>>(mq, mg, pk, st);
-        if (e == cudaSuccess) e = launch_pass<Geo<D, kDV>>(mq, mg, pv, st);
-        if (e == cudaSuccess) e = launch_join<Geo<D, kDK>>(pk, st);
-        if (e == cudaSuccess) e = launch_join<Geo<D, kDV>>(pv, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDK>>(mq, mg, pk, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDV>>(mq, mg, pv, st);
     } else {
-        pk.acc_out[0] = dk;
-        pk.acc_out[1] = dv;
-        e = launch_pass<Geo<D, kDKV>>(mq, mg, pk, st);
-        if (e == cudaSuccess) e = launch_join<Geo<D, kDKV>>(pk, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDKV>>(mq, mg, pk, st);
     }
-    return e;
+    if (e != cudaSuccess) return e;
+    // (no keys, or no queries: no tile has more than a step)
+    if (none || no_q) return cudaSuccess;
+    const int ctas = num_sms();
+    return DependentLaunch(dim3(ctas - 1, 3 * (D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<D>, pq, pk, pv, ctas);
 }
 
 }  // namespace
