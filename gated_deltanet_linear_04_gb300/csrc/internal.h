@@ -241,11 +241,15 @@ struct PromptSeqs {
 
 // A list of work: tiles of `tile` tokens of queries (or keys) that meet the
 // others in steps of `step`; for `ctas` CTAs with shares of `least` steps or
-// more; `blank`: the steps' time that a tile's start and end take.
+// more; `blank`: the steps' time that a tile's start and end take; if no tile
+// can have more than `whole` steps, none is split, and nothing is to be joined.
 struct PromptList {
     bool keys;
-    int tile, step, ctas, least, blank;
+    int tile, step, ctas, least, blank, whole;
 };
+
+// Whether the list's tiles are split: if one can have more than `whole` steps.
+bool prompt_splits(const PromptSizes &s, const PromptSeqs &q, const PromptList &l);
 
 size_t prompt_list_bytes(const PromptSizes &s, const PromptList &l);
 prompt::List prompt_list_at(const PromptSizes &s, const PromptList &l, void *ws);

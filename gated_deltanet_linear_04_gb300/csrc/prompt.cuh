@@ -27,15 +27,18 @@ struct __align__(16) Unit {
     long long pad2;
 };
 
-struct Start {             // where a CTA's share begins
+struct __align__(16) Start {   // a CTA's share
     int head, unit;
-    long long offset;      // steps into the unit, blank ones first
+    long long offset;      // where it begins: steps into the unit, blank ones first
+    long long left;        // its steps
+    int units, blank;      // of the list: units of a key head, blank steps of a unit
+    Unit u;                // the first unit
 };
 
 struct Header {
     long long steps;       // of one key head
-    long long share;       // of a CTA
-    int units, blank;      // blank steps of a unit
+    long long share;       // of a CTA (but for lists whose tiles are not split)
+    int units, blank;
     long long pad;
 };
 
@@ -76,7 +79,7 @@ __device__ __forceinline__ Seq load_seq(const Sequences &p, int s) {
 // A CTA's way through its share.
 struct Walk {
     const Unit *units;
-    int n_units, heads, blank;
+    int n_units, blank;
     long long left;        // steps of the share after the current unit's
     int head, unit, first, last;   // the current unit's steps first .. last - 1
     Unit u;
@@ -115,20 +118,19 @@ struct Walk {
             ++head;
         }
     }
-    __device__ __forceinline__ bool begin(const List &l, int cta, int heads_) {
-        const Header h = *l.header;
-        const long long total = h.steps * heads_, x = h.share * cta;
-        left = total - x < h.share ? total - x : h.share;
-        if (left <= 0) return false;
+    __device__ __forceinline__ bool begin(const List &l, int cta) {
+        const Start *s = l.start + cta;
+        const int4 *p = reinterpret_cast<const int4 *>(s);
+        const int4 a = p[0], b = p[1];
+        ahead[0] = p[2];
+        ahead[1] = p[3];
+        left = ((long long)(uint32_t)b.x) | ((long long)b.y << 32);
         units = l.unit;
-        n_units = h.units;
-        blank = h.blank;
-        heads = heads_;
-        const Start s = l.start[cta];
-        head = s.head;
-        unit = s.unit;
-        ask(unit);
-        return open(s.offset);
+        n_units = b.z;
+        blank = b.w;
+        head = a.x;
+        unit = a.y;
+        return left > 0 && open(((long long)(uint32_t)a.z) | ((long long)a.w << 32));
     }
     // the same values in every lane, and known to be (for loops of a whole warp)
     __device__ __forceinline__ void uniform() {
@@ -154,16 +156,16 @@ struct Parts {
     Unit u;
 };
 
-__device__ __forceinline__ Parts parts_from(const List &l, int cta, int ctas, int heads) {
+__device__ __forceinline__ Parts parts_from(const List &l, int cta) {
     Parts r;
     r.n = 0;
     const Header h = *l.header;
-    const long long total = h.steps * heads, x1 = h.share * (cta + 1);
-    if (cta + 1 >= ctas || x1 >= total) return r;
     const Start s = l.start[cta + 1];
-    const long long mine = s.offset - h.blank;   // steps before x1
-    if (mine <= 0 || mine > h.share) return r;   // (begins after x1, or before this share)
-    r.u = l.unit[s.unit];
+    const long long mine = s.offset - h.blank;   // steps of the unit that the next CTA goes on with, before it
+    if (s.left <= 0 || mine <= 0) return r;
+    const long long x1 = h.share * (cta + 1);
+    if (mine > h.share) return r;                // (it began before this share)
+    r.u = s.u;
     r.head = s.head;
     const long long end = x1 - s.offset + h.blank + r.u.steps;
     r.n = (int)((end - 1) / h.share) - cta + 1;

@@ -230,7 +230,8 @@ __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, 256;" ::: "me
 
 template <class G>
 __global__ void __launch_bounds__(G::THREADS, 1)
-prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const Params p) {
+prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
+                       const __grid_constant__ Params p) {
     constexpr int D = G::D;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
@@ -287,7 +288,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
 
     const Waits wait{p.err, &dead};
     Walk w;
-    const bool any = w.begin(p.list, blockIdx.x, p.Hkv);
+    const bool any = w.begin(p.list, blockIdx.x);
     if (any && warp == G::WARPS) {
         // ---- loads
         if (umma::elect_one()) {
@@ -682,9 +683,9 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
 
 // Split tiles' parts added up: 32 channels of 128 rows a block.
 template <class G>
-__device__ __forceinline__ void join_parts(const Params &p, int ctas, int slice, uint8_t (&turn)[4][G::TURN]) {
+__device__ __forceinline__ void join_parts(const Params &p, int slice, uint8_t (&turn)[4][G::TURN]) {
     constexpr int D = G::D;
-    const Parts part = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
+    const Parts part = parts_from(p.list, blockIdx.x);
     if (part.n == 0) return;
     const int a = slice / (D / 32), c = slice % (D / 32), r = threadIdx.x;
     const RowOut o = row_out<G>(p, part.u, part.head, r);
@@ -693,17 +694,26 @@ __device__ __forceinline__ void join_parts(const Params &p, int ctas, int slice,
     float x[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) x[k] = 0.0f;
-    for (int i = 0; i < part.n; ++i) {
-        const size_t slot = 2 * (size_t)(blockIdx.x + i) + (i == 0 ? 1 : 0);
-        const float4 *src = reinterpret_cast<const float4 *>(p.part) + ((slot * G::ACCS + a) * (D / 4) + c * 8) * 128 + r;
+    // (two parts' loads at a time)
+    for (int i = 0; i < part.n; i += 2) {
+        float4 v[2][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float4 v = src[(size_t)k * 128];
-            x[4 * k] += v.x;
-            x[4 * k + 1] += v.y;
-            x[4 * k + 2] += v.z;
-            x[4 * k + 3] += v.w;
+        for (int z = 0; z < 2; ++z) {
+            const size_t slot = 2 * (size_t)(blockIdx.x + i + z) + (i + z == 0 ? 1 : 0);
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + ((slot * G::ACCS + a) * (D / 4) + c * 8) * 128 + r;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[z][k] = i + z < part.n ? src[(size_t)k * 128] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                x[4 * k] += v[z][k].x;
+                x[4 * k + 1] += v[z][k].y;
+                x[4 * k + 2] += v[z][k].z;
+                x[4 * k + 3] += v[z][k].w;
+            }
     }
     const bool of_p = a == 1 || !G::HAS_DP;
     float check = 0.0f;
@@ -716,18 +726,18 @@ __device__ __forceinline__ void join_parts(const Params &p, int ctas, int slice,
 
 // All three (dQ, dK, dV): blockIdx.y is the accumulator and its channels.
 template <int D>
-__global__ void __launch_bounds__(128) prompt_backward_join_kernel(const Params q, const Params k, const Params v, int ctas) {
+__global__ void __launch_bounds__(128) prompt_backward_join_kernel(const __grid_constant__ Params q, const __grid_constant__ Params k, const __grid_constant__ Params v) {
     __shared__ __align__(16) uint8_t turn[4][Geo<D, kDQ>::TURN];
     attn::grid_dep_enter();
     const int slice = blockIdx.y;
     if (slice < D / 32) {
-        join_parts<Geo<D, kDQ>>(q, ctas, slice, turn);
+        join_parts<Geo<D, kDQ>>(q, slice, turn);
     } else if constexpr (D <= 128) {
-        join_parts<Geo<D, kDKV>>(k, ctas, slice - D / 32, turn);
+        join_parts<Geo<D, kDKV>>(k, slice - D / 32, turn);
     } else if (slice < 2 * (D / 32)) {
-        join_parts<Geo<D, kDK>>(k, ctas, slice - D / 32, turn);
+        join_parts<Geo<D, kDK>>(k, slice - D / 32, turn);
     } else {
-        join_parts<Geo<D, kDV>>(v, ctas, slice - 2 * (D / 32), turn);
+        join_parts<Geo<D, kDV>>(v, slice - 2 * (D / 32), turn);
     }
 }
 
@@ -804,11 +814,11 @@ __global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams
 constexpr int kBlank = 9;
 
 PromptList q_list(const PromptSizes &s) {
-    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, kBlank};
+    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, kBlank, 6};
 }
 
 PromptList k_list(const PromptSizes &s) {
-    return PromptList{true, 128, kRows / (s.Hq / s.Hkv), num_sms(), 4, kBlank};
+    return PromptList{true, 128, kRows / (s.Hq / s.Hkv), num_sms(), 4, kBlank, 6};
 }
 
 struct Workspace {
@@ -922,9 +932,8 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     }
     if (e != cudaSuccess) return e;
     // (no keys, or no queries: no tile has more than a step)
-    if (none || no_q) return cudaSuccess;
-    const int ctas = num_sms();
-    return DependentLaunch(dim3(ctas - 1, 3 * (D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<D>, pq, pk, pv, ctas);
+    if (none || no_q || !(prompt_splits(s, seqs, lists[0]) || prompt_splits(s, seqs, lists[1]))) return cudaSuccess;
+    return DependentLaunch(dim3(num_sms() - 1, 3 * (D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<D>, pq, pk, pv);
 }
 
 }  // namespace

@@ -282,7 +282,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
 
     const Waits wait{p.err, &dead};
     Walk w;
-    const bool any = w.begin(p.list, blockIdx.x, p.Hkv);
+    const bool any = w.begin(p.list, blockIdx.x);
     if (any && warp == G::WARPS) {
         // ---- loads.  The whole warp goes through the loop, as for the products.
         if (umma::elect_one()) {
@@ -571,11 +571,11 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             l = ex[r] + ex[128 + r];
             const float f = 1.0f / l;
             const RowsOut rows = rows_out<D>(p, o);
-            Gates gates[2];
-            if (gated) {
-                gates[0] = ask_gates(rows, half * DH);
-                if (DH > 32) gates[1] = ask_gates(rows, half * DH + 32);
-            }
+            constexpr int AHEAD = TWICE ? 1 : 2;   // groups whose gates are asked for (there are no registers for more)
+            Gates gates[AHEAD];
+            if (gated)
+#pragma unroll
+                for (int z = 0; z < AHEAD; ++z) gates[z] = ask_gates(rows, half * DH + z * 32);
             wait(o_done(tile, step - 1), o_phase(step - 1));
             umma::fence_after_sync();
             // (not unrolled: the code would be fetched anew for every tile)
@@ -593,10 +593,15 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 if (whole) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
-                    const Gates now = gates[0];
-                    gates[0] = gates[1];
-                    if (gated && c + 2 < DH / 32) gates[1] = ask_gates(rows, d + 64);
-                    write_group(turn, rows, o, gated, now, d, x, f);
+                    if (AHEAD > 1) {
+                        const Gates now = gates[0];
+                        gates[0] = gates[AHEAD - 1];
+                        if (gated && c + AHEAD < DH / 32) gates[AHEAD - 1] = ask_gates(rows, d + AHEAD * 32);
+                        write_group(turn, rows, o, gated, now, d, x, f);
+                    } else {
+                        write_group(turn, rows, o, gated, gates[0], d, x, f);
+                        if (gated && c + 1 < DH / 32) gates[0] = ask_gates(rows, d + 32);
+                    }
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
                                   ((size_t)slot * (D / 4) + d / 4) * (G::TILES * 128) + tile * 128 + r;
@@ -649,11 +654,11 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(const Params p) {
 
 // A split unit's parts joined: 32 channels of 128 rows a block.
 template <int D>
-__global__ void __launch_bounds__(128) prompt_join_kernel(const Params p, int ctas) {
+__global__ void __launch_bounds__(128) prompt_join_kernel(const Params p) {
     constexpr int ROWS = Geo<D>::TILES * 128;
     __shared__ __align__(16) uint8_t turn[4][Geo<D>::TURN];
     attn::grid_dep_enter();
-    const Parts part = parts_from(p.list, blockIdx.x, ctas, p.Hkv);
+    const Parts part = parts_from(p.list, blockIdx.x);
     if (part.n == 0) return;
     const int tile = blockIdx.y / (D / 32), c = blockIdx.y % (D / 32), r = threadIdx.x, row = tile * 128 + r;
     const RowOut o = row_out<D>(p, part.u, part.head, tile, r);
@@ -693,7 +698,7 @@ PromptList list_of(const PromptSizes &s) {
     const int tpt = 128 / (s.Hq / s.Hkv);
     // A tile's start and end in steps (T = 8192, 256 channels: 2 481 us, 4 380, 6 351, 8 355; packed, 128 channels: 2 445,
     // 4 460, 6 468: with two tiles one's end runs beside the other's steps).
-    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4, s.D == 256 ? 6 : 2};
+    return PromptList{false, tpt * tiles_of(s.D), kKeys, num_sms(), 4, s.D == 256 ? 6 : 2, 4};
 }
 
 struct Workspace {
@@ -710,7 +715,7 @@ Workspace workspace(const PromptSizes &s) {
 }
 
 template <int D>
-cudaError_t launch_d(const PromptSizes &s, Params &p, cudaStream_t st) {
+cudaError_t launch_d(const PromptSizes &s, Params &p, bool splits, cudaStream_t st) {
     using G = Geo<D>;
     if (!(p.scale > 0.0f)) return DependentLaunch(dim3(8 * num_sms()), dim3(256), 0, st)(prompt_rows_kernel<D>, p);
     static unsigned long long done = 0;
@@ -726,8 +731,8 @@ cudaError_t launch_d(const PromptSizes &s, Params &p, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int ctas = num_sms();
     e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, p);
-    if (e != cudaSuccess) return e;
-    return DependentLaunch(dim3(ctas - 1, G::TILES * (D / 32)), dim3(128), 0, st)(prompt_join_kernel<D>, p, ctas);
+    if (e != cudaSuccess || !splits) return e;
+    return DependentLaunch(dim3(ctas - 1, G::TILES * (D / 32)), dim3(128), 0, st)(prompt_join_kernel<D>, p);
 }
 
 }  // namespace
@@ -759,9 +764,10 @@ cudaError_t launch_attn_prefill(const PromptSizes &s, const HeadsIn &q, const He
     p.tpt = 128 / p.G;
     p.scale = scale;
     p.scale2 = scale * kLog2e;
-    if (s.D == 64) return launch_d<64>(s, p, st);
-    if (s.D == 128) return launch_d<128>(s, p, st);
-    return launch_d<256>(s, p, st);
+    const bool splits = prompt_splits(s, seqs, list);
+    if (s.D == 64) return launch_d<64>(s, p, splits, st);
+    if (s.D == 128) return launch_d<128>(s, p, splits, st);
+    return launch_d<256>(s, p, splits, st);
 }
 
 }  // namespace gdn

@@ -10,7 +10,7 @@ namespace {
 
 using namespace prompt;
 
-constexpr int kThreads = 1024, kCached = 2048;
+constexpr int kThreads = 1024, kCached = 2048, kSeqs = 1024;
 
 struct ListParams {
     Header *header;
@@ -20,6 +20,7 @@ struct ListParams {
     int keys;          // tiles of keys, steps of queries; or the other way round
     int tile, step;    // tokens
     int ctas, heads, least, blank;   // least: steps of a share
+    int whole;         // no tile is split
 };
 
 struct PlanParams {
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
     __shared__ long long sums[32];
     __shared__ long long cached[kCached];
     __shared__ int first_cached[kCached];
+    __shared__ Seq seqs[kSeqs];
     __shared__ int bad;
     const ListParams &l = p.l[blockIdx.x];
     const int tid = threadIdx.x, B = p.s.B;
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
         long long n = 0;
         if (s < B) {
             const Seq q = load_seq(p.s, s);
+            if (s < kSeqs) seqs[s] = q;
             ok = ok && q.ok;
             if (q.ok) n = ((l.keys ? q.slot_k : q.slot_q) + (long long)l.tile - 1) / l.tile;
         }
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
         Unit unit = {};
         if (u < units) {
             const int s = B <= kCached ? last_not_above(first_cached, B, (int)u) : last_not_above(l.seq_first, B, (int)u);
-            unit = make_unit(load_seq(p.s, s), (int)u - (B <= kCached ? first_cached[s] : l.seq_first[s]), l);
+            unit = make_unit(s < kSeqs ? seqs[s] : load_seq(p.s, s), (int)u - (B <= kCached ? first_cached[s] : l.seq_first[s]), l);
         }
         long long sum;
         unit.pre = total + block_scan(u < units ? (long long)unit.steps + l.blank : 0, sums, sum);
@@ -145,16 +148,19 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
     __syncthreads();
     const long long all = total * l.heads;
     long long share = (all + l.ctas - 1) / l.ctas;
-    if (share < l.least) share = l.least;
+    if (!l.whole && share < l.least) share = l.least;
     if (tid == 0) *l.header = Header{total, share, (int)units, l.blank, 0};
-    for (int c = tid; c < l.ctas; c += kThreads) {
+    // where a share begins; if no tile is to be split, at the tile's end that is nearer
+    auto begin = [&](int c, Start &s) -> long long {
         const long long x = share * c;
-        if (x >= all) break;
-        const int head = (int)(x / total);
-        const long long r = x - head * total;
-        int u;
+        s = Start{};
+        s.units = (int)units;
+        s.blank = l.blank;
+        if (x >= all) return all;
+        s.head = (int)(x / total);
+        const long long r = x - s.head * total;
         if (units <= kCached) {
-            u = last_not_above(cached, (int)units, r);
+            s.unit = last_not_above(cached, (int)units, r);
         } else {
             int lo = 0, hi = (int)units;
             while (hi - lo > 1) {
@@ -164,10 +170,31 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PlanParams 
                 else
                     hi = mid;
             }
-            u = lo;
+            s.unit = lo;
         }
-        const long long pre = units <= kCached ? cached[u] : l.unit[u].pre;
-        l.start[c] = Start{head, u, r - pre};
+        s.u = l.unit[s.unit];
+        s.offset = r - s.u.pre;
+        if (s.offset == 0 || !l.whole) return x;
+        const long long rest = s.u.steps + l.blank - s.offset;
+        if (s.offset <= rest) {
+            const long long back = s.offset;
+            s.offset = 0;
+            return x - back;
+        }
+        if (x + rest >= all) return all;
+        if (++s.unit == units) {
+            s.unit = 0;
+            ++s.head;
+        }
+        s.u = l.unit[s.unit];
+        s.offset = 0;
+        return x + rest;
+    };
+    for (int c = tid; c < l.ctas; c += kThreads) {
+        Start s, next;
+        const long long x = begin(c, s);
+        s.left = begin(c + 1, next) - x;
+        l.start[c] = s;
     }
 }
 
@@ -182,6 +209,12 @@ size_t prompt_list_bytes(const PromptSizes &s, const PromptList &l) {
            up256(sizeof(int) * ((size_t)s.B + 1));
 }
 
+bool prompt_splits(const PromptSizes &s, const PromptSeqs &q, const PromptList &l) {
+    // (the tokens that a sequence can have at most)
+    const long long n = l.keys ? (q.cu_q != nullptr ? s.Nq : s.Nq / s.B) : (q.cu_k != nullptr ? s.Nk : s.Nk / s.B);
+    return (n + l.step - 1) / l.step > l.whole;
+}
+
 cudaError_t launch_prompt_plan(const PromptSizes &s, const PromptSeqs &q, const PromptList *lists, int n, void *const *ws,
                                unsigned *err, cudaStream_t st) {
     PlanParams p = {};
@@ -192,7 +225,7 @@ cudaError_t launch_prompt_plan(const PromptSizes &s, const PromptSeqs &q, const 
         const List a = prompt_list_at(s, l, ws[i]);
         char *end = static_cast<char *>(ws[i]) + prompt_list_bytes(s, l) - up256(sizeof(int) * ((size_t)s.B + 1));
         p.l[i] = ListParams{a.header, a.start, a.unit, reinterpret_cast<int *>(end), l.keys ? 1 : 0, l.tile, l.step,
-                            l.ctas, s.Hkv, l.least, l.blank};
+                            l.ctas, s.Hkv, l.least, l.blank, prompt_splits(s, q, l) ? 0 : 1};
     }
     return DependentLaunch(dim3(n), dim3(kThreads), 0, st)(prompt_plan_kernel, p);
 }
