@@ -13,7 +13,7 @@
 //
 // Sums are 64-bit integers in units of 2^-60: exact whatever their order, so
 // that a token does not depend on how a row is split.  Probabilities from 2^-37
-// on enter exactly, of smaller ones whole units.
+// on enter exactly, smaller ones rounded to the unit.
 //
 // B = 128, V = 131072: see the table of cases; one row of 32003: a launch and a
 // chain of five loads.
@@ -37,15 +37,55 @@ struct Params {
 
 using Sum = unsigned long long;
 
-// A probability within [0, 1].
-__device__ __forceinline__ float clamped(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }   // (NaN: 0)
-
-// ... in units of 2^-60, what is below them cut off: its 24 bits shifted to their place.  (A conversion to 64-bit
-// integers takes this GPU's few double-precision units: with it the largest case took 73 us.)
-__device__ __forceinline__ Sum fixed(float p) {
-    const uint32_t b = __float_as_uint(p);
-    return ((Sum)((b & 0x7fffffu) | 0x800000u) << 37) >> min(127u - (b >> 23), 63u);
+// Two f32 in one register pair.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
 }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 less(F2 a, F2 b) {   // a - b
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(b.v), "l"(pair(-1.0f, -1.0f).v), "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ int bits_apart(F2 x) {   // the first's bits less the second's
+    int a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x.v));
+    return a - b;
+}
+
+// p - min(p, q) in whole units of 2^-60 (each of the two rounded to them), as
+// three digits: of 2^-23, 2^-46 and 2^-60.  Adding 1 (1.5 2^-23, 1.5 2^-37) to a
+// value below it leaves the value's multiple of 2^-23 (2^-46, 2^-60) in the
+// sum's bits and, taken off again, an exact rest for the next digit; of p and
+// min(p, q) at once, so that what was added cancels.  NaN and what is below 0
+// count as 0, what is above 1 as 1.  (A conversion to 64-bit integers runs on
+// this GPU's few double-precision units, shifts take three times as many
+// instructions: 73 and 38 us for the largest case.)
+struct Digits {
+    int a, b, c;
+    __device__ __forceinline__ void add_above(float p, float q) {
+        p = fminf(fmaxf(p, 0.0f), 1.0f);
+        const F2 one = pair(1.0f, 1.0f), next = pair(1.5f * 0x1p-23f, 1.5f * 0x1p-23f), last = pair(1.5f * 0x1p-37f, 1.5f * 0x1p-37f);
+        const F2 x = pair(p, fminf(p, fmaxf(q, 0.0f)));
+        const F2 s = add(x, one), rest = less(x, less(s, one));
+        const F2 s2 = add(rest, next), rest2 = less(rest, less(s2, next));
+        a += bits_apart(s);
+        b += bits_apart(s2);
+        c += bits_apart(add(rest2, last));
+    }
+    __device__ __forceinline__ Sum value() const {
+        return (Sum)(((long long)a << 37) + ((long long)b << 14) + (long long)c);
+    }
+};
 
 // What is drawn from: p, or p above q, or p without one token.
 struct Rest {
@@ -130,23 +170,34 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
     const int chunk = (each + 31) / 32 * kBatch;
     const long long start = (long long)piece * each * kBatch;
     const int first = (int)min(start, (long long)V), last = (int)min(start + (long long)each * kBatch, (long long)V);
-    // the batch of 32 x kAhead tokens from i: token i + 32 k + lane in v[k]
-    auto batch = [&](int i, Sum (&v)[kAhead]) {
+    // the batch of 32 x kAhead tokens from i: token i + 32 k + lane by use(k, p, q)
+    auto batch = [&](int i, auto &&use) {
         float x[kAhead], y[kAhead];
-        const bool full = i + kBatch <= last;
+        const float *p0 = rest.p + i + lane, *q0 = rest.q + i + lane;
+        if (i + kBatch <= last) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int at = i + k * 32 + lane;
-            const bool there = full || at < last;
-            x[k] = there ? rest.p[at] : 0.0f;
-            y[k] = there && rest.q != nullptr ? rest.q[at] : 0.0f;
-        }
+            for (int k = 0; k < kAhead; ++k) x[k] = p0[k * 32];
+            if (rest.q != nullptr) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const float p1 = i + k * 32 + lane == rest.without ? 0.0f : clamped(x[k]);
-            v[k] = fixed(p1);
-            if (rest.q != nullptr) v[k] -= fixed(fminf(p1, clamped(y[k])));   // p - min(p, q)
+                for (int k = 0; k < kAhead; ++k) y[k] = q0[k * 32];
+            } else {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) y[k] = 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool there = i + k * 32 + lane < last;
+                x[k] = there ? p0[k * 32] : 0.0f;
+                y[k] = there && rest.q != nullptr ? q0[k * 32] : 0.0f;
+            }
         }
+        if (rest.without >= i && rest.without < i + kBatch)
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i + k * 32 + lane == rest.without) x[k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) use(k, x[k], y[k]);
     };
     Sum total = 0, before = 0, mine = 0, of_chunk = 0;
     for (int round = 0; round < 2; ++round) {
@@ -154,10 +205,9 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
         for (int c = 0, i = first; i < last; ++c) {
             Sum s = 0;
             for (const int end = min(i + chunk, last); i < end; i += kBatch) {
-                Sum v[kAhead];
-                batch(i, v);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) s += v[k];
+                Digits d{0, 0, 0};
+                batch(i, [&](int, float p, float q) { d.add_above(p, q); });
+                s += d.value();
             }
             s = warp_total(s);
             if (lane == c) of_chunk = s;
@@ -192,7 +242,11 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
     const int end = min(first + (hit + 1) * chunk, last);
     for (int i = first + hit * chunk; i < end; i += kBatch) {
         Sum v[kAhead];
-        batch(i, v);
+        batch(i, [&](int k, float p, float q) {
+            Digits d{0, 0, 0};
+            d.add_above(p, q);
+            v[k] = d.value();
+        });
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const Sum line = warp_total(v[k]);
