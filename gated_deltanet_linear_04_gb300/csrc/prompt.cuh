@@ -172,6 +172,12 @@ __device__ __forceinline__ Parts parts_from(const List &l, int cta) {
     return r;
 }
 
+__device__ __forceinline__ float lg2(float x) {   // (off by less than 2^-22)
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Waits of a CTA's roles: after one that gave up, none waits any more (`dead`,
 // in shared memory).  False: not there.  The loop is out of line: it would be
 // in the code some twenty times, and a tile's start and end run through code
@@ -230,6 +236,17 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
+}
+
+// x *= f; returns whether one of them is not finite.
+__device__ __forceinline__ bool scaled(float (&x)[32], float f) {
+    float check = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        x[k] *= f;
+        check = fmaf(x[k], 0.0f, check);   // (0 times an infinity or NaN)
+    }
+    return check != 0.0f;
 }
 
 // Byte offset of 16 bytes (chunk 0 or 1) of a row in a warp's 32 x 32 bytes: no

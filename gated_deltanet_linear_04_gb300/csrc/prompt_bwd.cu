@@ -184,21 +184,19 @@ __device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, cons
     }
 }
 
-// 32 channels from d of the warp's rows, scaled and rounded (0 for rows that
-// are padding).
+// 32 channels from d of the warp's rows, rounded (0 for rows that are padding).
 template <int D>
-__device__ __forceinline__ void write_group(uint8_t *turn, uint16_t *const (&rows)[2], bool valid, int d, const float *x,
-                                            float f) {
+__device__ __forceinline__ void write_group(uint8_t *turn, uint16_t *const (&rows)[2], bool valid, int d, const float *x) {
     const int lane = threadIdx.x & 31;
+    const bool some = __any_sync(0xffffffffu, !valid);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = x[16 * h + 8 * i + k] * f;
-            const uint4 w = attn::pack8(y);
-            *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = valid ? w : make_uint4(0, 0, 0, 0);
+            const float *y = x + 16 * h + 8 * i;
+            uint4 w = make_uint4(attn::pack2(y[0], y[1]), attn::pack2(y[2], y[3]), attn::pack2(y[4], y[5]), attn::pack2(y[6], y[7]));
+            if (some && !valid) w = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = w;
         }
         __syncwarp();
 #pragma unroll
@@ -652,11 +650,9 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     umma::tmem_ld32(lanes + a * D + d, v);
                     umma::tmem_ld_wait();
                     if (whole) {
-                        float check = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) check = fmaf(v[k], 0.0f, check);
-                        write_group<D>(turn, rows, valid, d, v, f);
-                        mend_rows<G>(p, o, w.u, r, of_p, valid && check != 0.0f, p.acc_out[a], d, d + 32);
+                        const bool bad = scaled(v, f);
+                        write_group<D>(turn, rows, valid, d, v);
+                        mend_rows<G>(p, o, w.u, r, of_p, valid && bad, p.acc_out[a], d, d + 32);
                     } else {
                         float4 *dst = reinterpret_cast<float4 *>(p.part) +
                                       (((size_t)slot * G::ACCS + a) * (D / 4) + d / 4) * 128 + r;
@@ -716,12 +712,10 @@ __device__ __forceinline__ void join_parts(const Params &p, int slice, uint8_t (
             }
     }
     const bool of_p = a == 1 || !G::HAS_DP;
-    float check = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) check = fmaf(x[k], 0.0f, check);
+    const bool bad = scaled(x, of_p ? 1.0f : p.scale);
     const bool valid = o.valid && (G::KEYS || part.u.lim0 + (int)(o.token - part.u.a0) > 0);
-    write_group<D>(turn[threadIdx.x >> 5], rows, valid, c * 32, x, of_p ? 1.0f : p.scale);
-    mend_rows<G>(p, o, part.u, r, of_p, valid && check != 0.0f, p.acc_out[a], c * 32, c * 32 + 32);
+    write_group<D>(turn[threadIdx.x >> 5], rows, valid, c * 32, x);
+    mend_rows<G>(p, o, part.u, r, of_p, valid && bad, p.acc_out[a], c * 32, c * 32 + 32);
 }
 
 // All three (dQ, dK, dV): blockIdx.y is the accumulator and its channels.

@@ -66,6 +66,7 @@ struct Params {
 struct Bars {
     uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2];
     float most[2][2][2][128];   // [tile][step parity][half][row]: what the halves of a row tell each other
+    float sum[2][2][128];       // [tile][half][row], at a tile's end
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -169,37 +170,38 @@ __device__ __forceinline__ Gates ask_gates(const RowsOut &r, int d) {
     return g;
 }
 
-// 32 channels from d of the warp's rows: lane i's x of row i scaled, gated,
-// rounded, written.
-__device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, const RowOut &o, bool gated, const Gates &gates,
-                                            int d, const float *x, float f) {
+// 32 channels from d of the warp's rows: lane i's x of row i, gated, rounded,
+// written.  `zero`: the row sees nothing.
+__device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, bool zero, bool gated, const Gates &gates, int d,
+                                            const float *x) {
     const int lane = threadIdx.x & 31;
+    const bool some = __any_sync(0xffffffffu, zero);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        uint4 w[2];
         if (gated) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 *reinterpret_cast<uint4 *>(turn + turn_at(16 * k + (lane >> 1), lane & 1)) = gates.v[h][k];
             __syncwarp();
-        }
-        float y[2][8];
+            float y[2][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float *xs = x + 16 * h + 8 * i;
-            if (gated) {
+            for (int i = 0; i < 2; ++i) {
                 attn::unpack8(*reinterpret_cast<const uint4 *>(turn + turn_at(lane, i)), y[i]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[i][k] = xs[k] * f * rcp_fast(1.0f + exp_fast(-y[i][k]));
-            } else {
+                for (int k = 0; k < 8; ++k) y[i][k] = x[16 * h + 8 * i + k] * rcp_fast(1.0f + exp_fast(-y[i][k]));
+                w[i] = attn::pack8(y[i]);
+            }
+        } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[i][k] = xs[k] * f;
+            for (int i = 0; i < 2; ++i) {
+                const float *y = x + 16 * h + 8 * i;
+                w[i] = make_uint4(attn::pack2(y[0], y[1]), attn::pack2(y[2], y[3]), attn::pack2(y[4], y[5]), attn::pack2(y[6], y[7]));
             }
         }
+        if (some && zero) w[0] = w[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 w = attn::pack8(y[i]);
-            *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = o.keys > 0 ? w : make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4 *>(turn + turn_at(lane, i)) = w[i];
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -564,11 +566,10 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             // the unit's results
             const int slot = w.slot(blockIdx.x);
-            float check = 0.0f;
-            float *ex = bars.most[tile][step & 1][0];
-            ex[half * 128 + r] = l;
+            bool bad = false;
+            bars.sum[tile][half][r] = l;
             pair_sync(tile);
-            l = ex[r] + ex[128 + r];
+            l = bars.sum[tile][0][r] + bars.sum[tile][1][r];
             const float f = 1.0f / l;
             const RowsOut rows = rows_out<D>(p, o);
             constexpr int AHEAD = TWICE ? 1 : 2;   // groups whose gates are asked for (there are no registers for more)
@@ -591,15 +592,14 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                     if (lane == 0) mbar_arrive(&bars.o_free[tile]);
                 }
                 if (whole) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
+                    bad |= scaled(x, f);
                     if (AHEAD > 1) {
                         const Gates now = gates[0];
                         gates[0] = gates[AHEAD - 1];
                         if (gated && c + AHEAD < DH / 32) gates[AHEAD - 1] = ask_gates(rows, d + AHEAD * 32);
-                        write_group(turn, rows, o, gated, now, d, x, f);
+                        write_group(turn, rows, o.keys == 0, gated, now, d, x);
                     } else {
-                        write_group(turn, rows, o, gated, gates[0], d, x, f);
+                        write_group(turn, rows, o.keys == 0, gated, gates[0], d, x);
                         if (gated && c + 1 < DH / 32) gates[0] = ask_gates(rows, d + 32);
                     }
                 } else {
@@ -612,12 +612,13 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
             }
             if (whole) {
-                if (half == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-                mend_rows<D>(p, o, w.u, w.head, check != 0.0f, half * DH, (half + 1) * DH);
+                if (half == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
+                mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
             } else if (half == 0) {
                 p.part_ml[(size_t)slot * (G::TILES * 128) + tile * 128 + r] = make_float2(m, l);
             }
-            pair_sync(tile);   // (the exchange's readers)
+            // (the halves start the next tile together: without it chunks over long prefixes take 126 us, with it 118)
+            if (G::TILES == 1) pair_sync(tile);
         } while (w.next());
         umma::fence_before_sync();
     }
@@ -684,12 +685,10 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const Params p) {
         }
     }
     const float f = 1.0f / l;
-    float check = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) check = fmaf(x[k] * f, 0.0f, check);
-    write_group(turn[threadIdx.x >> 5], rows, o, p.gate.p != nullptr, gates, c * 32, x, f);
-    if (c == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
-    mend_rows<D>(p, o, part.u, part.head, check != 0.0f, c * 32, c * 32 + 32);
+    const bool bad = scaled(x, f);
+    write_group(turn[threadIdx.x >> 5], rows, o.keys == 0, p.gate.p != nullptr, gates, c * 32, x);
+    if (c == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
+    mend_rows<D>(p, o, part.u, part.head, bad, c * 32, c * 32 + 32);
 }
 
 int tiles_of(int D) { return D <= 128 ? 2 : 1; }
