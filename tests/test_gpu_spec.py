@@ -77,6 +77,22 @@ def test_borders(spec, V):
                         assert 0 <= got < V
 
 
+@pytest.mark.parametrize("V", [17, 64, 5000, 131072])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_rows_that_are_no_probabilities_give_some_token(spec, V, drafted):
+    """Sums of 16 and more pass 64 bits."""
+    B, T = 6, 3
+    g = torch.Generator().manual_seed(V)
+    target = torch.rand(B, T + 1, V, generator=g) * torch.tensor([1.0, 1.0, 4.0, 1e30, 0.01, math.inf]).view(B, 1, 1)
+    tokens = torch.randint(0, V, (B, T), generator=g).to(I32)
+    draft = torch.rand(B, T, V, generator=g) * 0.5 if drafted else None
+    out, keep = call(spec, target, tokens, torch.rand(B, T + 1, generator=g), draft)
+    for b in range(B):
+        a = int(keep[b]) - 1
+        assert 0 <= a <= T and torch.equal(out[b, :a], tokens[b, :a])
+        assert 0 <= int(out[b, a]) < V and (out[b, a + 1:] == -1).all()
+
+
 def test_a_cumulative_sum_next_to_u(spec):
     """Sums that are exact in binary, u on the border between two tokens."""
     V = 256
