@@ -238,6 +238,36 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     return r;
 }
 
+// A row of D bf16 in a warp, D / 32 channels a lane.
+template <int D>
+__device__ __forceinline__ void lane_row(const uint16_t *p, float (&x)[D / 32]) {
+    constexpr int N = D / 32;
+    const uint16_t *q = p + (threadIdx.x & 31) * N;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(q)[i];
+        x[2 * i] = __uint_as_float(w << 16);
+        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ float row_dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) t = fmaf(a[i], b[i], t);
+    return warp_sum(t);
+}
+
+// Every channel of the row is NaN (and stays so: no more keys have to be read).
+template <int N>
+__device__ __forceinline__ bool all_nan(const float (&x)[N]) {
+    bool nan = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) nan = nan && x[i] != x[i];
+    return __all_sync(0xffffffffu, nan);
+}
+
 // x *= f; returns whether one of them is not finite.
 __device__ __forceinline__ bool scaled(float (&x)[32], float f) {
     float check = 0.0f;

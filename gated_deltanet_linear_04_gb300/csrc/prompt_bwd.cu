@@ -111,22 +111,7 @@ __device__ __forceinline__ RowOut row_out(const Params &p, const Unit &u, int he
 // ---------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void lane_row(const HeadsIn &h, long long n, int head, float (&x)[D / 32]) {
-    constexpr int N = D / 32;
-    const uint16_t *q = h.p + n * h.ts + head * h.hs + (threadIdx.x & 31) * N;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(q)[i];
-        x[2 * i] = __uint_as_float(w << 16);
-        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-}
-
-template <int D>
-__device__ __forceinline__ float row_dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) t = fmaf(a[i], b[i], t);
-    return warp_sum(t);
+    prompt::lane_row<D>(h.p + n * h.ts + head * h.hs, x);
 }
 
 // One row's dQ (KEYS false: query (token, head), over `n` keys from `first`) or
@@ -161,6 +146,7 @@ __device__ __noinline__ void exact_row(const Params &p, long long token, int hea
                 for (int c = 0; c < N; ++c) acc[c] = fmaf(ds, x[c], acc[c]);
             }
         }
+        if (all_nan(acc)) break;
     }
     const float f = KEYS && of_p ? 1.0f : p.scale;
 #pragma unroll

@@ -226,7 +226,8 @@ __device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, cons
         const int h = (int)(at - n * p.Hq);
         exact_row<D>(p.q.p + n * p.q.ts + h * p.q.hs, p.k.p + u.b0 * p.k.ts + head * p.k.hs, p.k.ts,
                      p.v.p + u.b0 * p.v.ts + head * p.v.hs, p.v.ts, keys, p.scale,
-                     p.gate.p == nullptr ? nullptr : p.gate.p + n * p.gate.ts + h * p.gate.hs, p.out + at * D, d0, d1);
+                     p.gate.p == nullptr ? nullptr : p.gate.p + n * p.gate.ts + h * p.gate.hs, p.out + at * D, d0, d1,
+                     false);
     }
 }
 
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(const Params p) {
             const long long n = o.at / p.Hq;
             const int hq = (int)(o.at - n * p.Hq);
             lse = exact_row<D>(p.q.p + n * p.q.ts + hq * p.q.hs, p.k.p + u.b0 * p.k.ts + head * p.k.hs, p.k.ts,
-                               p.v.p + u.b0 * p.v.ts + head * p.v.hs, p.v.ts, o.keys, p.scale, o.gate, p.out + o.at * D, 0, D);
+                               p.v.p + u.b0 * p.v.ts + head * p.v.hs, p.v.ts, o.keys, p.scale, o.gate, p.out + o.at * D, 0, D, true);
         } else {
             for (int d = lane; d < D; d += 32) p.out[o.at * D + d] = 0;
         }

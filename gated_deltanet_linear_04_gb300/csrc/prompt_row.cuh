@@ -9,32 +9,12 @@
 namespace gdn {
 namespace prompt {
 
-template <int D>
-__device__ __forceinline__ void lane_row(const uint16_t *p, float (&x)[D / 32]) {
-    constexpr int N = D / 32;
-    const uint16_t *q = p + (threadIdx.x & 31) * N;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(q)[i];
-        x[2 * i] = __uint_as_float(w << 16);
-        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-}
-
-template <int D>
-__device__ __forceinline__ float row_dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) t = fmaf(a[i], b[i], t);
-    return warp_sum(t);
-}
-
 // out[d0 .. d1) of the row that sees the first `keys` keys at k, v (> 0);
-// returns its lse.
+// returns its lse (`want_lse`; else a row that has become NaN ends there).
 template <int D>
 __device__ __noinline__ float exact_row(const uint16_t *q, const uint16_t *k, long long k_ts, const uint16_t *v,
                                        long long v_ts, int keys, float scale, const uint16_t *gate, uint16_t *out, int d0,
-                                        int d1) {
+                                        int d1, bool want_lse) {
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31;
     float qx[N], o[N], l = 0.0f, m = -INFINITY;
@@ -55,6 +35,7 @@ __device__ __noinline__ float exact_row(const uint16_t *q, const uint16_t *k, lo
         lane_row<D>(v + j * v_ts, x);
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = fmaf(w, x[i], o[i] * f);
+        if (!want_lse && all_nan(o)) break;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {

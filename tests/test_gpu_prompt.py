@@ -245,6 +245,24 @@ def test_scales(attn, D, scale, std):  # noqa: F811
         near(c.bwd(attn, out, lse)[n], w, t, n)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("which", ["q", "k", "v", "dout"])
+def test_inputs_that_are_all_nan(attn, D, which):  # noqa: F811
+    """NaN where the formulas give NaN, and numbers elsewhere."""
+    c = make((8, 2, D, [700, 3], [700, 40], True, False))
+    out, lse = attn.attn_prefill(c.d, c.q, c.k, c.v, return_lse=True, **c.kw)
+    x = {"q": c.q, "k": c.k, "v": c.v, "dout": c.dout}
+    x[which].fill_(math.nan)
+    if which != "dout":
+        out, lse = attn.attn_prefill(c.d, c.q, c.k, c.v, return_lse=True, **c.kw)
+        assert out.isnan().all() and (lse.isnan().all() if which != "v" else lse.isfinite().all())
+    got = attn.attn_prefill_backward(c.d, c.q, c.k, c.v, out, lse, c.dout, **c.kw)
+    # dV = P^T dO; dQ and dK take the values through dP and delta
+    finite = {"q": (), "k": (), "v": ("dv",), "dout": ()}[which]
+    for name, g in got.items():
+        assert (g.isfinite() if name in finite else g.isnan()).all(), name
+
+
 def test_gradients_match_differences(attn):  # noqa: F811
     """Of a sum of outputs, along random directions: the forward pass itself,
     in 64 bits of the definition, at points a step away."""
