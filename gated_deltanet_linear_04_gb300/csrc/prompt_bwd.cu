@@ -291,8 +291,25 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 tma_load_4d(dst, map, 0, token, sub, head, bar);
             }
         };
+        bool first = true;
         do {
             w.uniform();
+            if (!first) {   // (the tile's resident rows on their way to L2 while the steps before are worked on)
+#pragma unroll 1
+                for (int r = lane; r < 128; r += 32) {
+                    const RowOut o = row_out<G>(p, w.u, w.head, r);
+                    if (!o.valid) continue;
+                    const uint16_t *x = p.a1.p + o.token * p.a1.ts + o.head * p.a1.hs;
+                    const uint16_t *y = p.a2.p + o.token * p.a2.ts + o.head * p.a2.hs;
+#pragma unroll
+                    for (int c = 0; c < D; c += 64) {
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(x + c));
+                        if (G::HAS_DP) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + c));
+                    }
+                }
+                __syncwarp();
+            }
+            first = false;
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
                 if (wait(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
@@ -455,7 +472,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             const bool second = G::HAS_DP && half == 1;
             const HeadsIn &h = second ? p.a2 : p.a1;
             const uint4 *src = reinterpret_cast<const uint4 *>(h.p + o.token * h.ts + o.head * h.hs);
-#pragma unroll 1
+#pragma unroll(D <= 128 ? 2 : 1)
             for (int c = G::HAS_DP ? 0 : half; c < D / 64; c += G::HAS_DP ? 1 : 2) {
                 uint4 x[8];
 #pragma unroll
@@ -487,16 +504,22 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         int step = 0, st = 0, units = 0;
         uint32_t ph = 0;
         bool more = true;
-        while (more) {
-            float nlse = -INFINITY, delta = 0.0f;
-            int keys = 0;
+        float nlse = -INFINITY, delta = 0.0f;
+        int keys = 0;
+        auto row_stats = [&](const RowOut &o, const Unit &u) {
+            nlse = -INFINITY;
+            delta = 0.0f;
+            keys = 0;
             if (!G::KEYS && o.valid) {
-                keys = max(w.u.lim0 + (int)(o.token - w.u.a0), 0);
+                keys = max(u.lim0 + (int)(o.token - u.a0), 0);
                 if (keys > 0) {
                     nlse = -kLog2e * p.lse[o.at];
                     delta = p.delta[o.at];
                 }
             }
+        };
+        row_stats(o, w.u);
+        while (more) {
             for (int i = w.first; i < w.last; ++i, ++step) {
                 const int xb = step % G::XB, stat = st;
                 const uint32_t stat_phase = ph;
@@ -614,14 +637,15 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             // the next tile's resident rows, then this one's results
             Walk y = w;
             more = y.next();
-            RowOut next = o;
-            if (more) {
-                next = row_out<G>(p, y.u, y.head, r);
-                load_resident(next);
-            }
             const bool whole = w.whole();
             const int slot = w.slot(blockIdx.x);
             const bool valid = o.valid && (!G::KEYS || w.u.n_b > 0) && (G::KEYS || keys > 0);
+            RowOut next = o;
+            if (more) {
+                next = row_out<G>(p, y.u, y.head, r);
+                row_stats(next, y.u);
+                load_resident(next);
+            }
             wait(&bars.acc_done, units & 1);
             umma::fence_after_sync();
 #pragma unroll 1
