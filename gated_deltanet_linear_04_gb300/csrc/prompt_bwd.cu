@@ -37,7 +37,7 @@ struct Geo {
     static constexpr bool KEYS = KIND != kDQ;                       // the resident rows are keys
     static constexpr bool HAS_DP = KIND != kDV, HAS_P = KIND == kDKV || KIND == kDV;   // dP needed; P accumulated
     static constexpr int ACCS = (HAS_DP ? 1 : 0) + (HAS_P ? 1 : 0);
-    static constexpr bool A2_SMEM = D == 256 && HAS_DP;
+    static constexpr bool A2_SMEM = D == 256 && HAS_DP, A2_RING = D <= 128 && HAS_DP;   // how the second tile comes and stays
     static constexpr int A1_COL = ACCS * D, A2_COL = A1_COL + D / 2, S_COL = HAS_DP && !A2_SMEM ? A2_COL + D / 2 : A2_COL;
     static_assert(S_COL + 128 <= 512, "");
     static constexpr int SUB = kRows * 128;                         // bytes of 64 rows of 64 channels
@@ -71,11 +71,11 @@ struct Params {
     uint16_t *acc_out[2];
     float *part;             // [slot][acc][D / 4][128][4]
     unsigned *err;
-    int Hq, Hkv, G, tile, tps;   // tile: tokens of a resident tile; tps: of a step
+    int Hq, Hkv, G, box, tps;   // tokens: of 64 query rows, of a step
 };
 
 struct Bars {
-    uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free;
+    uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, a2_full, a2_free, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free;
     uint64_t stats_full[kStats], stats_free[kStats];
 };
 
@@ -96,10 +96,12 @@ struct RowOut {
 template <class G>
 __device__ __forceinline__ RowOut row_out(const Params &p, const Unit &u, int head, int r) {
     RowOut o;
-    const int t = G::KEYS ? r : r / p.G;
-    o.head = G::KEYS ? head : head * p.G + r - t * p.G;
-    o.mine = t < p.tile && t < u.slot_a;
-    o.valid = t < p.tile && t < u.n_a;
+    // (queries: two boxes of 64 rows, G heads of a token after the other)
+    const int x = (r & (kRows - 1)) / p.G, t = G::KEYS ? r : r / kRows * p.box + x;
+    o.head = G::KEYS ? head : head * p.G + (r & (kRows - 1)) - x * p.G;
+    const bool row = G::KEYS || x < p.box;
+    o.mine = row && t < u.slot_a;
+    o.valid = row && t < u.n_a;
     o.token = (long long)u.a0 + t;
     o.at = o.token * (G::KEYS ? p.Hkv : p.Hq) + o.head;
     return o;
@@ -215,6 +217,7 @@ __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, 256;" ::: "me
 template <class G>
 __global__ void __launch_bounds__(G::THREADS, 1)
 prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
+                       const __grid_constant__ CUtensorMap res1, const __grid_constant__ CUtensorMap res2,
                        const __grid_constant__ Params p) {
     constexpr int D = G::D;
     extern __shared__ uint8_t raw[];
@@ -241,6 +244,8 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             mbar_init(&bars.empty2[i], 1);
         }
         mbar_init(&bars.a_full, G::WARPS);
+        mbar_init(&bars.a2_full, 1);
+        mbar_init(&bars.a2_free, 1);
         mbar_init(&bars.s_free, G::ROWS_WARPS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
@@ -278,54 +283,73 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         if (umma::elect_one()) {
             prefetch_tmap(&map1);
             prefetch_tmap(&map2);
+            prefetch_tmap(&res1);
+            prefetch_tmap(&res2);
         }
-        int s1 = 0, s2 = 0;
+        int s1 = 0, s2 = 0, units = 0;
         uint32_t ph1 = 0, ph2 = 0;
-        // `subs` groups of 64 channels from group `sub`
-        auto load = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int head, int token, int sub, int subs) {
-            if (G::KEYS) {
-                mbar_expect_tx(bar, (uint32_t)(subs * 128 * p.tps * p.G));
+        auto pass1 = [&] {
+            if (++s1 == G::N1) {
+                s1 = 0;
+                ph1 ^= 1;
+            }
+        };
+        auto pass2 = [&] {
+            if (++s2 == G::N2) {
+                s2 = 0;
+                ph2 ^= 1;
+            }
+        };
+        // 64 rows of queries or keys, `subs` groups of 64 channels from group `sub`
+        auto load = [&](bool queries, const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int head, int token, int sub, int subs) {
+            if (queries) {
+                mbar_expect_tx(bar, (uint32_t)(subs * 128 * p.box * p.G));
                 for (int i = 0; i < subs; ++i) tma_load_3d(dst + i * G::SUB, map, (sub + i) * 64, head * p.G, token, bar);
             } else {
                 mbar_expect_tx(bar, (uint32_t)(subs * G::SUB));
                 tma_load_4d(dst, map, 0, token, sub, head, bar);
             }
         };
-        bool first = true;
         do {
             w.uniform();
-            if (!first) {   // (the tile's resident rows on their way to L2 while the steps before are worked on)
+            // the resident rows, 64 in a stage, come through the rings before the steps
+            const int half = G::KEYS ? kRows : p.box;   // tokens of 64 rows
 #pragma unroll 1
-                for (int r = lane; r < 128; r += 32) {
-                    const RowOut o = row_out<G>(p, w.u, w.head, r);
-                    if (!o.valid) continue;
-                    const uint16_t *x = p.a1.p + o.token * p.a1.ts + o.head * p.a1.hs;
-                    const uint16_t *y = p.a2.p + o.token * p.a2.ts + o.head * p.a2.hs;
-#pragma unroll
-                    for (int c = 0; c < D; c += 64) {
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(x + c));
-                        if (G::HAS_DP) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + c));
-                    }
+            for (int h = 0; h < 2; ++h) {
+                if (wait(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
+                    load(!G::KEYS, &res1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, w.u.a0 + h * half, 0, D / 64);
+                pass1();
+                if (G::A2_RING) {
+                    if (wait(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
+                        load(!G::KEYS, &res2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, w.u.a0 + h * half, 0, D / 64);
+                    pass2();
                 }
-                __syncwarp();
             }
-            first = false;
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
                 if (wait(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
-                    load(&map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
-                if (++s1 == G::N1) {
-                    s1 = 0;
-                    ph1 ^= 1;
+                    load(G::KEYS, &map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
+                pass1();
+                if (G::A2_SMEM && i == w.first) {   // the second resident tile, to where it stays
+                    if ((units == 0 || wait(&bars.a2_free, (units - 1) & 1)) && umma::elect_one()) {
+                        mbar_expect_tx(&bars.a2_full, G::KEYS ? 128 * D * 2 : 2 * p.box * p.G * D * 2);
+#pragma unroll 1
+                        for (int c = 0; c < 2 * (D / 64); ++c) {
+                            uint8_t *dst = smem + c * G::SUB;
+                            if (G::KEYS)
+                                tma_load_4d(dst, &res2, 0, w.u.a0 + (c & 1) * half, c >> 1, w.head, &bars.a2_full);
+                            else
+                                tma_load_3d(dst, &res2, (c >> 1) * 64, w.head * p.G, w.u.a0 + (c & 1) * half, &bars.a2_full);
+                        }
+                    }
+                    ++units;
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP2; ++c) {
                     if (wait(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
-                        load(&map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c, G::STAGE2 / G::SUB);
-                    if (++s2 == G::N2) {
-                        s2 = 0;
-                        ph2 ^= 1;
-                    }
+                        load(G::KEYS, &map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c,
+                             G::STAGE2 / G::SUB);
+                    pass2();
                 }
             }
         } while (__any_sync(0xffffffffu, w.next()));
@@ -333,6 +357,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             for (int i = 0; i < 5; ++i) {
                 if (i < 4) mbar_try_wait(&bars.full1[i], 0);
                 mbar_try_wait(&bars.full2[i], 0);
+                if (i == 4) mbar_try_wait(&bars.a2_full, 0);
             }
     } else if (any && warp == G::WARPS + 1) {
         // ---- products
@@ -353,6 +378,10 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             if (!acc && done > 0) wait(&bars.acc_free, (done - 1) & 1);
             umma::fence_after_sync();
             const uint64_t a = d_x + (uint32_t)(xb * G::XT * (G::XTILE >> 4));
+            if (!acc) {   // (a new tile: its resident rows have had two stages)
+                t1 = (t1 + 2) % G::N1;
+                if (G::A2_RING) t2 = (t2 + 2) % G::N2;
+            }
             if (G::HAS_DP) {
                 umma::warp_mma_bf16_k64_bt(base, a, d_t1 + (uint32_t)(t1 * (G::STAGE >> 4)), id_a, acc);
                 umma::warp_mma_commit(&bars.empty1[t1]);
@@ -375,7 +404,22 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         bool more = true;
         while (more) {
             w.uniform();
-            wait(&bars.a_full, units++ & 1);
+            wait(&bars.a_full, units & 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // the stages of the resident rows, which are in the tensor memory now
+                if (umma::elect_one()) {
+                    mbar_arrive(&bars.empty1[s1]);
+                    if (G::A2_RING) mbar_arrive(&bars.empty2[s2]);
+                }
+                if (++s1 == G::N1) {
+                    s1 = 0;
+                    ph1 ^= 1;
+                }
+                if (G::A2_RING && ++s2 == G::N2) {
+                    s2 = 0;
+                    ph2 ^= 1;
+                }
+            }
             for (int i = w.first; i < w.last; ++i, ++step) {
                 if (step > 0) wait(&bars.s_free, (step - 1) & 1);
                 wait(&bars.full1[s1], ph1);
@@ -389,6 +433,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     s1 = 0;
                     ph1 ^= 1;
                 }
+                if (G::A2_SMEM && i == w.first) wait(&bars.a2_full, units & 1);
 #pragma unroll 1
                 for (int h = 0; h < G::PER_STEP2; ++h) {
                     wait(&bars.full2[s2], ph2);
@@ -411,6 +456,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     }
                 }
                 umma::warp_mma_commit(&bars.s_full[step & 1]);
+                if (G::A2_SMEM && i + 1 == w.last) umma::warp_mma_commit(&bars.a2_free);
                 ++waiting;
                 // (of this tile: with products two steps later those of the last tile are through, see below)
                 if (waiting > G::LATER) {
@@ -418,10 +464,12 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     --waiting;
                 }
             }
+            ++units;
             more = __any_sync(0xffffffffu, w.next());
-            // One step later: the next tile's first scores come before this one's last products.  Two: not, as their rows'
-            // warps would wait for these before they take the scores.
-            if (G::LATER > 1 || !more)
+            // One step later: the next tile's first scores come before this one's last products, if the ring has room for
+            // the last step, two stages of resident rows and the first step.  Two: not, as their rows' warps would wait for
+            // these before they take the scores.
+            if (G::LATER > 1 || (G::HAS_DP && G::N1 < 4) || !more)
                 for (; waiting > 0; --waiting) accumulate(step - waiting, waiting == 1);
         }
         wait(&bars.acc_done, (done - 1) & 1);   // every product is through before the tensor memory goes back
@@ -467,37 +515,37 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         const int half = warp >> 2, r = (warp & 3) * 32 + lane, col0 = G::TURNS ? 0 : half * 32;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         uint8_t *turn = smem + G::X_AT + warp * G::TURN;
-        // the resident rows: half of the warps brings A1, half A2
+        // The resident rows from the stages that they came in (the `at1`th and next of the first ring, the `at2`th and next of
+        // the second) to the tensor memory: half of the warps takes A1, half A2, or each half of A1's channels.
+        int at1 = 0, at2 = 0;
         auto load_resident = [&](const RowOut &o) {
-            const bool second = G::HAS_DP && half == 1;
-            const HeadsIn &h = second ? p.a2 : p.a1;
-            const uint4 *src = reinterpret_cast<const uint4 *>(h.p + o.token * h.ts + o.head * h.hs);
+            const int h = r / kRows, rr = r & (kRows - 1);
+            const bool second = G::A2_RING && half == 1;
+            const int n = second ? (at2 + h) % G::N2 : (at1 + h) % G::N1;
+            wait(second ? &bars.full2[n] : &bars.full1[n], ((second ? (at2 + h) / G::N2 : (at1 + h) / G::N1)) & 1);
+            uint8_t *src = smem + (second ? G::RING2 + n * G::STAGE2 : G::RING1 + n * G::STAGE);
 #pragma unroll(D <= 128 ? 2 : 1)
-            for (int c = G::HAS_DP ? 0 : half; c < D / 64; c += G::HAS_DP ? 1 : 2) {
-                uint4 x[8];
+            for (int c = G::A2_RING ? 0 : half; c < D / 64; c += G::A2_RING ? 1 : 2) {
+                float y[32];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = o.valid ? src[c * 8 + k] : make_uint4(0, 0, 0, 0);
-                if (second && G::A2_SMEM) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(smem + c * 128 * 128 + umma::sw128(r, k * 16)) = x[k];
-                } else {
-                    float y[32];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        y[4 * k] = __uint_as_float(x[k].x);
-                        y[4 * k + 1] = __uint_as_float(x[k].y);
-                        y[4 * k + 2] = __uint_as_float(x[k].z);
-                        y[4 * k + 3] = __uint_as_float(x[k].w);
-                    }
-                    umma::tmem_st32(lanes + (second ? G::A2_COL : G::A1_COL) + c * 32, y);
+                for (int k = 0; k < 8; ++k) {
+                    uint4 *at = reinterpret_cast<uint4 *>(src + c * G::SUB + umma::sw128(rr, k * 16));
+                    const uint4 x = o.valid ? *at : make_uint4(0, 0, 0, 0);
+                    y[4 * k] = __uint_as_float(x.x);
+                    y[4 * k + 1] = __uint_as_float(x.y);
+                    y[4 * k + 2] = __uint_as_float(x.z);
+                    y[4 * k + 3] = __uint_as_float(x.w);
+                    if (G::KEYS && rr >= p.tps * p.G) *at = make_uint4(0, 0, 0, 0);   // (no token's in the steps, see above)
                 }
+                umma::tmem_st32(lanes + (second ? G::A2_COL : G::A1_COL) + c * 32, y);
             }
             umma::tmem_st_wait();
             fence_proxy_async_smem();
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.a_full);
+            at1 += 2;
+            at2 += 2;
         };
         RowOut o = row_out<G>(p, w.u, w.head, r);
         load_resident(o);
@@ -644,6 +692,8 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             if (more) {
                 next = row_out<G>(p, y.u, y.head, r);
                 row_stats(next, y.u);
+                at1 += w.last - w.first;
+                at2 += w.last - w.first;
                 load_resident(next);
             }
             wait(&bars.acc_done, units & 1);
@@ -818,7 +868,7 @@ __global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams
 constexpr int kBlank = 9;
 
 PromptList q_list(const PromptSizes &s) {
-    return PromptList{false, 128 / (s.Hq / s.Hkv), kRows, num_sms(), 4, kBlank, 6};
+    return PromptList{false, 2 * (kRows / (s.Hq / s.Hkv)), kRows, num_sms(), 4, kBlank, 6};
 }
 
 PromptList k_list(const PromptSizes &s) {
@@ -843,11 +893,12 @@ Workspace workspace(const PromptSizes &s, bool gated) {
 }
 
 template <class G>
-cudaError_t launch_pass(const CUtensorMap &m1, const CUtensorMap &m2, const Params &p, cudaStream_t st) {
+cudaError_t launch_pass(const CUtensorMap &m1, const CUtensorMap &m2, const CUtensorMap &r1, const CUtensorMap &r2,
+                        const Params &p, cudaStream_t st) {
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, prompt_backward_kernel<G>, G::SMEM);
     if (e != cudaSuccess) return e;
-    return DependentLaunch(dim3(num_sms()), dim3(G::THREADS), G::SMEM, st)(prompt_backward_kernel<G>, m1, m2, p);
+    return DependentLaunch(dim3(num_sms()), dim3(G::THREADS), G::SMEM, st)(prompt_backward_kernel<G>, m1, m2, r1, r2, p);
 }
 
 template <int D>
@@ -905,6 +956,7 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     p.Hq = s.Hq;
     p.Hkv = s.Hkv;
     p.G = G;
+    p.box = tps;
     auto part = [&](int i) { return reinterpret_cast<float *>(ws + w.part[i]); };
 
     Params pq = p;
@@ -913,26 +965,24 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     pq.a2 = g;
     pq.acc_out[0] = dq;
     pq.part = part(0);
-    pq.tile = lists[0].tile;
     pq.tps = kRows;
     Params pk = p;
     pk.list = prompt_list_at(s, lists[1], at[1]);
     pk.a1 = k;
     pk.a2 = v;
     pk.part = part(1);
-    pk.tile = 128;
     pk.tps = tps;
     Params pv = pk;
     pk.acc_out[0] = dk;
     pk.acc_out[1] = dv;
     pv.acc_out[0] = dv;
     pv.part = part(2);
-    if (!no_q) e = launch_pass<Geo<D, kDQ>>(mk, mv, pq, st);
+    if (!no_q) e = launch_pass<Geo<D, kDQ>>(mk, mv, mq, mg, pq, st);
     if constexpr (D == 256) {
-        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDK>>(mq, mg, pk, st);
-        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDV>>(mq, mg, pv, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDK>>(mq, mg, mk, mv, pk, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDV>>(mq, mg, mk, mv, pv, st);
     } else {
-        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDKV>>(mq, mg, pk, st);
+        if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDKV>>(mq, mg, mk, mv, pk, st);
     }
     if (e != cudaSuccess) return e;
     // (no keys, or no queries: no tile has more than a step)

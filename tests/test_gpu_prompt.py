@@ -329,6 +329,21 @@ def test_lengths_are_clamped_to_their_slots(attn):  # noqa: F811
     assert (out == 0).all() and (lse == -math.inf).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(16, 2), (16, 16), (10, 2)])
+def test_many_tiles_of_many_steps_each(attn, D, heads):  # noqa: F811
+    """Every CTA goes through several tiles, of queries and of keys."""
+    c = make((*heads, D, [700, 1300, 257, 600], [900, 1300, 300, 600], True, True))
+    out, lse = c.fwd(attn)
+    want, wlse, tol, ltol = c.want_fwd()
+    near(out, want, tol, "out")
+    near(lse, wlse, ltol, "lse")
+    got = c.bwd(attn, out, lse)
+    for n, (w, t) in c.want_bwd().items():
+        near(got[n], w, t, n)
+    assert status() == 0
+
+
 def test_empty_sides(attn):  # noqa: F811
     d = wl.AttnDims(B=2, T=5, Hq=4, Hkv=2, D=128)
     q, none = torch.randn(2, 5, 4, 128, device=DEV).to(BF16), torch.empty(2, 0, 2, 128, device=DEV, dtype=BF16)
