@@ -46,7 +46,12 @@ struct Geo {
     static constexpr int WARPS = 4 * HALVES * TILES;
     static constexpr int THREADS = 32 * (WARPS + 2);
     static constexpr int TURN = 32 * 32;                   // bytes in which a warp turns 16 channels of its rows into rows
-    static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + WARPS * TURN + 1024;
+    // Results go through stages of the ring, into which their gates come by TMA, and out by TMA (packed, 128 channels: 300 us;
+    // turned into rows by each warp 343).  With 256 channels they would take four of nine stages while the next tile's keys
+    // and values need them: there they are turned (T = 8192: 353 us; through the ring 367).
+    static constexpr bool STAGED = TILES == 2;
+    static constexpr int RESULTS = STAGED ? TILES * (D / 64) : 0;   // stages of a unit's results
+    static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + (STAGED ? 0 : WARPS * TURN) + 1024;
     static constexpr int S_COL = TILES * D;                // two buffers of 128 columns
     static_assert(SMEM + 6144 <= 227 * 1024, "");
 };
@@ -81,6 +86,18 @@ __device__ __forceinline__ void pair_sync(int tile) {
         asm volatile("bar.sync 1, 256;" ::: "memory");
     else
         asm volatile("bar.sync 2, 256;" ::: "memory");
+}
+
+// `threads` threads meet (barrier `id`); whether one of them has x.
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, %2, %3, a;\n\t"
+        "selp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
 }
 
 // Scores that are not to be seen (from `lim` on) are -infinity.
@@ -212,6 +229,25 @@ __device__ __forceinline__ void write_group(uint8_t *turn, const RowsOut &r, boo
     }
 }
 
+// 32 channels of a row into its place in a stage (from byte b of the row on),
+// over its gate if there is one.
+__device__ __forceinline__ void put_group(uint8_t *stage, int r, int b, bool zero, bool gated, const float *x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(stage + umma::sw128(r, b + i * 16));
+        float y[8];
+        if (gated) {
+            attn::unpack8(*at, y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k] * rcp_fast(1.0f + exp_fast(-y[k]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[8 * i + k];
+        }
+        *at = zero ? make_uint4(0, 0, 0, 0) : attn::pack8(y);
+    }
+}
+
 // The warp's rows that are not finite once more, by the definition.
 template <int D>
 __device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, const Unit &u, int head, bool bad, int d0,
@@ -234,7 +270,8 @@ __device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, cons
 template <int D_>
 __global__ void __launch_bounds__(Geo<D_>::THREADS, 1)
 prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                      const __grid_constant__ CUtensorMap v_map, const Params p) {
+                      const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap gate_map,
+                      const __grid_constant__ CUtensorMap out_map, const Params p) {
     using G = Geo<D_>;
     constexpr int D = D_;
     extern __shared__ uint8_t raw[];
@@ -348,6 +385,23 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (G::TILES == 1 && n > 0) load_values();
             if (n > 0 && i == w.last) {
+                if (G::STAGED && w.whole()) {   // stages for the results, with the gates in them
+                    if (!more)     // (where the next unit's keys would be: the place of these is known without it)
+                        for (int c = 0; c < G::PER_STEP; ++c) stage_done();
+#pragma unroll 1
+                    for (int c = 0; c < G::RESULTS; ++c) {
+                        if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                            if (p.gate.p != nullptr) {
+                                mbar_expect_tx(&bars.full[stage], 128 * p.tpt * p.G);
+                                tma_load_3d(ring + stage * G::STAGE, &gate_map, c % (D / 64) * 64, w.head * p.G,
+                                            w.u.a0 + c / (D / 64) * p.tpt, &bars.full[stage]);
+                            } else {
+                                mbar_arrive(&bars.full[stage]);
+                            }
+                        }
+                        stage_done();
+                    }
+                }
                 if (!__any_sync(0xffffffffu, w.next())) break;
                 w.uniform();
                 i = w.first;
@@ -459,6 +513,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             ++step;
             if (++i == w.last) {
                 ++done;
+                if (G::STAGED && w.whole())
+                    for (int c = 0; c < G::RESULTS; ++c) pass(stage, phase);
                 if (!__any_sync(0xffffffffu, w.next())) break;
                 w.uniform();
                 i = w.first;
@@ -475,14 +531,18 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         constexpr int COLS = 64, DH = D / 2;
         const int tile = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), o_at = lanes + tile * D + half * DH;
-        uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;
+        uint8_t *turn = ring + G::STAGES * G::STAGE + warp * G::TURN;   // (if not STAGED)
+        // who writes a stage of results: a warpgroup, or with 64 channels both of a tile
+        constexpr bool SHARED = DH < 64;
+        const bool leader = G::STAGED && (warp & 3) == 0 && lane == 0 && (!SHARED || half == 0);
+        const int team = SHARED ? 1 + tile : 3 + tile * 2 + half, team_size = SHARED ? 256 : 128;
         const float f2 = p.scale2;
-        int step = 0;
+        int step = 0, wholes = 0;
         do {
             const RowOut o = row_out<D>(p, w.u, w.head, tile, r);
             const bool whole = w.whole(), gated = p.gate.p != nullptr && whole;
             float m = -INFINITY, l = 0.0f;   // m: of the scores in powers of two; l: of this half's keys
-            if (gated && o.gate != nullptr)   // (on its way to L2 before it is needed)
+            if (!G::STAGED && gated && o.gate != nullptr)   // (on its way to L2 before it is needed)
                 for (int d = half * DH; d < (half + 1) * DH; d += 64)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(o.gate + d));
             for (int i = w.first; i < w.last; ++i, ++step) {
@@ -572,12 +632,17 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             pair_sync(tile);
             l = bars.sum[tile][0][r] + bars.sum[tile][1][r];
             const float f = 1.0f / l;
-            const RowsOut rows = rows_out<D>(p, o);
-            constexpr int AHEAD = TWICE ? 1 : 2;   // groups whose gates are asked for (there are no registers for more)
-            Gates gates[AHEAD];
-            if (gated)
+            // the first of the tile's result stages, as the loading warp counts: behind all steps' keys and values, the next
+            // unit's first keys and the results before
+            const int at0 = (2 * step + 1) * G::PER_STEP + wholes * G::RESULTS + tile * (D / 64);
+            RowsOut rows;
+            Gates gates[2];   // asked for two groups ahead
+            if (!G::STAGED) {
+                rows = rows_out<D>(p, o);
+                if (gated)
 #pragma unroll
-                for (int z = 0; z < AHEAD; ++z) gates[z] = ask_gates(rows, half * DH + z * 32);
+                    for (int z = 0; z < 2; ++z) gates[z] = ask_gates(rows, half * DH + z * 32);
+            }
             wait(o_done(tile, step - 1), o_phase(step - 1));
             umma::fence_after_sync();
             // (not unrolled: the code would be fetched anew for every tile)
@@ -592,17 +657,18 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.o_free[tile]);
                 }
-                if (whole) {
+                if (whole && !G::STAGED) {
                     bad |= scaled(x, f);
-                    if (AHEAD > 1) {
-                        const Gates now = gates[0];
-                        gates[0] = gates[AHEAD - 1];
-                        if (gated && c + AHEAD < DH / 32) gates[AHEAD - 1] = ask_gates(rows, d + AHEAD * 32);
-                        write_group(turn, rows, o.keys == 0, gated, now, d, x);
-                    } else {
-                        write_group(turn, rows, o.keys == 0, gated, gates[0], d, x);
-                        if (gated && c + 1 < DH / 32) gates[0] = ask_gates(rows, d + 32);
-                    }
+                    const Gates now = gates[0];
+                    gates[0] = gates[1];
+                    if (gated && c + 2 < DH / 32) gates[1] = ask_gates(rows, d + 64);
+                    write_group(turn, rows, o.keys == 0, gated, now, d, x);
+                } else if (whole) {
+                    const int at = at0 + d / 64;
+                    // (the stage's last use is over: it was two steps' products back, or this tile's results)
+                    wait(&bars.full[at % G::STAGES], (at / G::STAGES) & 1);
+                    bad |= scaled(x, f);
+                    put_group(ring + at % G::STAGES * G::STAGE, r, d % 64 * 2, o.keys == 0, gated, x);
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o) +
                                   ((size_t)slot * (D / 4) + d / 4) * (G::TILES * 128) + tile * 128 + r;
@@ -614,13 +680,52 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (whole) {
                 if (half == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
-                mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
+                if (!G::STAGED) {
+                    mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
+                } else {
+                    const bool complete = (tile + 1) * p.tpt <= w.u.slot_a;   // all rows are the sequence's
+                    if (!complete) {
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = lane; i < 32 * DH / 8; i += 32) {
+                            const int rr = (warp & 3) * 32 + i / (DH / 8), d = half * DH + i % (DH / 8) * 8;
+                            const RowOut to = row_out<D>(p, w.u, w.head, tile, rr);
+                            if (to.mine)
+                                *reinterpret_cast<uint4 *>(p.out + to.at * D + d) = *reinterpret_cast<const uint4 *>(
+                                    ring + (at0 + d / 64) % G::STAGES * G::STAGE + umma::sw128(rr, d % 64 * 2));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    const bool any = any_of(team, team_size, bad);
+                    if (leader) {
+                        constexpr int N = SHARED ? 1 : DH / 64;
+                        const int at = at0 + (SHARED ? 0 : half * N);
+                        if (complete) {
+                            for (int c = 0; c < N; ++c)
+                                tma_store_3d(&out_map, (SHARED ? 0 : half * DH) + c * 64, w.head * p.G, w.u.a0 + tile * p.tpt,
+                                             ring + (at + c) % G::STAGES * G::STAGE);
+                            bulk_commit();
+                            if (any)
+                                bulk_wait_all();   // (rows that are written once more)
+                            else
+                                bulk_wait_read();
+                        }
+                        for (int c = 0; c < N; ++c) mbar_arrive(&bars.empty[(at + c) % G::STAGES]);
+                    }
+                    __syncwarp();
+                    if (any) {
+                        any_of(team, team_size, false);
+                        mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
+                    }
+                    ++wholes;
+                }
             } else if (half == 0) {
                 p.part_ml[(size_t)slot * (G::TILES * 128) + tile * 128 + r] = make_float2(m, l);
             }
             // (the halves start the next tile together: without it chunks over long prefixes take 126 us, with it 118)
             if (G::TILES == 1) pair_sync(tile);
         } while (w.next());
+        if (leader) bulk_wait_all();
         umma::fence_before_sync();
     }
     __syncthreads();
@@ -721,16 +826,18 @@ cudaError_t launch_d(const PromptSizes &s, Params &p, bool splits, cudaStream_t 
     static unsigned long long done = 0;
     cudaError_t e = set_max_smem(done, prompt_forward_kernel<D>, G::SMEM);
     if (e != cudaSuccess) return e;
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, gate, out;
     // (no keys: nothing of what is loaded counts, but a map needs a tensor)
     const bool none = s.Nk == 0;
     const HeadsIn dummy{p.q.p, 0, 0};
-    if (!queries_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) ||
+    const HeadsIn results{p.out, (long long)s.Hq * D, D};
+    if (!queries_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) || !queries_map(&out, results, s.Nq, s.Hq, D, p.G, p.tpt) ||
+        !queries_map(&gate, p.gate.p != nullptr ? p.gate : results, s.Nq, s.Hq, D, p.G, p.tpt) ||
         !keys_map(&k, none ? dummy : p.k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kKeys, 1) ||
         !keys_map(&v, none ? dummy : p.v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, G::VK, D / 64))
         return cudaErrorInvalidValue;
     const int ctas = num_sms();
-    e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, p);
+    e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, gate, out, p);
     if (e != cudaSuccess || !splits) return e;
     return DependentLaunch(dim3(ctas - 1, G::TILES * (D / 32)), dim3(128), 0, st)(prompt_join_kernel<D>, p);
 }
