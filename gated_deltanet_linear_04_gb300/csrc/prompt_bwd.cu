@@ -691,10 +691,10 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             RowOut next = o;
             if (more) {
                 next = row_out<G>(p, y.u, y.head, r);
-                row_stats(next, y.u);
                 at1 += w.last - w.first;
                 at2 += w.last - w.first;
                 load_resident(next);
+                row_stats(next, y.u);
             }
             wait(&bars.acc_done, units & 1);
             umma::fence_after_sync();
@@ -864,8 +864,9 @@ __global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams
     }
 }
 
-// A tile's start and end in steps (T = 8192: 2 1888 us, 6 1640, 9 1570, 12 1575; packed, 128 channels: 523, 463, 459, 463).
-constexpr int kBlank = 9;
+// A tile's start and end in steps (T = 8192: 2 1483 us, 3 1439, 4 1440, 6 1446, 9 1492; packed, 128 channels: 391, 381, 368,
+// 369, 383).
+constexpr int kBlank = 4;
 
 PromptList q_list(const PromptSizes &s) {
     return PromptList{false, 2 * (kRows / (s.Hq / s.Hkv)), kRows, num_sms(), 4, kBlank, 6};
