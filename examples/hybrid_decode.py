@@ -1,7 +1,9 @@
 """A Gated DeltaNet layer's core and a full-attention layer's core side by
 side, as the layers of a hybrid model use them: a training step of the
-attention layer's norm and rotation, a ragged prompt into the paged e4m3
-cache, and decode steps of both layers replayed as one CUDA graph.
+attention layer (positions on three axes, as of tokens of an image), ragged
+prompts into the paged e4m3 cache and their attention, decode steps of both
+layers replayed as one CUDA graph, and a step of drafted tokens that are
+verified.
 
 The projections around the cores are random matrices.  Run on a GB300 after
 ``python -c "import __graft_entry__ as g; g.build()"``:
@@ -17,7 +19,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
-from gated_deltanet_linear_04_gb300 import attn, gdn, workloads as wl  # noqa: E402
+from gated_deltanet_linear_04_gb300 import attn, gdn, spec, workloads as wl  # noqa: E402
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -33,16 +35,23 @@ def visible_attention(q, k, v, first):
     return torch.einsum("bhtl,blhd->bthd", torch.softmax(s, -1), v)
 
 
-def training_step(d, qkv, wq, wk, freqs):
-    """Forward and backward of the attention layer from its packed projection;
-    returns the gradients of q, k and the norm weights."""
+def training_step(d, qkv, gate, dout, wq, wk, freqs, axes, pos):
+    """Forward and backward of the attention layer's core from its packed
+    projection and its gate, for the output's gradient dout: the output and
+    the gradients of q, k, v, the gate and the norm weights."""
     q, k, v = split(d, qkv)
-    pos = torch.arange(d.T, dtype=I32, device=q.device).expand(d.B, -1).contiguous()
-    qr, kr = attn.qk_norm_rope(d, q, k, wq, wk, freqs, pos)
-    qa, ka = qr.clone().requires_grad_(), kr.clone().requires_grad_()
-    out = visible_attention(qa, ka, v, torch.zeros(d.B, dtype=torch.long, device=q.device))
-    dq, dk = torch.autograd.grad(out.square().mean() * 1e3, (qa, ka))
-    return attn.qk_norm_rope_backward(d, q, k, wq, wk, freqs, pos, dq.contiguous(), dk.contiguous())
+    qr, kr = attn.qk_norm_rope_axes(d, q, k, wq, wk, freqs, axes, pos)
+    out, lse = attn.attn_prefill(d, qr, kr, v, gate=gate, return_lse=True)
+    g = attn.attn_prefill_backward(d, qr, kr, v, out, lse, dout, gate=gate)
+    grads = attn.qk_norm_rope_axes_backward(d, q, k, wq, wk, freqs, axes, pos, g["dq"], g["dk"])
+    return out, dict(grads, dv=g["dv"], dgate=g["dgate"])
+
+
+def image_positions(d, start, width, dev):
+    """[3, B, T]: tokens of an image of `width` columns (its time, row, column), from `start` on."""
+    t = torch.arange(d.T, device=dev)
+    at = torch.stack([torch.zeros_like(t), t // width, t % width]) + start
+    return at.to(I32)[:, None].expand(-1, d.B, -1).contiguous()
 
 
 def split(d, qkv):
@@ -61,20 +70,29 @@ def main(rows=8, prompt=700, steps=16):
     freqs = attn.rope_freqs(attn.rope_inv_freq(d.Drot, 1e7), dev)
     width = (d.Hq + 2 * d.Hkv) * d.D
 
-    # training: gradients through the norm and the rotation
+    # training: gradients through norm, rotation and attention
     dt = d.with_(B=1, T=64)
-    grads = training_step(dt, torch.randn((1, 64, width), device=dev).to(BF16), wq, wk, freqs)
+    axes = attn.rope_axes([12, 10, 10], cyclic=True, device=dev)
+    x = torch.randn((1, 64, width), device=dev).to(BF16)
+    gate, dout = (torch.randn((1, 64, d.Hq, d.D), device=dev).to(BF16) for _ in range(2))
+    out, grads = training_step(dt, x, gate, dout, wq, wk, freqs, axes, image_positions(dt, 0, 8, dev))
     for name, g in grads.items():
         assert torch.isfinite(g.float()).all(), name
 
     # serving: prompts of different lengths into the cache, pages in any order
-    pages = -(-(prompt + steps) // P)
+    pages = -(-(prompt + steps + 4) // P)
     cache = attn.KVCache.empty(d, B * pages, P, attn.E4M3, dev)
     table = torch.randperm(B * pages, device=dev).view(B, pages).to(I32)
     length = torch.linspace(1, prompt, B, device=dev).round().to(I32)
     start = torch.zeros(B, dtype=I32, device=dev)
-    attn.kv_append(d, *split(d, torch.randn((B, prompt, width), device=dev).to(BF16)), wq, wk, freqs, cache, table,
-                   start, length)
+    q = attn.kv_append(d, *split(d, torch.randn((B, prompt, width), device=dev).to(BF16)), wq, wk, freqs, cache, table,
+                       start, length)
+    # the prompts' attention over what the cache holds; rows are aligned at their ends
+    k, v = attn.kv_read(d, cache, table, start, length)
+    out = attn.attn_prefill(d, q, k, v, n_q=length, n_k=length)
+    want = visible_attention(q, k, v, start.long())
+    valid = (torch.arange(prompt, device=dev) < length[:, None])[..., None, None]
+    worst = float(((out.float() - want) * valid).norm() / (want * valid).norm())
 
     # one step of both layers; inputs and outputs in fixed buffers, replayed as a graph
     da, dg = d.with_(T=1), wl.Dims(B=B, T=1, Hk=16, Hv=32, Dk=128, Dv=128)
@@ -102,7 +120,6 @@ def main(rows=8, prompt=700, steps=16):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y, q, out, lse = step()
-    worst = 0.0
     for _ in range(steps):
         qkv.normal_()
         gate.normal_()
@@ -113,10 +130,37 @@ def main(rows=8, prompt=700, steps=16):
         want = visible_attention(q, k, v, (pos - 1).long()) * torch.sigmoid(gate.float())
         worst = max(worst, float((out.float() - want).norm() / want.norm()))
         assert torch.isfinite(y.float()).all()
+
+    # a step of drafted tokens: a window of the last token and T drafts through both layers, then which of them stand
+    T, V = 3, 1000
+    dw, dgw = d.with_(T=T + 1), dg.with_(T=T + 1)
+    xw = {k: v.to(dev) for k, v in wl.make_activations(dgw, 4).items()}
+    head = torch.randn((d.Hq * d.D, V), device=dev) * 0.3
+
+    def window(keep):   # advances the state by keep tokens
+        return gdn.decode_window(dgw, xw["qkv"], gdn_in["conv_w"], gdn_in["conv_state"], xw["a"], xw["b"],
+                                 gdn_in["A_log"], gdn_in["dt_bias"], gdn_in["state"], keep)
+
+    y = window(torch.zeros(B, dtype=I32, device=dev))
+    q = attn.kv_append(dw, *split(dw, torch.randn((B, T + 1, width), device=dev).to(BF16)), wq, wk, freqs, cache, table, pos)
+    gate = torch.randn((B, T + 1, d.Hq, d.D), device=dev).to(BF16)
+    out = attn.attn_decode(dw, q, cache, table, pos, gate=gate)
+    n = int(pos.max()) + T + 1
+    k, v = attn.kv_read(d.with_(T=n), cache, table, start, pos + T + 1)
+    want = visible_attention(q, k, v, pos.long()) * torch.sigmoid(gate.float())
+    worst = max(worst, float((out.float() - want).norm() / want.norm()))
+    logits = out.float().view(B, T + 1, -1) @ head
+    target, draft = torch.softmax(logits, -1), torch.softmax(logits[:, :T] + torch.randn((B, T, V), device=dev), -1)
+    drafted = torch.multinomial(draft.view(-1, V), 1).view(B, T).to(I32)
+    tokens, keep = spec.verify(target, drafted, torch.rand((B, T + 1), device=dev), draft=draft)
+    window(keep)
+    pos.add_(keep)                                # (positions behind are written again by the next step)
+    assert torch.isfinite(y.float()).all() and ((tokens >= 0).sum(1) == keep).all()
+
     status = gdn.gdn_device_status()
     assert status == gdn.GDN_OK, gdn.status_string(status)
-    print("%d rows, prompts up to %d, %d steps: attention within %.1e (relative) of the plain form" % (
-        B, prompt, steps, worst))
+    print("%d rows, prompts up to %d, %d steps, %d of %d drafts stood: attention within %.1e (relative) of the plain form" % (
+        B, prompt, steps, int(keep.sum()) - B, B * T, worst))
     return worst
 
 

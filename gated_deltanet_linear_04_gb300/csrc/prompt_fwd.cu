@@ -15,14 +15,25 @@
 //     and values come by TMA in tiles of 128 into a ring of 128-byte-swizzled
 //     stages; S = Q K^T and O are accumulated in tensor memory, P goes back
 //     there as the A operand of its product.
-//   - One warp loads, one thread issues the products, the others do the
-//     softmax.  Up to 128 channels: two tiles of 128 rows at a time share the
-//     keys, one warpgroup each, so that one's softmax runs beside the other's
-//     products.  256 channels: O alone takes half of the tensor memory; one
-//     tile, two buffers of S, the next step's scores beside this one's softmax.
+//   - One warp loads, one issues the products (as a whole warp: umma.cuh), the
+//     others do the softmax, half of a step's keys each warpgroup.  Up to 128
+//     channels: two tiles of 128 rows at a time share the keys, two warpgroups
+//     each, so that one's softmax runs beside the other's products.  256
+//     channels: O alone takes half of the tensor memory; one tile, two buffers of
+//     S, the next step's scores beside this one's softmax.
 //   - All tiles of all sequences and key heads are one list of steps, cut into
 //     equal shares for one CTA per SM (prompt.cuh): no SM waits for the longest
 //     tile, and a few rows with many keys use all of them.
+//
+// Measured on a GB300 (operations of seen pairs; a large bf16 product of the
+// library reaches 1882 TFLOP/s): 8192 tokens, 16 query heads on 2, 256 channels,
+// gate: 353-358 us, 1540 TFLOP/s; 8 sequences of 100 to 4093 tokens packed, 32
+// on 8, 128 channels: 300 us, 1247; 512 tokens behind long prefixes: 119 us, 1370;
+// one prompt of 77 tokens: 11 us, two launches.  With 256 channels a step takes
+// some 2300 cycles for 2048 cycles of products, and a tile's end 13000 (its
+// results, of all warps) beside which only the next tile's first scores run.
+// With 128 channels keys, values and P's reads fill the shared memory's
+// bandwidth next to the tensor cores, 2600 cycles for 2048.
 #include "prompt_row.cuh"
 #include "umma.cuh"
 
