@@ -842,11 +842,14 @@ cudaError_t launch_d(const PromptSizes &s, Params &p, bool splits, cudaStream_t 
     const bool none = s.Nk == 0;
     const HeadsIn dummy{p.q.p, 0, 0};
     const HeadsIn results{p.out, (long long)s.Hq * D, D};
-    if (!queries_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) || !queries_map(&out, results, s.Nq, s.Hq, D, p.G, p.tpt) ||
-        !queries_map(&gate, p.gate.p != nullptr ? p.gate : results, s.Nq, s.Hq, D, p.G, p.tpt) ||
+    if (!queries_map(&q, p.q, s.Nq, s.Hq, D, p.G, p.tpt) ||
+        (G::STAGED && !queries_map(&out, results, s.Nq, s.Hq, D, p.G, p.tpt)) ||
+        (G::STAGED && p.gate.p != nullptr && !queries_map(&gate, p.gate, s.Nq, s.Hq, D, p.G, p.tpt)) ||
         !keys_map(&k, none ? dummy : p.k, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, kKeys, 1) ||
         !keys_map(&v, none ? dummy : p.v, none ? 1 : s.Nk, none ? 1 : s.Hkv, D, G::VK, D / 64))
         return cudaErrorInvalidValue;
+    if (!G::STAGED) out = q;   // (not used)
+    if (!G::STAGED || p.gate.p == nullptr) gate = q;
     const int ctas = num_sms();
     e = DependentLaunch(dim3(ctas), dim3(G::THREADS), G::SMEM, st)(prompt_forward_kernel<D>, q, k, v, gate, out, p);
     if (e != cudaSuccess || !splits) return e;
