@@ -24,10 +24,10 @@
 //   - The lists, shares and joins are those of the forward pass (prompt.cuh).
 //
 // Measured on a GB300, per 10 D operations of a seen pair: 8192 tokens, 16 query
-// heads on 2, 256 channels, gate: 1440 us, 955 TFLOP/s (dQ 507, dK 496, dV 339,
-// gate and delta 56, tensor cores 71 to 78 % busy); 8 sequences of 100 to 2045
-// tokens packed, 32 on 8, 128 channels: 368 us, 650 TFLOP/s (dQ 146, dK and dV
-// 176, gate and delta 33).  Steps are bound by the shared memory's bandwidth: dQ
+// heads on 2, 256 channels, gate: 1440-1465 us, 940-955 TFLOP/s (dQ 507, dK 496,
+// dV 339, gate and delta 47, join 23, tensor cores 71 to 78 % busy); 8 sequences of 100 to 2045
+// tokens packed, 32 on 8, 128 channels: 365 us, 656 TFLOP/s (dQ 146, dK and dV
+// 176).  Steps are bound by the shared memory's bandwidth: dQ
 // with 128 channels reads 64 KB and writes 48 for 768 cycles of products, some
 // 900 cycles at 128 bytes a clock (a second buffer of S and dP changed nothing:
 // 382 us for 383).  Pairs of CTAs that share the rows that pass by would halve
@@ -811,7 +811,9 @@ __global__ void __launch_bounds__(128) prompt_backward_join_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // before the passes: delta = rowsum(dout out), and with a gate dO = dout
 // sigmoid(gate), rounded to bf16 for the products, and the gate's own gradient.
-// Memory-bound; a group of D / 8 lanes takes a row.
+// Memory-bound: 47 us for the 335 MB of 8192 tokens (16 heads of 256 channels,
+// gate), 7.1 TB/s with what stays in L2; a tile's rows in one block, one
+// after another, took 56.
 // ---------------------------------------------------------------------------
 struct PrepareParams {
     List list;
@@ -826,47 +828,56 @@ struct PrepareParams {
 
 template <int D>
 __global__ void __launch_bounds__(256) prompt_prepare_kernel(const PrepareParams p) {
-    constexpr int LPR = D / 8, RPB = 256 / LPR;
+    // a group of LPR lanes takes two rows of an item of 2 RPB rows: all loads of both, then the rest
+    constexpr int LPR = D / 8, RPB = 256 / LPR, ROWS = 2 * RPB;   // (4096 / D)
     const int sub = threadIdx.x / LPR, d = threadIdx.x % LPR * 8;
     attn::grid_dep_enter();
     const Header h = *p.list.header;
-    const long long units = (long long)h.units * p.Hkv;
+    const int rows = p.tile * p.G, parts = (rows + ROWS - 1) / ROWS;
+    const long long per_head = (long long)h.units * parts, items = per_head * p.Hkv;
     const bool gated = p.gate.p != nullptr;
-    for (long long x = blockIdx.x; x < units; x += gridDim.x) {
-        const int head = (int)(x / h.units);
-        const Unit u = p.list.unit[x - (long long)head * h.units];
-        for (int r0 = 0; r0 < p.tile * p.G; r0 += RPB) {
-            const int r = r0 + sub, t = r / p.G, hq = head * p.G + r - t * p.G;
-            const bool mine = r < p.tile * p.G && t < u.slot_a;
-            const long long n = (long long)u.a0 + t, at = n * p.Hq + hq;
-            uint4 z = make_uint4(0, 0, 0, 0), zg = z;
-            float sum = 0.0f;
-            if (mine && t < u.n_a) {
-                float a[8], b[8];
-                attn::unpack8(*reinterpret_cast<const uint4 *>(p.dout + at * D + d), a);
-                attn::unpack8(*reinterpret_cast<const uint4 *>(p.out + at * D + d), b);
+    for (long long x = blockIdx.x; x < items; x += gridDim.x) {
+        const int head = (int)(x / per_head), y = (int)(x - head * per_head), unit = y / parts;
+        const Unit u = p.list.unit[unit];
+        long long at[2];
+        bool mine[2];
+        uint4 dout[2], out[2], gate[2];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum = fmaf(a[k], b[k], sum);
-                if (gated) {
-                    float g[8], y[8];
-                    attn::unpack8(*reinterpret_cast<const uint4 *>(p.gate.p + n * p.gate.ts + hq * p.gate.hs + d), g);
+        for (int i = 0; i < 2; ++i) {
+            const int r = (y - unit * parts) * ROWS + i * RPB + sub, t = r / p.G, hq = head * p.G + r - t * p.G;
+            const long long n = (long long)u.a0 + t;
+            at[i] = n * p.Hq + hq;
+            mine[i] = r < rows && t < u.slot_a;
+            const bool there = mine[i] && t < u.n_a;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            dout[i] = there ? *reinterpret_cast<const uint4 *>(p.dout + at[i] * D + d) : none;
+            out[i] = there ? *reinterpret_cast<const uint4 *>(p.out + at[i] * D + d) : none;
+            gate[i] = there && gated ? *reinterpret_cast<const uint4 *>(p.gate.p + n * p.gate.ts + hq * p.gate.hs + d) : none;
+        }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float e = exp_fast(-g[k]), sg = rcp_fast(1.0f + e);
-                        y[k] = a[k] * sg;
-                        a[k] *= b[k] * (e < INFINITY ? e * sg : 1.0f);   // 1 - sigmoid
-                    }
-                    z = attn::pack8(y);
-                    zg = attn::pack8(a);
+        for (int i = 0; i < 2; ++i) {
+            float a[8], b[8], sum = 0.0f;
+            attn::unpack8(dout[i], a);
+            attn::unpack8(out[i], b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum = fmaf(a[k], b[k], sum);
+            if (gated) {   // (padding: zeros)
+                float g[8], z[8];
+                attn::unpack8(gate[i], g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float e = exp_fast(-g[k]), sg = rcp_fast(1.0f + e);
+                    z[k] = a[k] * sg;
+                    a[k] *= b[k] * (e < INFINITY ? e * sg : 1.0f);   // 1 - sigmoid
                 }
-            }
-            if (gated && mine) {
-                *reinterpret_cast<uint4 *>(p.d_o + at * D + d) = z;
-                *reinterpret_cast<uint4 *>(p.dgate + at * D + d) = zg;
+                if (mine[i]) {
+                    *reinterpret_cast<uint4 *>(p.d_o + at[i] * D + d) = attn::pack8(z);
+                    *reinterpret_cast<uint4 *>(p.dgate + at[i] * D + d) = attn::pack8(a);
+                }
             }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, LPR);
-            if (d == 0 && mine) p.delta[at] = sum;
+            if (d == 0 && mine[i]) p.delta[at[i]] = sum;
         }
     }
     // rows behind the last sequence, which its last steps may bring along: finite
@@ -942,7 +953,8 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     r.tile = lists[0].tile;
     r.B = s.B;
     r.Nq = s.Nq;
-    const long long most = ((s.Nq + r.tile - 1) / r.tile + s.B) * s.Hkv, fill = 8LL * num_sms();
+    const int parts = (r.tile * G + 4096 / D - 1) / (4096 / D);   // items of a tile
+    const long long most = ((s.Nq + r.tile - 1) / r.tile + s.B) * s.Hkv * parts, fill = 16LL * num_sms();
     if (s.Nq > 0) e = DependentLaunch(dim3((unsigned)(most < fill ? most : fill)), dim3(256), 0, st)(prompt_prepare_kernel<D>, r);
     if (e != cudaSuccess) return e;
 
