@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long b = blockIdx.x / ctas;
     const int T = p.T, V = p.V;
+    cluster_arrive_relaxed();   // (this CTA runs: the others may write its sums; they wait for that before they do)
     attn::grid_dep_enter();
     const float *target = p.target + b * (T + 1) * V, *draft = p.draft == nullptr ? nullptr : p.draft + b * T * V;
     const int32_t *tokens = p.tokens + b * T;
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
             if (lane == c) of_chunk = s;
         }
         mine = warp_total(of_chunk);
+        if (round == 0) cluster_wait_acquire();
         if (lane < ctas) *cluster.map_shared_rank(&sums[rank][warp], lane) = mine;
         cluster.sync();
         total = before = 0;
