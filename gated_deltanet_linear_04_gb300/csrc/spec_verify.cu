@@ -65,6 +65,9 @@ __device__ __forceinline__ int bits_apart(F2 x) {   // the first's bits less the
     return a - b;
 }
 
+// What a number counts as: its nearest value in [0, 1], NaN as 0.
+__device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.0f), 1.0f); }
+
 // p - min(p, q) in whole units of 2^-60 (each of the two rounded to them), as
 // three digits: of 2^-23, 2^-46 and 2^-60.  Adding 1 (1.5 2^-23, 1.5 2^-37) to a
 // value below it leaves the value's multiple of 2^-23 (2^-46, 2^-60) in the
@@ -76,7 +79,7 @@ __device__ __forceinline__ int bits_apart(F2 x) {   // the first's bits less the
 struct Digits {
     int a, b, c;
     __device__ __forceinline__ void add_above(float p, float q) {
-        p = fminf(fmaxf(p, 0.0f), 1.0f);
+        p = probability(p);
         const F2 one = pair(1.0f, 1.0f), next = pair(1.5f * 0x1p-23f, 1.5f * 0x1p-23f), last = pair(1.5f * 0x1p-37f, 1.5f * 0x1p-37f);
         const F2 x = pair(p, fminf(p, fmaxf(q, 0.0f)));
         const F2 s = add(x, one), rest = less(x, less(s, one));
@@ -147,9 +150,9 @@ __global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const Params p
             if (t < n) {
                 const int x = tokens[t];
                 if (x >= 0 && x < V) {
-                    const float q = draft == nullptr ? 1.0f : draft[(long long)t * V + x];
+                    const float q = draft == nullptr ? 1.0f : probability(draft[(long long)t * V + x]);
                     // (both sides exact in 64 bits)
-                    ok = (double)p.u[b * (T + 1) + t] * (double)q < (double)target[(long long)t * V + x];
+                    ok = (double)p.u[b * (T + 1) + t] * (double)q < (double)probability(target[(long long)t * V + x]);
                 }
             }
             const unsigned m = __ballot_sync(0xffffffffu, ok);
