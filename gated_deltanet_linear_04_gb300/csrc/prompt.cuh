@@ -198,6 +198,11 @@ struct Waits {
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
         return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_long(bar, parity, err, dead);
     }
+    // The same answer in all lanes of the warp, for what is elected by it: when waits give up, one lane may still find the
+    // phase complete and another not, and an election has to be reached by every lane that it names.
+    __device__ __forceinline__ bool together(uint64_t *bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    }
 };
 
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;

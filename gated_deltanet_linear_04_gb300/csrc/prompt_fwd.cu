@@ -357,7 +357,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         auto load_values = [&] {
 #pragma unroll 1
             for (int c = 0; c < G::PER_STEP; ++c) {
-                if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
                     mbar_expect_tx(&bars.full[stage], G::STAGE);
                     tma_load_4d(ring + stage * G::STAGE, &v_map, 0, w.u.b0 + i * kKeys + c * G::VK, 0, w.head, &bars.full[stage]);
                 }
@@ -374,7 +374,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (more) {
                 if (j == x.first) {
-                    const bool free = wait(&bars.q_free, (units & 1) ^ 1);
+                    const bool free = wait.together(&bars.q_free, (units & 1) ^ 1);
                     ++units;
                     if (free && umma::elect_one()) {
                         mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
@@ -386,7 +386,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP; ++c) {
-                    if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                    if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
                         mbar_expect_tx(&bars.full[stage], G::STAGE);
                         tma_load_4d(ring + stage * G::STAGE, &k_map, 0, x.u.b0 + j * kKeys, c, x.head, &bars.full[stage]);
                     }
@@ -401,7 +401,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                         for (int c = 0; c < G::PER_STEP; ++c) stage_done();
 #pragma unroll 1
                     for (int c = 0; c < G::RESULTS; ++c) {
-                        if (wait(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                        if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
                             if (p.gate.p != nullptr) {
                                 mbar_expect_tx(&bars.full[stage], 128 * p.tpt * p.G);
                                 tma_load_3d(ring + stage * G::STAGE, &gate_map, c % (D / 64) * 64, w.head * p.G,
