@@ -192,16 +192,13 @@ __device__ __noinline__ inline bool wait_long(uint64_t *bar, uint32_t parity, un
     return false;
 }
 
+// (Lanes may get different answers when waits give up: what the whole warp has to reach, as an election, does not go by
+// them.  The elected lane waits.)
 struct Waits {
     unsigned *err;
     volatile int *dead;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
         return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) || wait_long(bar, parity, err, dead);
-    }
-    // The same answer in all lanes of the warp, for what is elected by it: when waits give up, one lane may still find the
-    // phase complete and another not, and an election has to be reached by every lane that it names.
-    __device__ __forceinline__ bool together(uint64_t *bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, (*this)(bar, parity));
     }
 };
 

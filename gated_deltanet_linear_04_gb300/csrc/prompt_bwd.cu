@@ -329,22 +329,22 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             const int half = G::KEYS ? kRows : p.box;   // tokens of 64 rows
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if (wait.together(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
+                if (umma::elect_one() && wait(&bars.empty1[s1], ph1 ^ 1))
                     load(!G::KEYS, &res1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, w.u.a0 + h * half, 0, D / 64);
                 pass1();
                 if (G::A2_RING) {
-                    if (wait.together(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
+                    if (umma::elect_one() && wait(&bars.empty2[s2], ph2 ^ 1))
                         load(!G::KEYS, &res2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, w.u.a0 + h * half, 0, D / 64);
                     pass2();
                 }
             }
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
-                if (wait.together(&bars.empty1[s1], ph1 ^ 1) && umma::elect_one())
+                if (umma::elect_one() && wait(&bars.empty1[s1], ph1 ^ 1))
                     load(G::KEYS, &map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
                 pass1();
                 if (G::A2_SMEM && i == w.first) {   // the second resident tile, to where it stays
-                    if ((units == 0 || wait.together(&bars.a2_free, (units - 1) & 1)) && umma::elect_one()) {
+                    if (umma::elect_one() && (units == 0 || wait(&bars.a2_free, (units - 1) & 1))) {
                         mbar_expect_tx(&bars.a2_full, G::KEYS ? 128 * D * 2 : 2 * p.box * p.G * D * 2);
 #pragma unroll 1
                         for (int c = 0; c < 2 * (D / 64); ++c) {
@@ -359,7 +359,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP2; ++c) {
-                    if (wait.together(&bars.empty2[s2], ph2 ^ 1) && umma::elect_one())
+                    if (umma::elect_one() && wait(&bars.empty2[s2], ph2 ^ 1))
                         load(G::KEYS, &map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c,
                              G::STAGE2 / G::SUB);
                     pass2();

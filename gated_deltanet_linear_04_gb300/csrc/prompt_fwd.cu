@@ -357,7 +357,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         auto load_values = [&] {
 #pragma unroll 1
             for (int c = 0; c < G::PER_STEP; ++c) {
-                if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
                     mbar_expect_tx(&bars.full[stage], G::STAGE);
                     tma_load_4d(ring + stage * G::STAGE, &v_map, 0, w.u.b0 + i * kKeys + c * G::VK, 0, w.head, &bars.full[stage]);
                 }
@@ -374,19 +374,18 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (more) {
                 if (j == x.first) {
-                    const bool free = wait.together(&bars.q_free, (units & 1) ^ 1);
-                    ++units;
-                    if (free && umma::elect_one()) {
+                    if (umma::elect_one() && wait(&bars.q_free, (units & 1) ^ 1)) {
                         mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
 #pragma unroll 1
                         for (int c = 0; c < G::TILES * (D / 64); ++c)
                             tma_load_3d(smem + c * G::SUB, &q_map, c % (D / 64) * 64, x.head * p.G,
                                         x.u.a0 + c / (D / 64) * p.tpt, &bars.q_full);
                     }
+                    ++units;
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP; ++c) {
-                    if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                    if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
                         mbar_expect_tx(&bars.full[stage], G::STAGE);
                         tma_load_4d(ring + stage * G::STAGE, &k_map, 0, x.u.b0 + j * kKeys, c, x.head, &bars.full[stage]);
                     }
@@ -401,7 +400,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                         for (int c = 0; c < G::PER_STEP; ++c) stage_done();
 #pragma unroll 1
                     for (int c = 0; c < G::RESULTS; ++c) {
-                        if (wait.together(&bars.empty[stage], phase ^ 1) && umma::elect_one()) {
+                        if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
                             if (p.gate.p != nullptr) {
                                 mbar_expect_tx(&bars.full[stage], 128 * p.tpt * p.G);
                                 tma_load_3d(ring + stage * G::STAGE, &gate_map, c % (D / 64) * 64, w.head * p.G,

@@ -18,7 +18,7 @@ def test_elections_go_by_answers_given_together(name):
     """An election names all lanes of its warp: what guards it has to be the
     same in all of them, also when some lanes' waits give up."""
     text = source(name)
-    guarded = re.findall(r"if \((.*?)umma::elect_one\(\)\)", text)
+    guarded = re.findall(r"(?:if \(|return )(.*?)umma::elect_one\(\)", text)
     assert len(guarded) >= 5
     for condition in guarded:
         assert not re.search(r"\bwait\(", condition), condition
