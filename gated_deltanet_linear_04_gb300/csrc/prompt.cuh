@@ -202,6 +202,26 @@ struct Waits {
     }
 };
 
+// Waits for a copy or products that are under way, whether or not a wait has given up (`dead` says that nobody is to wait
+// for what may never be issued; what was issued ends, in microseconds).
+__device__ __noinline__ inline void wait_end(uint64_t *bar, uint32_t parity, unsigned *err) {
+    for (uint32_t i = 0; i < kSpinLimit / 16; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+    atomicOr(err, kErrMbarTimeout);
+}
+
+// The phase that a copy was last issued for, for each of N barriers: what a CTA that gave up waits for before it ends.
+template <int N>
+struct Issued {
+    uint8_t last[N];   // 0: none, 1 + parity
+    __device__ __forceinline__ void copy(int i, uint32_t phase) { last[i] = (uint8_t)(1 + phase); }
+    __device__ __forceinline__ void land(uint64_t *bars, unsigned *err) const {
+#pragma unroll 1
+        for (int i = 0; i < N; ++i)
+            if (last[i] != 0) wait_end(&bars[i], last[i] - 1u, err);
+    }
+};
+
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {

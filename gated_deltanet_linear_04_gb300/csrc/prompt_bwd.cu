@@ -88,8 +88,11 @@ struct Params {
 };
 
 struct Bars {
-    uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, a2_full, a2_free, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free;
+    uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, a2_full, a2_free, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free, end;
     uint64_t stats_full[kStats], stats_free[kStats];
+    Issued<4> issued1;
+    Issued<5> issued2;
+    Issued<1> issued_a2;
 };
 
 // (s_full and x_free: of even and odd steps.  A wait for a phase is sound if the one before it is over, and each warpgroup
@@ -266,6 +269,10 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             mbar_init(&bars.x_free[i], 1);
         }
         mbar_init(&bars.acc_done, 1);
+        mbar_init(&bars.end, 1);
+        bars.issued1 = {};
+        bars.issued2 = {};
+        bars.issued_a2 = {};
         mbar_init(&bars.acc_free, G::WARPS);
         for (int i = 0; i < kStats; ++i) {
             mbar_init(&bars.stats_full[i], 1);
@@ -301,6 +308,20 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         }
         int s1 = 0, s2 = 0, units = 0;
         uint32_t ph1 = 0, ph2 = 0;
+        bool up = true;   // no wait has given up: after one, nothing is loaded any more
+        // the ring's stage is free: in the lane that fills it
+        auto free1 = [&] {
+            if (!umma::elect_one()) return false;
+            up = up && wait(&bars.empty1[s1], ph1 ^ 1);
+            if (up) bars.issued1.copy(s1, ph1);
+            return up;
+        };
+        auto free2 = [&] {
+            if (!umma::elect_one()) return false;
+            up = up && wait(&bars.empty2[s2], ph2 ^ 1);
+            if (up) bars.issued2.copy(s2, ph2);
+            return up;
+        };
         auto pass1 = [&] {
             if (++s1 == G::N1) {
                 s1 = 0;
@@ -329,22 +350,23 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             const int half = G::KEYS ? kRows : p.box;   // tokens of 64 rows
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if (umma::elect_one() && wait(&bars.empty1[s1], ph1 ^ 1))
+                if (free1())
                     load(!G::KEYS, &res1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, w.u.a0 + h * half, 0, D / 64);
                 pass1();
                 if (G::A2_RING) {
-                    if (umma::elect_one() && wait(&bars.empty2[s2], ph2 ^ 1))
+                    if (free2())
                         load(!G::KEYS, &res2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, w.u.a0 + h * half, 0, D / 64);
                     pass2();
                 }
             }
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
-                if (umma::elect_one() && wait(&bars.empty1[s1], ph1 ^ 1))
+                if (free1())
                     load(G::KEYS, &map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
                 pass1();
                 if (G::A2_SMEM && i == w.first) {   // the second resident tile, to where it stays
-                    if (umma::elect_one() && (units == 0 || wait(&bars.a2_free, (units - 1) & 1))) {
+                    if (umma::elect_one() && (up = up && (units == 0 || wait(&bars.a2_free, (units - 1) & 1)))) {
+                        bars.issued_a2.copy(0, units & 1);
                         mbar_expect_tx(&bars.a2_full, G::KEYS ? 128 * D * 2 : 2 * p.box * p.G * D * 2);
 #pragma unroll 1
                         for (int c = 0; c < 2 * (D / 64); ++c) {
@@ -359,19 +381,13 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP2; ++c) {
-                    if (umma::elect_one() && wait(&bars.empty2[s2], ph2 ^ 1))
+                    if (free2())
                         load(G::KEYS, &map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c,
                              G::STAGE2 / G::SUB);
                     pass2();
                 }
             }
         } while (__any_sync(0xffffffffu, w.next()));
-        if (dead)   // let the copies in flight land
-            for (int i = 0; i < 5; ++i) {
-                if (i < 4) mbar_try_wait(&bars.full1[i], 0);
-                mbar_try_wait(&bars.full2[i], 0);
-                if (i == 4) mbar_try_wait(&bars.a2_full, 0);
-            }
     } else if (any && warp == G::WARPS + 1) {
         // ---- products
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), at = smem_u32(smem);
@@ -485,7 +501,9 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             if (G::LATER > 1 || (G::HAS_DP && G::N1 < 4) || !more)
                 for (; waiting > 0; --waiting) accumulate(step - waiting, waiting == 1);
         }
-        wait(&bars.acc_done, (done - 1) & 1);   // every product is through before the tensor memory goes back
+        // every product is through before the tensor memory goes back
+        umma::warp_mma_commit(&bars.end);
+        wait_end(&bars.end, 0, p.err);
     } else if (G::KEYS && any && warp == G::WARPS + 2) {
         // ---- the statistics of the rows that pass by
         int st = 0;
@@ -747,6 +765,11 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     }
     __syncthreads();
     umma::fence_after_sync();
+    if (dead && threadIdx.x == 0) {
+        bars.issued1.land(bars.full1, p.err);
+        bars.issued2.land(bars.full2, p.err);
+        bars.issued_a2.land(&bars.a2_full, p.err);
+    }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
 

@@ -80,7 +80,9 @@ struct Params {
 };
 
 struct Bars {
-    uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2], end;
+    Issued<9> issued;
+    Issued<1> issued_q;
     float most[2][2][2][128];   // [tile][step parity][half][row]: what the halves of a row tell each other
     float sum[2][2][128];       // [tile][half][row], at a tile's end
 };
@@ -305,6 +307,9 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         }
         mbar_init(&bars.q_full, 1);
         mbar_init(&bars.q_free, 1);
+        mbar_init(&bars.end, 1);
+        bars.issued = {};
+        bars.issued_q = {};
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4 * G::HALVES);
@@ -343,11 +348,19 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         }
         int stage = 0, units = 0;
         uint32_t phase = 0;
+        bool up = true;   // no wait has given up: after one, nothing is loaded any more
         auto stage_done = [&] {
             if (++stage == G::STAGES) {
                 stage = 0;
                 phase ^= 1;
             }
+        };
+        // the stage is free: in the lane that fills it
+        auto free = [&] {
+            if (!umma::elect_one()) return false;
+            up = up && wait(&bars.empty[stage], phase ^ 1);
+            if (up) bars.issued.copy(stage, phase);
+            return up;
         };
         // one loop: the keys of step n and the values of step n - 1, in the order of their products
         w.uniform();
@@ -357,7 +370,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         auto load_values = [&] {
 #pragma unroll 1
             for (int c = 0; c < G::PER_STEP; ++c) {
-                if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
+                if (free()) {
                     mbar_expect_tx(&bars.full[stage], G::STAGE);
                     tma_load_4d(ring + stage * G::STAGE, &v_map, 0, w.u.b0 + i * kKeys + c * G::VK, 0, w.head, &bars.full[stage]);
                 }
@@ -374,7 +387,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (more) {
                 if (j == x.first) {
-                    if (umma::elect_one() && wait(&bars.q_free, (units & 1) ^ 1)) {
+                    if (umma::elect_one() && (up = up && wait(&bars.q_free, (units & 1) ^ 1))) {
+                        bars.issued_q.copy(0, units & 1);
                         mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
 #pragma unroll 1
                         for (int c = 0; c < G::TILES * (D / 64); ++c)
@@ -385,7 +399,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP; ++c) {
-                    if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
+                    if (free()) {
                         mbar_expect_tx(&bars.full[stage], G::STAGE);
                         tma_load_4d(ring + stage * G::STAGE, &k_map, 0, x.u.b0 + j * kKeys, c, x.head, &bars.full[stage]);
                     }
@@ -400,7 +414,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                         for (int c = 0; c < G::PER_STEP; ++c) stage_done();
 #pragma unroll 1
                     for (int c = 0; c < G::RESULTS; ++c) {
-                        if (umma::elect_one() && wait(&bars.empty[stage], phase ^ 1)) {
+                        if (free()) {
                             if (p.gate.p != nullptr) {
                                 mbar_expect_tx(&bars.full[stage], 128 * p.tpt * p.G);
                                 tma_load_3d(ring + stage * G::STAGE, &gate_map, c % (D / 64) * 64, w.head * p.G,
@@ -417,8 +431,6 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 i = w.first;
             }
         }
-        if (dead)   // let the copies in flight land
-            for (int i = 0; i < G::STAGES; ++i) mbar_try_wait(&bars.full[i], 0);
     } else if (any && warp == G::WARPS + 1) {
         // ---- products.  The whole warp goes through the loop, so that operands stay uniform; one lane issues.
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -531,8 +543,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
         }
         // every product is through before the tensor memory goes back
-        for (int i = G::TILES == 1 && step > 1 ? step - 2 : step - 1; i < step; ++i)
-            for (int t = 0; t < G::TILES; ++t) wait(o_done(t, i), o_phase(i));
+        commit(&bars.end);
+        wait_end(&bars.end, 0, p.err);
     } else if (any) {
         // ---- softmax and results.  Two warpgroups a tile, each with half of a step's keys and half of the channels.  One
         // tile: the scores stay in registers.  Two tiles, sixteen warps with 96 registers: they are read twice, for their
@@ -740,6 +752,10 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     }
     __syncthreads();
     umma::fence_after_sync();
+    if (dead && threadIdx.x == 0) {
+        bars.issued.land(bars.full, p.err);
+        bars.issued_q.land(&bars.q_full, p.err);
+    }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
 
