@@ -90,9 +90,8 @@ struct Params {
 struct Bars {
     uint64_t full1[4], empty1[4], full2[5], empty2[5], a_full, a2_full, a2_free, s_full[2], s_free, x_full[2], x_free[2], acc_done, acc_free, end;
     uint64_t stats_full[kStats], stats_free[kStats];
-    Issued<4> issued1;
-    Issued<5> issued2;
-    Issued<1> issued_a2;
+    Loaded loaded1, loaded2;
+    int units;   // whose second resident tile was loaded
 };
 
 // (s_full and x_free: of even and odd steps.  A wait for a phase is sound if the one before it is over, and each warpgroup
@@ -251,6 +250,8 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     }
     if (threadIdx.x == 32) {
         dead = 0;
+        bars.loaded1 = bars.loaded2 = {0, 0};
+        bars.units = 0;
         for (int i = 0; i < 5; ++i) {
             if (i < 4) {
                 mbar_init(&bars.full1[i], 1);
@@ -270,9 +271,6 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         }
         mbar_init(&bars.acc_done, 1);
         mbar_init(&bars.end, 1);
-        bars.issued1 = {};
-        bars.issued2 = {};
-        bars.issued_a2 = {};
         mbar_init(&bars.acc_free, G::WARPS);
         for (int i = 0; i < kStats; ++i) {
             mbar_init(&bars.stats_full[i], 1);
@@ -308,20 +306,6 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         }
         int s1 = 0, s2 = 0, units = 0;
         uint32_t ph1 = 0, ph2 = 0;
-        bool up = true;   // no wait has given up: after one, nothing is loaded any more
-        // the ring's stage is free: in the lane that fills it
-        auto free1 = [&] {
-            if (!umma::elect_one()) return false;
-            up = up && wait(&bars.empty1[s1], ph1 ^ 1);
-            if (up) bars.issued1.copy(s1, ph1);
-            return up;
-        };
-        auto free2 = [&] {
-            if (!umma::elect_one()) return false;
-            up = up && wait(&bars.empty2[s2], ph2 ^ 1);
-            if (up) bars.issued2.copy(s2, ph2);
-            return up;
-        };
         auto pass1 = [&] {
             if (++s1 == G::N1) {
                 s1 = 0;
@@ -350,23 +334,26 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             const int half = G::KEYS ? kRows : p.box;   // tokens of 64 rows
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                if (free1())
+                if (!wait.together(&bars.empty1[s1], ph1 ^ 1)) goto loaded;
+                if (umma::elect_one())
                     load(!G::KEYS, &res1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, w.u.a0 + h * half, 0, D / 64);
                 pass1();
                 if (G::A2_RING) {
-                    if (free2())
+                    if (!wait.together(&bars.empty2[s2], ph2 ^ 1)) goto loaded;
+                    if (umma::elect_one())
                         load(!G::KEYS, &res2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, w.u.a0 + h * half, 0, D / 64);
                     pass2();
                 }
             }
             for (int i = w.first; i < w.last; ++i) {
                 const int token = w.u.b0 + i * p.tps;
-                if (free1())
+                if (!wait.together(&bars.empty1[s1], ph1 ^ 1)) goto loaded;
+                if (umma::elect_one())
                     load(G::KEYS, &map1, smem + G::RING1 + s1 * G::STAGE, &bars.full1[s1], w.head, token, 0, D / 64);
                 pass1();
                 if (G::A2_SMEM && i == w.first) {   // the second resident tile, to where it stays
-                    if (umma::elect_one() && (up = up && (units == 0 || wait(&bars.a2_free, (units - 1) & 1)))) {
-                        bars.issued_a2.copy(0, units & 1);
+                    if (units > 0 && !wait.together(&bars.a2_free, (units - 1) & 1)) goto loaded;
+                    if (umma::elect_one()) {
                         mbar_expect_tx(&bars.a2_full, G::KEYS ? 128 * D * 2 : 2 * p.box * p.G * D * 2);
 #pragma unroll 1
                         for (int c = 0; c < 2 * (D / 64); ++c) {
@@ -381,13 +368,18 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP2; ++c) {
-                    if (free2())
+                    if (!wait.together(&bars.empty2[s2], ph2 ^ 1)) goto loaded;
+                    if (umma::elect_one())
                         load(G::KEYS, &map2, smem + G::RING2 + s2 * G::STAGE2, &bars.full2[s2], w.head, token, c,
                              G::STAGE2 / G::SUB);
                     pass2();
                 }
             }
         } while (__any_sync(0xffffffffu, w.next()));
+    loaded:
+        bars.loaded1 = {s1, ph1};
+        bars.loaded2 = {s2, ph2};
+        bars.units = units;
     } else if (any && warp == G::WARPS + 1) {
         // ---- products
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0), at = smem_u32(smem);
@@ -766,9 +758,9 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     __syncthreads();
     umma::fence_after_sync();
     if (dead && threadIdx.x == 0) {
-        bars.issued1.land(bars.full1, p.err);
-        bars.issued2.land(bars.full2, p.err);
-        bars.issued_a2.land(&bars.a2_full, p.err);
+        for (int i = 0; i < G::N1; ++i) wait_end(&bars.full1[i], bars.loaded1.parity(i), p.err);
+        for (int i = 0; i < G::N2; ++i) wait_end(&bars.full2[i], bars.loaded2.parity(i), p.err);
+        if (G::A2_SMEM) wait_end(&bars.a2_full, (bars.units & 1) ^ 1, p.err);
     }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }

@@ -81,8 +81,8 @@ struct Params {
 
 struct Bars {
     uint64_t full[9], empty[9], q_full, q_free, s_full[2], p_full[2], o_done[2], o_free[2], end;
-    Issued<9> issued;
-    Issued<1> issued_q;
+    Loaded loaded;
+    int units, passed;   // units whose queries were loaded; the first stage of those that were passed over, or -1
     float most[2][2][2][128];   // [tile][step parity][half][row]: what the halves of a row tell each other
     float sum[2][2][128];       // [tile][half][row], at a tile's end
 };
@@ -301,6 +301,9 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     }
     if (threadIdx.x == 32) {
         dead = 0;
+        bars.loaded = {0, 0};
+        bars.units = 0;
+        bars.passed = -1;
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
@@ -308,8 +311,6 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         mbar_init(&bars.q_full, 1);
         mbar_init(&bars.q_free, 1);
         mbar_init(&bars.end, 1);
-        bars.issued = {};
-        bars.issued_q = {};
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4 * G::HALVES);
@@ -348,19 +349,11 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         }
         int stage = 0, units = 0;
         uint32_t phase = 0;
-        bool up = true;   // no wait has given up: after one, nothing is loaded any more
         auto stage_done = [&] {
             if (++stage == G::STAGES) {
                 stage = 0;
                 phase ^= 1;
             }
-        };
-        // the stage is free: in the lane that fills it
-        auto free = [&] {
-            if (!umma::elect_one()) return false;
-            up = up && wait(&bars.empty[stage], phase ^ 1);
-            if (up) bars.issued.copy(stage, phase);
-            return up;
         };
         // one loop: the keys of step n and the values of step n - 1, in the order of their products
         w.uniform();
@@ -370,16 +363,18 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         auto load_values = [&] {
 #pragma unroll 1
             for (int c = 0; c < G::PER_STEP; ++c) {
-                if (free()) {
+                if (!wait.together(&bars.empty[stage], phase ^ 1)) return false;
+                if (umma::elect_one()) {
                     mbar_expect_tx(&bars.full[stage], G::STAGE);
                     tma_load_4d(ring + stage * G::STAGE, &v_map, 0, w.u.b0 + i * kKeys + c * G::VK, 0, w.head, &bars.full[stage]);
                 }
                 stage_done();
             }
             ++i;
+            return true;
         };
         for (int n = 0;; ++n) {
-            if (G::TILES == 2 && n > 0) load_values();
+            if (G::TILES == 2 && n > 0 && !load_values()) goto loaded;
             if (more && j == x.last) {
                 more = __any_sync(0xffffffffu, x.next());
                 x.uniform();
@@ -387,8 +382,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (more) {
                 if (j == x.first) {
-                    if (umma::elect_one() && (up = up && wait(&bars.q_free, (units & 1) ^ 1))) {
-                        bars.issued_q.copy(0, units & 1);
+                    if (!wait.together(&bars.q_free, (units & 1) ^ 1)) goto loaded;
+                    if (umma::elect_one()) {
                         mbar_expect_tx(&bars.q_full, G::TILES * D * 2 * p.tpt * p.G);
 #pragma unroll 1
                         for (int c = 0; c < G::TILES * (D / 64); ++c)
@@ -399,7 +394,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
 #pragma unroll 1
                 for (int c = 0; c < G::PER_STEP; ++c) {
-                    if (free()) {
+                    if (!wait.together(&bars.empty[stage], phase ^ 1)) goto loaded;
+                    if (umma::elect_one()) {
                         mbar_expect_tx(&bars.full[stage], G::STAGE);
                         tma_load_4d(ring + stage * G::STAGE, &k_map, 0, x.u.b0 + j * kKeys, c, x.head, &bars.full[stage]);
                     }
@@ -407,14 +403,17 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 }
                 ++j;
             }
-            if (G::TILES == 1 && n > 0) load_values();
+            if (G::TILES == 1 && n > 0 && !load_values()) goto loaded;
             if (n > 0 && i == w.last) {
                 if (G::STAGED && w.whole()) {   // stages for the results, with the gates in them
-                    if (!more)     // (where the next unit's keys would be: the place of these is known without it)
+                    if (!more) {   // (where the next unit's keys would be: the place of these is known without it)
+                        bars.passed = stage;
                         for (int c = 0; c < G::PER_STEP; ++c) stage_done();
+                    }
 #pragma unroll 1
                     for (int c = 0; c < G::RESULTS; ++c) {
-                        if (free()) {
+                        if (!wait.together(&bars.empty[stage], phase ^ 1)) goto loaded;
+                        if (umma::elect_one()) {
                             if (p.gate.p != nullptr) {
                                 mbar_expect_tx(&bars.full[stage], 128 * p.tpt * p.G);
                                 tma_load_3d(ring + stage * G::STAGE, &gate_map, c % (D / 64) * 64, w.head * p.G,
@@ -431,6 +430,9 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                 i = w.first;
             }
         }
+    loaded:
+        bars.loaded = {stage, phase};
+        bars.units = units;
     } else if (any && warp == G::WARPS + 1) {
         // ---- products.  The whole warp goes through the loop, so that operands stay uniform; one lane issues.
         const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -753,8 +755,11 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
     __syncthreads();
     umma::fence_after_sync();
     if (dead && threadIdx.x == 0) {
-        bars.issued.land(bars.full, p.err);
-        bars.issued_q.land(&bars.q_full, p.err);
+        for (int i = 0; i < G::STAGES; ++i) {
+            const bool passed = bars.passed >= 0 && (i + G::STAGES - bars.passed) % G::STAGES < G::PER_STEP;
+            wait_end(&bars.full[i], bars.loaded.parity(i) ^ (uint32_t)passed, p.err);
+        }
+        wait_end(&bars.q_full, (bars.units & 1) ^ 1, p.err);
     }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
 }
