@@ -291,6 +291,16 @@ __device__ __forceinline__ bool all_nan(const float (&x)[N]) {
     return __all_sync(0xffffffffu, nan);
 }
 
+// Whether a row in memory is finite.
+template <int D>
+__device__ __forceinline__ bool finite_row(const uint16_t *p) {
+    float x[D / 32], check = 0.0f;
+    lane_row<D>(p, x);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) check = fmaf(x[i], 0.0f, check);   // (0 times an infinity or NaN)
+    return __all_sync(0xffffffffu, check == 0.0f);
+}
+
 // x *= f; returns whether one of them is not finite.
 __device__ __forceinline__ bool scaled(float (&x)[32], float f) {
     float check = 0.0f;

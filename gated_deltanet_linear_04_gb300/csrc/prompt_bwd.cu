@@ -83,6 +83,7 @@ struct Params {
     float *delta;
     uint16_t *acc_out[2];
     float *part;             // [slot][acc][D / 4][128][4]
+    int *again;              // [CTA]: rows of its whole tiles are not finite, and are left to the joins; null: no joins follow
     unsigned *err;
     int Hq, Hkv, G, box, tps;   // tokens: of 64 query rows, of a step
 };
@@ -238,7 +239,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead;
+    __shared__ int dead, again;   // again: rows are not finite
     __shared__ __align__(16) Stats stats[G::KEYS ? kStats : 1];
     __shared__ float swap[G::KEYS || G::TURNS ? 1 : 256];   // deltas of a tile of one step: [half][row]
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -249,7 +250,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         umma::tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        dead = 0;
+        dead = again = 0;
         bars.loaded1 = bars.loaded2 = {0, 0};
         bars.units = 0;
         for (int i = 0; i < 5; ++i) {
@@ -735,7 +736,12 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                     if (whole) {
                         const bool bad = scaled(v, f);
                         write_group<D>(turn, rows, valid, d, v);
-                        mend_rows<G>(p, o, w.u, r, of_p, valid && bad, p.acc_out[a], d, d + 32);
+                        // (where no joins follow a row meets six steps' others at most; what meets more would take longer
+                        // than the bounded waits of the other warps allow)
+                        if (p.again == nullptr)
+                            mend_rows<G>(p, o, w.u, r, of_p, valid && bad, p.acc_out[a], d, d + 32);
+                        else if (valid && bad)
+                            again = 1;
                     } else {
                         float4 *dst = reinterpret_cast<float4 *>(p.part) +
                                       (((size_t)slot * G::ACCS + a) * (D / 4) + d / 4) * 128 + r;
@@ -763,12 +769,33 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
         if (G::A2_SMEM) wait_end(&bars.a2_full, (bars.units & 1) ^ 1, p.err);
     }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0 && p.again != nullptr) p.again[blockIdx.x] = again && !dead;
+}
+
+// The rows of a CTA's whole tiles that are not finite once more, a row a warp (the `at`th of `warps`).
+template <class G>
+__device__ __noinline__ void rows_again(const Params &p, int cta, int at, int warps) {
+    Walk w;
+    if (!w.begin(p.list, cta)) return;
+    do {
+        if (!w.whole()) continue;
+        for (int x = at; x < 128 * G::ACCS; x += warps) {
+            const int r = x % 128, a = x / 128;
+            const RowOut o = row_out<G>(p, w.u, w.head, r);
+            const int n = G::KEYS ? w.u.n_b : w.u.lim0 + (int)(o.token - w.u.a0);
+            uint16_t *out = p.acc_out[a] + o.at * G::D;
+            if (!o.valid || n <= 0 || finite_row<G::D>(out)) continue;
+            exact_row<G::D, G::KEYS>(p, o.token, o.head, w.u.b0, n, r, w.u.lim0, a == 1 || !G::HAS_DP, out, 0, G::D);
+        }
+    } while (w.next());
 }
 
 // Split tiles' parts added up: 32 channels of 128 rows a block.
 template <class G>
 __device__ __forceinline__ void join_parts(const Params &p, int slice, uint8_t (&turn)[4][G::TURN]) {
     constexpr int D = G::D;
+    if (p.again[blockIdx.x] != 0) rows_again<G>(p, blockIdx.x, slice * 4 + (threadIdx.x >> 5), G::ACCS * (D / 32) * 4);
+    if (blockIdx.x + 1 == gridDim.x) return;   // (no tile goes on behind the last share)
     const Parts part = parts_from(p.list, blockIdx.x);
     if (part.n == 0) return;
     const int a = slice / (D / 32), c = slice % (D / 32), r = threadIdx.x;
@@ -916,7 +943,7 @@ PromptList k_list(const PromptSizes &s) {
 }
 
 struct Workspace {
-    size_t k, d_o, delta, part[3], total;
+    size_t k, d_o, delta, part[3], again, total;
 };
 
 Workspace workspace(const PromptSizes &s, bool gated) {
@@ -928,7 +955,8 @@ Workspace workspace(const PromptSizes &s, bool gated) {
     w.part[0] = w.d_o + (gated ? up256((size_t)s.Nq * s.Hq * s.D * 2) : 0);
     w.part[1] = w.part[0] + part;
     w.part[2] = w.part[1] + part;      // (up to 128 channels: the second half of dK and dV's)
-    w.total = w.part[2] + part;
+    w.again = w.part[2] + part;
+    w.total = w.again + up256(3 * (size_t)num_sms() * sizeof(int));
     return w;
 }
 
@@ -1013,7 +1041,13 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
     pk.a2 = v;
     pk.part = part(1);
     pk.tps = tps;
+    // (no keys, or no queries: no tile has more than a step)
+    const bool joined = !none && !no_q && (prompt_splits(s, seqs, lists[0]) || prompt_splits(s, seqs, lists[1]));
+    int *again = joined ? reinterpret_cast<int *>(ws + w.again) : nullptr;
+    pq.again = again;
+    pk.again = joined ? again + num_sms() : nullptr;
     Params pv = pk;
+    pv.again = joined ? again + 2 * num_sms() : nullptr;
     pk.acc_out[0] = dk;
     pk.acc_out[1] = dv;
     pv.acc_out[0] = dv;
@@ -1026,9 +1060,8 @@ cudaError_t launch_d(const PromptSizes &s, const PromptSeqs &seqs, const HeadsIn
         if (e == cudaSuccess && !none) e = launch_pass<Geo<D, kDKV>>(mq, mg, mk, mv, pk, st);
     }
     if (e != cudaSuccess) return e;
-    // (no keys, or no queries: no tile has more than a step)
-    if (none || no_q || !(prompt_splits(s, seqs, lists[0]) || prompt_splits(s, seqs, lists[1]))) return cudaSuccess;
-    return DependentLaunch(dim3(num_sms() - 1, 3 * (D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<D>, pq, pk, pv);
+    if (!joined) return cudaSuccess;
+    return DependentLaunch(dim3(num_sms(), 3 * (D / 32)), dim3(128), 0, st)(prompt_backward_join_kernel<D>, pq, pk, pv);
 }
 
 }  // namespace

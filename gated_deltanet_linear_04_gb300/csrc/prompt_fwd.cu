@@ -101,17 +101,7 @@ __device__ __forceinline__ void pair_sync(int tile) {
         asm volatile("bar.sync 2, 256;" ::: "memory");
 }
 
-// `threads` threads meet (barrier `id`); whether one of them has x.
-__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, %2, %3, a;\n\t"
-        "selp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(id), "r"(threads)
-        : "memory");
-    return r != 0;
-}
+__device__ __forceinline__ void team_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // Scores that are not to be seen (from `lim` on) are -infinity.
 __device__ __forceinline__ void hide(float (&s)[32], int lim) {
@@ -280,17 +270,36 @@ __device__ __forceinline__ void mend_rows(const Params &p, const RowOut &o, cons
     }
 }
 
+// Behind the CTA's roles: the rows of its whole tiles that are not finite once more, by the definition, a row a warp.  (Not
+// before: a row of many keys takes longer than the bounded waits of the roles allow.)
+template <int D>
+__device__ __forceinline__ void rows_again(const Params &p) {
+    Walk w;
+    if (!w.begin(p.list, blockIdx.x)) return;
+    do {
+        if (!w.whole()) continue;   // (joined later, in prompt_join_kernel)
+        for (int r = threadIdx.x >> 5; r < Geo<D>::TILES * 128; r += Geo<D>::THREADS / 32) {
+            const RowOut o = row_out<D>(p, w.u, w.head, r / 128, r % 128);
+            if (!o.mine || o.keys == 0 || finite_row<D>(p.out + o.at * D)) continue;
+            const long long n = o.at / p.Hq;
+            const int h = (int)(o.at - n * p.Hq);
+            exact_row<D>(p.q.p + n * p.q.ts + h * p.q.hs, p.k.p + w.u.b0 * p.k.ts + w.head * p.k.hs, p.k.ts,
+                         p.v.p + w.u.b0 * p.v.ts + w.head * p.v.hs, p.v.ts, o.keys, p.scale, o.gate, p.out + o.at * D, 0, D, false);
+        }
+    } while (w.next());
+}
+
 template <int D_>
 __global__ void __launch_bounds__(Geo<D_>::THREADS, 1)
 prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap gate_map,
-                      const __grid_constant__ CUtensorMap out_map, const Params p) {
+                      const __grid_constant__ CUtensorMap out_map, const __grid_constant__ Params p) {
     using G = Geo<D_>;
     constexpr int D = D_;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead;
+    __shared__ int dead, again;   // again: rows are not finite
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *ring = smem + G::TILES * G::QTILE;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -300,7 +309,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         umma::tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        dead = 0;
+        dead = again = 0;
         bars.loaded = {0, 0};
         bars.units = 0;
         bars.passed = -1;
@@ -704,9 +713,8 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
             }
             if (whole) {
                 if (half == 0 && p.lse != nullptr && o.mine) p.lse[o.at] = o.keys > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
-                if (!G::STAGED) {
-                    mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
-                } else {
+                if (bad && o.keys > 0) again = 1;
+                if (G::STAGED) {
                     const bool complete = (tile + 1) * p.tpt <= w.u.slot_a;   // all rows are the sequence's
                     if (!complete) {
                         __syncwarp();
@@ -720,7 +728,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                         }
                     }
                     fence_proxy_async_smem();
-                    const bool any = any_of(team, team_size, bad);
+                    team_sync(team, team_size);
                     if (leader) {
                         constexpr int N = SHARED ? 1 : DH / 64;
                         const int at = at0 + (SHARED ? 0 : half * N);
@@ -729,18 +737,11 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
                                 tma_store_3d(&out_map, (SHARED ? 0 : half * DH) + c * 64, w.head * p.G, w.u.a0 + tile * p.tpt,
                                              ring + (at + c) % G::STAGES * G::STAGE);
                             bulk_commit();
-                            if (any)
-                                bulk_wait_all();   // (rows that are written once more)
-                            else
-                                bulk_wait_read();
+                            bulk_wait_read();
                         }
                         for (int c = 0; c < N; ++c) mbar_arrive(&bars.empty[(at + c) % G::STAGES]);
                     }
                     __syncwarp();
-                    if (any) {
-                        any_of(team, team_size, false);
-                        mend_rows<D>(p, o, w.u, w.head, bad, half * DH, (half + 1) * DH);
-                    }
                     ++wholes;
                 }
             } else if (half == 0) {
@@ -762,6 +763,7 @@ prompt_forward_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_co
         wait_end(&bars.q_full, (bars.units & 1) ^ 1, p.err);
     }
     if (warp == 0) umma::tmem_dealloc(tmem, 512);
+    if (again && !dead) rows_again<D>(p);
 }
 
 // Every row by the definition: for scales that are not positive, whose scores'
