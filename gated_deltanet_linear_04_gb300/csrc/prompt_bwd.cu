@@ -241,7 +241,7 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
     __shared__ uint32_t tmem_slot;
     __shared__ int dead, again;   // again: rows are not finite
     __shared__ __align__(16) Stats stats[G::KEYS ? kStats : 1];
-    __shared__ float swap[G::KEYS || G::TURNS ? 1 : 256];   // deltas of a tile of one step: [half][row]
+    __shared__ float swap[G::KEYS || G::TURNS ? 1 : 256];   // deltas of rows of few keys: [half][row]
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -584,10 +584,8 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
             keys = 0;
             if (!G::KEYS && o.valid) {
                 keys = max(u.lim0 + (int)(o.token - u.a0), 0);
-                if (keys > 0) {
-                    nlse = -kLog2e * p.lse[o.at];
-                    delta = p.delta[o.at];
-                }
+                if (keys > 0) nlse = -kLog2e * p.lse[o.at];
+                if (keys > kRows) delta = p.delta[o.at];   // (else known at step 0; later steps have nothing for the row)
             }
         };
         row_stats(o, w.u);
@@ -656,20 +654,23 @@ prompt_backward_kernel(const __grid_constant__ CUtensorMap map1, const __grid_co
                         for (int k = 0; k < G::COLS; ++k)
                             if (k >= lim) s[k / 32][k % 32] = dp[k / 32][k % 32] = 0.0f;
                     }
-                    if (w.u.steps == 1) {
-                        // all of a row's keys at hand: its delta from P and dP themselves (the output's rounding to bf16 is
-                        // too coarse for rows of few keys), also for the kernels that come after
+                    if (i == 0 && w.u.lim0 <= kRows) {
+                        // rows that see no key behind this step: their delta from P and dP themselves (the output's rounding
+                        // to bf16 is too coarse for rows of few keys), also for the kernels that come after
                         float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                         for (int k = 0; k < G::COLS; ++k) t[k & 3] = fmaf(s[k / 32][k % 32], dp[k / 32][k % 32], t[k & 3]);
-                        delta = (t[0] + t[1]) + (t[2] + t[3]);
+                        float sum = (t[0] + t[1]) + (t[2] + t[3]);
                         if (!G::TURNS) {
-                            swap[half * 128 + r] = delta;
+                            swap[half * 128 + r] = sum;
                             meet();
-                            delta = swap[r] + swap[128 + r];
+                            sum = swap[r] + swap[128 + r];
                             meet();
                         }
-                        if (o.valid && (G::TURNS || half == 0)) p.delta[o.at] = delta;
+                        if (keys <= kRows) {
+                            delta = sum;
+                            if (o.valid && (G::TURNS || half == 0)) p.delta[o.at] = delta;
+                        }
                     }
                 }
                 if (step >= G::XB) wait(&bars.x_free[(step - G::XB) & 1], ((step - G::XB) >> 1) & 1);

@@ -641,9 +641,9 @@ GDN_API gdn_status gdn_attn_prefill(const gdn_attn_dims *dims, int64_t q_rows, i
  *          bytes (gated: whether there is a gate) on the device that runs the
  *          call: work lists, delta, dO and partial sums
  * P and dS are rounded to bf16 for their products, dO too where there is a gate;
- * delta is taken from out, for queries that see no more than 64 keys mostly from
- * P and dP themselves, where out's rounding would be too coarse.  Sums are f32 in
- * a fixed order: equal calls give equal bits.  Padding gives zeros, rows in no
+ * delta is taken from out, for queries that see no more than 64 keys from P and
+ * dP themselves, where out's rounding would be too coarse.  Sums are f32 in a
+ * fixed order: equal calls give equal bits.  Padding gives zeros, rows in no
  * slot are left as they were; a query that sees no key has no gradient. */
 GDN_API size_t gdn_attn_prefill_backward_workspace_size(const gdn_attn_dims *dims, int64_t q_rows, int64_t k_rows,
                                                         int32_t gated);
