@@ -39,7 +39,7 @@ struct RowParams {
     HeadsIn q, k, v;
     const float *wq, *wk;
     const uint64_t *freqs;
-    const int32_t *pos;     // dense: [B, T], null with several axes; append: [B]
+    const int32_t *pos;     // dense: [B, T], not read with several axes; append: [B]
     const uint8_t *mask;
     const int32_t *n_new;
     const uint16_t *dq_out, *dk_out;
@@ -175,14 +175,14 @@ __device__ __forceinline__ F2 partners(const Row &x, int k) {
 // for channels that do not turn.  The warp computes the angles together, into
 // its table; four entries behind them hold (1, 0).  With several axes a pair
 // turns by the token's position on its own.
-template <bool INTER>
+template <bool INTER, bool AXES>
 __device__ __forceinline__ void lane_angles(const RowParams &p, float2 *table, const Pieces &pc, unsigned bt,
                                             long long pos, bool back, Row &a, Row &b) {
     const int lane = threadIdx.x & 31, half = p.R / 2;
     __syncwarp();   // (the previous token's readers)
     for (int i = lane; i < half; i += 32) {
         long long at = pos;
-        if (p.axes.axis != nullptr) at = p.axes.pos[(long long)min((int)p.axes.axis[i], p.axes.n - 1) * p.B * p.T + bt];
+        if (AXES) at = p.axes.pos[(long long)min((int)p.axes.axis[i], p.axes.n - 1) * p.B * p.T + bt];
         rope_angle(at, p.freqs[i], table[i].x, table[i].y);
     }
     if (lane < 4) table[half + lane] = make_float2(1.0f, 0.0f);
@@ -256,7 +256,7 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-template <int D, bool INTER, int MODE, int ROWS>
+template <int D, bool INTER, int MODE, int ROWS, bool AXES>
 __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, GROUP = ROWS < 4 ? ROWS : 4;
     extern __shared__ __align__(16) uint16_t stages[];
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
     } else if (!on) {
         return;
     }
-    const long long pos = MODE == kDense ? (p.pos != nullptr ? p.pos[bt] : 0) : (long long)p.pos[b] + t;
+    const long long pos = MODE != kDense ? (long long)p.pos[b] + t : AXES ? 0 : p.pos[bt];
     long long at = -1;   // the cache row of head h0
     if (MODE != kDense && !isq) {
         at = cache_row(p.c, p.Hkv, p.c.table + (long long)b * p.c.width, pos, 0);
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) row_forward_kernel(const RowParam
     Row A, B;
     const float *wp = isq ? p.wq : p.wk;
     const bool norm = !isv && wp != nullptr;
-    if (!isv) lane_angles<INTER>(p, tables[warp], pc, bt, pos, false, A, B);
+    if (!isv) lane_angles<INTER, AXES>(p, tables[warp], pc, bt, pos, false, A, B);
     if (norm) {
         const Row w = load_weights(wp, pc);
 #pragma unroll
@@ -409,7 +409,7 @@ constexpr int kBwdRows = 4;
 // Backward: a CTA belongs to one part of the heads (p.aq CTAs to each of q's, the
 // first; p.ak to each of k's), its warps go from token to token; it sums its share
 // of dw and leaves it in `partial`.
-template <int D, bool INTER>
+template <int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(const RowParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kBwdRows, HALF = ROWS * RPW * D, STAGE = 2 * HALF;
     extern __shared__ __align__(16) uint16_t stages[];
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) row_backward_kernel(cons
             continue;
         }
         Row a, b;
-        lane_angles<INTER>(p, tables[warp], pc, bt, p.pos != nullptr ? p.pos[bt] : 0, true, a, b);
+        lane_angles<INTER, AXES>(p, tables[warp], pc, bt, AXES ? 0 : p.pos[bt], true, a, b);
         cp_async_wait<1>();
         __syncwarp();
         const uint16_t *src = ring + stage * STAGE + sub * D;
@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *partial, 
 
 int chunks_of(int heads, int rows) { return (heads + rows - 1) / rows; }
 
-template <int D, bool INTER, int MODE, int ROWS>
-cudaError_t launch_forward_rows(RowParams p, cudaStream_t st) {
+template <int D, bool INTER, int MODE, int ROWS, bool AXES>
+cudaError_t launch_forward_axes(RowParams p, cudaStream_t st) {
     constexpr int RPW = 32 / (D / 8);
     constexpr size_t smem = (size_t)kWarps * ROWS * RPW * D * 2;
     p.cq = chunks_of(p.Hq, ROWS * RPW);
@@ -565,10 +565,17 @@ cudaError_t launch_forward_rows(RowParams p, cudaStream_t st) {
     const long long tokens = (long long)p.B * p.T, ctas = (tokens + kWarps - 1) / kWarps;
     if (tokens > 0x7fffffffLL - kWarps) return cudaErrorNotSupported;
     static unsigned long long done = 0;
-    cudaError_t e = set_max_smem(done, row_forward_kernel<D, INTER, MODE, ROWS>, smem);
+    cudaError_t e = set_max_smem(done, row_forward_kernel<D, INTER, MODE, ROWS, AXES>, smem);
     if (e != cudaSuccess) return e;
     return DependentLaunch(dim3((unsigned)ctas, p.cq + p.ck * (MODE == kDense ? 1 : 2)), dim3(kThreads), smem,
-                           st)(row_forward_kernel<D, INTER, MODE, ROWS>, p);
+                           st)(row_forward_kernel<D, INTER, MODE, ROWS, AXES>, p);
+}
+
+// (Positions on one axis have kernels of their own: asked at run time it takes a token 1 % longer, 2.5 % in the gradients.)
+template <int D, bool INTER, int MODE, int ROWS>
+cudaError_t launch_forward_rows(const RowParams &p, cudaStream_t st) {
+    return p.axes.axis != nullptr ? launch_forward_axes<D, INTER, MODE, ROWS, true>(p, st)
+                                  : launch_forward_axes<D, INTER, MODE, ROWS, false>(p, st);
 }
 
 // Eight rows a warp, or one where there are too few tokens to fill the GPU (16 +
@@ -583,19 +590,20 @@ cudaError_t launch_forward(const RowParams &p, bool inter, cudaStream_t st) {
     return inter ? launch_forward_rows<D, true, MODE, 8>(p, st) : launch_forward_rows<D, false, MODE, 8>(p, st);
 }
 
-template <int D, bool INTER>
+template <int D, bool INTER, bool AXES>
 cudaError_t launch_backward_i(const RowParams &p, cudaStream_t st) {
     constexpr size_t smem = (size_t)kWarps * kStages * 2 * kBwdRows * 512;   // (a warp's rows: 512 bytes)
     static unsigned long long done = 0;
-    cudaError_t e = set_max_smem(done, row_backward_kernel<D, INTER>, smem);
+    cudaError_t e = set_max_smem(done, row_backward_kernel<D, INTER, AXES>, smem);
     if (e != cudaSuccess) return e;
     return DependentLaunch(dim3(p.cq * p.aq + p.ck * p.ak), dim3(kThreads), smem,
-                           st)(row_backward_kernel<D, INTER>, p);
+                           st)(row_backward_kernel<D, INTER, AXES>, p);
 }
 
 template <int D>
 cudaError_t launch_backward_rows(const RowParams &p, bool inter, cudaStream_t st) {
-    return inter ? launch_backward_i<D, true>(p, st) : launch_backward_i<D, false>(p, st);
+    if (p.axes.axis != nullptr) return inter ? launch_backward_i<D, true, true>(p, st) : launch_backward_i<D, false, true>(p, st);
+    return inter ? launch_backward_i<D, true, false>(p, st) : launch_backward_i<D, false, false>(p, st);
 }
 
 template <int MODE>
@@ -609,14 +617,15 @@ cudaError_t launch_forward_d(const RowParams &p, int D, bool inter, cudaStream_t
 }
 
 RowParams row_params(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq, const float *wk,
-                     const uint64_t *freqs, const int32_t *pos) {
+                     const uint64_t *freqs, const int32_t *pos, const AxesIn &axes) {
     RowParams p = {};
     p.q = q;
     p.k = k;
     p.wq = wq;
     p.wk = wk;
     p.freqs = freqs;
-    p.pos = pos;
+    p.axes = axes;
+    p.pos = pos != nullptr ? pos : axes.pos;   // (several axes of which no pair turns: as one)
     p.B = s.B;
     p.T = s.T;
     p.Hq = s.Hq;
@@ -653,8 +662,7 @@ struct BackwardGrid {
 cudaError_t launch_qk_norm_rope(const AttnSizes &s, const HeadsIn &q, const HeadsIn &k, const float *wq,
                                 const float *wk, const uint64_t *freqs, const int32_t *pos, const uint8_t *mask,
                                 uint16_t *q_out, uint16_t *k_out, cudaStream_t st, const AxesIn &axes) {
-    RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
-    p.axes = axes;
+    RowParams p = row_params(s, q, k, wq, wk, freqs, pos, axes);
     p.mask = mask;
     p.q_out = q_out;
     p.k_out = k_out;
@@ -665,8 +673,7 @@ cudaError_t launch_kv_append(const AttnSizes &s, const HeadsIn &q, const HeadsIn
                              const float *wq, const float *wk, const uint64_t *freqs, const PagedCache &c,
                              const int32_t *pos, const int32_t *n_new, uint16_t *q_out, unsigned *err,
                              cudaStream_t st, const AxesIn &axes) {
-    RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
-    p.axes = axes;
+    RowParams p = row_params(s, q, k, wq, wk, freqs, pos, axes);
     p.v = v;
     p.c = c;
     p.n_new = n_new;
@@ -685,8 +692,7 @@ cudaError_t launch_qk_norm_rope_backward(const AttnSizes &s, const HeadsIn &q, c
                                          const uint8_t *mask, const uint16_t *dq_out, const uint16_t *dk_out,
                                          uint16_t *dq, uint16_t *dk, float *dwq, float *dwk, void *ws,
                                          cudaStream_t st, const AxesIn &axes) {
-    RowParams p = row_params(s, q, k, wq, wk, freqs, pos);
-    p.axes = axes;
+    RowParams p = row_params(s, q, k, wq, wk, freqs, pos, axes);
     p.mask = mask;
     p.dq_out = dq_out;
     p.dk_out = dk_out;
