@@ -317,7 +317,10 @@ def attn_prefill(dims, q, k, v, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=N
     prefix; the last query of a sequence sees its last key.  q [B, T, Hq, D] and
     k, v [B, Tk, Hkv, D] with lengths n_q, n_k (None: all), or packed: q [N, Hq,
     D] with offsets cu_q [B + 1], k, v [M, Hkv, D] with cu_k (None: cu_q).  Returns
-    out shaped as q, or (out, lse)."""
+    out shaped as q, or (out, lse).  Rows in no slot (before cu_q[0], from cu_q[B]
+    on; all rows, if the offsets are not in order: GDN_ERR_BAD_OFFSETS) are not
+    written: in these new tensors they hold whatever their memory did.  Where such
+    rows are read, hand tensors of your own to gdn_attn_prefill."""
     c = _dims(dims)
     return _bind().attn_prefill(_at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, dims.D ** -0.5 if scale is None else scale,
                                 None, None, bool(return_lse), workspace, _handle(stream))
@@ -326,7 +329,10 @@ def attn_prefill(dims, q, k, v, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=N
 def attn_prefill_backward(dims, q, k, v, out, lse, dout, cu_q=None, cu_k=None, n_q=None, n_k=None, gate=None, scale=None,
                           workspace=None, stream=None):
     """Gradients of attn_prefill, from its inputs, its results out and lse, and
-    the gradient of out; returns a dict dq, dk, dv and, with a gate, dgate (bf16)."""
+    the gradient of out; returns a dict dq, dk, dv and, with a gate, dgate (bf16).
+    Rows in no slot are not written, as in attn_prefill: mask them, or hand zeroed
+    tensors to gdn_attn_prefill_backward, before their sum goes into another
+    gradient (a norm's weights)."""
     c = _dims(dims)
     dq, dk, dv, dgate = _bind().attn_prefill_backward(
         _at(c), q, k, v, cu_q, cu_k, n_q, n_k, gate, dims.D ** -0.5 if scale is None else scale, out, lse, dout, None, None,

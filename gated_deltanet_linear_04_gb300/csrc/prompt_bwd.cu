@@ -23,11 +23,12 @@
 //     shared memory, the A operands of the accumulating products.
 //   - The lists, shares and joins are those of the forward pass (prompt.cuh).
 //
-// Measured on a GB300, per 10 D operations of a seen pair: 8192 tokens, 16 query
-// heads on 2, 256 channels, gate: 1440-1465 us, 940-955 TFLOP/s (dQ 507, dK 496,
-// dV 339, gate and delta 47, join 23, tensor cores 71 to 78 % busy); 8 sequences of 100 to 2045
-// tokens packed, 32 on 8, 128 channels: 365 us, 656 TFLOP/s (dQ 146, dK and dV
-// 176).  Steps are bound by the shared memory's bandwidth: dQ
+// Measured on a GB300, per 10 D operations of a seen pair, calls on fresh inputs
+// (in brackets on the same again and again): 8192 tokens, 16 query heads on 2, 256
+// channels, gate: 1540-1600 us, 860-895 TFLOP/s (1480-1550; dQ 501, dK 504, dV 361,
+// gate and delta 49, join 23, tensor cores 71 to 78 % busy); 8 sequences of 100 to
+// 2045 tokens packed, 32 on 8, 128 channels: 370 us, 646 TFLOP/s (369; dQ 146, dK and
+// dV 178).  Steps are bound by the shared memory's bandwidth: dQ
 // with 128 channels reads 64 KB and writes 48 for 768 cycles of products, some
 // 900 cycles at 128 bytes a clock (a second buffer of S and dP changed nothing:
 // 382 us for 383).  Pairs of CTAs that share the rows that pass by would halve

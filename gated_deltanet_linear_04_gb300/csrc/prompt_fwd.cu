@@ -26,12 +26,13 @@
 //     tile, and a few rows with many keys use all of them.
 //
 // Measured on a GB300 (operations of seen pairs; a large bf16 product of the
-// library reaches 1882 TFLOP/s): 8192 tokens, 16 query heads on 2, 256 channels,
-// gate: 353-358 us, 1540 TFLOP/s; 8 sequences of 100 to 4093 tokens packed, 32
-// on 8, 128 channels: 300 us, 1247; 512 tokens behind long prefixes: 119 us, 1370;
-// one prompt of 77 tokens: 11 us, two launches.  With 256 channels a step takes
-// some 2300 cycles for 2048 cycles of products, and a tile's end 13000 (its
-// results, of all warps) beside which only the next tile's first scores run.
+// library reaches 1882 TFLOP/s; calls on fresh inputs, in brackets on the same
+// again and again): 8192 tokens, 16 query heads on 2, 256 channels, gate: 383 us,
+// 1435 TFLOP/s (352, 1560); 8 sequences of 100 to 4093 tokens packed, 32 on 8, 128
+// channels: 310 us, 1206 (301, 1243); 512 tokens behind long prefixes: 123 us, 1325
+// (119, 1370); one prompt of 77 tokens: 11 to 13 us, two launches.  With 256 channels
+// a step takes some 2300 cycles for 2048 cycles of products, and a tile's end 13000
+// (its results, of all warps) beside which only the next tile's first scores run.
 // With 128 channels keys, values and P's reads fill the shared memory's
 // bandwidth next to the tensor cores, 2600 cycles for 2048.
 #include "prompt_row.cuh"
@@ -57,8 +58,8 @@ struct Geo {
     static constexpr int WARPS = 4 * HALVES * TILES;
     static constexpr int THREADS = 32 * (WARPS + 2);
     static constexpr int TURN = 32 * 32;                   // bytes in which a warp turns 16 channels of its rows into rows
-    // Results go through stages of the ring, into which their gates come by TMA, and out by TMA (packed, 128 channels: 300 us;
-    // turned into rows by each warp 343).  With 256 channels they would take four of nine stages while the next tile's keys
+    // Results go through stages of the ring, into which their gates come by TMA, and out by TMA (packed, 128 channels, the
+    // same inputs again: 300 us; turned into rows by each warp 343).  With 256 channels they would take four of nine stages while the next tile's keys
     // and values need them: there they are turned (T = 8192: 353 us; through the ring 367).
     static constexpr bool STAGED = TILES == 2;
     static constexpr int RESULTS = STAGED ? TILES * (D / 64) : 0;   // stages of a unit's results

@@ -1,7 +1,8 @@
 // One query row of a prompt's attention by the definition, key by key, in a
 // warp: for rows whose result on the tensor cores is not finite.  There a
 // masked weight of 0 meets whatever value lies in an unseen slot, and 0 times
-// an infinity or NaN is NaN; here unseen keys are not touched.
+// an infinity or NaN is NaN; here unseen keys are not touched.  Some 0.7 us a
+// key: not for warps beside which others wait with a limit.
 #pragma once
 
 #include "prompt.cuh"

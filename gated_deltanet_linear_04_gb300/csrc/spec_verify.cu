@@ -16,10 +16,12 @@
 // on enter exactly, smaller ones rounded to the unit.
 //
 // B = 128, four drafts, V = 131072, half of the rows with a draft's row to read
-// (125 MB): 29.6 us, 4.2 TB/s: the reads' own time is 18.5 us, the rest is the
-// launch, the chain of three loads before a row is known, the clusters' meeting
-// and the second look at a piece.  One row of 32003: 5.4 us, a launch and a chain
-// of five loads.
+// (125 MB): 29.1 us, 4.3 TB/s.  The reads' own time is 18.5 us.  About half of the
+// rest is the launch, the chain of three loads before a row is known, the clusters'
+// meeting and the second look at a piece (what one row takes, 5.4 us); the other
+// half is that a thread has eight loads (sixteen with a draft) in flight, 32 to
+// 64 KB an SM, and none while it sums their digits.  One row of 32003: 5.4 us, a
+// launch and a chain of five loads.
 #include <cooperative_groups.h>
 
 #include "attn.cuh"
