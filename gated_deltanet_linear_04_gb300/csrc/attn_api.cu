@@ -104,18 +104,17 @@ bool ok_axes(const AttnSizes &s, const gdn::AxesIn &x, bool several, size_t n) {
     return !several || ((x.axis != nullptr || s.Drot == 0) && x.n >= 1 && x.n <= 8 && gdn::ok(x.pos, n, 4));
 }
 
-gdn_status norm_rope(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
-                            int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
-                            const float *wq, const float *wk, const uint64_t *freqs, const int32_t *pos,
-                            const uint8_t *mask, uint16_t *q_out, uint16_t *k_out, gdn_stream stream, bool several,
-                            const gdn::AxesIn &axes) {
+gdn_status norm_rope(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,
+                     const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride, const float *wq,
+                     const float *wk, const uint64_t *freqs, const int32_t *pos, const uint8_t *mask, uint16_t *q_out,
+                     uint16_t *k_out, gdn_stream stream, bool several, const gdn::AxesIn &axes) {
     AttnSizes s;
     gdn_status st = gdn::check(dims, &s);
     if (st != GDN_OK) return st;
     const size_t n = (size_t)s.B * s.T;
     const HeadsIn hq{q, q_token_stride, q_head_stride}, hk{k, k_token_stride, k_head_stride};
-    if (!gdn::ok_heads(hq, n) || !gdn::ok_heads(hk, n) || !gdn::ok_norm(s, wq, wk, freqs) || !gdn::ok(pos, several ? 0 : n, 4) || !ok_axes(s, axes, several, n) ||
-        !gdn::ok(q_out, n) || !gdn::ok(k_out, n))
+    if (!gdn::ok_heads(hq, n) || !gdn::ok_heads(hk, n) || !gdn::ok_norm(s, wq, wk, freqs) ||
+        !gdn::ok(pos, several ? 0 : n, 4) || !ok_axes(s, axes, several, n) || !gdn::ok(q_out, n) || !gdn::ok(k_out, n))
         return GDN_ERR_INVALID_ARG;
     if (n == 0) return GDN_OK;
     return gdn::from(
@@ -124,19 +123,19 @@ gdn_status norm_rope(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_tok
 }
 
 gdn_status norm_rope_backward(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
-                                     int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
-                                     int64_t k_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
-                                     const int32_t *pos, const uint8_t *mask, const uint16_t *dq_out,
-                                     const uint16_t *dk_out, uint16_t *dq, uint16_t *dk, float *dwq, float *dwk,
-                                     void *workspace, size_t ws_bytes, gdn_stream stream, bool several, const gdn::AxesIn &axes) {
+                              int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
+                              const float *wq, const float *wk, const uint64_t *freqs, const int32_t *pos,
+                              const uint8_t *mask, const uint16_t *dq_out, const uint16_t *dk_out, uint16_t *dq,
+                              uint16_t *dk, float *dwq, float *dwk, void *workspace, size_t ws_bytes,
+                              gdn_stream stream, bool several, const gdn::AxesIn &axes) {
     AttnSizes s;
     gdn_status st = gdn::check(dims, &s);
     if (st != GDN_OK) return st;
     const size_t n = (size_t)s.B * s.T;
     const HeadsIn hq{q, q_token_stride, q_head_stride}, hk{k, k_token_stride, k_head_stride};
-    if (!gdn::ok_heads(hq, n) || !gdn::ok_heads(hk, n) || !gdn::ok_norm(s, wq, wk, freqs) || !gdn::ok(pos, several ? 0 : n, 4) ||
-        !ok_axes(s, axes, several, n) ||
-        !gdn::ok(dq_out, n) || !gdn::ok(dk_out, n) || !gdn::ok(dq, n) || !gdn::ok(dk, n))
+    if (!gdn::ok_heads(hq, n) || !gdn::ok_heads(hk, n) || !gdn::ok_norm(s, wq, wk, freqs) ||
+        !gdn::ok(pos, several ? 0 : n, 4) || !ok_axes(s, axes, several, n) || !gdn::ok(dq_out, n) ||
+        !gdn::ok(dk_out, n) || !gdn::ok(dq, n) || !gdn::ok(dk, n))
         return GDN_ERR_INVALID_ARG;
     const bool norm = wq != nullptr;
     if (!gdn::ok(dwq, norm) || !gdn::ok(dwk, norm) || (!norm && (dwq != nullptr || dwk != nullptr)))
@@ -156,11 +155,11 @@ gdn_status norm_rope_backward(const gdn_attn_dims *dims, const uint16_t *q, int6
 }
 
 gdn_status kv_append(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,
-                         const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
-                         int64_t v_token_stride, int64_t v_head_stride, const float *wq, const float *wk,
-                         const uint64_t *freqs, const gdn_kv_cache *cache, const int32_t *page_table,
-                         int32_t table_width, const int32_t *pos, const int32_t *n_new, uint16_t *q_out,
-                         gdn_stream stream, bool several, const gdn::AxesIn &axes) {
+                     const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
+                     int64_t v_token_stride, int64_t v_head_stride, const float *wq, const float *wk,
+                     const uint64_t *freqs, const gdn_kv_cache *cache, const int32_t *page_table, int32_t table_width,
+                     const int32_t *pos, const int32_t *n_new, uint16_t *q_out, gdn_stream stream, bool several,
+                     const gdn::AxesIn &axes) {
     AttnSizes s;
     PagedCache c;
     gdn_status st = gdn::check(dims, &s);
@@ -188,17 +187,17 @@ gdn_status gdn_qk_norm_rope(const gdn_attn_dims *dims, const uint16_t *q, int64_
                             int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
                             const float *wq, const float *wk, const uint64_t *freqs, const int32_t *pos,
                             const uint8_t *mask, uint16_t *q_out, uint16_t *k_out, gdn_stream stream) {
-    return norm_rope(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, pos, mask, q_out, k_out,
-                     stream, false, gdn::AxesIn());
+    return norm_rope(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, pos,
+                     mask, q_out, k_out, stream, false, gdn::AxesIn());
 }
 
 gdn_status gdn_qk_norm_rope_axes(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
-                            int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
-                            const float *wq, const float *wk, const uint64_t *freqs, const uint8_t *axes, int32_t n_axes,
-                            const int32_t *pos,
-                            const uint8_t *mask, uint16_t *q_out, uint16_t *k_out, gdn_stream stream) {
-    return norm_rope(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, nullptr, mask, q_out, k_out,
-                     stream, true, gdn::AxesIn{axes, n_axes, pos});
+                                 int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                 int64_t k_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
+                                 const uint8_t *axes, int32_t n_axes, const int32_t *pos, const uint8_t *mask,
+                                 uint16_t *q_out, uint16_t *k_out, gdn_stream stream) {
+    return norm_rope(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, nullptr,
+                     mask, q_out, k_out, stream, true, gdn::AxesIn{axes, n_axes, pos});
 }
 
 size_t gdn_qk_norm_rope_backward_workspace_size(const gdn_attn_dims *dims) {
@@ -213,18 +212,21 @@ gdn_status gdn_qk_norm_rope_backward(const gdn_attn_dims *dims, const uint16_t *
                                      const int32_t *pos, const uint8_t *mask, const uint16_t *dq_out,
                                      const uint16_t *dk_out, uint16_t *dq, uint16_t *dk, float *dwq, float *dwk,
                                      void *workspace, size_t ws_bytes, gdn_stream stream) {
-    return norm_rope_backward(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, pos, mask,
-                              dq_out, dk_out, dq, dk, dwq, dwk, workspace, ws_bytes, stream, false, gdn::AxesIn());
+    return norm_rope_backward(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs,
+                              pos, mask, dq_out, dk_out, dq, dk, dwq, dwk, workspace, ws_bytes, stream, false,
+                              gdn::AxesIn());
 }
 
 gdn_status gdn_qk_norm_rope_axes_backward(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
-                                     int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
-                                     int64_t k_head_stride, const float *wq, const float *wk, const uint64_t *freqs,
-                                     const uint8_t *axes, int32_t n_axes, const int32_t *pos, const uint8_t *mask, const uint16_t *dq_out,
-                                     const uint16_t *dk_out, uint16_t *dq, uint16_t *dk, float *dwq, float *dwk,
-                                     void *workspace, size_t ws_bytes, gdn_stream stream) {
-    return norm_rope_backward(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs, nullptr, mask,
-                              dq_out, dk_out, dq, dk, dwq, dwk, workspace, ws_bytes, stream, true, gdn::AxesIn{axes, n_axes, pos});
+                                          int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride,
+                                          int64_t k_head_stride, const float *wq, const float *wk,
+                                          const uint64_t *freqs, const uint8_t *axes, int32_t n_axes,
+                                          const int32_t *pos, const uint8_t *mask, const uint16_t *dq_out,
+                                          const uint16_t *dk_out, uint16_t *dq, uint16_t *dk, float *dwq, float *dwk,
+                                          void *workspace, size_t ws_bytes, gdn_stream stream) {
+    return norm_rope_backward(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, wq, wk, freqs,
+                              nullptr, mask, dq_out, dk_out, dq, dk, dwq, dwk, workspace, ws_bytes, stream, true,
+                              gdn::AxesIn{axes, n_axes, pos});
 }
 
 gdn_status gdn_kv_append(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,
@@ -233,19 +235,21 @@ gdn_status gdn_kv_append(const gdn_attn_dims *dims, const uint16_t *q, int64_t q
                          const uint64_t *freqs, const gdn_kv_cache *cache, const int32_t *page_table,
                          int32_t table_width, const int32_t *pos, const int32_t *n_new, uint16_t *q_out,
                          gdn_stream stream) {
-    return kv_append(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, wq, wk,
-                     freqs, cache, page_table, table_width, pos, n_new, q_out, stream, false, gdn::AxesIn());
+    return kv_append(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, v, v_token_stride,
+                     v_head_stride, wq, wk, freqs, cache, page_table, table_width, pos, n_new, q_out, stream, false,
+                     gdn::AxesIn());
 }
 
-gdn_status gdn_kv_append_axes(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride, int64_t q_head_stride,
-                         const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t *v,
-                         int64_t v_token_stride, int64_t v_head_stride, const float *wq, const float *wk,
-                         const uint64_t *freqs, const uint8_t *axes, int32_t n_axes, const int32_t *rope_pos,
-                         const gdn_kv_cache *cache, const int32_t *page_table,
-                         int32_t table_width, const int32_t *pos, const int32_t *n_new, uint16_t *q_out,
-                         gdn_stream stream) {
-    return kv_append(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, wq, wk,
-                     freqs, cache, page_table, table_width, pos, n_new, q_out, stream, true, gdn::AxesIn{axes, n_axes, rope_pos});
+gdn_status gdn_kv_append_axes(const gdn_attn_dims *dims, const uint16_t *q, int64_t q_token_stride,
+                              int64_t q_head_stride, const uint16_t *k, int64_t k_token_stride, int64_t k_head_stride,
+                              const uint16_t *v, int64_t v_token_stride, int64_t v_head_stride, const float *wq,
+                              const float *wk, const uint64_t *freqs, const uint8_t *axes, int32_t n_axes,
+                              const int32_t *rope_pos, const gdn_kv_cache *cache, const int32_t *page_table,
+                              int32_t table_width, const int32_t *pos, const int32_t *n_new, uint16_t *q_out,
+                              gdn_stream stream) {
+    return kv_append(dims, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, v, v_token_stride,
+                     v_head_stride, wq, wk, freqs, cache, page_table, table_width, pos, n_new, q_out, stream, true,
+                     gdn::AxesIn{axes, n_axes, rope_pos});
 }
 
 gdn_status gdn_kv_read(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const int32_t *page_table,
