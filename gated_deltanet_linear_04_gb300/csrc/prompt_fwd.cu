@@ -59,8 +59,8 @@ struct Geo {
     static constexpr int THREADS = 32 * (WARPS + 2);
     static constexpr int TURN = 32 * 32;                   // bytes in which a warp turns 16 channels of its rows into rows
     // Results go through stages of the ring, into which their gates come by TMA, and out by TMA (packed, 128 channels, the
-    // same inputs again: 300 us; turned into rows by each warp 343).  With 256 channels they would take four of nine stages while the next tile's keys
-    // and values need them: there they are turned (T = 8192: 353 us; through the ring 367).
+    // same inputs again: 300 us; turned into rows by each warp 343).  With 256 channels they would take four of nine stages
+    // while the next tile's keys and values need them: there they are turned (T = 8192: 353 us; through the ring 367).
     static constexpr bool STAGED = TILES == 2;
     static constexpr int RESULTS = STAGED ? TILES * (D / 64) : 0;   // stages of a unit's results
     static constexpr int SMEM = TILES * QTILE + STAGES * STAGE + (STAGED ? 0 : WARPS * TURN) + 1024;
@@ -102,7 +102,10 @@ __device__ __forceinline__ void pair_sync(int tile) {
         asm volatile("bar.sync 2, 256;" ::: "memory");
 }
 
-__device__ __forceinline__ void team_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+// `threads` threads meet (barrier `id`).
+__device__ __forceinline__ void team_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 // Scores that are not to be seen (from `lim` on) are -infinity.
 __device__ __forceinline__ void hide(float (&s)[32], int lim) {
